@@ -416,6 +416,99 @@ SKG_API skg_status skg_group_check(skg_group_t group);
 /* Free the group (after its work finished). */
 SKG_API skg_status skg_group_destroy(skg_group_t group);
 
+/*
+ * The 8-bit path -- W8A8 projections of a decode layer or a prompt: weights and
+ * activations as 8-bit integers, half the weight bytes of skg_run.
+ *
+ *   rows:        q[m,k] in [-127, 127] (int8) with one fp32 scale per row m;
+ *                q[m,k] * scale[m] is the value it stands for.
+ *   projection:  y[m,n] = x_scale[m] * w_scale[n] * sum_k x[m,k] W[n,k]  (+ residual[m,n])
+ *
+ * Activations are rows per token (skg_rmsnorm_q8, skg_quantize_q8); a weight
+ * [N,K] is quantised once, rows per output channel, by skg_quantize_q8 too.
+ * These are serving operators: they have no gradients.
+ *
+ * Quantising a row v: scale = max|v| / 127, q = v * (127 / max|v|) rounded to
+ * the nearest integer, half to even.  A row of zeros has scale 0 and q = 0.  A
+ * row with a value that is not finite (NaN, infinity) has scale NaN and q = 0:
+ * a projection of that row is NaN, and no other row is affected.
+ *
+ * skg_rmsnorm_q8 -- residual addition, root-mean-square norm and quantisation
+ * of M >= 0 rows of any length K >= 1, in one kernel on `stream`:
+ *     h = x + residual (or x);   v = h / sqrt(mean(h^2) + eps) * gamma
+ *   x        bf16 [M, K], row stride ldx >= K elements; read-only
+ *   residual bf16 [M, K], row stride ldr >= K, or NULL
+ *   gamma    bf16 [K], or NULL for ones
+ *   h        bf16 [M, K], row stride ldh >= K, or NULL: the sum, rounded once
+ *            (the norm goes on from the unrounded sum); only with a residual.
+ *            May be the residual itself (same address and stride), or x
+ *   y        bf16 [M, K] dense, or NULL: v rounded once, for a bf16 projection
+ *   q, scale int8 [M, K] dense and fp32 [M]: the quantised rows of v
+ *   Any alignment the element types allow; 16-byte aligned rows are fastest.
+ *   M == 0 launches nothing.  Outputs must not overlap inputs except h as said.
+ * Errors: SKG_ERR_INVALID_ARG (sizes, strides, NULL, eps negative or not
+ * finite, h without residual), SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_rmsnorm_q8(int M, int K, float eps, const void *x, size_t ldx, const void *residual,
+                                  size_t ldr, const void *gamma, void *h, size_t ldh, void *y, void *q,
+                                  float *scale, void *stream);
+
+/*
+ * skg_quantize_q8 -- the rows of x, or of silu(gate) * x with
+ * silu(g) = g / (1 + exp(-g)), quantised as above: M >= 0 rows of any K >= 1.
+ *   x, gate  bf16 [M, K], row strides ldx, ldg >= K; gate may be NULL.  Both may
+ *            be halves of one [M, 2K] tensor
+ *   q, scale int8 [M, K] dense and fp32 [M]
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_quantize_q8(int M, int K, const void *x, size_t ldx, const void *gate, size_t ldg, void *q,
+                                   float *scale, void *stream);
+
+/* What an 8-bit plan will launch. */
+typedef struct skg_q8_plan_desc {
+    int M, N, K, epilogue;
+    int static_weights;         /* see skg_q8_plan */
+} skg_q8_plan_desc;
+
+typedef struct skg_q8_plan_s *skg_q8_plan_t;
+
+/*
+ * skg_q8_plan_query -- the launch of an 8-bit projection on a GPU with num_sms
+ * SMs, without touching any GPU.  1 <= M <= 262144 tokens, N >= 1, K a multiple
+ * of 16 in [16, 131056] (so that no sum of K products of 8-bit integers can
+ * leave 32 bits), epilogue as for skg_plan.
+ * Errors: SKG_ERR_INVALID_ARG (M, N, num_sms, epilogue, NULL),
+ * SKG_ERR_UNSUPPORTED (K, M above the limits).
+ */
+SKG_API skg_status skg_q8_plan_query(int M, int N, int K, int epilogue, int num_sms, skg_q8_plan_desc *out);
+
+/*
+ * skg_q8_plan -- build a plan for (M,N,K,epilogue) on the current device.
+ * static_weights != 0 promises that W and w_scale of every skg_q8_run were
+ * written long before it: by work that had completed before the kernel that
+ * precedes the run in its stream was launched.  The run may then request weight
+ * bytes while that kernel still finishes.  0: everything is read after it.
+ * Errors: as skg_q8_plan_query, plus SKG_ERR_CUDA.  *out is NULL on failure.
+ */
+SKG_API skg_status skg_q8_plan(int M, int N, int K, int epilogue, int static_weights, skg_q8_plan_t *out);
+
+/*
+ * skg_q8_run -- the 8-bit projection on `stream`.
+ *   x        int8 [M,K] dense, 16-byte aligned; x_scale fp32 [M]
+ *   W        int8 [N,K] dense, 16-byte aligned; w_scale fp32 [N]
+ *   residual bf16 [M,N], non-NULL iff the epilogue is SKG_EPI_BF16_RESIDUAL
+ *   y        [M,N] bf16 (fp32 for SKG_EPI_FP32); must not overlap the inputs
+ * The sum over k is the exact integer, so the result does not depend on the
+ * launch shape; it is scaled in fp32 as (sum * x_scale) * w_scale, the residual
+ * is added in fp32, and the result is rounded once.
+ * Allocates nothing.  Errors: SKG_ERR_INVALID_ARG, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_q8_run(skg_q8_plan_t plan, const void *x, const float *x_scale, const void *W,
+                              const float *w_scale, const void *residual, void *y, void *stream);
+
+/* Free the plan (after its work finished). */
+SKG_API skg_status skg_q8_plan_destroy(skg_q8_plan_t plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,4 +6,4 @@ computed by the CUDA kernels of ``lib/libskg.so`` behind the C ABI of
 synthetic operands; ``build`` compiles the library.
 """
 from . import skg  # noqa: F401
-from .skg import Plan, SkgError  # noqa: F401
+from .skg import Plan, Q8Plan, SkgError  # noqa: F401

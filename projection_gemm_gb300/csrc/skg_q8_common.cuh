@@ -1,0 +1,42 @@
+// skg_q8_common.cuh -- device code shared by the 8-bit path's kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "skg_q8_internal.h"
+
+namespace skg {
+
+__device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+
+__device__ __forceinline__ uint16_t f32_to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
+// silu(g) = g / (1 + exp(-g)), from exp(-|g|) so that neither side overflows
+// (at g = -89 exp(-g) has left fp32 while the quotient has not).
+__device__ __forceinline__ float silu(float g)
+{
+    const float e = __expf(-fabsf(g));
+    return g * __fdividef(g < 0.0f ? e : 1.0f, 1.0f + e);
+}
+
+// One output from its exact integer sum: the same four fp32 operations in the
+// same order in every kernel (no contraction), so that they agree bit for bit.
+__device__ __forceinline__ float q8_scaled(int sum, float xs, float ws)
+{
+    return __fmul_rn(__fmul_rn(__int2float_rn(sum), xs), ws);
+}
+
+__device__ __forceinline__ void q8_store(const Q8LinearParams &p, int m, int n, int sum, float xs, float ws)
+{
+    const size_t o = static_cast<size_t>(m) * p.N + n;
+    float v = q8_scaled(sum, xs, ws);
+    if (p.epilogue == SKG_EPI_FP32) {
+        static_cast<float *>(p.y)[o] = v;
+        return;
+    }
+    if (p.epilogue == SKG_EPI_BF16_RESIDUAL)
+        v = __fadd_rn(v, bf16_to_f32(p.res[o]));
+    static_cast<uint16_t *>(p.y)[o] = f32_to_bf16(v);
+}
+
+} // namespace skg

@@ -1,0 +1,44 @@
+// skg_q8_internal.h -- shared between the host ABI of the 8-bit path
+// (skg_q8_api.cu) and its kernels.  Not part of the public ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "skg.h"
+
+namespace skg {
+
+// One launch over the rows of a norm (gamma, eps) or a quantiser (gate).
+// Row strides are in elements.
+struct Q8RowParams {
+    const uint16_t *x;        // bf16 [M, K], row stride ldx
+    const uint16_t *second;   // residual (norm) or gate (quantiser), or null
+    const uint16_t *gamma;    // norm: bf16 [K], or null for ones
+    uint16_t *h;              // norm: bf16 x + residual, or null
+    uint16_t *y;              // norm: bf16 normalised rows, or null
+    int8_t *q;                // [M, K] dense
+    float *scale;             // [M]
+    size_t ldx, ld2, ldh;
+    int M, K;
+    float eps;
+};
+
+// y[m, n] = x_scale[m] * w_scale[n] * sum_k x[m, k] W[n, k] (+ residual).
+struct Q8LinearParams {
+    const int8_t *x;          // [M, K]
+    const float *x_scale;     // [M]
+    const int8_t *W;          // [N, K]
+    const float *w_scale;     // [N]
+    const uint16_t *res;      // bf16 [M, N] or null
+    void *y;                  // [M, N] bf16 or fp32
+    int M, N, K, epilogue;
+};
+
+cudaError_t launch_q8_norm(const Q8RowParams &p, cudaStream_t s);
+cudaError_t launch_q8_quantize(const Q8RowParams &p, cudaStream_t s);
+cudaError_t launch_q8_gemv(const Q8LinearParams &p, cudaStream_t s);
+
+} // namespace skg

@@ -41,6 +41,7 @@ EXPORTS = (
     "skg_run_noalloc", "skg_noalloc_check", "skg_plan_set_k_shard", "skg_combine_partials", "skg_plan_set_l2_ahead", "skg_plan_set_next_weight",
     "skg_plan_set_reducers",
     "skg_group", "skg_group_run", "skg_group_info", "skg_group_check", "skg_group_destroy",
+    "skg_rmsnorm_q8", "skg_quantize_q8", "skg_q8_plan_query", "skg_q8_plan", "skg_q8_run", "skg_q8_plan_destroy",
 )
 
 
@@ -66,6 +67,16 @@ class skg_plan_desc(ctypes.Structure):
         d = {f: getattr(self, f) for f, _ in self._fields_}
         d["kernel"] = KERNEL_NAMES.get(self.kernel_kind, "?")
         return d
+
+
+class skg_q8_plan_desc(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int), ("epilogue", ctypes.c_int),
+        ("static_weights", ctypes.c_int),
+    ]
+
+    def as_dict(self) -> dict:
+        return {f: getattr(self, f) for f, _ in self._fields_}
 
 
 _lib = None
@@ -106,6 +117,12 @@ def load(path: str = LIB_PATH):
     lib.skg_group_info.argtypes = [vp, P(i), P(i), P(i), P(i)]
     lib.skg_group_check.argtypes = [vp]
     lib.skg_group_destroy.argtypes = [vp]
+    lib.skg_rmsnorm_q8.argtypes = [i, i, ctypes.c_float, vp, sz, vp, sz, vp, vp, sz, vp, vp, vp, vp]
+    lib.skg_quantize_q8.argtypes = [i, i, vp, sz, vp, sz, vp, vp, vp]
+    lib.skg_q8_plan_query.argtypes = [i, i, i, i, i, P(skg_q8_plan_desc)]
+    lib.skg_q8_plan.argtypes = [i, i, i, i, i, P(vp)]
+    lib.skg_q8_run.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.skg_q8_plan_destroy.argtypes = [vp]
     for name in EXPORTS:
         getattr(lib, name).restype = ctypes.c_int
     lib.skg_last_error.restype = ctypes.c_char_p
@@ -349,6 +366,110 @@ class Group:
     def close(self):
         if self.handle:
             skg_group_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ------------------------------------------------------------ the 8-bit path
+def _bad(what: str):
+    raise SkgError(SKG_ERR_INVALID_ARG, what)
+
+
+def _rows(t, name, M, K, dtype) -> int:
+    """Row stride of a [M, K] tensor whose rows are contiguous."""
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != 2 or t.shape[0] != M or t.shape[1] != K:
+        _bad(f"{name} must be a CUDA tensor [{M}, {K}] of {dtype}")
+    ld, one = t.stride()
+    if M <= 1:
+        ld = K
+    if (one != 1 and K > 1) or ld < K:
+        _bad(f"{name}: elements of a row must be contiguous and rows must not overlap")
+    return ld
+
+
+def _dense(t, name, shape, dtype):
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        _bad(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
+    return t.data_ptr()
+
+
+def skg_rmsnorm_q8(x, residual, gamma, eps: float, h, q, scale, y=None, stream=None):
+    """x, residual, h: bf16 [M, K] (rows may be strided); gamma bf16 [K]; q int8 [M, K];
+    scale fp32 [M]; y bf16 [M, K].  residual, gamma, h and y may be None."""
+    import torch
+    bf16 = torch.bfloat16
+    if x.dim() != 2:
+        _bad("x must be [M, K]")
+    M, K = x.shape
+    ldx = _rows(x, "x", M, K, bf16)
+    ldr = 0 if residual is None else _rows(residual, "residual", M, K, bf16)
+    ldh = 0 if h is None else _rows(h, "h", M, K, bf16)
+    _check(load().skg_rmsnorm_q8(
+        M, K, eps, x.data_ptr(), ldx, _ptr(residual), ldr,
+        None if gamma is None else _dense(gamma, "gamma", (K,), bf16), _ptr(h), ldh,
+        None if y is None else _dense(y, "y", (M, K), bf16), _dense(q, "q", (M, K), torch.int8),
+        _dense(scale, "scale", (M,), torch.float32), _stream(stream)))
+
+
+def skg_quantize_q8(x, gate, q, scale, stream=None):
+    """x, gate: bf16 [M, K] (rows may be strided; gate may be None); q int8 [M, K]; scale fp32 [M]."""
+    import torch
+    if x.dim() != 2:
+        _bad("x must be [M, K]")
+    M, K = x.shape
+    ldx = _rows(x, "x", M, K, torch.bfloat16)
+    ldg = 0 if gate is None else _rows(gate, "gate", M, K, torch.bfloat16)
+    _check(load().skg_quantize_q8(M, K, x.data_ptr(), ldx, _ptr(gate), ldg, _dense(q, "q", (M, K), torch.int8),
+                                  _dense(scale, "scale", (M,), torch.float32), _stream(stream)))
+
+
+def skg_q8_plan_query(M: int, N: int, K: int, epilogue, num_sms: int) -> dict:
+    d = skg_q8_plan_desc()
+    _check(load().skg_q8_plan_query(M, N, K, _epi(epilogue), num_sms, ctypes.byref(d)))
+    return d.as_dict()
+
+
+def skg_q8_plan(M: int, N: int, K: int, epilogue, static_weights: bool = False) -> int:
+    h = ctypes.c_void_p()
+    _check(load().skg_q8_plan(M, N, K, _epi(epilogue), 1 if static_weights else 0, ctypes.byref(h)))
+    return h.value
+
+
+def skg_q8_run(plan: int, x, x_scale, W, w_scale, residual, y, stream=None):
+    _check(load().skg_q8_run(plan, _ptr(x), _ptr(x_scale), _ptr(W), _ptr(w_scale), _ptr(residual), _ptr(y),
+                             _stream(stream)))
+
+
+def skg_q8_plan_destroy(plan: int):
+    _check(load().skg_q8_plan_destroy(plan))
+
+
+class Q8Plan:
+    """Owns one 8-bit projection plan; run checks the tensors against it."""
+
+    def __init__(self, M: int, N: int, K: int, epilogue="bf16", static_weights: bool = False):
+        self.M, self.N, self.K = M, N, K
+        self.epilogue = _epi(epilogue)
+        self.handle = skg_q8_plan(M, N, K, self.epilogue, static_weights)
+
+    def run(self, x, x_scale, W, w_scale, residual, y, stream=None):
+        import torch
+        M, N, K = self.M, self.N, self.K
+        out = torch.float32 if self.epilogue == SKG_EPI_FP32 else torch.bfloat16
+        _check(load().skg_q8_run(
+            self.handle, _dense(x, "x", (M, K), torch.int8), _dense(x_scale, "x_scale", (M,), torch.float32),
+            _dense(W, "W", (N, K), torch.int8), _dense(w_scale, "w_scale", (N,), torch.float32),
+            None if residual is None else _dense(residual, "residual", (M, N), torch.bfloat16),
+            _dense(y, "y", (M, N), out), _stream(stream)))
+
+    def close(self):
+        if self.handle:
+            skg_q8_plan_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

@@ -1,0 +1,103 @@
+"""The 8-bit path's host side without a GPU: the plan query's limits and the
+refusals of every entry point (each is refused before anything is launched)."""
+import ctypes
+
+import pytest
+
+from projection_gemm_gb300 import build, skg
+
+SMS = 152
+FAKE = 1 << 20          # an address that is never read: the calls below are refused or launch nothing
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    skg.load()
+
+
+@pytest.mark.parametrize("args,status", [
+    ((0, 128, 128, "bf16", SMS), skg.SKG_ERR_INVALID_ARG),
+    ((4, 0, 128, "bf16", SMS), skg.SKG_ERR_INVALID_ARG),
+    ((4, 128, 128, 3, SMS), skg.SKG_ERR_INVALID_ARG),
+    ((4, 128, 128, -1, SMS), skg.SKG_ERR_INVALID_ARG),
+    ((4, 128, 128, "bf16", 0), skg.SKG_ERR_INVALID_ARG),
+    ((4, 128, 0, "bf16", SMS), skg.SKG_ERR_UNSUPPORTED),
+    ((4, 128, 24, "bf16", SMS), skg.SKG_ERR_UNSUPPORTED),
+    ((4, 128, 131072, "bf16", SMS), skg.SKG_ERR_UNSUPPORTED),
+    (((1 << 18) + 1, 128, 128, "bf16", SMS), skg.SKG_ERR_UNSUPPORTED),
+])
+def test_query_refusals(args, status):
+    with pytest.raises(skg.SkgError) as e:
+        skg.skg_q8_plan_query(*args)
+    assert e.value.status == status and skg.skg_last_error()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (64, 7168, 7168), (1 << 18, 3, 131056)])
+def test_query_limits_are_inside(M, N, K):
+    d = skg.skg_q8_plan_query(M, N, K, "fp32", SMS)
+    assert (d["M"], d["N"], d["K"], d["epilogue"]) == (M, N, K, skg.SKG_EPI_FP32)
+
+
+def _norm(M=2, K=8, eps=1e-6, x=FAKE, ldx=8, r=None, ldr=0, gamma=None, h=None, ldh=0, y=None, q=FAKE, s=FAKE):
+    return skg.load().skg_rmsnorm_q8(M, K, eps, x, ldx, r, ldr, gamma, h, ldh, y, q, s, None)
+
+
+def _quant(M=2, K=8, x=FAKE, ldx=8, g=None, ldg=0, q=FAKE, s=FAKE):
+    return skg.load().skg_quantize_q8(M, K, x, ldx, g, ldg, q, s, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(M=-1), dict(K=0), dict(x=None), dict(q=None), dict(s=None), dict(ldx=7), dict(eps=-1.0),
+    dict(eps=float("nan")), dict(eps=float("inf")), dict(h=FAKE, ldh=8), dict(r=FAKE, ldr=7),
+    dict(r=FAKE, ldr=8, h=FAKE, ldh=7),
+])
+def test_norm_refuses(kw):
+    assert _norm(**kw) == skg.SKG_ERR_INVALID_ARG
+    assert "skg_rmsnorm_q8" in skg.skg_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=FAKE + 1), dict(s=FAKE + 2), dict(r=FAKE + 1, ldr=8), dict(gamma=FAKE + 1), dict(y=FAKE + 1),
+    dict(r=FAKE, ldr=8, h=FAKE + 1, ldh=8),
+])
+def test_norm_refuses_misaligned(kw):
+    assert _norm(**kw) == skg.SKG_ERR_ALIGNMENT
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), skg.SKG_ERR_INVALID_ARG), (dict(K=0), skg.SKG_ERR_INVALID_ARG),
+    (dict(x=None), skg.SKG_ERR_INVALID_ARG), (dict(q=None), skg.SKG_ERR_INVALID_ARG),
+    (dict(s=None), skg.SKG_ERR_INVALID_ARG), (dict(ldx=7), skg.SKG_ERR_INVALID_ARG),
+    (dict(g=FAKE, ldg=7), skg.SKG_ERR_INVALID_ARG), (dict(g=FAKE + 1, ldg=8), skg.SKG_ERR_ALIGNMENT),
+    (dict(x=FAKE + 1), skg.SKG_ERR_ALIGNMENT),
+])
+def test_quantize_refuses(kw, status):
+    assert _quant(**kw) == status
+
+
+def test_no_rows_launch_nothing():
+    assert _norm(M=0) == skg.SKG_OK and _norm(M=0, x=None, q=None, s=None) == skg.SKG_OK
+    assert _quant(M=0) == skg.SKG_OK
+
+
+def test_plan_handles_are_checked():
+    lib = skg.load()
+    assert lib.skg_q8_run(None, FAKE, FAKE, FAKE, FAKE, None, FAKE, None) == skg.SKG_ERR_INVALID_ARG
+    assert lib.skg_q8_plan(4, 128, 128, 0, 0, None) == skg.SKG_ERR_INVALID_ARG
+    assert lib.skg_q8_plan_query(4, 128, 128, 0, SMS, None) == skg.SKG_ERR_INVALID_ARG
+    assert lib.skg_q8_plan_destroy(None) == skg.SKG_OK
+    h = ctypes.c_void_p(FAKE)
+    assert lib.skg_q8_plan(4, 128, 20, 0, 0, ctypes.byref(h)) == skg.SKG_ERR_UNSUPPORTED
+    assert h.value is None
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    x = torch.zeros(2, 32, dtype=torch.bfloat16)
+    q, s = torch.zeros(2, 32, dtype=torch.int8), torch.zeros(2)
+    for call in (lambda: skg.skg_rmsnorm_q8(x, None, None, 1e-6, None, q, s),
+                 lambda: skg.skg_quantize_q8(x, None, q, s)):
+        with pytest.raises(skg.SkgError) as e:
+            call()
+        assert e.value.status == skg.SKG_ERR_INVALID_ARG
