@@ -464,10 +464,22 @@ SKG_API skg_status skg_rmsnorm_q8(int M, int K, float eps, const void *x, size_t
 SKG_API skg_status skg_quantize_q8(int M, int K, const void *x, size_t ldx, const void *gate, size_t ldg, void *q,
                                    float *scale, void *stream);
 
+typedef enum skg_q8_kernel_kind {
+    SKG_Q8_KERNEL_DP4A = 1,     /* CUDA cores: int8 dot products, one output channel per warp */
+    SKG_Q8_KERNEL_TC = 2        /* TMA + tcgen05 on integers widened to fp16, exact */
+} skg_q8_kernel_kind;
+
 /* What an 8-bit plan will launch. */
 typedef struct skg_q8_plan_desc {
+    int kernel_kind;            /* skg_q8_kernel_kind */
     int M, N, K, epilogue;
     int static_weights;         /* see skg_q8_plan */
+    int m_tile;                 /* tokens per tile (TC: 16, 32, 64, 128 or 192) or per warp (DP4A) */
+    int tiles;                  /* output tiles: 128 channels x m_tile tokens (TC) */
+    int full_waves;             /* TC: whole tiles each CTA computes before the rest is shared */
+    int shared_ctas;            /* TC: CTAs that share the K ranges of the tiles left over */
+    int grid, threads, smem_bytes, stages, ctas_per_sm;
+    size_t workspace_bytes;     /* TC: int32 sums and counters of shared tiles, and x as fp16 for M > 64 */
 } skg_q8_plan_desc;
 
 typedef struct skg_q8_plan_s *skg_q8_plan_t;
@@ -478,7 +490,7 @@ typedef struct skg_q8_plan_s *skg_q8_plan_t;
  * of 16 in [16, 131056] (so that no sum of K products of 8-bit integers can
  * leave 32 bits), epilogue as for skg_plan.
  * Errors: SKG_ERR_INVALID_ARG (M, N, num_sms, epilogue, NULL),
- * SKG_ERR_UNSUPPORTED (K, M above the limits).
+ * SKG_ERR_UNSUPPORTED (K, M above the limits, or more than 2^30 tiles).
  */
 SKG_API skg_status skg_q8_plan_query(int M, int N, int K, int epilogue, int num_sms, skg_q8_plan_desc *out);
 
@@ -488,6 +500,8 @@ SKG_API skg_status skg_q8_plan_query(int M, int N, int K, int epilogue, int num_
  * written long before it: by work that had completed before the kernel that
  * precedes the run in its stream was launched.  The run may then request weight
  * bytes while that kernel still finishes.  0: everything is read after it.
+ * Allocates the launch's workspace and a mapped host word for device-side error
+ * reports; free the plan with skg_q8_plan_destroy.
  * Errors: as skg_q8_plan_query, plus SKG_ERR_CUDA.  *out is NULL on failure.
  */
 SKG_API skg_status skg_q8_plan(int M, int N, int K, int epilogue, int static_weights, skg_q8_plan_t *out);
@@ -501,10 +515,34 @@ SKG_API skg_status skg_q8_plan(int M, int N, int K, int epilogue, int static_wei
  * The sum over k is the exact integer, so the result does not depend on the
  * launch shape; it is scaled in fp32 as (sum * x_scale) * w_scale, the residual
  * is added in fp32, and the result is rounded once.
- * Allocates nothing.  Errors: SKG_ERR_INVALID_ARG, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
+ * Allocates nothing.  One run of a plan may be in flight at a time (the
+ * workspace is shared); concurrent streams need separate plans.
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_ALIGNMENT, SKG_ERR_DEVICE_TIMEOUT
+ * (reported by an earlier launch of this plan), SKG_ERR_CUDA.
  */
 SKG_API skg_status skg_q8_run(skg_q8_plan_t plan, const void *x, const float *x_scale, const void *W,
                               const float *w_scale, const void *residual, void *y, void *stream);
+
+/*
+ * skg_q8_plan_force -- override of the kernel choice (tests and measurements):
+ * kind (an skg_q8_kernel_kind, 0 keeps), and for TC m_tile (16, 32, 64, 128,
+ * 192; 0 = chosen) and ctas, the most CTAs launched (0 = chosen).  Results do
+ * not change.  A larger workspace is allocated where needed and the old one kept
+ * until the plan is destroyed, as by skg_plan_force.
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_q8_plan_force(skg_q8_plan_t plan, int kind, int m_tile, int ctas);
+
+/* Copy the plan's launch description into *out. */
+SKG_API skg_status skg_q8_plan_info(skg_q8_plan_t plan, skg_q8_plan_desc *out);
+
+/* Synchronise the plan's last stream and report a bounded wait that ran out
+ * since the last check (SKG_ERR_DEVICE_TIMEOUT, then cleared) or a pending CUDA
+ * error, as skg_plan_check.  skg_q8_run reports such a timeout too. */
+SKG_API skg_status skg_q8_plan_check(skg_q8_plan_t plan);
+
+/* skg_debug_wait_timeout with the word of an 8-bit plan. */
+SKG_API skg_status skg_q8_debug_wait_timeout(skg_q8_plan_t plan, unsigned long long timeout_ns, void *stream);
 
 /* Free the plan (after its work finished). */
 SKG_API skg_status skg_q8_plan_destroy(skg_q8_plan_t plan);

@@ -340,19 +340,7 @@ EncodeTiledFn get_encode()
 // zero fill outside the tensor.
 skg_status encode_2d(CUtensorMap *m, const void *base, int rows, int cols, int box_rows)
 {
-    EncodeTiledFn enc = get_encode();
-    if (!enc)
-        return fail(SKG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBlockK), static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
-                           box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        return fail(SKG_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for [%d,%d]", (int)r, rows, cols);
-    return SKG_OK;
+    return encode_tiled_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols, box_rows);
 }
 
 constexpr int kMapCache = 4;
@@ -412,6 +400,24 @@ skg_status set_error(skg_status st, const char *fmt, ...)
     va_end(ap);
     g_last_error = buf;
     return st;
+}
+
+skg_status encode_tiled_2d(CUtensorMap *m, CUtensorMapDataType type, int elem_bytes, const void *base, int rows,
+                           int cols, int box_rows)
+{
+    EncodeTiledFn enc = get_encode();
+    if (!enc)
+        return fail(SKG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem_bytes};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem_bytes), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(m, type, 2, const_cast<void *>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(SKG_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for [%d,%d]", (int)r, rows, cols);
+    return SKG_OK;
 }
 
 skg_status prepare_splitk_launch(int M, int N, int K, int epi, const void *x, const void *W,

@@ -138,6 +138,7 @@ constexpr unsigned kErrTimeoutProducer = 1u << 0;
 constexpr unsigned kErrTimeoutMma = 1u << 1;
 constexpr unsigned kErrTimeoutEpilogue = 1u << 2;
 constexpr unsigned kErrTimeoutDebug = 1u << 3;
+constexpr unsigned kErrTimeoutWiden = 1u << 4;
 
 // Bytes of fp32 split-K partials: S x ceil(N / 128) tiles x [M][128].
 inline size_t tc_partial_bytes(int M, int N, int split)
@@ -182,6 +183,11 @@ cudaError_t launch_combine(const float *const *partials, int ranks, const uint16
 cudaError_t launch_debug_wait(unsigned int *err, unsigned long long timeout_ns, cudaStream_t s);
 // Records a failure message for skg_last_error and returns st.
 skg_status set_error(skg_status st, const char *fmt, ...);
+
+// 2-D row-major [rows, cols] of elem_bytes-wide elements, dense, read in boxes
+// of [box_rows, 128 bytes] with the 128-byte swizzle, zero outside the tensor.
+skg_status encode_tiled_2d(CUtensorMap *m, CUtensorMapDataType type, int elem_bytes, const void *base, int rows,
+                           int cols, int box_rows);
 
 // Everything one split-K launch needs, worked out on the host without
 // allocating: the checks of skg_run, the launch shape the picker chooses on

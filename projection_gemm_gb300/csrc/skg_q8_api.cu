@@ -1,7 +1,9 @@
 // skg_q8_api.cu -- host side of the 8-bit path of include/skg.h: argument
 // checks, plans and launches.
+#include <algorithm>
 #include <cstdint>
 #include <new>
+#include <vector>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -14,6 +16,14 @@ using namespace skg;
 
 struct skg_q8_plan_s {
     skg_q8_plan_desc d;
+    int num_sms = 0;
+    char *ws = nullptr;               // int32 sums, counters, then x as fp16
+    size_t ws_cap = 0;
+    std::vector<void *> retired;      // outgrown workspaces: a captured graph may still use them
+    bool dirty = false;               // a launch gave up and may have left sums behind
+    unsigned int *err_host = nullptr; // mapped pinned word
+    unsigned int *err_dev = nullptr;
+    cudaStream_t last_stream = nullptr;
 };
 
 namespace {
@@ -40,6 +50,86 @@ skg_status launched(cudaError_t e, const char *who)
 {
     return e == cudaSuccess ? SKG_OK
                             : set_error(SKG_ERR_CUDA, "%s: %s (%s)", who, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+constexpr int kQ8Band = 8;            // token tiles per band of the tile order
+constexpr int kQ8BlockK = 128;        // k per unit of the tensor-core kernel
+constexpr int kDp4aMaxM = 2;
+
+size_t sums_bytes(const skg_q8_plan_desc &d)
+{
+    return static_cast<size_t>(d.shared_ctas) * (static_cast<size_t>(d.m_tile) * kTileN * 4);
+}
+
+size_t counter_bytes(const skg_q8_plan_desc &d) { return (static_cast<size_t>(d.shared_ctas) * 4 + 255) / 256 * 256; }
+
+// Tokens per tile: the smallest of 16, 32, 64 that holds M; above 64, 128 or
+// 192, whichever pads M less (192 where they tie: fewer passes over W).
+int choose_tile(int M)
+{
+    if (M <= 64)
+        return M <= 16 ? 16 : (M <= 32 ? 32 : 64);
+    const int a = (M + 127) / 128 * 128, b = (M + 191) / 192 * 192;
+    return a < b ? 128 : 192;
+}
+
+skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int ctas, int num_sms, const char *who)
+{
+    d->kernel_kind = kind ? kind : (d->M <= kDp4aMaxM ? SKG_Q8_KERNEL_DP4A : SKG_Q8_KERNEL_TC);
+    d->m_tile = d->tiles = d->full_waves = d->shared_ctas = d->smem_bytes = d->stages = 0;
+    d->workspace_bytes = 0;
+    if (d->kernel_kind == SKG_Q8_KERNEL_DP4A) {
+        d->m_tile = d->M == 1 ? 1 : 8;
+        d->threads = 256;
+        d->ctas_per_sm = 8;
+        const long long grid = (static_cast<long long>(d->N) + 7) / 8 * ((d->M + d->m_tile - 1) / d->m_tile);
+        if (grid > (1ll << 30))
+            return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^30 CTAs", who);
+        d->grid = static_cast<int>(grid);
+        return SKG_OK;
+    }
+    d->m_tile = m_tile ? m_tile : choose_tile(d->M);
+    const Q8TcShape sh = q8_tc_shape(d->m_tile);
+    const long long tiles = (static_cast<long long>(d->N) + kTileN - 1) / kTileN * ((d->M + d->m_tile - 1) / d->m_tile);
+    if (tiles > (1ll << 30))
+        return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^30 tiles", who);
+    const int nkb = (d->K + kQ8BlockK - 1) / kQ8BlockK;
+    const int most = ctas ? ctas : num_sms * sh.ctas_per_sm;
+    d->tiles = static_cast<int>(tiles);
+    d->grid = static_cast<int>(std::min<long long>(most, tiles * nkb));
+    d->full_waves = d->tiles / d->grid;
+    const int left = d->tiles % d->grid;
+    d->shared_ctas = static_cast<int>(std::min<long long>(d->grid, static_cast<long long>(left) * nkb));
+    d->threads = sh.threads;
+    d->smem_bytes = sh.smem_bytes;
+    d->stages = sh.stages;
+    d->ctas_per_sm = sh.ctas_per_sm;
+    d->workspace_bytes = sums_bytes(*d) + counter_bytes(*d);
+    if (d->m_tile > 64)
+        d->workspace_bytes += static_cast<size_t>(d->M) * d->K * 2;
+    return SKG_OK;
+}
+
+// A workspace for the plan's launch, its sums and counters zero.
+skg_status ensure_workspace(skg_q8_plan_s *p, const char *who)
+{
+    const size_t need = p->d.workspace_bytes;
+    cudaError_t e = cudaSuccess;
+    if (need > p->ws_cap) {
+        char *ws = nullptr;
+        e = cudaMalloc(reinterpret_cast<void **>(&ws), need);
+        if (e != cudaSuccess)
+            return launched(e, who);
+        if (p->ws)
+            p->retired.push_back(p->ws);
+        p->ws = ws;
+        p->ws_cap = need;
+    }
+    if (need)
+        e = cudaMemset(p->ws, 0, sums_bytes(p->d) + counter_bytes(p->d));
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(nullptr);
+    return launched(e, who);
 }
 
 } // namespace
@@ -124,8 +214,10 @@ skg_status skg_q8_plan_query(int M, int N, int K, int epilogue, int num_sms, skg
     d.N = N;
     d.K = K;
     d.epilogue = epilogue;
-    *out = d;
-    return SKG_OK;
+    const skg_status st = fill_launch(&d, 0, 0, 0, num_sms, who);
+    if (st == SKG_OK)
+        *out = d;
+    return st;
 }
 
 skg_status skg_q8_plan(int M, int N, int K, int epilogue, int static_weights, skg_q8_plan_t *out)
@@ -135,15 +227,69 @@ skg_status skg_q8_plan(int M, int N, int K, int epilogue, int static_weights, sk
         return set_error(SKG_ERR_INVALID_ARG, "%s: out is NULL", who);
     *out = nullptr;
     skg_q8_plan_desc d;
-    const skg_status st = skg_q8_plan_query(M, N, K, epilogue, 1, &d);
+    skg_status st = skg_q8_plan_query(M, N, K, epilogue, 1, &d);     // the arguments alone
     if (st != SKG_OK)
         return st;
-    d.static_weights = static_weights != 0;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return launched(e, who);
     skg_q8_plan_s *p = new (std::nothrow) skg_q8_plan_s();
     if (!p)
         return set_error(SKG_ERR_CUDA, "%s: out of host memory", who);
     p->d = d;
+    p->d.static_weights = static_weights != 0;
+    p->num_sms = sms;
+    st = fill_launch(&p->d, 0, 0, 0, sms, who);
+    if (st == SKG_OK)
+        st = launched(cudaHostAlloc(reinterpret_cast<void **>(&p->err_host), sizeof(unsigned int), cudaHostAllocMapped), who);
+    if (st == SKG_OK) {
+        *p->err_host = 0;
+        st = launched(cudaHostGetDevicePointer(reinterpret_cast<void **>(&p->err_dev), p->err_host, 0), who);
+    }
+    if (st == SKG_OK)
+        st = ensure_workspace(p, who);
+    if (st != SKG_OK) {
+        skg_q8_plan_destroy(p);
+        return st;
+    }
     *out = p;
+    return SKG_OK;
+}
+
+skg_status skg_q8_plan_force(skg_q8_plan_t p, int kind, int m_tile, int ctas)
+{
+    static const char who[] = "skg_q8_plan_force";
+    if (!p)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: plan is NULL", who);
+    if (kind != 0 && kind != SKG_Q8_KERNEL_DP4A && kind != SKG_Q8_KERNEL_TC)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: unknown kernel kind %d", who, kind);
+    if (m_tile != 0 && m_tile != 16 && m_tile != 32 && m_tile != 64 && m_tile != 128 && m_tile != 192)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile must be 0, 16, 32, 64, 128 or 192 (got %d)", who, m_tile);
+    if (ctas < 0 || ctas > (1 << 16))
+        return set_error(SKG_ERR_INVALID_ARG, "%s: ctas must be in [0, 65536] (got %d)", who, ctas);
+    skg_q8_plan_desc d = p->d;
+    const int k = kind ? kind : d.kernel_kind;
+    if (k == SKG_Q8_KERNEL_DP4A && (m_tile || ctas))
+        return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile and ctas belong to the tensor-core kernel", who);
+    skg_status st = fill_launch(&d, k, m_tile, ctas, p->num_sms, who);
+    if (st != SKG_OK)
+        return st;
+    const skg_q8_plan_desc old = p->d;
+    p->d = d;
+    st = ensure_workspace(p, who);
+    if (st != SKG_OK)
+        p->d = old;
+    return st;
+}
+
+skg_status skg_q8_plan_info(skg_q8_plan_t p, skg_q8_plan_desc *out)
+{
+    if (!p || !out)
+        return set_error(SKG_ERR_INVALID_ARG, "skg_q8_plan_info: plan and out must be non-NULL");
+    *out = p->d;
     return SKG_OK;
 }
 
@@ -165,6 +311,12 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
     if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(y, d.epilogue == SKG_EPI_FP32 ? 4 : 2) ||
         !aligned(residual, 2))
         return set_error(SKG_ERR_ALIGNMENT, "%s: a scale, y or residual misses its element alignment", who);
+    if (__atomic_exchange_n(p->err_host, 0u, __ATOMIC_ACQ_REL) != 0) {
+        p->dirty = true;
+        return set_error(SKG_ERR_DEVICE_TIMEOUT, "%s: an earlier launch of this plan ran out of a bounded wait", who);
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    p->last_stream = s;
     Q8LinearParams g = {};
     g.x = static_cast<const int8_t *>(x);
     g.x_scale = x_scale;
@@ -176,11 +328,86 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
     g.N = d.N;
     g.K = d.K;
     g.epilogue = d.epilogue;
-    return launched(launch_q8_gemv(g, static_cast<cudaStream_t>(stream)), who);
+    if (d.kernel_kind == SKG_Q8_KERNEL_DP4A)
+        return launched(launch_q8_gemv(g, s), who);
+
+    Q8TcParams t = {};
+    t.g = g;
+    t.ws = reinterpret_cast<int *>(p->ws);
+    t.counters = reinterpret_cast<unsigned *>(p->ws + sums_bytes(d));
+    t.err = p->err_dev;
+    t.nkb = (d.K + kQ8BlockK - 1) / kQ8BlockK;
+    t.n_tiles = (d.N + kTileN - 1) / kTileN;
+    t.m_tiles = (d.M + d.m_tile - 1) / d.m_tile;
+    t.full = d.full_waves;
+    t.rem_units = d.tiles % d.grid * t.nkb;
+    t.rem_ctas = d.shared_ctas;
+    t.band = kQ8Band;
+    t.static_w = d.static_weights;
+    t.timeout_ns = kDefaultTimeoutNs;
+    CUtensorMap tmW, tmX;
+    skg_status st = encode_tiled_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, d.N, d.K, kTileN);
+    if (st != SKG_OK)
+        return st;
+    cudaError_t e = cudaSuccess;
+    if (p->dirty) {
+        e = cudaMemsetAsync(p->ws, 0, sums_bytes(d) + counter_bytes(d), s);
+        p->dirty = e != cudaSuccess;
+    }
+    if (d.m_tile > 64) {
+        void *x16 = p->ws + sums_bytes(d) + counter_bytes(d);
+        st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x16, d.M, d.K, d.m_tile);
+        if (st == SKG_OK && e == cudaSuccess)
+            e = launch_q8_widen(g.x, x16, static_cast<size_t>(d.M) * d.K, p->num_sms, s);
+    } else {
+        st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, d.M, d.K, d.m_tile);
+    }
+    if (st != SKG_OK)
+        return st;
+    if (e == cudaSuccess)
+        e = launch_q8_tc(tmW, tmX, t, d.m_tile, d.grid, s);
+    return launched(e, who);
+}
+
+skg_status skg_q8_plan_check(skg_q8_plan_t p)
+{
+    static const char who[] = "skg_q8_plan_check";
+    if (!p)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: plan is NULL", who);
+    cudaError_t e = p->last_stream ? cudaStreamSynchronize(p->last_stream) : cudaDeviceSynchronize();
+    if (e == cudaSuccess)
+        e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return launched(e, who);
+    const unsigned w = __atomic_exchange_n(p->err_host, 0u, __ATOMIC_ACQ_REL);
+    if (w != 0) {
+        p->dirty = true;
+        return set_error(SKG_ERR_DEVICE_TIMEOUT, "a kernel of this plan ran out of a bounded wait (bits 0x%x)", w);
+    }
+    return SKG_OK;
+}
+
+skg_status skg_q8_debug_wait_timeout(skg_q8_plan_t p, unsigned long long timeout_ns, void *stream)
+{
+    static const char who[] = "skg_q8_debug_wait_timeout";
+    if (!p)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: plan is NULL", who);
+    if (timeout_ns == 0 || timeout_ns > 10000000000ull)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: timeout_ns must be in (0, 10 s]", who);
+    p->last_stream = static_cast<cudaStream_t>(stream);
+    return launched(launch_debug_wait(p->err_dev, timeout_ns, p->last_stream), who);
 }
 
 skg_status skg_q8_plan_destroy(skg_q8_plan_t p)
 {
+    if (!p)
+        return SKG_OK;
+    if (p->ws)
+        cudaFree(p->ws);
+    for (void *w : p->retired)
+        cudaFree(w);
+    if (p->err_host)
+        cudaFreeHost(p->err_host);
     delete p;
     return SKG_OK;
 }

@@ -37,6 +37,27 @@ struct Q8LinearParams {
     int M, N, K, epilogue;
 };
 
+// The tensor-core kernel's launch: tiles of 128 channels x m_tile tokens; each
+// of grid CTAs takes `full` whole tiles, then rem_ctas of them share the
+// rem_units units (tile, 128 k) of the tiles left over.
+struct Q8TcParams {
+    Q8LinearParams g;
+    int *ws;                  // [rem_ctas][m_tile][128] int32, zero between runs
+    unsigned *counters;       // [rem_ctas], zero between runs
+    unsigned *err;
+    int nkb, n_tiles, m_tiles, full, rem_units, rem_ctas, band, static_w;
+    unsigned long long timeout_ns;
+};
+
+struct Q8TcShape {
+    int ctas_per_sm, smem_bytes, threads, stages;
+};
+
+Q8TcShape q8_tc_shape(int m_tile);
+cudaError_t launch_q8_tc(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8TcParams &p, int m_tile, int grid,
+                         cudaStream_t s);
+cudaError_t launch_q8_widen(const int8_t *x, void *out, size_t elements, int num_sms, cudaStream_t s);
+
 cudaError_t launch_q8_norm(const Q8RowParams &p, cudaStream_t s);
 cudaError_t launch_q8_quantize(const Q8RowParams &p, cudaStream_t s);
 cudaError_t launch_q8_gemv(const Q8LinearParams &p, cudaStream_t s);

@@ -33,6 +33,10 @@ SKG_KERNEL_GEMV = 1
 SKG_KERNEL_SPLITK_TC = 2
 KERNEL_NAMES = {SKG_KERNEL_GEMV: "gemv", SKG_KERNEL_SPLITK_TC: "splitk_tc"}
 
+SKG_Q8_KERNEL_DP4A = 1
+SKG_Q8_KERNEL_TC = 2
+Q8_KERNEL_NAMES = {SKG_Q8_KERNEL_DP4A: "q8_dp4a", SKG_Q8_KERNEL_TC: "q8_tc"}
+
 # Every symbol include/skg.h declares.
 EXPORTS = (
     "skg_plan_query", "skg_plan", "skg_plan_force", "skg_plan_force_kernel", "skg_plan_set_pdl", "skg_run",
@@ -42,6 +46,7 @@ EXPORTS = (
     "skg_plan_set_reducers",
     "skg_group", "skg_group_run", "skg_group_info", "skg_group_check", "skg_group_destroy",
     "skg_rmsnorm_q8", "skg_quantize_q8", "skg_q8_plan_query", "skg_q8_plan", "skg_q8_run", "skg_q8_plan_destroy",
+    "skg_q8_plan_force", "skg_q8_plan_info", "skg_q8_plan_check", "skg_q8_debug_wait_timeout",
 )
 
 
@@ -71,12 +76,16 @@ class skg_plan_desc(ctypes.Structure):
 
 class skg_q8_plan_desc(ctypes.Structure):
     _fields_ = [
-        ("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int), ("epilogue", ctypes.c_int),
-        ("static_weights", ctypes.c_int),
+        *((f, ctypes.c_int) for f in (
+            "kernel_kind", "M", "N", "K", "epilogue", "static_weights", "m_tile", "tiles", "full_waves", "shared_ctas",
+            "grid", "threads", "smem_bytes", "stages", "ctas_per_sm")),
+        ("workspace_bytes", ctypes.c_size_t),
     ]
 
     def as_dict(self) -> dict:
-        return {f: getattr(self, f) for f, _ in self._fields_}
+        d = {f: getattr(self, f) for f, _ in self._fields_}
+        d["kernel"] = Q8_KERNEL_NAMES.get(self.kernel_kind, "?")
+        return d
 
 
 _lib = None
@@ -123,6 +132,10 @@ def load(path: str = LIB_PATH):
     lib.skg_q8_plan.argtypes = [i, i, i, i, i, P(vp)]
     lib.skg_q8_run.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
     lib.skg_q8_plan_destroy.argtypes = [vp]
+    lib.skg_q8_plan_force.argtypes = [vp, i, i, i]
+    lib.skg_q8_plan_info.argtypes = [vp, P(skg_q8_plan_desc)]
+    lib.skg_q8_plan_check.argtypes = [vp]
+    lib.skg_q8_debug_wait_timeout.argtypes = [vp, ctypes.c_ulonglong, vp]
     for name in EXPORTS:
         getattr(lib, name).restype = ctypes.c_int
     lib.skg_last_error.restype = ctypes.c_char_p
@@ -445,6 +458,24 @@ def skg_q8_run(plan: int, x, x_scale, W, w_scale, residual, y, stream=None):
                              _stream(stream)))
 
 
+def skg_q8_plan_force(plan: int, kind: int = 0, m_tile: int = 0, ctas: int = 0):
+    _check(load().skg_q8_plan_force(plan, kind, m_tile, ctas))
+
+
+def skg_q8_plan_info(plan: int) -> dict:
+    d = skg_q8_plan_desc()
+    _check(load().skg_q8_plan_info(plan, ctypes.byref(d)))
+    return d.as_dict()
+
+
+def skg_q8_plan_check(plan: int):
+    _check(load().skg_q8_plan_check(plan))
+
+
+def skg_q8_debug_wait_timeout(plan: int, timeout_ns: int, stream=None):
+    _check(load().skg_q8_debug_wait_timeout(plan, int(timeout_ns), _stream(stream)))
+
+
 def skg_q8_plan_destroy(plan: int):
     _check(load().skg_q8_plan_destroy(plan))
 
@@ -466,6 +497,15 @@ class Q8Plan:
             _dense(W, "W", (N, K), torch.int8), _dense(w_scale, "w_scale", (N,), torch.float32),
             None if residual is None else _dense(residual, "residual", (M, N), torch.bfloat16),
             _dense(y, "y", (M, N), out), _stream(stream)))
+
+    def force(self, kind: int = 0, m_tile: int = 0, ctas: int = 0):
+        skg_q8_plan_force(self.handle, kind, m_tile, ctas)
+
+    def info(self) -> dict:
+        return skg_q8_plan_info(self.handle)
+
+    def check(self):
+        skg_q8_plan_check(self.handle)
 
     def close(self):
         if self.handle:

@@ -101,3 +101,42 @@ def test_binding_refuses_host_tensors():
         with pytest.raises(skg.SkgError) as e:
             call()
         assert e.value.status == skg.SKG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1024, 1024), (3, 384, 7168), (16, 7168, 7168), (64, 7168, 16384), (65, 640, 16),
+                                   (333, 5001, 4112), (4096, 12288, 7168), (1 << 18, 128, 48)])
+def test_query_describes_a_launch_that_covers_every_tile(M, N, K):
+    d = skg.skg_q8_plan_query(M, N, K, "bf16", SMS)
+    assert d["grid"] >= 1 and d["threads"] % 32 == 0
+    if d["kernel"] == "q8_dp4a":
+        assert d["workspace_bytes"] == 0
+        return
+    assert d["m_tile"] >= min(M, 128) or M > 128
+    assert d["tiles"] == -(-N // 128) * -(-M // d["m_tile"])
+    nkb = -(-K // 128)
+    left = d["tiles"] - d["full_waves"] * d["grid"]
+    assert 0 <= left < d["grid"] <= SMS * d["ctas_per_sm"]
+    assert d["shared_ctas"] == min(d["grid"], left * nkb)
+    assert d["smem_bytes"] * d["ctas_per_sm"] <= 227 * 1024
+    wide = M * K * 2 if d["m_tile"] > 64 else 0
+    sums = d["shared_ctas"] * d["m_tile"] * 512
+    assert sums + wide <= d["workspace_bytes"] <= sums + wide + 4 * d["shared_ctas"] + 256
+
+
+@pytest.mark.parametrize("units,ctas,nkb", [(1, 1, 1), (7, 7, 7), (56 * 56, 304, 56), (3 * 56, 168, 56), (16 * 151, 152, 16),
+                                            (1024 * 37, 151, 1024), (303, 303, 1), (5 * 9, 13, 9)])
+def test_shared_units_are_cut_into_runs_that_name_their_tiles(units, ctas, nkb):
+    """The kernel's arithmetic: CTA c takes units [c U / C, (c + 1) U / C), and
+    the CTA that holds unit u is ((u + 1) C - 1) / U: what a shared tile's
+    slot and its count of arrivals are taken from."""
+    owner = {}
+    for c in range(ctas):
+        lo, hi = c * units // ctas, (c + 1) * units // ctas
+        assert hi > lo                                   # C <= U: no CTA is without work
+        for u in range(lo, hi):
+            owner[u] = c
+    assert sorted(owner) == list(range(units))
+    assert all(((u + 1) * ctas - 1) // units == owner[u] for u in range(units))
+    starts = [owner[t * nkb] for t in range(units // nkb)
+              if owner[t * nkb] != owner[min(units - 1, t * nkb + nkb - 1)]]
+    assert len(starts) == len(set(starts))               # one slot per shared tile

@@ -412,3 +412,89 @@ def test_binding_refuses_wrong_tensors():
     plan.run(*good)                                       # and the plan still works
     assert R.same_bits(c.y, c.want())
     plan.close()
+
+
+# ------------------------------------------------------------------------- every kernel at every shape
+TILES = (16, 32, 64, 128, 192)
+
+
+@pytest.mark.parametrize("m_tile", TILES)
+@pytest.mark.parametrize("M,N,K,ctas", [(1, 128, 1024, 0), (2, 1000, 2064, 0), (16, 300, 1040, 7), (33, 257, 16400, 0),
+                                        (64, 130, 4096, 5), (70, 640, 1152, 1), (200, 384, 3104, 3), (193, 129, 16, 0),
+                                        (130, 2000, 528, 11), (385, 1000, 2048, 148)])
+def test_every_tile_gives_the_same_bits(M, N, K, ctas, m_tile):
+    """The tensor-core kernel at every tile, with few CTAs too (whole tiles, shared tiles and both)."""
+    c = Linear(M, N, K, "bf16_residual", 6)
+    want = c.want()
+    plan = skg.Q8Plan(M, N, K, "bf16_residual")
+    plan.force(skg.SKG_Q8_KERNEL_TC, m_tile, ctas)
+    d = plan.info()
+    assert d["m_tile"] == m_tile and d["kernel"] == "q8_tc"
+    for _ in range(3):
+        c.y.fill_(float("nan"))
+        c.run(plan)
+        assert R.same_bits(c.y, want)
+    plan.check()
+    plan.close()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 77, 1040), (2, 128, 512), (9, 1001, 4112), (64, 256, 7168)])
+def test_dp4a_kernel_at_any_batch(M, N, K):
+    c = Linear(M, N, K, "fp32", 7)
+    plan = skg.Q8Plan(M, N, K, "fp32")
+    plan.force(skg.SKG_Q8_KERNEL_DP4A)
+    assert R.same_bits(c.run(plan), c.want())
+    plan.close()
+
+
+@pytest.mark.parametrize("m_tile", TILES)
+@pytest.mark.parametrize("v", [(-128, -128), (127, -128)])
+def test_largest_sums_on_every_tile(m_tile, v):
+    M, N, K = 20, 130, 131056
+    x = torch.full((M, K), v[0], dtype=torch.int8, device="cuda")
+    W = torch.full((N, K), v[1], dtype=torch.int8, device="cuda")
+    x[0, 0], W[1, K - 1] = 1, 1
+    one = torch.ones(N, device="cuda")
+    y = torch.empty(M, N, dtype=torch.float32, device="cuda")
+    plan = skg.Q8Plan(M, N, K, "fp32")
+    plan.force(skg.SKG_Q8_KERNEL_TC, m_tile)
+    plan.run(x, one[:M], W, one, None, y)
+    assert torch.equal(y, (x.double() @ W.double().t()).float())
+    plan.close()
+
+
+def test_plans_share_no_state_between_streams():
+    """Two plans of one shape on two streams at once."""
+    M, N, K = 48, 2000, 4096
+    cs = [Linear(M, N, K, "fp32", 20 + i) for i in range(2)]
+    plans = [skg.Q8Plan(M, N, K, "fp32", static_weights=True) for _ in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    want = [c.want() for c in cs]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for c, p, s in zip(cs, plans, streams):
+            c.run(p, s)
+    for c, p, w in zip(cs, plans, want):
+        p.check()
+        assert R.same_bits(c.y, w)
+        p.close()
+
+
+def test_bounded_wait_is_reported_and_the_plan_recovers():
+    c = Linear(24, 500, 4096, "fp32", 8)
+    plan = skg.Q8Plan(24, 500, 4096, "fp32")
+    want = c.want()
+    skg.skg_q8_debug_wait_timeout(plan.handle, 2_000_000)
+    with pytest.raises(skg.SkgError) as e:
+        plan.check()
+    assert e.value.status == skg.SKG_ERR_DEVICE_TIMEOUT
+    plan.check()
+    skg.skg_q8_debug_wait_timeout(plan.handle, 1_000_000)
+    torch.cuda.synchronize()
+    with pytest.raises(skg.SkgError) as e:
+        c.run(plan)
+    assert e.value.status == skg.SKG_ERR_DEVICE_TIMEOUT
+    c.run(plan)
+    assert R.same_bits(c.y, want)
+    plan.check()
+    plan.close()
