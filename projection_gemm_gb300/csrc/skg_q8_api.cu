@@ -54,11 +54,13 @@ skg_status launched(cudaError_t e, const char *who)
 
 constexpr int kQ8Band = 8;            // token tiles per band of the tile order
 constexpr int kQ8BlockK = 128;        // k per unit of the tensor-core kernel
+constexpr int kQ8L2Ahead = 0;
 constexpr int kDp4aMaxM = 2;
 
 size_t sums_bytes(const skg_q8_plan_desc &d)
 {
-    return static_cast<size_t>(d.shared_ctas) * (static_cast<size_t>(d.m_tile) * kTileN * 4);
+    const bool own = d.m_tile <= 64 && d.full_waves > 0 && d.K > 1024;     // whole tiles of several accumulations
+    return (static_cast<size_t>(d.shared_ctas) + (own ? d.grid : 0)) * (static_cast<size_t>(d.m_tile) * kTileN * 4);
 }
 
 size_t counter_bytes(const skg_q8_plan_desc &d) { return (static_cast<size_t>(d.shared_ctas) * 4 + 255) / 256 * 256; }
@@ -344,6 +346,7 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
     t.rem_ctas = d.shared_ctas;
     t.band = kQ8Band;
     t.static_w = d.static_weights;
+    t.ahead = kQ8L2Ahead;
     t.timeout_ns = kDefaultTimeoutNs;
     CUtensorMap tmW, tmX;
     skg_status st = encode_tiled_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, d.N, d.K, kTileN);

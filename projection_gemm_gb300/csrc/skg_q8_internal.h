@@ -42,10 +42,12 @@ struct Q8LinearParams {
 // rem_units units (tile, 128 k) of the tiles left over.
 struct Q8TcParams {
     Q8LinearParams g;
-    int *ws;                  // [rem_ctas][m_tile][128] int32, zero between runs
+    int *ws;                  // slots of [m_tile][128] int32, zero between runs: rem_ctas, then (m_tile <= 64
+                              // and more than one accumulation a tile) one per CTA for its whole tiles
     unsigned *counters;       // [rem_ctas], zero between runs
     unsigned *err;
     int nkb, n_tiles, m_tiles, full, rem_units, rem_ctas, band, static_w;
+    int ahead;                // static weights: units after the ring requested into L2 before the wait
     unsigned long long timeout_ns;
 };
 

@@ -40,20 +40,22 @@ namespace {
 
 constexpr int kQ8BlockK = 128;                       // k of one unit: 128 bytes of a W row
 constexpr int kExactBlocks = 1024 / kQ8BlockK;       // units summed by the MMA from a fresh accumulator
-constexpr int kWidenWarps = 4;
+constexpr int kWidenSets = 2;                        // sets of 4 warps, on alternate units
+constexpr int kWidenWarps = 4 * kWidenSets;
 constexpr uint32_t kQ8WBytes = kTileN * kQ8BlockK;   // 16 KB
 
 template <int MT, bool WIDE>
 struct Q8Shape {
-    static constexpr int kEpiWarps = WIDE ? MT / 16 : (MT == 16 ? 4 : 8);
+    static constexpr int kEpiWarps = WIDE ? MT / 16 : (MT <= 32 ? 4 : 8);
     static constexpr int kCols = MT * 4 / kEpiWarps;         // accumulator columns of an epilogue thread
     static constexpr int kThreads = 32 * (kWidenWarps + kEpiWarps + 2);
     static constexpr int kTmaWarp = kWidenWarps + kEpiWarps;
     static constexpr int kMmaWarp = kTmaWarp + 1;
     static constexpr int kCtas = WIDE ? 1 : 2;               // per SM
-    static constexpr int kStages = WIDE ? 4 : (MT == 64 ? 3 : (MT == 32 ? 4 : 5));   // W (and int8 x) ring
+    static constexpr int kStages = WIDE ? 4 : (MT <= 32 ? 4 : 3);   // W (and int8 x) ring
     static constexpr int kXStages = WIDE ? (MT > 128 ? 3 : 4) : 0;                   // fp16 x ring (WIDE)
-    static constexpr int kOps = WIDE && MT <= 128 ? 4 : 2;   // widened operand buffers
+    static constexpr int kOps = WIDE && MT <= 128 ? 4 : (MT <= 32 ? 3 : 2);          // widened operand buffers
+    static_assert(kStages >= kOps && kOps >= kWidenSets, "the widen warps' waits need this");
     static constexpr uint32_t kRawX = WIDE ? 0 : MT * kQ8BlockK;
     static constexpr uint32_t kX16 = MT * kQ8BlockK * 2;     // fp16 x of one k-block: two 64-wide halves
     static constexpr uint32_t kTmemCols = 2 * MT + kOps * 64 <= 256 ? 256 : 512;
@@ -152,33 +154,33 @@ __device__ __forceinline__ bool q8_epi_and(bool v)
     return out != 0;
 }
 
-// A thread's columns (tokens m0...) of one output channel n, 8 at a time so
-// that their loads are in flight together.
+// NC outputs (tokens m0...) of one channel n from their sums, 4 at a time so
+// that their loads are in flight together and few registers hold them.
 template <int EPI, int NC>
 __device__ __forceinline__ void store_columns_as(const Q8LinearParams &g, int m0, int n, const int (&acc)[NC])
 {
     const int valid = g.M - m0;
-    const float ws = __ldg(g.w_scale + n);
+    const float ws = __ldcg(g.w_scale + n);
     const float *xsp = g.x_scale + m0;
     size_t at = static_cast<size_t>(m0) * g.N + n;
 #pragma unroll
-    for (int c0 = 0; c0 < NC; c0 += 8) {
-        float v[8];
+    for (int c0 = 0; c0 < NC; c0 += 4) {
+        float v[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            v[c] = c0 + c < valid ? q8_scaled(acc[c0 + c], __ldg(xsp + c0 + c), ws) : 0.0f;
+        for (int c = 0; c < 4; ++c)
+            v[c] = c0 + c < valid ? q8_scaled(acc[c0 + c], __ldcg(xsp + c0 + c), ws) : 0.0f;
         if (EPI == SKG_EPI_BF16_RESIDUAL) {
             const uint16_t *r = g.res + at;
-            uint16_t b[8];
+            uint16_t b[4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c, r += g.N)
-                b[c] = c0 + c < valid ? __ldg(r) : 0;
+            for (int c = 0; c < 4; ++c, r += g.N)
+                b[c] = c0 + c < valid ? __ldcg(r) : 0;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
+            for (int c = 0; c < 4; ++c)
                 v[c] = __fadd_rn(v[c], bf16_to_f32(b[c]));
         }
 #pragma unroll
-        for (int c = 0; c < 8; ++c, at += g.N) {
+        for (int c = 0; c < 4; ++c, at += g.N) {
             if (c0 + c < valid) {
                 if (EPI == SKG_EPI_FP32)
                     static_cast<float *>(g.y)[at] = v[c];
@@ -200,6 +202,46 @@ __device__ __forceinline__ void store_columns(const Q8LinearParams &g, int m0, i
         store_columns_as<SKG_EPI_BF16_RESIDUAL>(g, m0, n, acc);
     else
         store_columns_as<SKG_EPI_BF16>(g, m0, n, acc);
+}
+
+// 16 accumulator columns of this thread's TMEM lane as integers (they are
+// integers below 2^24 in fp32: the conversion is exact).
+__device__ __forceinline__ void load_sums(uint32_t taddr, int (&v)[16])
+{
+    uint32_t r[2][8];
+    tmem_ld_x8(taddr, r[0]);
+    tmem_ld_x8(taddr + 8, r[1]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        asm volatile("" : "+r"(r[c >> 3][c & 7]));
+        v[c] = __float2int_rn(__uint_as_float(r[c >> 3][c & 7]));
+    }
+}
+
+// Add sums to a slot's columns (stride 128), those below `valid`.
+template <int NC>
+__device__ __forceinline__ void add_sums(int *slot, int valid, const int (&v)[NC])
+{
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+        if (c < valid)
+            asm volatile("red.relaxed.gpu.global.add.s32 [%0], %1;" :: "l"(slot + c * kTileN), "r"(v[c]) : "memory");
+}
+
+// Read 8 columns of a slot and leave them at zero for the next run.
+__device__ __forceinline__ void take_sums(int *slot, int valid, int (&v)[8])
+{
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        v[c] = 0;
+        if (c < valid)
+            asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v[c]) : "l"(slot + c * kTileN) : "memory");
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        if (c < valid)
+            asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" :: "l"(slot + c * kTileN), "r"(0) : "memory");
 }
 
 template <int MT, bool WIDE>
@@ -233,10 +275,10 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
         tma_prefetch_desc(&tmX);
         for (int i = 0; i < S; ++i) {
             mbar_init(&wfull[i], 1);
-            mbar_init(&wempty[i], kWidenWarps);
+            mbar_init(&wempty[i], 4);
         }
         for (int i = 0; i < OPS; ++i) {
-            mbar_init(&opfull[i], kWidenWarps);
+            mbar_init(&opfull[i], 4);
             mbar_init(&opempty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -288,6 +330,20 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
                     }
                 }
                 issued_w = ahead;
+                // ... and the rest of this CTA's weights from HBM into L2, up to p.ahead units
+                int asked = 0;
+                if (ahead == S) {
+                    Q8Walk rest(p, cta);
+                    int skip = ahead;
+                    while (asked < p.ahead && rest.next(p, cta, s)) {
+                        int nt, mt;
+                        tile_at(p, s.tile, nt, mt);
+                        int kb = s.kb0 + min(skip, s.kb1 - s.kb0);
+                        skip -= kb - s.kb0;
+                        for (; kb < s.kb1 && asked < p.ahead; ++kb, ++asked)
+                            tma_prefetch_l2_2d(&tmW, kb * kQ8BlockK, nt * kTileN);
+                    }
+                }
             }
             pdl_wait();
             while (ok && walk.next(p, cta, s)) {
@@ -386,12 +442,17 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
         }
     } else if (warp < kWidenWarps) {
         // --------------------------------------------------------------- widen
-        const int row = warp * 32 + lane;
-        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + 2 * MT;
-        for (int j = 0; j < blocks; ++j) {
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * MT;
+        for (int j = warp >> 2; j < blocks; j += kWidenSets) {
             const int sl = j % S, b = j % OPS;
-            const bool ok = mbar_wait(&wfull[sl], (j / S) & 1, p.timeout_ns, &flags[0]) &&
-                            mbar_wait(&opempty[b], ((j / OPS) & 1) ^ 1, p.timeout_ns, &flags[0]);
+            // The operand buffer first: once the MMA of unit j - OPS is done, unit
+            // j - S <= j - OPS has been widened, so the ring slot's barrier is at
+            // most one phase behind and its parity says which.  (The sets run
+            // apart: by the parity alone, a slot still waiting for unit j - S
+            // looks like one that holds unit j.)
+            const bool ok = mbar_wait(&opempty[b], ((j / OPS) & 1) ^ 1, p.timeout_ns, &flags[0]) &&
+                            mbar_wait(&wfull[sl], (j / S) & 1, p.timeout_ns, &flags[0]);
             if (!__all_sync(0xFFFFFFFFu, ok)) {      // the whole warp goes on, or none of it
                 q8_fail(p, &flags[0], kErrTimeoutWiden);
                 break;
@@ -409,9 +470,9 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
             if constexpr (!WIDE) {
                 const uint8_t *xs = sXraw + sl * Sh::kRawX;
                 uint8_t *xd = sX16 + b * Sh::kX16;
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < MT / 16; ++i) {
-                    const int c = (threadIdx.x & 7), m = i * 16 + (threadIdx.x >> 3);
+                    const int c = lane & 7, m = i * 16 + quarter * 4 + (lane >> 3);
                     uint32_t r[8];
                     widen16(*reinterpret_cast<const uint4 *>(xs + m * 128 + ((c ^ (m & 7)) << 4)), r);
                     uint8_t *dst = xd + (c >> 2) * (MT * 128) + m * 128;
@@ -443,7 +504,25 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
             int nt, mt;
             tile_at(p, s.tile, nt, mt);
             const int n = nt * kTileN + row, m0 = mt * MT + col0;
-            int acc[NC];
+            const int valid = p.g.M - m0;
+            const bool whole = s.kb0 == 0 && s.kb1 == p.nkb;
+            const bool direct = whole && (WIDE || p.nkb <= kExactBlocks);
+            // The sums' slot.  A tile shared by several CTAs: CTA c begins at
+            // unit floor(c units / ctas), so the CTA that holds unit u is
+            // floor(((u + 1) ctas - 1) / units), and the slot is that of the
+            // tile's first unit.  A whole tile of several accumulations (not
+            // WIDE): a slot of this CTA's own.
+            int first = p.rem_ctas + cta, last = first;
+            if (!whole) {
+                const int t = s.tile - p.full * static_cast<int>(gridDim.x);
+                const long long u0 = static_cast<long long>(t) * p.nkb;
+                first = static_cast<int>(((u0 + 1) * p.rem_ctas - 1) / p.rem_units);
+                last = static_cast<int>(((u0 + p.nkb) * p.rem_ctas - 1) / p.rem_units);
+            }
+            int *slot = p.ws + static_cast<size_t>(first) * (MT * kTileN) + col0 * kTileN + row;
+            // WIDE adds the accumulations of a segment in registers; with few
+            // columns, where registers are scarce, each goes to its slot.
+            int acc[WIDE ? NC : 1];
             bool ok = true;
             for (int kb = s.kb0; kb < s.kb1; kb += kExactBlocks, ++chunk) {
                 const int t = chunk & 1;
@@ -453,18 +532,18 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
                     break;
                 }
                 tc_fence_after();
-                const bool fresh = kb == s.kb0;
-#pragma unroll
+#pragma unroll(WIDE ? NC / 16 : 1)
                 for (int c0 = 0; c0 < NC; c0 += 16) {
-                    uint32_t r[2][8];
-                    tmem_ld_x8(lane_base + static_cast<uint32_t>(t * MT + c0), r[0]);
-                    tmem_ld_x8(lane_base + static_cast<uint32_t>(t * MT + c0 + 8), r[1]);
-                    tmem_wait_ld();
+                    int v[16];
+                    load_sums(lane_base + static_cast<uint32_t>(t * MT + c0), v);
+                    if constexpr (WIDE) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        asm volatile("" : "+r"(r[c >> 3][c & 7]));
-                        const int v = __float2int_rn(__uint_as_float(r[c >> 3][c & 7]));
-                        acc[c0 + c] = fresh ? v : acc[c0 + c] + v;
+                        for (int c = 0; c < 16; ++c)
+                            acc[c0 + c] = kb == s.kb0 ? v[c] : acc[c0 + c] + v[c];
+                    } else if (direct) {
+                        store_columns<16>(p.g, m0 + c0, n, v);
+                    } else {
+                        add_sums<16>(slot + c0 * kTileN, valid - c0, v);
                     }
                 }
                 tc_fence_before();
@@ -474,45 +553,38 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
             }
             if (!q8_epi_and<ET>(ok && !flags[0]))
                 break;
-            if (s.kb0 == 0 && s.kb1 == p.nkb) {
-                store_columns<NC>(p.g, m0, n, acc);
+            if (direct) {
+                if constexpr (WIDE)
+                    store_columns<NC>(p.g, m0, n, acc);
                 continue;
             }
-            // A shared tile.  CTA c begins at unit floor(c units / ctas); the
-            // CTA that holds unit u is therefore floor(((u + 1) ctas - 1) / units).
-            const int t = s.tile - p.full * static_cast<int>(gridDim.x);
-            const long long u0 = static_cast<long long>(t) * p.nkb;
-            const int first = static_cast<int>(((u0 + 1) * p.rem_ctas - 1) / p.rem_units);
-            const int last = static_cast<int>(((u0 + p.nkb) * p.rem_ctas - 1) / p.rem_units);
-            int *ws = p.ws + static_cast<size_t>(first) * MT * kTileN + static_cast<size_t>(col0) * kTileN + row;
-            const int valid = p.g.M - m0;
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-                if (c < valid)
-                    asm volatile("red.relaxed.gpu.global.add.s32 [%0], %1;" :: "l"(ws + c * kTileN), "r"(acc[c]) : "memory");
-            // The barrier orders every thread's additions before one thread's
-            // acq_rel arrival; the last arrival's acquire, passed on by the
-            // next barrier, orders its reads after everyone's additions.
-            q8_epi_sync<ET>();
-            if (ew == 0 && lane == 0) {
-                unsigned old;
-                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p.counters + first) : "memory");
-                flags[1] = old == static_cast<unsigned>(last - first);
-                if (old == static_cast<unsigned>(last - first))
-                    p.counters[first] = 0;
-            }
-            q8_epi_sync<ET>();
-            if (flags[1]) {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    if (c < valid) {
-                        acc[c] = __ldcg(ws + c * kTileN);
-                        __stcg(ws + c * kTileN, 0);
-                    }
+            if (!whole) {
+                if constexpr (WIDE)
+                    add_sums<NC>(slot, valid, acc);
+                // The barrier orders every thread's additions before one thread's
+                // acq_rel arrival; the last arrival's acquire, passed on by the
+                // next barrier, orders its reads after everyone's additions.
+                q8_epi_sync<ET>();
+                if (ew == 0 && lane == 0) {
+                    unsigned old;
+                    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                                 : "=r"(old) : "l"(p.counters + first) : "memory");
+                    flags[1] = old == static_cast<unsigned>(last - first);
+                    if (old == static_cast<unsigned>(last - first))
+                        p.counters[first] = 0;
                 }
-                store_columns<NC>(p.g, m0, n, acc);
+                q8_epi_sync<ET>();
+                const bool mine = flags[1] != 0;
+                q8_epi_sync<ET>();       // read by all before the next tile writes it
+                if (!mine)
+                    continue;
             }
-            q8_epi_sync<ET>();           // flags[1] is read by all before the next tile writes it
+#pragma unroll 1
+            for (int c0 = 0; c0 < NC; c0 += 8) {
+                int v[8];
+                take_sums(slot + c0 * kTileN, valid - c0, v);
+                store_columns<8>(p.g, m0 + c0, n, v);
+            }
         }
     }
 

@@ -393,52 +393,63 @@ def _bad(what: str):
     raise SkgError(SKG_ERR_INVALID_ARG, what)
 
 
-def _rows(t, name, M, K, dtype) -> int:
-    """Row stride of a [M, K] tensor whose rows are contiguous."""
-    if t.dtype is not dtype or not t.is_cuda or t.dim() != 2 or t.shape[0] != M or t.shape[1] != K:
-        _bad(f"{name} must be a CUDA tensor [{M}, {K}] of {dtype}")
+def _rows(t, name, shape, dtype) -> int:
+    """Row stride of a tensor of `shape` [M, K] whose rows are contiguous."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        _bad(f"{name} must be a CUDA tensor {list(shape)} of {dtype}")
+    if t.is_contiguous():
+        return shape[1]
     ld, one = t.stride()
-    if M <= 1:
-        ld = K
-    if (one != 1 and K > 1) or ld < K:
+    if (one != 1 and shape[1] > 1) or ld < shape[1]:
         _bad(f"{name}: elements of a row must be contiguous and rows must not overlap")
     return ld
 
 
-def _dense(t, name, shape, dtype):
-    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+def _dense(t, name, shape, dtype) -> int:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         _bad(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
     return t.data_ptr()
+
+
+def _stream_of(stream, t):
+    """The given stream, or the current one of t's device (the raw handle: a
+    decode step's calls are short enough for a Stream object to show)."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def skg_rmsnorm_q8(x, residual, gamma, eps: float, h, q, scale, y=None, stream=None):
     """x, residual, h: bf16 [M, K] (rows may be strided); gamma bf16 [K]; q int8 [M, K];
     scale fp32 [M]; y bf16 [M, K].  residual, gamma, h and y may be None."""
     import torch
-    bf16 = torch.bfloat16
-    if x.dim() != 2:
+    bf16, shape = torch.bfloat16, x.shape
+    if len(shape) != 2:
         _bad("x must be [M, K]")
-    M, K = x.shape
-    ldx = _rows(x, "x", M, K, bf16)
-    ldr = 0 if residual is None else _rows(residual, "residual", M, K, bf16)
-    ldh = 0 if h is None else _rows(h, "h", M, K, bf16)
+    M, K = shape
+    ldx = _rows(x, "x", shape, bf16)
+    ldr = 0 if residual is None else _rows(residual, "residual", shape, bf16)
+    ldh = 0 if h is None else _rows(h, "h", shape, bf16)
     _check(load().skg_rmsnorm_q8(
-        M, K, eps, x.data_ptr(), ldx, _ptr(residual), ldr,
-        None if gamma is None else _dense(gamma, "gamma", (K,), bf16), _ptr(h), ldh,
-        None if y is None else _dense(y, "y", (M, K), bf16), _dense(q, "q", (M, K), torch.int8),
-        _dense(scale, "scale", (M,), torch.float32), _stream(stream)))
+        M, K, eps, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
+        None if gamma is None else _dense(gamma, "gamma", (K,), bf16), None if h is None else h.data_ptr(), ldh,
+        None if y is None else _dense(y, "y", shape, bf16), _dense(q, "q", shape, torch.int8),
+        _dense(scale, "scale", (M,), torch.float32), _stream_of(stream, x)))
 
 
 def skg_quantize_q8(x, gate, q, scale, stream=None):
     """x, gate: bf16 [M, K] (rows may be strided; gate may be None); q int8 [M, K]; scale fp32 [M]."""
     import torch
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         _bad("x must be [M, K]")
-    M, K = x.shape
-    ldx = _rows(x, "x", M, K, torch.bfloat16)
-    ldg = 0 if gate is None else _rows(gate, "gate", M, K, torch.bfloat16)
-    _check(load().skg_quantize_q8(M, K, x.data_ptr(), ldx, _ptr(gate), ldg, _dense(q, "q", (M, K), torch.int8),
-                                  _dense(scale, "scale", (M,), torch.float32), _stream(stream)))
+    M, K = shape
+    ldx = _rows(x, "x", shape, torch.bfloat16)
+    ldg = 0 if gate is None else _rows(gate, "gate", shape, torch.bfloat16)
+    _check(load().skg_quantize_q8(
+        M, K, x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg, _dense(q, "q", shape, torch.int8),
+        _dense(scale, "scale", (M,), torch.float32), _stream_of(stream, x)))
 
 
 def skg_q8_plan_query(M: int, N: int, K: int, epilogue, num_sms: int) -> dict:
@@ -496,7 +507,7 @@ class Q8Plan:
             self.handle, _dense(x, "x", (M, K), torch.int8), _dense(x_scale, "x_scale", (M,), torch.float32),
             _dense(W, "W", (N, K), torch.int8), _dense(w_scale, "w_scale", (N,), torch.float32),
             None if residual is None else _dense(residual, "residual", (M, N), torch.bfloat16),
-            _dense(y, "y", (M, N), out), _stream(stream)))
+            _dense(y, "y", (M, N), out), _stream_of(stream, x)))
 
     def force(self, kind: int = 0, m_tile: int = 0, ctas: int = 0):
         skg_q8_plan_force(self.handle, kind, m_tile, ctas)

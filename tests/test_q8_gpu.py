@@ -421,7 +421,8 @@ TILES = (16, 32, 64, 128, 192)
 @pytest.mark.parametrize("m_tile", TILES)
 @pytest.mark.parametrize("M,N,K,ctas", [(1, 128, 1024, 0), (2, 1000, 2064, 0), (16, 300, 1040, 7), (33, 257, 16400, 0),
                                         (64, 130, 4096, 5), (70, 640, 1152, 1), (200, 384, 3104, 3), (193, 129, 16, 0),
-                                        (130, 2000, 528, 11), (385, 1000, 2048, 148)])
+                                        (130, 2000, 528, 11), (385, 1000, 2048, 148),
+                                        (64, 1024, 16384, 0), (50, 3000, 2064, 9)])
 def test_every_tile_gives_the_same_bits(M, N, K, ctas, m_tile):
     """The tensor-core kernel at every tile, with few CTAs too (whole tiles, shared tiles and both)."""
     c = Linear(M, N, K, "bf16_residual", 6)
