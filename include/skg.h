@@ -465,7 +465,7 @@ SKG_API skg_status skg_quantize_q8(int M, int K, const void *x, size_t ldx, cons
                                    float *scale, void *stream);
 
 typedef enum skg_q8_kernel_kind {
-    SKG_Q8_KERNEL_DP4A = 1,     /* CUDA cores: int8 dot products, one output channel per warp */
+    SKG_Q8_KERNEL_STREAM = 1,   /* M <= 16: W streams into registers, warp-level fp16 MMA, exact */
     SKG_Q8_KERNEL_TC = 2        /* TMA + tcgen05 on integers widened to fp16, exact */
 } skg_q8_kernel_kind;
 
@@ -474,12 +474,13 @@ typedef struct skg_q8_plan_desc {
     int kernel_kind;            /* skg_q8_kernel_kind */
     int M, N, K, epilogue;
     int static_weights;         /* see skg_q8_plan */
-    int m_tile;                 /* tokens per tile (TC: 16, 32, 64, 128 or 192) or per warp (DP4A) */
-    int tiles;                  /* output tiles: 128 channels x m_tile tokens (TC) */
+    int m_tile;                 /* tokens per tile (STREAM: 8 or 16; TC: 32, 64, 128 or 192) */
+    int n_tile;                 /* output channels per tile (STREAM: 16, 32 or 48 a CTA; TC: 128) */
+    int tiles;                  /* output tiles */
     int full_waves;             /* TC: whole tiles each CTA computes before the rest is shared */
     int shared_ctas;            /* TC: CTAs that share the K ranges of the tiles left over */
     int grid, threads, smem_bytes, stages, ctas_per_sm;
-    size_t workspace_bytes;     /* TC: int32 sums and counters of shared tiles, and x as fp16 for M > 64 */
+    size_t workspace_bytes;     /* TC: partial sums and counters of shared tiles, and x as fp16 for M > 64 */
 } skg_q8_plan_desc;
 
 typedef struct skg_q8_plan_s *skg_q8_plan_t;
@@ -525,11 +526,11 @@ SKG_API skg_status skg_q8_run(skg_q8_plan_t plan, const void *x, const float *x_
 
 /*
  * skg_q8_plan_force -- override of the kernel choice (tests and measurements):
- * kind (an skg_q8_kernel_kind, 0 keeps), and for TC m_tile (16, 32, 64, 128,
+ * kind (an skg_q8_kernel_kind, 0 keeps; STREAM: M <= 16), and for TC m_tile (32, 64, 128,
  * 192; 0 = chosen) and ctas, the most CTAs launched (0 = chosen).  Results do
  * not change.  A larger workspace is allocated where needed and the old one kept
  * until the plan is destroyed, as by skg_plan_force.
- * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_CUDA.
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_CUDA.
  */
 SKG_API skg_status skg_q8_plan_force(skg_q8_plan_t plan, int kind, int m_tile, int ctas);
 

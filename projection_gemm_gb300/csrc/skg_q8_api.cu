@@ -17,10 +17,10 @@ using namespace skg;
 struct skg_q8_plan_s {
     skg_q8_plan_desc d;
     int num_sms = 0;
-    char *ws = nullptr;               // int32 sums, counters, then x as fp16
+    char *ws = nullptr;               // partial sums, counters, then x as fp16
     size_t ws_cap = 0;
     std::vector<void *> retired;      // outgrown workspaces: a captured graph may still use them
-    bool dirty = false;               // a launch gave up and may have left sums behind
+    bool dirty = false;               // a launch gave up and may have left counters behind
     unsigned int *err_host = nullptr; // mapped pinned word
     unsigned int *err_dev = nullptr;
     cudaStream_t last_stream = nullptr;
@@ -55,41 +55,45 @@ skg_status launched(cudaError_t e, const char *who)
 constexpr int kQ8Band = 8;            // token tiles per band of the tile order
 constexpr int kQ8BlockK = 128;        // k per unit of the tensor-core kernel
 constexpr int kQ8L2Ahead = 0;
-constexpr int kDp4aMaxM = 2;
+constexpr int kStreamMaxM = 16;
 
 size_t sums_bytes(const skg_q8_plan_desc &d)
 {
-    const bool own = d.m_tile <= 64 && d.full_waves > 0 && d.K > 1024;     // whole tiles of several accumulations
-    return (static_cast<size_t>(d.shared_ctas) + (own ? d.grid : 0)) * (static_cast<size_t>(d.m_tile) * kTileN * 4);
+    // where tiles are shared, or (two CTAs an SM) a whole tile takes more than one pair of accumulations
+    const bool used = d.shared_ctas > 0 || (d.m_tile <= 64 && d.K > 2048);
+    return used ? static_cast<size_t>(d.grid) * 2 * d.m_tile * kTileN * 4 : 0;
 }
 
 size_t counter_bytes(const skg_q8_plan_desc &d) { return (static_cast<size_t>(d.shared_ctas) * 4 + 255) / 256 * 256; }
 
-// Tokens per tile: the smallest of 16, 32, 64 that holds M; above 64, 128 or
+// Tokens per tile: 32 or 64 where that holds M; above 64, 128 or
 // 192, whichever pads M less (192 where they tie: fewer passes over W).
 int choose_tile(int M)
 {
     if (M <= 64)
-        return M <= 16 ? 16 : (M <= 32 ? 32 : 64);
+        return M <= 32 ? 32 : 64;
     const int a = (M + 127) / 128 * 128, b = (M + 191) / 192 * 192;
     return a < b ? 128 : 192;
 }
 
 skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int ctas, int num_sms, const char *who)
 {
-    d->kernel_kind = kind ? kind : (d->M <= kDp4aMaxM ? SKG_Q8_KERNEL_DP4A : SKG_Q8_KERNEL_TC);
+    d->kernel_kind = kind ? kind : (d->M <= kStreamMaxM ? SKG_Q8_KERNEL_STREAM : SKG_Q8_KERNEL_TC);
     d->m_tile = d->tiles = d->full_waves = d->shared_ctas = d->smem_bytes = d->stages = 0;
     d->workspace_bytes = 0;
-    if (d->kernel_kind == SKG_Q8_KERNEL_DP4A) {
-        d->m_tile = d->M == 1 ? 1 : 8;
-        d->threads = 256;
-        d->ctas_per_sm = 8;
-        const long long grid = (static_cast<long long>(d->N) + 7) / 8 * ((d->M + d->m_tile - 1) / d->m_tile);
-        if (grid > (1ll << 30))
-            return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^30 CTAs", who);
-        d->grid = static_cast<int>(grid);
+    if (d->kernel_kind == SKG_Q8_KERNEL_STREAM) {
+        if (d->M > kStreamMaxM)
+            return set_error(SKG_ERR_UNSUPPORTED, "%s: the streaming kernel takes at most %d tokens (M=%d)", who,
+                             kStreamMaxM, d->M);
+        const Q8StreamShape sh = q8_stream_shape(d->M, d->N, num_sms);
+        d->m_tile = d->M <= 8 ? 8 : 16;
+        d->n_tile = 16 * sh.groups;
+        d->tiles = d->grid = (d->N - 1) / d->n_tile + 1;
+        d->threads = 32 * sh.warps;
+        d->ctas_per_sm = sh.ctas_per_sm;
         return SKG_OK;
     }
+    d->n_tile = kTileN;
     d->m_tile = m_tile ? m_tile : choose_tile(d->M);
     const Q8TcShape sh = q8_tc_shape(d->m_tile);
     const long long tiles = (static_cast<long long>(d->N) + kTileN - 1) / kTileN * ((d->M + d->m_tile - 1) / d->m_tile);
@@ -112,7 +116,7 @@ skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int ctas, int 
     return SKG_OK;
 }
 
-// A workspace for the plan's launch, its sums and counters zero.
+// A workspace for the plan's launch, its counters zero.
 skg_status ensure_workspace(skg_q8_plan_s *p, const char *who)
 {
     const size_t need = p->d.workspace_bytes;
@@ -128,7 +132,7 @@ skg_status ensure_workspace(skg_q8_plan_s *p, const char *who)
         p->ws_cap = need;
     }
     if (need)
-        e = cudaMemset(p->ws, 0, sums_bytes(p->d) + counter_bytes(p->d));
+        e = cudaMemset(p->ws + sums_bytes(p->d), 0, counter_bytes(p->d));
     if (e == cudaSuccess)
         e = cudaStreamSynchronize(nullptr);
     return launched(e, who);
@@ -266,15 +270,15 @@ skg_status skg_q8_plan_force(skg_q8_plan_t p, int kind, int m_tile, int ctas)
     static const char who[] = "skg_q8_plan_force";
     if (!p)
         return set_error(SKG_ERR_INVALID_ARG, "%s: plan is NULL", who);
-    if (kind != 0 && kind != SKG_Q8_KERNEL_DP4A && kind != SKG_Q8_KERNEL_TC)
+    if (kind != 0 && kind != SKG_Q8_KERNEL_STREAM && kind != SKG_Q8_KERNEL_TC)
         return set_error(SKG_ERR_INVALID_ARG, "%s: unknown kernel kind %d", who, kind);
-    if (m_tile != 0 && m_tile != 16 && m_tile != 32 && m_tile != 64 && m_tile != 128 && m_tile != 192)
-        return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile must be 0, 16, 32, 64, 128 or 192 (got %d)", who, m_tile);
+    if (m_tile != 0 && m_tile != 32 && m_tile != 64 && m_tile != 128 && m_tile != 192)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile must be 0, 32, 64, 128 or 192 (got %d)", who, m_tile);
     if (ctas < 0 || ctas > (1 << 16))
         return set_error(SKG_ERR_INVALID_ARG, "%s: ctas must be in [0, 65536] (got %d)", who, ctas);
     skg_q8_plan_desc d = p->d;
     const int k = kind ? kind : d.kernel_kind;
-    if (k == SKG_Q8_KERNEL_DP4A && (m_tile || ctas))
+    if (k == SKG_Q8_KERNEL_STREAM && (m_tile || ctas))
         return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile and ctas belong to the tensor-core kernel", who);
     skg_status st = fill_launch(&d, k, m_tile, ctas, p->num_sms, who);
     if (st != SKG_OK)
@@ -330,8 +334,8 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
     g.N = d.N;
     g.K = d.K;
     g.epilogue = d.epilogue;
-    if (d.kernel_kind == SKG_Q8_KERNEL_DP4A)
-        return launched(launch_q8_gemv(g, s), who);
+    if (d.kernel_kind == SKG_Q8_KERNEL_STREAM)
+        return launched(launch_q8_stream(g, {d.n_tile / 16, d.threads / 32, d.ctas_per_sm}, d.static_weights != 0, s), who);
 
     Q8TcParams t = {};
     t.g = g;
@@ -354,7 +358,7 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
         return st;
     cudaError_t e = cudaSuccess;
     if (p->dirty) {
-        e = cudaMemsetAsync(p->ws, 0, sums_bytes(d) + counter_bytes(d), s);
+        e = cudaMemsetAsync(t.counters, 0, counter_bytes(d), s);
         p->dirty = e != cudaSuccess;
     }
     if (d.m_tile > 64) {

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "skg_q8_internal.h"
 
@@ -17,6 +18,20 @@ __device__ __forceinline__ float silu(float g)
 {
     const float e = __expf(-fabsf(g));
     return g * __fdividef(g < 0.0f ? e : 1.0f, 1.0f + e);
+}
+
+// Four int8 of a word as four fp16: with the sign bit flipped a byte b is
+// b + 128 in 0..255; as the low byte of fp16 0x6400 it reads 1024 + b + 128,
+// exactly, and 1152 is taken off again.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t t = w ^ 0x80808080u;
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t a = __byte_perm(t, 0x64646464u, 0x4140), b = __byte_perm(t, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&b), off);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
 }
 
 // One output from its exact integer sum: the same four fp32 operations in the

@@ -42,8 +42,7 @@ struct Q8LinearParams {
 // rem_units units (tile, 128 k) of the tiles left over.
 struct Q8TcParams {
     Q8LinearParams g;
-    int *ws;                  // slots of [m_tile][128] int32, zero between runs: rem_ctas, then (m_tile <= 64
-                              // and more than one accumulation a tile) one per CTA for its whole tiles
+    int *ws;                  // two slots of [m_tile][128] int32 for each CTA
     unsigned *counters;       // [rem_ctas], zero between runs
     unsigned *err;
     int nkb, n_tiles, m_tiles, full, rem_units, rem_ctas, band, static_w;
@@ -62,6 +61,13 @@ cudaError_t launch_q8_widen(const int8_t *x, void *out, size_t elements, int num
 
 cudaError_t launch_q8_norm(const Q8RowParams &p, cudaStream_t s);
 cudaError_t launch_q8_quantize(const Q8RowParams &p, cudaStream_t s);
-cudaError_t launch_q8_gemv(const Q8LinearParams &p, cudaStream_t s);
+
+// The streaming kernel's launch: CTAs of 16 x groups channels.
+struct Q8StreamShape {
+    int groups, warps, ctas_per_sm;
+};
+
+Q8StreamShape q8_stream_shape(int M, int N, int num_sms);
+cudaError_t launch_q8_stream(const Q8LinearParams &p, const Q8StreamShape &shape, bool static_w, cudaStream_t s);
 
 } // namespace skg

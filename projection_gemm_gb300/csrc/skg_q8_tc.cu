@@ -46,22 +46,22 @@ constexpr uint32_t kQ8WBytes = kTileN * kQ8BlockK;   // 16 KB
 
 template <int MT, bool WIDE>
 struct Q8Shape {
-    static constexpr int kEpiWarps = WIDE ? MT / 16 : (MT <= 32 ? 4 : 8);
+    static constexpr int kEpiWarps = WIDE ? MT / 16 : (MT == 32 ? 4 : 8);
     static constexpr int kCols = MT * 4 / kEpiWarps;         // accumulator columns of an epilogue thread
     static constexpr int kThreads = 32 * (kWidenWarps + kEpiWarps + 2);
     static constexpr int kTmaWarp = kWidenWarps + kEpiWarps;
     static constexpr int kMmaWarp = kTmaWarp + 1;
     static constexpr int kCtas = WIDE ? 1 : 2;               // per SM
-    static constexpr int kStages = WIDE ? 4 : (MT <= 32 ? 4 : 3);   // W (and int8 x) ring
+    static constexpr int kStages = WIDE ? 4 : (MT == 32 ? 4 : 3);   // W (and int8 x) ring
     static constexpr int kXStages = WIDE ? (MT > 128 ? 3 : 4) : 0;                   // fp16 x ring (WIDE)
-    static constexpr int kOps = WIDE && MT <= 128 ? 4 : (MT <= 32 ? 3 : 2);          // widened operand buffers
+    static constexpr int kOps = WIDE && MT <= 128 ? 4 : (MT == 32 ? 3 : 2);          // widened operand buffers
     static_assert(kStages >= kOps && kOps >= kWidenSets, "the widen warps' waits need this");
     static constexpr uint32_t kRawX = WIDE ? 0 : MT * kQ8BlockK;
     static constexpr uint32_t kX16 = MT * kQ8BlockK * 2;     // fp16 x of one k-block: two 64-wide halves
     static constexpr uint32_t kTmemCols = 2 * MT + kOps * 64 <= 256 ? 256 : 512;
     static constexpr uint32_t kIdesc = idesc_f16_f32(kTileN, MT);
     static constexpr int kBars = 2 * kStages + 2 * kXStages + 2 * kOps + 5;
-    static constexpr int kSmem = 1024 + kStages * (kQ8WBytes + kRawX) + (WIDE ? kXStages : kOps) * kX16 + kBars * 8 + 16;
+    static constexpr int kSmem = 1024 + kStages * (kQ8WBytes + kRawX) + (WIDE ? kXStages : kOps) * kX16 + kBars * 8 + 48;
 };
 
 // The segments of one CTA in order: whole tiles, then its share of the rest.
@@ -112,20 +112,6 @@ __device__ __forceinline__ void q8_fail(const Q8TcParams &p, volatile int *abort
     *abort = 1;
     if (p.err)
         atomicOr(p.err, bit);
-}
-
-// Four int8 of a word as four fp16: with the sign bit flipped a byte b is
-// b + 128 in 0..255; as the low byte of fp16 0x6400 it reads 1024 + b + 128,
-// exactly, and 1152 is taken off again.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
-{
-    const uint32_t t = w ^ 0x80808080u;
-    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-    uint32_t a = __byte_perm(t, 0x64646464u, 0x4140), b = __byte_perm(t, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), off);
-    const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&b), off);
-    lo = *reinterpret_cast<const uint32_t *>(&x);
-    hi = *reinterpret_cast<const uint32_t *>(&y);
 }
 
 __device__ __forceinline__ void widen16(const uint4 &v, uint32_t *r)
@@ -219,29 +205,64 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, int (&v)[16])
     }
 }
 
-// Add sums to a slot's columns (stride 128), those below `valid`.
-template <int NC>
-__device__ __forceinline__ void add_sums(int *slot, int valid, const int (&v)[NC])
+// A thread's 16 columns of a slot ([m_tile][128] int32; a warp covers 32
+// consecutive channels of a column).
+__device__ __forceinline__ void put_sums(int *slot, int valid, const int (&v)[16])
 {
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int c = 0; c < 16; ++c)
         if (c < valid)
-            asm volatile("red.relaxed.gpu.global.add.s32 [%0], %1;" :: "l"(slot + c * kTileN), "r"(v[c]) : "memory");
+            __stcg(slot + c * kTileN, v[c]);
 }
 
-// Read 8 columns of a slot and leave them at zero for the next run.
-__device__ __forceinline__ void take_sums(int *slot, int valid, int (&v)[8])
+// Four neighbouring channels of one token.
+__device__ __forceinline__ void store_four(const Q8LinearParams &g, int m, int n, const int4 &v)
 {
+    const float xs = __ldcg(g.x_scale + m);
+    const int s[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        v[c] = 0;
-        if (c < valid)
-            asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v[c]) : "l"(slot + c * kTileN) : "memory");
+    for (int i = 0; i < 4; ++i)
+        if (n + i < g.N)
+            q8_store(g, m, n + i, s[i], xs, __ldcg(g.w_scale + n + i));
+}
+
+// The sum of a shared tile's slots, by all threads of the CTA that arrived
+// last: CTA `first` holds the tile's first units in its slot 1, the others
+// theirs in slot 0.  Eight 16-byte loads of a thread are in flight together.
+template <int MT, int THREADS>
+__device__ __forceinline__ void finish_tile(const Q8TcParams &p, int m0, int n0, int first, int last)
+{
+    const int items = min(MT, p.g.M - m0) * (kTileN / 4);
+    const int4 *base = reinterpret_cast<const int4 *>(p.ws);
+    const int4 zero = make_int4(0, 0, 0, 0);
+    for (int i0 = threadIdx.x; i0 < items; i0 += 2 * THREADS) {
+        int4 sum[2] = {zero, zero};
+        for (int c0 = first; c0 <= last; c0 += 4) {
+            int4 v[4][2];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int4 *slot = base + static_cast<size_t>(2 * (c0 + c) + (c0 + c == first)) * (MT * kTileN / 4);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    v[c][h] = c0 + c <= last && i0 + h * THREADS < items ? __ldcg(slot + i0 + h * THREADS) : zero;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    sum[h].x += v[c][h].x;
+                    sum[h].y += v[c][h].y;
+                    sum[h].z += v[c][h].z;
+                    sum[h].w += v[c][h].w;
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = i0 + h * THREADS;
+            if (i < items)
+                store_four(p.g, m0 + i / (kTileN / 4), n0 + i % (kTileN / 4) * 4, sum[h]);
+        }
     }
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-        if (c < valid)
-            asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" :: "l"(slot + c * kTileN), "r"(0) : "memory");
 }
 
 template <int MT, bool WIDE>
@@ -266,7 +287,8 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
     uint64_t *xfull = drain + 1;         // [SX]
     uint64_t *xempty = xfull + SX;       // [SX]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(xempty + SX);
-    volatile int *flags = reinterpret_cast<volatile int *>(tmem_slot + 1);  // [0] abort, [1] last
+    volatile int *flags = reinterpret_cast<volatile int *>(tmem_slot + 1);  // [0] abort, [1] tiles to finish
+    volatile int *finish = flags + 2;    // [2] x (tile, first CTA, last CTA)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = static_cast<int>(blockIdx.x);
@@ -506,84 +528,109 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
             const int n = nt * kTileN + row, m0 = mt * MT + col0;
             const int valid = p.g.M - m0;
             const bool whole = s.kb0 == 0 && s.kb1 == p.nkb;
-            const bool direct = whole && (WIDE || p.nkb <= kExactBlocks);
-            // The sums' slot.  A tile shared by several CTAs: CTA c begins at
-            // unit floor(c units / ctas), so the CTA that holds unit u is
-            // floor(((u + 1) ctas - 1) / units), and the slot is that of the
-            // tile's first unit.  A whole tile of several accumulations (not
-            // WIDE): a slot of this CTA's own.
-            int first = p.rem_ctas + cta, last = first;
-            if (!whole) {
-                const int t = s.tile - p.full * static_cast<int>(gridDim.x);
-                const long long u0 = static_cast<long long>(t) * p.nkb;
-                first = static_cast<int>(((u0 + 1) * p.rem_ctas - 1) / p.rem_units);
-                last = static_cast<int>(((u0 + p.nkb) * p.rem_ctas - 1) / p.rem_units);
-            }
-            int *slot = p.ws + static_cast<size_t>(first) * (MT * kTileN) + col0 * kTileN + row;
-            // WIDE adds the accumulations of a segment in registers; with few
-            // columns, where registers are scarce, each goes to its slot.
-            int acc[WIDE ? NC : 1];
+            // This CTA's two slots: 1 for a shared tile whose first units it
+            // has, 0 for any other (and to carry the sums of a whole tile).
+            int *slot = p.ws + static_cast<size_t>(2 * cta + (s.kb0 == 0 && !whole)) * (MT * kTileN) + col0 * kTileN + row;
             bool ok = true;
-            for (int kb = s.kb0; kb < s.kb1; kb += kExactBlocks, ++chunk) {
-                const int t = chunk & 1;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&afull[t], (chunk >> 1) & 1, p.timeout_ns, &flags[0]));
-                if (!ok) {
-                    q8_fail(p, &flags[0], kErrTimeoutEpilogue);
-                    break;
-                }
-                tc_fence_after();
-#pragma unroll(WIDE ? NC / 16 : 1)
-                for (int c0 = 0; c0 < NC; c0 += 16) {
-                    int v[16];
-                    load_sums(lane_base + static_cast<uint32_t>(t * MT + c0), v);
-                    if constexpr (WIDE) {
+            if constexpr (WIDE) {
+                // The accumulations of a segment are added in registers.
+                int acc[NC];
+                for (int kb = s.kb0; kb < s.kb1; kb += kExactBlocks, ++chunk) {
+                    const int t = chunk & 1;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&afull[t], (chunk >> 1) & 1, p.timeout_ns, &flags[0]));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c0 = 0; c0 < NC; c0 += 16) {
+                        int v[16];
+                        load_sums(lane_base + static_cast<uint32_t>(t * MT + c0), v);
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
                             acc[c0 + c] = kb == s.kb0 ? v[c] : acc[c0 + c] + v[c];
-                    } else if (direct) {
-                        store_columns<16>(p.g, m0 + c0, n, v);
-                    } else {
-                        add_sums<16>(slot + c0 * kTileN, valid - c0, v);
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&aempty[t]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&aempty[t]);
+                if (ok && whole) {
+                    store_columns<NC>(p.g, m0, n, acc);
+                } else if (ok) {
+#pragma unroll
+                    for (int c0 = 0; c0 < NC; c0 += 16)
+                        put_sums(slot + c0 * kTileN, valid - c0, *reinterpret_cast<const int(*)[16]>(&acc[c0]));
+                }
+            } else {
+                // Two CTAs share the SM's registers: accumulations go out in
+                // pairs (both TMEM buffers at once), and where a segment has
+                // more than one pair, by way of the slot.
+                for (int kb = s.kb0; kb < s.kb1; kb += 2 * kExactBlocks) {
+                    const bool pair = kb + kExactBlocks < s.kb1, end = kb + 2 * kExactBlocks >= s.kb1;
+                    const int t = chunk & 1;
+                    ok = mbar_wait(&afull[t], (chunk >> 1) & 1, p.timeout_ns, &flags[0]) &&
+                         (!pair || mbar_wait(&afull[t ^ 1], ((chunk + 1) >> 1) & 1, p.timeout_ns, &flags[0]));
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < NC; c0 += 16) {
+                        int v[16], u[16];
+                        load_sums(lane_base + static_cast<uint32_t>(t * MT + c0), v);
+                        if (pair) {
+                            load_sums(lane_base + static_cast<uint32_t>((t ^ 1) * MT + c0), u);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                v[c] += u[c];
+                        }
+                        if (kb > s.kb0) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                u[c] = c0 + c < valid ? __ldcg(slot + (c0 + c) * kTileN) : 0;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                v[c] += u[c];
+                        }
+                        if (end && whole)
+                            store_columns<16>(p.g, m0 + c0, n, v);
+                        else
+                            put_sums(slot + c0 * kTileN, valid - c0, v);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&aempty[t]);
+                        if (pair)
+                            mbar_arrive(&aempty[t ^ 1]);
+                    }
+                    chunk += pair ? 2 : 1;
+                }
             }
+            if (!ok)
+                q8_fail(p, &flags[0], kErrTimeoutEpilogue);
             if (!q8_epi_and<ET>(ok && !flags[0]))
                 break;
-            if (direct) {
-                if constexpr (WIDE)
-                    store_columns<NC>(p.g, m0, n, acc);
-                continue;
-            }
-            if (!whole) {
-                if constexpr (WIDE)
-                    add_sums<NC>(slot, valid, acc);
-                // The barrier orders every thread's additions before one thread's
-                // acq_rel arrival; the last arrival's acquire, passed on by the
-                // next barrier, orders its reads after everyone's additions.
-                q8_epi_sync<ET>();
-                if (ew == 0 && lane == 0) {
-                    unsigned old;
-                    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
-                                 : "=r"(old) : "l"(p.counters + first) : "memory");
-                    flags[1] = old == static_cast<unsigned>(last - first);
-                    if (old == static_cast<unsigned>(last - first))
-                        p.counters[first] = 0;
+            if (!whole && ew == 0 && lane == 0) {
+                // CTA c begins at unit floor(c units / ctas), so the CTA that
+                // holds unit u is floor(((u + 1) ctas - 1) / units).  The
+                // barrier above orders every thread's sums before this acq_rel
+                // arrival; the last arrival's acquire, passed on by the CTA's
+                // last barrier, orders its reads after everyone's sums.
+                const long long u0 = static_cast<long long>(s.tile - p.full * static_cast<int>(gridDim.x)) * p.nkb;
+                const int first = static_cast<int>(((u0 + 1) * p.rem_ctas - 1) / p.rem_units);
+                const int last = static_cast<int>(((u0 + p.nkb) * p.rem_ctas - 1) / p.rem_units);
+                unsigned old;
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                             : "=r"(old) : "l"(p.counters + first) : "memory");
+                if (old == static_cast<unsigned>(last - first)) {
+                    p.counters[first] = 0;
+                    const int k = flags[1];
+                    finish[3 * k] = s.tile;
+                    finish[3 * k + 1] = first;
+                    finish[3 * k + 2] = last;
+                    flags[1] = k + 1;
                 }
-                q8_epi_sync<ET>();
-                const bool mine = flags[1] != 0;
-                q8_epi_sync<ET>();       // read by all before the next tile writes it
-                if (!mine)
-                    continue;
-            }
-#pragma unroll 1
-            for (int c0 = 0; c0 < NC; c0 += 8) {
-                int v[8];
-                take_sums(slot + c0 * kTileN, valid - c0, v);
-                store_columns<8>(p.g, m0 + c0, n, v);
             }
         }
     }
@@ -594,6 +641,13 @@ q8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CU
     if (warp == Sh::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem_base, Sh::kTmemCols);
+    }
+    // Shared tiles that this CTA was the last to add to (at most two): every
+    // warp is free by now.
+    for (int k = 0; k < flags[1] && !flags[0]; ++k) {
+        int nt, mt;
+        tile_at(p, finish[3 * k], nt, mt);
+        finish_tile<MT, Sh::kThreads>(p, mt * MT, nt * kTileN, finish[3 * k + 1], finish[3 * k + 2]);
     }
 }
 
@@ -655,7 +709,6 @@ cudaError_t launch_shape(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q
 Q8TcShape q8_tc_shape(int m_tile)
 {
     switch (m_tile) {
-    case 16: return {2, Q8Shape<16, false>::kSmem, Q8Shape<16, false>::kThreads, Q8Shape<16, false>::kStages};
     case 32: return {2, Q8Shape<32, false>::kSmem, Q8Shape<32, false>::kThreads, Q8Shape<32, false>::kStages};
     case 64: return {2, Q8Shape<64, false>::kSmem, Q8Shape<64, false>::kThreads, Q8Shape<64, false>::kStages};
     case 128: return {1, Q8Shape<128, true>::kSmem, Q8Shape<128, true>::kThreads, Q8Shape<128, true>::kStages};
@@ -667,7 +720,6 @@ cudaError_t launch_q8_tc(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q
                          cudaStream_t s)
 {
     switch (m_tile) {
-    case 16: return launch_shape<16, false>(tmW, tmX, p, grid, s);
     case 32: return launch_shape<32, false>(tmW, tmX, p, grid, s);
     case 64: return launch_shape<64, false>(tmW, tmX, p, grid, s);
     case 128: return launch_shape<128, true>(tmW, tmX, p, grid, s);

@@ -33,9 +33,9 @@ SKG_KERNEL_GEMV = 1
 SKG_KERNEL_SPLITK_TC = 2
 KERNEL_NAMES = {SKG_KERNEL_GEMV: "gemv", SKG_KERNEL_SPLITK_TC: "splitk_tc"}
 
-SKG_Q8_KERNEL_DP4A = 1
+SKG_Q8_KERNEL_STREAM = 1
 SKG_Q8_KERNEL_TC = 2
-Q8_KERNEL_NAMES = {SKG_Q8_KERNEL_DP4A: "q8_dp4a", SKG_Q8_KERNEL_TC: "q8_tc"}
+Q8_KERNEL_NAMES = {SKG_Q8_KERNEL_STREAM: "q8_stream", SKG_Q8_KERNEL_TC: "q8_tc"}
 
 # Every symbol include/skg.h declares.
 EXPORTS = (
@@ -77,7 +77,7 @@ class skg_plan_desc(ctypes.Structure):
 class skg_q8_plan_desc(ctypes.Structure):
     _fields_ = [
         *((f, ctypes.c_int) for f in (
-            "kernel_kind", "M", "N", "K", "epilogue", "static_weights", "m_tile", "tiles", "full_waves", "shared_ctas",
+            "kernel_kind", "M", "N", "K", "epilogue", "static_weights", "m_tile", "n_tile", "tiles", "full_waves", "shared_ctas",
             "grid", "threads", "smem_bytes", "stages", "ctas_per_sm")),
         ("workspace_bytes", ctypes.c_size_t),
     ]

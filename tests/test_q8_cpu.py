@@ -108,8 +108,9 @@ def test_binding_refuses_host_tensors():
 def test_query_describes_a_launch_that_covers_every_tile(M, N, K):
     d = skg.skg_q8_plan_query(M, N, K, "bf16", SMS)
     assert d["grid"] >= 1 and d["threads"] % 32 == 0
-    if d["kernel"] == "q8_dp4a":
-        assert d["workspace_bytes"] == 0
+    assert (d["kernel"] == "q8_stream") == (M <= 16)
+    if d["kernel"] == "q8_stream":
+        assert d["workspace_bytes"] == 0 and d["grid"] == d["tiles"] == -(-N // d["n_tile"]) and M <= d["m_tile"]
         return
     assert d["m_tile"] >= min(M, 128) or M > 128
     assert d["tiles"] == -(-N // 128) * -(-M // d["m_tile"])
@@ -119,9 +120,21 @@ def test_query_describes_a_launch_that_covers_every_tile(M, N, K):
     assert d["shared_ctas"] == min(d["grid"], left * nkb)
     assert d["smem_bytes"] * d["ctas_per_sm"] <= 227 * 1024
     wide = M * K * 2 if d["m_tile"] > 64 else 0
-    own = d["grid"] if d["m_tile"] <= 64 and d["full_waves"] and K > 1024 else 0
-    sums = (d["shared_ctas"] + own) * d["m_tile"] * 512
+    used = d["shared_ctas"] > 0 or (d["m_tile"] <= 64 and K > 2048)
+    sums = d["grid"] * d["m_tile"] * 1024 if used else 0
     assert sums + wide <= d["workspace_bytes"] <= sums + wide + 4 * d["shared_ctas"] + 256
+
+
+@pytest.mark.parametrize("M", [1, 8, 9, 16])
+@pytest.mark.parametrize("N", [1, 384, 16 * SMS, 16 * SMS + 1, 32 * SMS, 32 * SMS + 1, 48 * SMS, 48 * SMS + 1, 12288, 200000])
+def test_streaming_launch_fills_as_few_slots_as_hold_it(M, N):
+    d = skg.skg_q8_plan_query(M, N, 1024, "bf16", SMS)
+    groups = -(-N // 16)
+    if groups <= 3 * SMS:
+        assert d["n_tile"] == 16 and d["ctas_per_sm"] == -(-groups // SMS)
+    else:
+        assert d["n_tile"] == (32 if M <= 8 else 48)
+    assert d["threads"] * d["ctas_per_sm"] <= 1024
 
 
 @pytest.mark.parametrize("units,ctas,nkb", [(1, 1, 1), (7, 7, 7), (56 * 56, 304, 56), (3 * 56, 168, 56), (16 * 151, 152, 16),
@@ -140,4 +153,8 @@ def test_shared_units_are_cut_into_runs_that_name_their_tiles(units, ctas, nkb):
     assert all(((u + 1) * ctas - 1) // units == owner[u] for u in range(units))
     starts = [owner[t * nkb] for t in range(units // nkb)
               if owner[t * nkb] != owner[min(units - 1, t * nkb + nkb - 1)]]
-    assert len(starts) == len(set(starts))               # one slot per shared tile
+    assert len(starts) == len(set(starts))               # one counter per shared tile
+    for c in range(ctas):                                # at most one shared tile begun, and one gone on with
+        mine = sorted({u // nkb for u in range(c * units // ctas, (c + 1) * units // ctas)})
+        shared = [t for t in mine if owner[t * nkb] != owner[t * nkb + nkb - 1]]
+        assert sum(owner[t * nkb] == c for t in shared) <= 1 and sum(owner[t * nkb] != c for t in shared) <= 1

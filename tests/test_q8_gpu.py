@@ -415,7 +415,7 @@ def test_binding_refuses_wrong_tensors():
 
 
 # ------------------------------------------------------------------------- every kernel at every shape
-TILES = (16, 32, 64, 128, 192)
+TILES = (32, 64, 128, 192)
 
 
 @pytest.mark.parametrize("m_tile", TILES)
@@ -439,12 +439,22 @@ def test_every_tile_gives_the_same_bits(M, N, K, ctas, m_tile):
     plan.close()
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 77, 1040), (2, 128, 512), (9, 1001, 4112), (64, 256, 7168)])
-def test_dp4a_kernel_at_any_batch(M, N, K):
-    c = Linear(M, N, K, "fp32", 7)
-    plan = skg.Q8Plan(M, N, K, "fp32")
-    plan.force(skg.SKG_Q8_KERNEL_DP4A)
+@pytest.mark.parametrize("M", [1, 5, 8, 9, 16])
+@pytest.mark.parametrize("N", [1, 77, 2432, 2433, 4864, 5000, 7296, 7297, 12288])
+@pytest.mark.parametrize("K", [16, 1040, 4112])
+def test_streaming_kernel_at_every_launch_shape(M, N, K):
+    c = Linear(M, N, K, "bf16_residual", 7)
+    plan = skg.Q8Plan(M, N, K, "bf16_residual", static_weights=(N + K) % 2 == 0)
+    assert plan.info()["kernel"] == "q8_stream"
     assert R.same_bits(c.run(plan), c.want())
+    plan.close()
+
+
+def test_streaming_kernel_refuses_more_tokens():
+    plan = skg.Q8Plan(17, 128, 128, "bf16")
+    with pytest.raises(skg.SkgError) as e:
+        plan.force(skg.SKG_Q8_KERNEL_STREAM)
+    assert e.value.status == skg.SKG_ERR_UNSUPPORTED and plan.info()["kernel"] == "q8_tc"
     plan.close()
 
 
