@@ -466,7 +466,9 @@ SKG_API skg_status skg_quantize_q8(int M, int K, const void *x, size_t ldx, cons
 
 typedef enum skg_q8_kernel_kind {
     SKG_Q8_KERNEL_STREAM = 1,   /* M <= 16: W streams into registers, warp-level fp16 MMA, exact */
-    SKG_Q8_KERNEL_TC = 2        /* TMA + tcgen05 on integers widened to fp16, exact */
+    SKG_Q8_KERNEL_SPLIT = 2,    /* M <= 64: TMA + tcgen05 on integers widened to fp16, exact; K split
+                                   over the CTAs of a cluster, joined in shared memory */
+    SKG_Q8_KERNEL_WIDE = 3      /* M > 64: the same arithmetic over whole tiles, x multicast to pairs of CTAs */
 } skg_q8_kernel_kind;
 
 /* What an 8-bit plan will launch. */
@@ -474,13 +476,12 @@ typedef struct skg_q8_plan_desc {
     int kernel_kind;            /* skg_q8_kernel_kind */
     int M, N, K, epilogue;
     int static_weights;         /* see skg_q8_plan */
-    int m_tile;                 /* tokens per tile (STREAM: 8 or 16; TC: 32, 64, 128 or 192) */
-    int n_tile;                 /* output channels per tile (STREAM: 16, 32 or 48 a CTA; TC: 128) */
+    int m_tile;                 /* tokens per tile (STREAM: 8 or 16; SPLIT: 32 or 64; WIDE: 128 or 192) */
+    int n_tile;                 /* output channels per tile (STREAM: 16, 32 or 48; SPLIT: 128; WIDE: 256, a pair's) */
     int tiles;                  /* output tiles */
-    int full_waves;             /* TC: whole tiles each CTA computes before the rest is shared */
-    int shared_ctas;            /* TC: CTAs that share the K ranges of the tiles left over */
+    int split_k;                /* SPLIT: CTAs of a cluster, sharing a tile's K (1..8); else 1 */
     int grid, threads, smem_bytes, stages, ctas_per_sm;
-    size_t workspace_bytes;     /* TC: partial sums and counters of shared tiles, and x as fp16 for M > 64 */
+    size_t workspace_bytes;     /* SPLIT: sums carried where a CTA has more than 2048 k; WIDE: x as fp16 */
 } skg_q8_plan_desc;
 
 typedef struct skg_q8_plan_s *skg_q8_plan_t;
@@ -491,7 +492,7 @@ typedef struct skg_q8_plan_s *skg_q8_plan_t;
  * of 16 in [16, 131056] (so that no sum of K products of 8-bit integers can
  * leave 32 bits), epilogue as for skg_plan.
  * Errors: SKG_ERR_INVALID_ARG (M, N, num_sms, epilogue, NULL),
- * SKG_ERR_UNSUPPORTED (K, M above the limits, or more than 2^30 tiles).
+ * SKG_ERR_UNSUPPORTED (K, M above the limits, or more than 2^27 tiles).
  */
 SKG_API skg_status skg_q8_plan_query(int M, int N, int K, int epilogue, int num_sms, skg_q8_plan_desc *out);
 
@@ -526,13 +527,13 @@ SKG_API skg_status skg_q8_run(skg_q8_plan_t plan, const void *x, const float *x_
 
 /*
  * skg_q8_plan_force -- override of the kernel choice (tests and measurements):
- * kind (an skg_q8_kernel_kind, 0 keeps; STREAM: M <= 16), and for TC m_tile (32, 64, 128,
- * 192; 0 = chosen) and ctas, the most CTAs launched (0 = chosen).  Results do
- * not change.  A larger workspace is allocated where needed and the old one kept
- * until the plan is destroyed, as by skg_plan_force.
+ * kind (an skg_q8_kernel_kind, 0 keeps; STREAM: M <= 16), m_tile (SPLIT: 32, 64;
+ * WIDE: 128, 192; 0 = chosen) and split_k (SPLIT: 1..8, no finer than K / 128;
+ * 0 = chosen).  Results do not change.  A larger workspace is allocated where
+ * needed and the old one kept until the plan is destroyed, as by skg_plan_force.
  * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_CUDA.
  */
-SKG_API skg_status skg_q8_plan_force(skg_q8_plan_t plan, int kind, int m_tile, int ctas);
+SKG_API skg_status skg_q8_plan_force(skg_q8_plan_t plan, int kind, int m_tile, int split_k);
 
 /* Copy the plan's launch description into *out. */
 SKG_API skg_status skg_q8_plan_info(skg_q8_plan_t plan, skg_q8_plan_desc *out);

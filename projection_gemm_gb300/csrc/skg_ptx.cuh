@@ -20,6 +20,16 @@ __device__ __forceinline__ uint64_t globaltimer_ns()
     return t;
 }
 
+// One lane of a converged warp, the same one each time.  Where the rest of the
+// code is the whole warp's, the compiler keeps addresses and descriptors in
+// uniform registers, which TMA and tcgen05 instructions read.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------------ PDL
 // Wait until the previous grid in the stream has completed and its memory is
 // visible.  The "memory" clobber keeps the compiler from moving any load of
@@ -376,11 +386,64 @@ __device__ __forceinline__ uint32_t map_shared_rank(uint32_t saddr, uint32_t ran
     return r;
 }
 
+// Arrive on the barrier at this (mapped) address of a CTA of the cluster.  What
+// it announces is in tensor memory (ordered by tcgen05.fence) or was written by
+// copies that this thread has waited for: no ordering of plain memory at cluster
+// scope is asked for, which would wait for all of the thread's stores.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+}
+
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr)
 {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
+}
+
+// ------------------------------------------------------- pairs of CTAs
+// The cta_group::2 forms of the tcgen05 operations above: two CTAs of a
+// cluster hold the halves of A (their own TMEM, M = 256) and of B (their own
+// shared memory, N / 2 rows each), and one thread of the first issues the MMA.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst_smem, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(dst_smem)), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void tmem_relinquish_pair()
+{
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                   uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// Arrive on this CTA's `bar`, or on `bar` of every CTA in `mask`, when the
+// MMAs issued so far by this thread are done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 :: "r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_pair_multicast(uint64_t *bar, uint16_t mask)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(smem_u32(bar)), "h"(mask) : "memory");
 }
 
 // ------------------------------------------------------------- bf16 bits

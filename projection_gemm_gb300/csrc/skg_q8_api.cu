@@ -17,10 +17,9 @@ using namespace skg;
 struct skg_q8_plan_s {
     skg_q8_plan_desc d;
     int num_sms = 0;
-    char *ws = nullptr;               // partial sums, counters, then x as fp16
+    void *ws = nullptr;               // carried sums (split) or x as fp16 (wide)
     size_t ws_cap = 0;
     std::vector<void *> retired;      // outgrown workspaces: a captured graph may still use them
-    bool dirty = false;               // a launch gave up and may have left counters behind
     unsigned int *err_host = nullptr; // mapped pinned word
     unsigned int *err_dev = nullptr;
     cudaStream_t last_stream = nullptr;
@@ -53,89 +52,97 @@ skg_status launched(cudaError_t e, const char *who)
 }
 
 constexpr int kQ8Band = 8;            // token tiles per band of the tile order
-constexpr int kQ8BlockK = 128;        // k per unit of the tensor-core kernel
-constexpr int kQ8L2Ahead = 0;
+constexpr int kQ8BlockK = 128;        // k per unit of the tcgen05 kernels
 constexpr int kStreamMaxM = 16;
+constexpr int kSplitMaxM = 64;
 
-size_t sums_bytes(const skg_q8_plan_desc &d)
+int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+
+// CTAs of a cluster of the split kernel: as many as one wave holds (at most the
+// portable 8), none without a unit of K.
+int choose_split(int tiles, int nkb, int slots)
 {
-    // where tiles are shared, or (two CTAs an SM) a whole tile takes more than one pair of accumulations
-    const bool used = d.shared_ctas > 0 || (d.m_tile <= 64 && d.K > 2048);
-    return used ? static_cast<size_t>(d.grid) * 2 * d.m_tile * kTileN * 4 : 0;
+    return std::max(1, std::min({8, nkb, slots / std::max(1, tiles)}));
 }
 
-size_t counter_bytes(const skg_q8_plan_desc &d) { return (static_cast<size_t>(d.shared_ctas) * 4 + 255) / 256 * 256; }
-
-// Tokens per tile: 32 or 64 where that holds M; above 64, 128 or
-// 192, whichever pads M less (192 where they tie: fewer passes over W).
-int choose_tile(int M)
+// Tokens per tile of the wide kernel: 128 or 192, whichever takes less time in
+// waves (a wave's time grows with the tile; 24 tokens' worth is fixed).
+int choose_wide_tile(int M, int n_pairs, int pairs)
 {
-    if (M <= 64)
-        return M <= 32 ? 32 : 64;
-    const int a = (M + 127) / 128 * 128, b = (M + 191) / 192 * 192;
-    return a < b ? 128 : 192;
+    long long best = 0;
+    int tile = 0;
+    for (const int t : {192, 128}) {
+        const long long waves = (static_cast<long long>(n_pairs) * ceil_div(M, t) + pairs - 1) / pairs;
+        const long long cost = waves * (t + 24);
+        if (!tile || cost < best) {
+            best = cost;
+            tile = t;
+        }
+    }
+    return tile;
 }
 
-skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int ctas, int num_sms, const char *who)
+skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int split, int num_sms, const char *who)
 {
-    d->kernel_kind = kind ? kind : (d->M <= kStreamMaxM ? SKG_Q8_KERNEL_STREAM : SKG_Q8_KERNEL_TC);
-    d->m_tile = d->tiles = d->full_waves = d->shared_ctas = d->smem_bytes = d->stages = 0;
+    if (!kind)
+        kind = d->M <= kStreamMaxM ? SKG_Q8_KERNEL_STREAM : (d->M <= kSplitMaxM ? SKG_Q8_KERNEL_SPLIT : SKG_Q8_KERNEL_WIDE);
+    d->kernel_kind = kind;
+    d->split_k = 1;
+    d->smem_bytes = d->stages = 0;
     d->workspace_bytes = 0;
-    if (d->kernel_kind == SKG_Q8_KERNEL_STREAM) {
+    if (kind == SKG_Q8_KERNEL_STREAM) {
         if (d->M > kStreamMaxM)
             return set_error(SKG_ERR_UNSUPPORTED, "%s: the streaming kernel takes at most %d tokens (M=%d)", who,
                              kStreamMaxM, d->M);
         const Q8StreamShape sh = q8_stream_shape(d->M, d->N, num_sms);
         d->m_tile = d->M <= 8 ? 8 : 16;
         d->n_tile = 16 * sh.groups;
-        d->tiles = d->grid = (d->N - 1) / d->n_tile + 1;
+        d->tiles = d->grid = ceil_div(d->N, d->n_tile);
         d->threads = 32 * sh.warps;
         d->ctas_per_sm = sh.ctas_per_sm;
         return SKG_OK;
     }
-    d->n_tile = kTileN;
-    d->m_tile = m_tile ? m_tile : choose_tile(d->M);
-    const Q8TcShape sh = q8_tc_shape(d->m_tile);
-    const long long tiles = (static_cast<long long>(d->N) + kTileN - 1) / kTileN * ((d->M + d->m_tile - 1) / d->m_tile);
-    if (tiles > (1ll << 30))
-        return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^30 tiles", who);
-    const int nkb = (d->K + kQ8BlockK - 1) / kQ8BlockK;
-    const int most = ctas ? ctas : num_sms * sh.ctas_per_sm;
+    const int nkb = ceil_div(d->K, kQ8BlockK), n_tiles = ceil_div(d->N, kTileN);
+    const bool wide = kind == SKG_Q8_KERNEL_WIDE;
+    d->n_tile = wide ? 2 * kTileN : kTileN;
+    if (!m_tile)
+        m_tile = wide ? choose_wide_tile(d->M, ceil_div(n_tiles, 2), std::max(1, num_sms / 2)) : (d->M <= 32 ? 32 : 64);
+    d->m_tile = m_tile;
+    const long long tiles = static_cast<long long>(ceil_div(d->N, d->n_tile)) * ceil_div(d->M, m_tile);
+    if (tiles > (1ll << 27))
+        return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^27 tiles", who);
     d->tiles = static_cast<int>(tiles);
-    d->grid = static_cast<int>(std::min<long long>(most, tiles * nkb));
-    d->full_waves = d->tiles / d->grid;
-    const int left = d->tiles % d->grid;
-    d->shared_ctas = static_cast<int>(std::min<long long>(d->grid, static_cast<long long>(left) * nkb));
+    const Q8TcShape sh = wide ? q8_wide_shape(m_tile) : q8_split_shape(m_tile);
     d->threads = sh.threads;
     d->smem_bytes = sh.smem_bytes;
     d->stages = sh.stages;
     d->ctas_per_sm = sh.ctas_per_sm;
-    d->workspace_bytes = sums_bytes(*d) + counter_bytes(*d);
-    if (d->m_tile > 64)
-        d->workspace_bytes += static_cast<size_t>(d->M) * d->K * 2;
+    if (wide) {
+        d->grid = 2 * std::min(d->tiles, std::max(1, num_sms / 2));
+        d->workspace_bytes = static_cast<size_t>(d->M) * d->K * 2;
+        return SKG_OK;
+    }
+    d->split_k = split ? std::min(split, nkb) : choose_split(d->tiles, nkb, num_sms * sh.ctas_per_sm);
+    d->grid = d->tiles * d->split_k;
+    if (ceil_div(nkb, d->split_k) * kQ8BlockK > 2048)
+        d->workspace_bytes = static_cast<size_t>(d->grid) * m_tile * kTileN * 4;
     return SKG_OK;
 }
 
-// A workspace for the plan's launch, its counters zero.
 skg_status ensure_workspace(skg_q8_plan_s *p, const char *who)
 {
     const size_t need = p->d.workspace_bytes;
-    cudaError_t e = cudaSuccess;
-    if (need > p->ws_cap) {
-        char *ws = nullptr;
-        e = cudaMalloc(reinterpret_cast<void **>(&ws), need);
-        if (e != cudaSuccess)
-            return launched(e, who);
-        if (p->ws)
-            p->retired.push_back(p->ws);
-        p->ws = ws;
-        p->ws_cap = need;
-    }
-    if (need)
-        e = cudaMemset(p->ws + sums_bytes(p->d), 0, counter_bytes(p->d));
-    if (e == cudaSuccess)
-        e = cudaStreamSynchronize(nullptr);
-    return launched(e, who);
+    if (need <= p->ws_cap)
+        return SKG_OK;
+    void *ws = nullptr;
+    const cudaError_t e = cudaMalloc(&ws, need);
+    if (e != cudaSuccess)
+        return launched(e, who);
+    if (p->ws)
+        p->retired.push_back(p->ws);
+    p->ws = ws;
+    p->ws_cap = need;
+    return SKG_OK;
 }
 
 } // namespace
@@ -265,22 +272,23 @@ skg_status skg_q8_plan(int M, int N, int K, int epilogue, int static_weights, sk
     return SKG_OK;
 }
 
-skg_status skg_q8_plan_force(skg_q8_plan_t p, int kind, int m_tile, int ctas)
+skg_status skg_q8_plan_force(skg_q8_plan_t p, int kind, int m_tile, int split_k)
 {
     static const char who[] = "skg_q8_plan_force";
     if (!p)
         return set_error(SKG_ERR_INVALID_ARG, "%s: plan is NULL", who);
-    if (kind != 0 && kind != SKG_Q8_KERNEL_STREAM && kind != SKG_Q8_KERNEL_TC)
+    if (kind < 0 || kind > SKG_Q8_KERNEL_WIDE)
         return set_error(SKG_ERR_INVALID_ARG, "%s: unknown kernel kind %d", who, kind);
-    if (m_tile != 0 && m_tile != 32 && m_tile != 64 && m_tile != 128 && m_tile != 192)
-        return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile must be 0, 32, 64, 128 or 192 (got %d)", who, m_tile);
-    if (ctas < 0 || ctas > (1 << 16))
-        return set_error(SKG_ERR_INVALID_ARG, "%s: ctas must be in [0, 65536] (got %d)", who, ctas);
     skg_q8_plan_desc d = p->d;
     const int k = kind ? kind : d.kernel_kind;
-    if (k == SKG_Q8_KERNEL_STREAM && (m_tile || ctas))
-        return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile and ctas belong to the tensor-core kernel", who);
-    skg_status st = fill_launch(&d, k, m_tile, ctas, p->num_sms, who);
+    const bool tile_ok = m_tile == 0 || (k == SKG_Q8_KERNEL_SPLIT && (m_tile == 32 || m_tile == 64)) ||
+                         (k == SKG_Q8_KERNEL_WIDE && (m_tile == 128 || m_tile == 192));
+    if (!tile_ok)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile %d is none of this kernel's", who, m_tile);
+    if (split_k < 0 || split_k > 8 || (split_k && k != SKG_Q8_KERNEL_SPLIT))
+        return set_error(SKG_ERR_INVALID_ARG, "%s: split_k must be in [1, 8], for the split kernel alone (got %d)", who,
+                         split_k);
+    skg_status st = fill_launch(&d, k, m_tile, split_k, p->num_sms, who);
     if (st != SKG_OK)
         return st;
     const skg_q8_plan_desc old = p->d;
@@ -317,10 +325,8 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
     if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(y, d.epilogue == SKG_EPI_FP32 ? 4 : 2) ||
         !aligned(residual, 2))
         return set_error(SKG_ERR_ALIGNMENT, "%s: a scale, y or residual misses its element alignment", who);
-    if (__atomic_exchange_n(p->err_host, 0u, __ATOMIC_ACQ_REL) != 0) {
-        p->dirty = true;
+    if (__atomic_exchange_n(p->err_host, 0u, __ATOMIC_ACQ_REL) != 0)
         return set_error(SKG_ERR_DEVICE_TIMEOUT, "%s: an earlier launch of this plan ran out of a bounded wait", who);
-    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     p->last_stream = s;
     Q8LinearParams g = {};
@@ -337,42 +343,44 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
     if (d.kernel_kind == SKG_Q8_KERNEL_STREAM)
         return launched(launch_q8_stream(g, {d.n_tile / 16, d.threads / 32, d.ctas_per_sm}, d.static_weights != 0, s), who);
 
-    Q8TcParams t = {};
-    t.g = g;
-    t.ws = reinterpret_cast<int *>(p->ws);
-    t.counters = reinterpret_cast<unsigned *>(p->ws + sums_bytes(d));
-    t.err = p->err_dev;
-    t.nkb = (d.K + kQ8BlockK - 1) / kQ8BlockK;
-    t.n_tiles = (d.N + kTileN - 1) / kTileN;
-    t.m_tiles = (d.M + d.m_tile - 1) / d.m_tile;
-    t.full = d.full_waves;
-    t.rem_units = d.tiles % d.grid * t.nkb;
-    t.rem_ctas = d.shared_ctas;
-    t.band = kQ8Band;
-    t.static_w = d.static_weights;
-    t.ahead = kQ8L2Ahead;
-    t.timeout_ns = kDefaultTimeoutNs;
+    const int nkb = ceil_div(d.K, kQ8BlockK), m_tiles = ceil_div(d.M, d.m_tile);
     CUtensorMap tmW, tmX;
     skg_status st = encode_tiled_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, d.N, d.K, kTileN);
     if (st != SKG_OK)
         return st;
-    cudaError_t e = cudaSuccess;
-    if (p->dirty) {
-        e = cudaMemsetAsync(t.counters, 0, counter_bytes(d), s);
-        p->dirty = e != cudaSuccess;
-    }
-    if (d.m_tile > 64) {
-        void *x16 = p->ws + sums_bytes(d) + counter_bytes(d);
-        st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x16, d.M, d.K, d.m_tile);
-        if (st == SKG_OK && e == cudaSuccess)
-            e = launch_q8_widen(g.x, x16, static_cast<size_t>(d.M) * d.K, p->num_sms, s);
-    } else {
+    if (d.kernel_kind == SKG_Q8_KERNEL_SPLIT) {
         st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, d.M, d.K, d.m_tile);
+        if (st != SKG_OK)
+            return st;
+        Q8SplitParams t = {};
+        t.g = g;
+        t.carry = static_cast<int *>(p->ws);
+        t.err = p->err_dev;
+        t.nkb = nkb;
+        t.m_tiles = m_tiles;
+        t.split = d.split_k;
+        t.static_w = d.static_weights;
+        t.vec4 = d.N % 4 == 0 && aligned(w_scale, 16) && aligned(residual, 8) &&
+                 aligned(y, d.epilogue == SKG_EPI_FP32 ? 16 : 8);
+        t.timeout_ns = kDefaultTimeoutNs;
+        return launched(launch_q8_split(tmW, tmX, t, d.m_tile, d.grid, s), who);
     }
+    st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p->ws, d.M, d.K, d.m_tile / 2);
     if (st != SKG_OK)
         return st;
+    Q8WideParams t = {};
+    t.g = g;
+    t.err = p->err_dev;
+    t.nkb = nkb;
+    t.n_pairs = ceil_div(d.N, 2 * kTileN);
+    t.m_tiles = m_tiles;
+    t.tiles = d.tiles;
+    t.band = kQ8Band;
+    t.static_w = d.static_weights;
+    t.timeout_ns = kDefaultTimeoutNs;
+    cudaError_t e = launch_q8_widen(g.x, p->ws, static_cast<size_t>(d.M) * d.K, p->num_sms, s);
     if (e == cudaSuccess)
-        e = launch_q8_tc(tmW, tmX, t, d.m_tile, d.grid, s);
+        e = launch_q8_wide(tmW, tmX, t, d.m_tile, d.grid, s);
     return launched(e, who);
 }
 
@@ -387,10 +395,8 @@ skg_status skg_q8_plan_check(skg_q8_plan_t p)
     if (e != cudaSuccess)
         return launched(e, who);
     const unsigned w = __atomic_exchange_n(p->err_host, 0u, __ATOMIC_ACQ_REL);
-    if (w != 0) {
-        p->dirty = true;
+    if (w != 0)
         return set_error(SKG_ERR_DEVICE_TIMEOUT, "a kernel of this plan ran out of a bounded wait (bits 0x%x)", w);
-    }
     return SKG_OK;
 }
 

@@ -37,16 +37,23 @@ struct Q8LinearParams {
     int M, N, K, epilogue;
 };
 
-// The tensor-core kernel's launch: tiles of 128 channels x m_tile tokens; each
-// of grid CTAs takes `full` whole tiles, then rem_ctas of them share the
-// rem_units units (tile, 128 k) of the tiles left over.
-struct Q8TcParams {
+// The split kernel's launch: clusters of `split` CTAs, one tile of 128 channels
+// x m_tile tokens each, K cut over the cluster in units of 128.
+struct Q8SplitParams {
     Q8LinearParams g;
-    int *ws;                  // two slots of [m_tile][128] int32 for each CTA
-    unsigned *counters;       // [rem_ctas], zero between runs
+    int *carry;               // [grid][m_tile][128] int32, where a CTA has more than 2048 k; else null
     unsigned *err;
-    int nkb, n_tiles, m_tiles, full, rem_units, rem_ctas, band, static_w;
-    int ahead;                // static weights: units after the ring requested into L2 before the wait
+    int nkb, m_tiles, split, static_w;
+    int vec4;                 // N a multiple of 4, w_scale, residual and y aligned for four channels at a time
+    unsigned long long timeout_ns;
+};
+
+// The wide kernel's launch: tiles of 2 x 128 channels x m_tile tokens, one per
+// pair of CTAs at a time.
+struct Q8WideParams {
+    Q8LinearParams g;
+    unsigned *err;
+    int nkb, n_pairs, m_tiles, tiles, band, static_w;
     unsigned long long timeout_ns;
 };
 
@@ -54,9 +61,12 @@ struct Q8TcShape {
     int ctas_per_sm, smem_bytes, threads, stages;
 };
 
-Q8TcShape q8_tc_shape(int m_tile);
-cudaError_t launch_q8_tc(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8TcParams &p, int m_tile, int grid,
-                         cudaStream_t s);
+Q8TcShape q8_split_shape(int m_tile);
+Q8TcShape q8_wide_shape(int m_tile);
+cudaError_t launch_q8_split(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8SplitParams &p, int m_tile, int grid,
+                            cudaStream_t s);
+cudaError_t launch_q8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8WideParams &p, int m_tile, int grid,
+                           cudaStream_t s);
 cudaError_t launch_q8_widen(const int8_t *x, void *out, size_t elements, int num_sms, cudaStream_t s);
 
 cudaError_t launch_q8_norm(const Q8RowParams &p, cudaStream_t s);

@@ -1,0 +1,466 @@
+// skg_q8_split.cu -- the 8-bit projection for a decode batch: tcgen05, with K
+// split over the CTAs of a cluster.
+//
+// sm_103a has no integer kind of tcgen05.mma, and 8-bit integers are exact in
+// fp16, as are their products (at most 2^14) and, in fp32, sums of up to 1024
+// such products (at most 2^24).  So the integers are widened to fp16 on chip,
+// multiplied with kind::f16 from a fresh accumulator every 1024 k, and the
+// accumulators are added as int32: the exact integer sum, for any split of K.
+//
+// Tile (swap-AB): 128 rows of W are the MMA's M, MT tokens its N.  A cluster of
+// S CTAs computes one tile; CTA r takes the r-th part of K in units of 128.
+// What bounds it is W from HBM: two CTAs of an SM hold 2 x 3 units (MT = 64) in
+// flight.  Roles of a CTA:
+//   8 warps   widen, two sets of 4 on alternate units: a thread reads its W
+//             row's 128 bytes from the TMA ring and writes them as fp16 to its
+//             TMEM lane (the MMA's A operand); the same warps widen the x tile
+//             into shared memory (the B operand)
+//   4 or 8    epilogue: accumulators to integers
+//   1 + 1     TMA; TMEM and MMA issue
+// Then the cluster's CTAs leave their sums in their own shared memory and each
+// adds up and stores 1/S of the tile's tokens, read from its peers.  Through
+// global memory instead (partial sums, an arrival counter, the last CTA adds
+// up) the same step took 6 us at M = 32 and 10 at M = 64: each round trip waits
+// 1 to 1.7 us behind the next launch's weights.
+//
+// Every wait is bounded; on expiry a thread records the timeout in the plan's
+// error word, raises the CTA's abort flag, waits for its own copies and MMAs,
+// and the CTA goes on to the cluster's barriers, frees its TMEM and returns.
+#include <algorithm>
+
+#include "skg_internal.h"
+#include "skg_ptx.cuh"
+#include "skg_q8_common.cuh"
+#include "skg_q8_internal.h"
+
+namespace skg {
+namespace {
+
+#include "skg_q8_tc_common.cuh"
+
+template <int MT>
+struct SplitShape {
+    static constexpr int kEpiWarps = MT / 8;
+    static constexpr int kCols = MT * 4 / kEpiWarps;         // accumulator columns of an epilogue thread: 32
+    static constexpr int kThreads = 32 * (kWidenWarps + kEpiWarps + 2);
+    static constexpr int kTmaWarp = kWidenWarps + kEpiWarps;
+    static constexpr int kMmaWarp = kTmaWarp + 1;
+    static constexpr int kStages = MT == 32 ? 4 : 3;         // ring of W and int8 x
+    static constexpr int kOps = MT == 32 ? 3 : 2;            // widened operand buffers
+    static_assert(kStages >= kOps && kOps >= kWidenSets, "the widen warps' waits need this");
+    static constexpr uint32_t kRawX = MT * kQ8BlockK;
+    static constexpr uint32_t kX16 = MT * kQ8BlockK * 2;     // fp16 x of one unit: two 64-wide halves
+    static constexpr uint32_t kTmemCols = 256;
+    static_assert(2 * MT + kOps * 64 <= 256, "two CTAs share the SM's tensor memory");
+    static constexpr uint32_t kIdesc = idesc_f16_f32(kTileN, MT);
+    static constexpr int kBars = 2 * kStages + 2 * kOps + 5;
+    static constexpr int kSmem = 1024 + kStages * (kQ8WBytes + kRawX) + kOps * kX16 + kBars * 8 + 16;
+    static_assert(kStages * (kQ8WBytes + kRawX) >= MT * kTileN * 4, "the sums take the ring's place");
+};
+
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr)
+{
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// What four neighbouring outputs (channels n.., token m) need besides their sums.
+struct Four {
+    float xs, ws[4];
+    uint16_t res[4];
+};
+
+__device__ __forceinline__ Four load_four(const Q8LinearParams &g, int m, int n, bool vec4)
+{
+    Four f;
+    f.xs = __ldcg(g.x_scale + m);
+    const size_t o = static_cast<size_t>(m) * g.N + n;
+    const bool res = g.epilogue == SKG_EPI_BF16_RESIDUAL;
+    if (vec4) {                          // n is a multiple of 4 and N too
+        const float4 w = n < g.N ? __ldcg(reinterpret_cast<const float4 *>(g.w_scale + n)) : make_float4(0, 0, 0, 0);
+        f.ws[0] = w.x, f.ws[1] = w.y, f.ws[2] = w.z, f.ws[3] = w.w;
+        const uint2 r = res && n < g.N ? __ldcg(reinterpret_cast<const uint2 *>(g.res + o)) : make_uint2(0, 0);
+        f.res[0] = r.x & 0xFFFF, f.res[1] = r.x >> 16, f.res[2] = r.y & 0xFFFF, f.res[3] = r.y >> 16;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f.ws[i] = n + i < g.N ? __ldcg(g.w_scale + n + i) : 0.0f;
+            f.res[i] = res && n + i < g.N ? __ldcg(g.res + o + i) : 0;
+        }
+    }
+    return f;
+}
+
+__device__ __forceinline__ void store_four(const Q8LinearParams &g, int m, int n, bool vec4, const Four &f, const int4 &sum)
+{
+    const int s[4] = {sum.x, sum.y, sum.z, sum.w};
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = q8_scaled(s[i], f.xs, f.ws[i]);
+        if (g.epilogue == SKG_EPI_BF16_RESIDUAL)
+            v[i] = __fadd_rn(v[i], bf16_to_f32(f.res[i]));
+    }
+    const size_t o = static_cast<size_t>(m) * g.N + n;
+    if (g.epilogue == SKG_EPI_FP32) {
+        float *y = static_cast<float *>(g.y) + o;
+        if (vec4 && n < g.N) {
+            *reinterpret_cast<float4 *>(y) = make_float4(v[0], v[1], v[2], v[3]);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < g.N)
+                y[i] = v[i];
+        return;
+    }
+    uint16_t *y = static_cast<uint16_t *>(g.y) + o;
+    if (vec4 && n < g.N) {
+        *reinterpret_cast<uint2 *>(y) = make_uint2(f32_to_bf16(v[0]) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16,
+                                                   f32_to_bf16(v[2]) | static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < g.N)
+            y[i] = f32_to_bf16(v[i]);
+}
+
+template <int MT>
+__global__ void __launch_bounds__(SplitShape<MT>::kThreads, 2)
+q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Q8SplitParams p)
+{
+    using Sh = SplitShape<MT>;
+    constexpr int S = Sh::kStages, OPS = Sh::kOps;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sW = smem;
+    uint8_t *sXraw = sW + S * kQ8WBytes;
+    uint8_t *sX16 = sXraw + S * Sh::kRawX;
+    uint64_t *wfull = reinterpret_cast<uint64_t *>(sX16 + OPS * Sh::kX16);
+    uint64_t *wempty = wfull + S;
+    uint64_t *opfull = wempty + S;
+    uint64_t *opempty = opfull + OPS;
+    uint64_t *afull = opempty + OPS;     // [2] accumulators
+    uint64_t *aempty = afull + 2;        // [2]
+    uint64_t *drain = aempty + 2;        // [1]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *flags = reinterpret_cast<volatile int *>(tmem_slot + 1);  // [0] abort
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile = static_cast<int>(blockIdx.x) / p.split, rank = static_cast<int>(blockIdx.x) % p.split;
+    const int n0 = tile / p.m_tiles * kTileN, m0 = tile % p.m_tiles * MT;
+    const int kb0 = rank * p.nkb / p.split, blocks = (rank + 1) * p.nkb / p.split - kb0;
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&wfull[i], 1);
+            mbar_init(&wempty[i], 4);
+        }
+        for (int i = 0; i < OPS; ++i) {
+            mbar_init(&opfull[i], 4);
+            mbar_init(&opempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&afull[i], 1);
+            mbar_init(&aempty[i], Sh::kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        flags[0] = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    uint32_t tmem_base = 0;
+    if (warp != Sh::kTmaWarp) {          // the TMA warp needs no TMEM: its first copies leave at once
+        if (warp == Sh::kMmaWarp) {
+            tmem_alloc(tmem_slot, Sh::kTmemCols);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        asm volatile("bar.sync 2, %0;" :: "n"(Sh::kThreads - 32) : "memory");
+        tc_fence_after();
+        tmem_base = *tmem_slot;
+    }
+
+    if (warp == Sh::kTmaWarp) {
+        // -------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            // W passes once where one token tile holds all of M
+            const uint64_t pol_w = p.m_tiles == 1 ? policy_evict_first() : policy_evict_normal();
+            const uint64_t pol_x = policy_evict_last();
+            auto load_w = [&](int j) {
+                mbar_arrive_expect_tx(&wfull[j % S], kQ8WBytes + Sh::kRawX);
+                tma_load_2d(sW + j % S * kQ8WBytes, &tmW, &wfull[j % S], (kb0 + j) * kQ8BlockK, n0, pol_w);
+            };
+            auto load_x = [&](int j) {
+                tma_load_2d(sXraw + j % S * Sh::kRawX, &tmX, &wfull[j % S], (kb0 + j) * kQ8BlockK, m0, pol_x);
+            };
+            if (!p.static_w)
+                pdl_wait();
+            const int first = min(S, blocks);
+            for (int j = 0; j < first; ++j)
+                load_w(j);
+            if (p.static_w)              // weights may be requested before the wait for the previous kernel
+                pdl_wait();
+            for (int j = 0; j < first; ++j)
+                load_x(j);
+            int j = first;
+            for (; j < blocks; ++j) {
+                if (!mbar_wait(&wempty[j % S], ((j / S) & 1) ^ 1, p.timeout_ns, &flags[0])) {
+                    q8_fail(p.err, &flags[0], kErrTimeoutProducer);
+                    break;
+                }
+                load_w(j);
+                load_x(j);
+            }
+            if (flags[0]) {              // abort: let every copy land before exit
+                volatile int never = 0;
+                for (int k = 0; k < S && k < j; ++k)
+                    mbar_wait(&wfull[k], ((j - 1 - k) / S) & 1, kDefaultTimeoutNs, &never);
+            }
+        }
+    } else if (warp == Sh::kMmaWarp) {
+        // ---------------------------------------------------------- MMA issuer
+        {
+            const bool leader = elect_one();
+            bool ok = true;
+            for (int j = 0; j < blocks; ++j) {
+                const int chunk = j / kExactBlocks, in_chunk = j % kExactBlocks, t = chunk & 1, b = j % OPS;
+                if (in_chunk == 0)
+                    ok = mbar_wait(&aempty[t], ((chunk >> 1) & 1) ^ 1, p.timeout_ns, &flags[0]);
+                ok = ok && mbar_wait(&opfull[b], (j / OPS) & 1, p.timeout_ns, &flags[0]);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) {
+                    q8_fail(p.err, &flags[0], kErrTimeoutMma);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t bx = smem_u32(sX16 + b * Sh::kX16);
+                const uint32_t d = tmem_base + static_cast<uint32_t>(t * MT);
+                const uint32_t a = tmem_base + static_cast<uint32_t>(2 * MT + b * 64);
+                const uint64_t b0 = smem_desc_kmajor_sw128(bx), b1 = smem_desc_kmajor_sw128(bx + MT * 128);
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < kQ8BlockK / 16; ++kk)
+                        tc_mma_f16_ts(d, a + 8 * kk, (kk < 4 ? b0 : b1) + 2 * (kk & 3), Sh::kIdesc,
+                                      (in_chunk > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(&opempty[b]);
+                    if (in_chunk == kExactBlocks - 1 || j + 1 == blocks)
+                        tc_commit(&afull[t]);
+                }
+                __syncwarp();
+            }
+            if (!ok) {                   // abort: wait for the MMAs already issued before TMEM is freed
+                if (leader)
+                    tc_commit(drain);
+                volatile int never = 0;
+                mbar_wait(drain, 0, kDefaultTimeoutNs, &never);
+            }
+        }
+    } else if (warp < kWidenWarps) {
+        // --------------------------------------------------------------- widen
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * MT;
+        for (int j = warp >> 2; j < blocks; j += kWidenSets) {
+            const int sl = j % S, b = j % OPS;
+            // The operand buffer first: once the MMA of unit j - OPS is done, unit
+            // j - S <= j - OPS has been widened, so the ring slot's barrier is at
+            // most one phase behind and its parity says which.  (The sets run
+            // apart: by the parity alone, a slot still waiting for unit j - S
+            // looks like one that holds unit j.)
+            const bool ok = mbar_wait(&opempty[b], ((j / OPS) & 1) ^ 1, p.timeout_ns, &flags[0]) &&
+                            mbar_wait(&wfull[sl], (j / S) & 1, p.timeout_ns, &flags[0]);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {      // the whole warp goes on, or none of it
+                q8_fail(p.err, &flags[0], kErrTimeoutWiden);
+                break;
+            }
+            tc_fence_after();
+            widen_row<8>(sW + sl * kQ8WBytes, row, 0, lane_base + b * 64);
+            const uint8_t *xs = sXraw + sl * Sh::kRawX;
+            uint8_t *xd = sX16 + b * Sh::kX16;
+#pragma unroll 2
+            for (int i = 0; i < MT / 16; ++i) {
+                const int c = lane & 7, m = i * 16 + quarter * 4 + (lane >> 3), cc = (c & 3) * 2;
+                uint32_t r[8];
+                widen16(*reinterpret_cast<const uint4 *>(xs + m * 128 + ((c ^ (m & 7)) << 4)), r);
+                uint8_t *dst = xd + (c >> 2) * (MT * 128) + m * 128;
+                *reinterpret_cast<uint4 *>(dst + ((cc ^ (m & 7)) << 4)) = make_uint4(r[0], r[1], r[2], r[3]);
+                *reinterpret_cast<uint4 *>(dst + (((cc + 1) ^ (m & 7)) << 4)) = make_uint4(r[4], r[5], r[6], r[7]);
+            }
+            fence_proxy_async_smem();
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&opfull[b]);
+                mbar_arrive(&wempty[sl]);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        constexpr int NC = Sh::kCols;
+        pdl_wait();                      // scales, residual, workspace and y only from here on
+        const int ew = warp - kWidenWarps;
+        const int row = (warp & 3) * 32 + lane;
+        const int col0 = (ew >> 2) * NC, valid = p.g.M - m0 - col0;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(col0);
+        // Accumulations leave TMEM in pairs, both buffers at once.  More than
+        // one pair (2048 k) is carried in global memory: registers and shared
+        // memory are taken, and it is read back long after.
+        int *carry = p.carry + static_cast<size_t>(blockIdx.x) * (MT * kTileN) + col0 * kTileN + row;
+        int *sums = reinterpret_cast<int *>(smem) + col0 * kTileN + row;
+        int chunk = 0;
+        for (int j = 0; j < blocks; j += 2 * kExactBlocks) {
+            const bool pair = j + kExactBlocks < blocks, end = j + 2 * kExactBlocks >= blocks;
+            const uint32_t ph = (chunk >> 1) & 1;
+            bool ok = mbar_wait(&afull[0], ph, p.timeout_ns, &flags[0]) &&
+                      (!pair || mbar_wait(&afull[1], ph, p.timeout_ns, &flags[0]));
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                q8_fail(p.err, &flags[0], kErrTimeoutEpilogue);
+                break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < NC; c0 += 16) {
+                int v[16], u[16];
+                load_sums(lane_base + static_cast<uint32_t>(c0), v);
+                if (pair) {
+                    load_sums(lane_base + static_cast<uint32_t>(MT + c0), u);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        v[c] += u[c];
+                }
+                if (j > 0) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        u[c] = c0 + c < valid ? __ldcg(carry + (c0 + c) * kTileN) : 0;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        v[c] += u[c];
+                }
+                if (!end) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (c0 + c < valid)
+                            __stcg(carry + (c0 + c) * kTileN, v[c]);
+                } else if (p.split == 1) {
+                    store_columns<16>(p.g, m0 + col0 + c0, n0 + row, v);
+                } else {
+                    // the ring is done with: the last MMA has read its operands
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        sums[(c0 + c) * kTileN] = v[c];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&aempty[0]);
+                mbar_arrive(&aempty[1]);
+            }
+            chunk += 2;
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    if (p.split > 1) {
+        // This CTA's share of the tile: tokens [t0, t1) of 128 channels, four channels a thread.
+        const int tokens = min(MT, p.g.M - m0);
+        const int t0 = rank * tokens / p.split, t1 = (rank + 1) * tokens / p.split;
+        const int n = n0 + (static_cast<int>(threadIdx.x) & 31) * 4;
+        const bool vec4 = p.vec4 != 0;
+        int m = t0 + static_cast<int>(threadIdx.x >> 5);
+        Four f = {};
+        pdl_wait();
+        if (m < t1)
+            f = load_four(p.g, m0 + m, n, vec4);     // on its way while the cluster meets
+        cluster_sync();
+        const uint32_t base = smem_u32(smem) + (threadIdx.x & 31) * 16;
+        while (m < t1) {
+            int4 sum = make_int4(0, 0, 0, 0);
+            int4 v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                v[r] = r < p.split ? ld_cluster_v4(map_shared_rank(base + m * (kTileN * 4), r)) : make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                sum.x += v[r].x;
+                sum.y += v[r].y;
+                sum.z += v[r].z;
+                sum.w += v[r].w;
+            }
+            store_four(p.g, m0 + m, n, vec4, f, sum);
+            m += Sh::kThreads / 32;
+            if (m < t1)
+                f = load_four(p.g, m0 + m, n, vec4);
+        }
+        cluster_sync();                  // no CTA leaves while a peer reads its sums
+    } else {
+        __syncthreads();
+    }
+    if (warp == Sh::kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, Sh::kTmemCols);
+    }
+}
+
+template <int MT>
+cudaError_t launch_shape(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8SplitParams &p, int grid, cudaStream_t s)
+{
+    using Sh = SplitShape<MT>;
+    static int attr_set[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    if (__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE) == 0) {
+        e = cudaFuncSetAttribute(q8_split_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(q8_split_kernel<MT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess)
+            return e;
+        __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(Sh::kThreads);
+    cfg.dynamicSmemBytes = Sh::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, q8_split_kernel<MT>, tmW, tmX, p);
+}
+
+template <int MT>
+Q8TcShape shape_of()
+{
+    return {2, SplitShape<MT>::kSmem, SplitShape<MT>::kThreads, SplitShape<MT>::kStages};
+}
+
+} // namespace
+
+Q8TcShape q8_split_shape(int m_tile) { return m_tile == 32 ? shape_of<32>() : shape_of<64>(); }
+
+cudaError_t launch_q8_split(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8SplitParams &p, int m_tile, int grid,
+                            cudaStream_t s)
+{
+    return m_tile == 32 ? launch_shape<32>(tmW, tmX, p, grid, s) : launch_shape<64>(tmW, tmX, p, grid, s);
+}
+
+} // namespace skg

@@ -34,8 +34,10 @@ SKG_KERNEL_SPLITK_TC = 2
 KERNEL_NAMES = {SKG_KERNEL_GEMV: "gemv", SKG_KERNEL_SPLITK_TC: "splitk_tc"}
 
 SKG_Q8_KERNEL_STREAM = 1
-SKG_Q8_KERNEL_TC = 2
-Q8_KERNEL_NAMES = {SKG_Q8_KERNEL_STREAM: "q8_stream", SKG_Q8_KERNEL_TC: "q8_tc"}
+SKG_Q8_KERNEL_SPLIT = 2
+SKG_Q8_KERNEL_WIDE = 3
+Q8_KERNEL_NAMES = {SKG_Q8_KERNEL_STREAM: "q8_stream", SKG_Q8_KERNEL_SPLIT: "q8_split",
+                   SKG_Q8_KERNEL_WIDE: "q8_wide"}
 
 # Every symbol include/skg.h declares.
 EXPORTS = (
@@ -77,7 +79,7 @@ class skg_plan_desc(ctypes.Structure):
 class skg_q8_plan_desc(ctypes.Structure):
     _fields_ = [
         *((f, ctypes.c_int) for f in (
-            "kernel_kind", "M", "N", "K", "epilogue", "static_weights", "m_tile", "n_tile", "tiles", "full_waves", "shared_ctas",
+            "kernel_kind", "M", "N", "K", "epilogue", "static_weights", "m_tile", "n_tile", "tiles", "split_k",
             "grid", "threads", "smem_bytes", "stages", "ctas_per_sm")),
         ("workspace_bytes", ctypes.c_size_t),
     ]
@@ -469,8 +471,8 @@ def skg_q8_run(plan: int, x, x_scale, W, w_scale, residual, y, stream=None):
                              _stream(stream)))
 
 
-def skg_q8_plan_force(plan: int, kind: int = 0, m_tile: int = 0, ctas: int = 0):
-    _check(load().skg_q8_plan_force(plan, kind, m_tile, ctas))
+def skg_q8_plan_force(plan: int, kind: int = 0, m_tile: int = 0, split_k: int = 0):
+    _check(load().skg_q8_plan_force(plan, kind, m_tile, split_k))
 
 
 def skg_q8_plan_info(plan: int) -> dict:
@@ -509,8 +511,8 @@ class Q8Plan:
             None if residual is None else _dense(residual, "residual", (M, N), torch.bfloat16),
             _dense(y, "y", (M, N), out), _stream_of(stream, x)))
 
-    def force(self, kind: int = 0, m_tile: int = 0, ctas: int = 0):
-        skg_q8_plan_force(self.handle, kind, m_tile, ctas)
+    def force(self, kind: int = 0, m_tile: int = 0, split_k: int = 0):
+        skg_q8_plan_force(self.handle, kind, m_tile, split_k)
 
     def info(self) -> dict:
         return skg_q8_plan_info(self.handle)

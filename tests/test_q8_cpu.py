@@ -108,21 +108,21 @@ def test_binding_refuses_host_tensors():
 def test_query_describes_a_launch_that_covers_every_tile(M, N, K):
     d = skg.skg_q8_plan_query(M, N, K, "bf16", SMS)
     assert d["grid"] >= 1 and d["threads"] % 32 == 0
-    assert (d["kernel"] == "q8_stream") == (M <= 16)
+    assert d["kernel"] == ("q8_stream" if M <= 16 else "q8_split" if M <= 64 else "q8_wide")
+    assert d["tiles"] == -(-N // d["n_tile"]) * -(-M // d["m_tile"])
     if d["kernel"] == "q8_stream":
-        assert d["workspace_bytes"] == 0 and d["grid"] == d["tiles"] == -(-N // d["n_tile"]) and M <= d["m_tile"]
+        assert d["workspace_bytes"] == 0 and d["grid"] == d["tiles"] and M <= d["m_tile"]
         return
-    assert d["m_tile"] >= min(M, 128) or M > 128
-    assert d["tiles"] == -(-N // 128) * -(-M // d["m_tile"])
     nkb = -(-K // 128)
-    left = d["tiles"] - d["full_waves"] * d["grid"]
-    assert 0 <= left < d["grid"] <= SMS * d["ctas_per_sm"]
-    assert d["shared_ctas"] == min(d["grid"], left * nkb)
     assert d["smem_bytes"] * d["ctas_per_sm"] <= 227 * 1024
-    wide = M * K * 2 if d["m_tile"] > 64 else 0
-    used = d["shared_ctas"] > 0 or (d["m_tile"] <= 64 and K > 2048)
-    sums = d["grid"] * d["m_tile"] * 1024 if used else 0
-    assert sums + wide <= d["workspace_bytes"] <= sums + wide + 4 * d["shared_ctas"] + 256
+    if d["kernel"] == "q8_split":
+        assert M <= d["m_tile"] and 1 <= d["split_k"] <= min(8, nkb) and d["grid"] == d["tiles"] * d["split_k"]
+        assert d["split_k"] == 1 or d["grid"] <= SMS * d["ctas_per_sm"]
+        carried = -(-nkb // d["split_k"]) > 16
+        assert d["workspace_bytes"] == (d["grid"] * d["m_tile"] * 512 if carried else 0)
+    else:
+        assert d["split_k"] == 1 and d["grid"] == 2 * min(d["tiles"], SMS // 2)
+        assert d["workspace_bytes"] == 2 * M * K
 
 
 @pytest.mark.parametrize("M", [1, 8, 9, 16])
@@ -137,24 +137,7 @@ def test_streaming_launch_fills_as_few_slots_as_hold_it(M, N):
     assert d["threads"] * d["ctas_per_sm"] <= 1024
 
 
-@pytest.mark.parametrize("units,ctas,nkb", [(1, 1, 1), (7, 7, 7), (56 * 56, 304, 56), (3 * 56, 168, 56), (16 * 151, 152, 16),
-                                            (1024 * 37, 151, 1024), (303, 303, 1), (5 * 9, 13, 9)])
-def test_shared_units_are_cut_into_runs_that_name_their_tiles(units, ctas, nkb):
-    """The kernel's arithmetic: CTA c takes units [c U / C, (c + 1) U / C), and
-    the CTA that holds unit u is ((u + 1) C - 1) / U: what a shared tile's
-    slot and its count of arrivals are taken from."""
-    owner = {}
-    for c in range(ctas):
-        lo, hi = c * units // ctas, (c + 1) * units // ctas
-        assert hi > lo                                   # C <= U: no CTA is without work
-        for u in range(lo, hi):
-            owner[u] = c
-    assert sorted(owner) == list(range(units))
-    assert all(((u + 1) * ctas - 1) // units == owner[u] for u in range(units))
-    starts = [owner[t * nkb] for t in range(units // nkb)
-              if owner[t * nkb] != owner[min(units - 1, t * nkb + nkb - 1)]]
-    assert len(starts) == len(set(starts))               # one counter per shared tile
-    for c in range(ctas):                                # at most one shared tile begun, and one gone on with
-        mine = sorted({u // nkb for u in range(c * units // ctas, (c + 1) * units // ctas)})
-        shared = [t for t in mine if owner[t * nkb] != owner[t * nkb + nkb - 1]]
-        assert sum(owner[t * nkb] == c for t in shared) <= 1 and sum(owner[t * nkb] != c for t in shared) <= 1
+@pytest.mark.parametrize("M,N,tile", [(65, 7168, 128), (192, 7168, 128), (256, 7168, 128), (1024, 7168, 128),
+                                      (4096, 12288, 192), (333, 5001, 128)])
+def test_wide_tile_takes_the_fewer_waves(M, N, tile):
+    assert skg.skg_q8_plan_query(M, N, 7168, "bf16", SMS)["m_tile"] == tile

@@ -415,27 +415,47 @@ def test_binding_refuses_wrong_tensors():
 
 
 # ------------------------------------------------------------------------- every kernel at every shape
-TILES = (32, 64, 128, 192)
+SHAPES = [(skg.SKG_Q8_KERNEL_SPLIT, t, k) for t in (32, 64) for k in range(1, 9)] + [
+    (skg.SKG_Q8_KERNEL_WIDE, t, 0) for t in (128, 192)]
 
 
-@pytest.mark.parametrize("m_tile", TILES)
-@pytest.mark.parametrize("M,N,K,ctas", [(1, 128, 1024, 0), (2, 1000, 2064, 0), (16, 300, 1040, 7), (33, 257, 16400, 0),
-                                        (64, 130, 4096, 5), (70, 640, 1152, 1), (200, 384, 3104, 3), (193, 129, 16, 0),
-                                        (130, 2000, 528, 11), (385, 1000, 2048, 148),
-                                        (64, 1024, 16384, 0), (50, 3000, 2064, 9)])
-def test_every_tile_gives_the_same_bits(M, N, K, ctas, m_tile):
-    """The tensor-core kernel at every tile, with few CTAs too (whole tiles, shared tiles and both)."""
+@pytest.mark.parametrize("kind,m_tile,split", SHAPES)
+@pytest.mark.parametrize("M,N,K", [(1, 128, 1024), (2, 1000, 2064), (16, 300, 1040), (33, 257, 16400), (64, 130, 4096),
+                                   (70, 640, 1152), (200, 384, 3104), (193, 129, 16), (130, 2000, 528), (385, 1000, 2048),
+                                   (64, 1024, 16384), (50, 3000, 2064), (20, 260, 1024)])
+def test_every_launch_shape_gives_the_same_bits(M, N, K, kind, m_tile, split):
+    """Both tcgen05 kernels at every tile and split, whatever the plan would choose."""
     c = Linear(M, N, K, "bf16_residual", 6)
     want = c.want()
-    plan = skg.Q8Plan(M, N, K, "bf16_residual")
-    plan.force(skg.SKG_Q8_KERNEL_TC, m_tile, ctas)
+    plan = skg.Q8Plan(M, N, K, "bf16_residual", static_weights=split % 2 == 0)
+    plan.force(kind, m_tile, split)
     d = plan.info()
-    assert d["m_tile"] == m_tile and d["kernel"] == "q8_tc"
+    assert d["m_tile"] == m_tile and d["kernel_kind"] == kind and d["split_k"] == max(1, min(split, -(-K // 128)))
     for _ in range(3):
         c.y.fill_(float("nan"))
         c.run(plan)
         assert R.same_bits(c.y, want)
     plan.check()
+    plan.close()
+
+
+@pytest.mark.parametrize("epilogue", ["bf16", "bf16_residual", "fp32"])
+@pytest.mark.parametrize("M,N", [(40, 512), (40, 514), (64, 1023), (100, 300)])
+def test_output_addresses(M, N, epilogue):
+    """y, residual and scales at addresses that only their element types allow."""
+    K = 1024
+    c = Linear(M, N, K, epilogue, 16)
+    want = c.want()
+    out = torch.full((M * N + 1,), 7.0, dtype=c.y.dtype, device="cuda")
+    c.y = out[1:].view(M, N)
+    for name in ("xs", "ws"):
+        v = getattr(c, name)
+        setattr(c, name, torch.cat([v[:1], v])[1:])
+    if c.res is not None:
+        c.res = torch.cat([c.res.flatten()[:1], c.res.flatten()])[1:].view(M, N)
+    plan = skg.Q8Plan(M, N, K, epilogue)
+    c.run(plan)
+    assert R.same_bits(c.y, want) and out[0] == 7
     plan.close()
 
 
@@ -454,13 +474,13 @@ def test_streaming_kernel_refuses_more_tokens():
     plan = skg.Q8Plan(17, 128, 128, "bf16")
     with pytest.raises(skg.SkgError) as e:
         plan.force(skg.SKG_Q8_KERNEL_STREAM)
-    assert e.value.status == skg.SKG_ERR_UNSUPPORTED and plan.info()["kernel"] == "q8_tc"
+    assert e.value.status == skg.SKG_ERR_UNSUPPORTED and plan.info()["kernel"] == "q8_split"
     plan.close()
 
 
-@pytest.mark.parametrize("m_tile", TILES)
+@pytest.mark.parametrize("kind,m_tile,split", SHAPES[::3])
 @pytest.mark.parametrize("v", [(-128, -128), (127, -128)])
-def test_largest_sums_on_every_tile(m_tile, v):
+def test_largest_sums_on_every_launch_shape(kind, m_tile, split, v):
     M, N, K = 20, 130, 131056
     x = torch.full((M, K), v[0], dtype=torch.int8, device="cuda")
     W = torch.full((N, K), v[1], dtype=torch.int8, device="cuda")
@@ -468,7 +488,7 @@ def test_largest_sums_on_every_tile(m_tile, v):
     one = torch.ones(N, device="cuda")
     y = torch.empty(M, N, dtype=torch.float32, device="cuda")
     plan = skg.Q8Plan(M, N, K, "fp32")
-    plan.force(skg.SKG_Q8_KERNEL_TC, m_tile)
+    plan.force(kind, m_tile, split)
     plan.run(x, one[:M], W, one, None, y)
     assert torch.equal(y, (x.double() @ W.double().t()).float())
     plan.close()
