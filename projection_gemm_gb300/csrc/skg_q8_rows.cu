@@ -8,134 +8,469 @@
 //
 // Everything is fp32 until the stores; h and y are each rounded once to bf16,
 // and the norm continues from the unrounded h.
+//
+// What bounds it is HBM for many rows and latency for few.  A row is read once:
+// its values stay in registers (up to 32 a thread) through the sum of squares
+// and the maximum, with one block barrier each, and what a thread loads is all
+// in flight together.  Rows that are not 16-byte aligned (any odd length) are
+// still read in 16-byte blocks, shifted into place; rows longer than 16384 take
+// three passes over memory.
+#include <algorithm>
+
+#include "skg_internal.h"
+#include "skg_ptx.cuh"
 #include "skg_q8_common.cuh"
 #include "skg_q8_internal.h"
 
 namespace skg {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr float kMaxFinite = 3.402823466e38f;
+constexpr int kWarpRows = 8;              // rows of a CTA where a warp takes a row
+constexpr int kMaxRow = 16384;            // longest row held in registers
+constexpr int kLongThreads = 1024;
 
-// Sum or maximum over the block; every thread gets the result.
-template <bool MAX>
-__device__ __forceinline__ float block_reduce(float v, float *sh)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        v = MAX ? fmaxf(v, u) : v + u;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = sh[0];
-#pragma unroll
-    for (int w = 1; w < kRowThreads / 32; ++w)
-        v = MAX ? fmaxf(v, sh[w]) : v + sh[w];
-    return v;
-}
-
-// A row's scale and the factor that takes a value to its integer.  A row of
-// zeros has scale 0 and integers 0.  A row with a value that is not finite
-// has scale NaN and integers 0, so that whatever it multiplies is NaN; amax
-// cannot say so by itself (fmaxf drops NaN), hence `finite`.  Below 1e-30 the
-// quotient 127 / amax would leave fp32's range: both are raised by 2^100,
+// A row's scale and the factor that takes a value to its integer, from the bits
+// of max|v| (|NaN| > infinity > every finite value, as integers).  A row of
+// zeros has scale 0 and integers 0.  A row with a value that is not finite has
+// scale NaN and integers 0, so that whatever it multiplies is NaN.  Below 1e-30
+// the quotient 127 / max would leave fp32's range: both are raised by 2^100,
 // which is exact.
 struct RowScale {
     float scale, up, factor;
+    bool finite;
 };
 
-__device__ __forceinline__ RowScale row_scale(float amax, bool finite)
+__device__ __forceinline__ RowScale row_scale(uint32_t max_bits)
 {
     RowScale r;
+    const float amax = __uint_as_float(max_bits);
+    r.finite = max_bits < 0x7F800000u;
     r.up = amax < 1e-30f ? 0x1p100f : 1.0f;
-    r.factor = amax > 0.0f && finite ? 127.0f / (amax * r.up) : 0.0f;
-    r.scale = finite ? amax / 127.0f : __int_as_float(0x7FC00000);
+    r.factor = amax > 0.0f && r.finite ? 127.0f / (amax * r.up) : 0.0f;
+    r.scale = r.finite ? amax / 127.0f : __int_as_float(0x7FC00000);
     return r;
 }
 
-__device__ __forceinline__ int8_t to_q8(float v, const RowScale &r, bool finite)
+// v * factor rounded to the nearest integer, half to even, as the low byte of
+// the fp32 sum with 1.5 * 2^23, which is rounded at the units.
+__device__ __forceinline__ uint32_t to_q8(float v, const RowScale &r)
 {
-    return finite ? static_cast<int8_t>(__float2int_rn((v * r.up) * r.factor)) : static_cast<int8_t>(0);
+    return __float_as_uint(fmaf(v, r.factor, 12582912.0f));
 }
 
+// max(m, |v|), NaN where either is.
+__device__ __forceinline__ float max_nan(float m, float v)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// 1 / sqrt(mean + eps) from the sum of squares of h; where that has left fp32's
+// range, `again` gives the sum with h taken 2^70 smaller (where h itself is not
+// finite, so is that sum, and the row).
+template <class F>
+__device__ __forceinline__ float inverse_rms(float sum, int K, float eps, F &&again)
+{
+    if (sum <= kMaxFinite)
+        return rsqrtf(sum / static_cast<float>(K) + eps);
+    sum = again(0x1p-70f);
+    return rsqrtf(sum / static_cast<float>(K) + eps * 0x1p-140f) * 0x1p-70f;
+}
+
+// ------------------------------------------------------------ rows in registers
+// Eight elements as loaded.  (Not by the read-only path: the kernel may have
+// started before its inputs were written.)
+struct Raw8 {
+    uint32_t w[4];
+};
+
+__device__ __forceinline__ void load_block(const uint16_t *p, uint32_t *w)
+{
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+}
+
+__device__ __forceinline__ float value(const Raw8 &r, int i)
+{
+    return i & 1 ? bf16hi(r.w[i >> 1]) : bf16lo(r.w[i >> 1]);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    return f32_to_bf16(lo) | static_cast<uint32_t>(f32_to_bf16(hi)) << 16;
+}
+
+// A row of bf16 read 8 elements at a time.  ANY: from an address of any
+// alignment, by the two 16-byte blocks around the eight elements; where those
+// reach beyond the row (near its ends), element by element.
+template <bool ANY>
+struct RowLoad {
+    uint32_t w[ANY ? 8 : 4];
+    int d = 0;               // the eight elements begin at element d of w
+
+    __device__ __forceinline__ void load(const uint16_t *row, int e, int K)
+    {
+#pragma unroll
+        for (int i = 0; i < (ANY ? 8 : 4); ++i)
+            w[i] = 0;
+        if constexpr (!ANY) {
+            if (e < K)
+                load_block(row + e, w);
+        } else {
+            d = phase(row, e);
+            if (e - d >= 0 && e - d + (d ? 16 : 8) <= K) {
+                load_block(row + (e - d), w);
+                if (d)
+                    load_block(row + (e - d) + 8, w + 4);
+            } else if (e + 8 > 0 && e < K) {
+                d = 0;
+                uint16_t h[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    h[i] = 0;
+                    if (e + i >= 0 && e + i < K)
+                        asm volatile("ld.global.u16 %0, [%1];" : "=h"(h[i]) : "l"(row + e + i));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = h[2 * i] | static_cast<uint32_t>(h[2 * i + 1]) << 16;
+            }
+        }
+    }
+
+    // Elements by which row + e lies beyond a 16-byte boundary.
+    static __device__ __forceinline__ int phase(const uint16_t *row, int e)
+    {
+        return static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) + static_cast<unsigned>(e)) & 7;
+    }
+
+    __device__ __forceinline__ Raw8 get() const
+    {
+        Raw8 r;
+        if constexpr (!ANY) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r.w[i] = w[i];
+        } else {
+            uint32_t u[6], t[5];
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+                u[i] = d & 4 ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+                t[i] = d & 2 ? u[i + 1] : u[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r.w[i] = d & 1 ? __funnelshift_r(t[i], t[i + 1], 16) : t[i];
+        }
+        return r;
+    }
+};
+
+// Eight values as bf16 at element e of a row; ANY: those inside the row, in the
+// widest pieces the address allows.
+template <bool ANY>
+__device__ __forceinline__ void store_bf16(uint16_t *row, int e, int K, const float *v)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    const int d = ANY ? RowLoad<true>::phase(row, e) : 0;
+    if (ANY && (e < 0 || e + 8 > K || d & 1)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i >= 0 && e + i < K)
+                row[e + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    } else if (ANY && d) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint32_t *>(row + e + 2 * i) = w[i];
+    } else if (e < K) {
+        *reinterpret_cast<uint4 *>(row + e) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Eight values as integers at element e of a row; row + e is 8-byte aligned.
+template <bool ANY>
+__device__ __forceinline__ void store_q8(int8_t *row, int e, int K, const float *v, const RowScale &r)
+{
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = __byte_perm(__byte_perm(to_q8(v[4 * i], r), to_q8(v[4 * i + 1], r), 0x0040),
+                           __byte_perm(to_q8(v[4 * i + 2], r), to_q8(v[4 * i + 3], r), 0x0040), 0x5410);
+    if (ANY && (e < 0 || e + 8 > K)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i >= 0 && e + i < K)
+                row[e + i] = static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3)));
+    } else if (e < K) {
+        *reinterpret_cast<uint2 *>(row + e) = make_uint2(w[0], w[1]);
+    }
+}
+
+// Sum and maximum over a row's threads: a warp (WARP), or the block, in a
+// buffer of one value a warp (each used for one reduction of the kernel).
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float *buf)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if constexpr (!WARP) {
+        if ((threadIdx.x & 31) == 0)
+            buf[threadIdx.x >> 5] = v;
+        __syncthreads();
+        const int lane = threadIdx.x & 31;
+        v = lane < static_cast<int>(blockDim.x >> 5) ? buf[lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    }
+    return v;
+}
+
+template <bool WARP>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *buf)
+{
+    v = __reduce_max_sync(0xFFFFFFFFu, v);
+    if constexpr (!WARP) {
+        if ((threadIdx.x & 31) == 0)
+            buf[threadIdx.x >> 5] = v;
+        __syncthreads();
+        const int lane = threadIdx.x & 31;
+        v = __reduce_max_sync(0xFFFFFFFFu, lane < static_cast<int>(blockDim.x >> 5) ? buf[lane] : 0u);
+    }
+    return v;
+}
+
+// VALUES a thread.  ANY: tensors of any alignment; the eights then lie where
+// the row of q is 8-byte aligned, so the first and the last may stick out.
+template <bool NORM, bool ANY, int VALUES, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : (VALUES == 8 ? 1024 : kMaxRow / VALUES), WARP ? 2 : VALUES / 16 + (VALUES == 8))
+q8_rows_kernel(const Q8RowParams p)
+{
+    constexpr int NV = VALUES / 8;
+    __shared__ float sums[2][32];
+    __shared__ uint32_t maxima[32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const size_t row = WARP ? static_cast<size_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    if (WARP && row >= static_cast<size_t>(p.M))
+        return;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x, T = WARP ? 32 : blockDim.x;
+    const uint16_t *x = p.x + row * p.ldx, *second = p.second ? p.second + row * p.ld2 : nullptr;
+    int8_t *q = p.q + row * p.K;
+    const int first = ANY ? t * 8 - static_cast<int>(reinterpret_cast<uintptr_t>(q) & 7) : t * 8;
+    const int step = T * 8;
+
+    float v[NV][8];
+    {
+        RowLoad<ANY> a[NV], w[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            a[j].load(x, first + j * step, p.K);
+        if (second) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                w[j].load(second, first + j * step, p.K);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const Raw8 xa = a[j].get();
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                v[j][c] = value(xa, c);
+            if (second) {
+                const Raw8 xw = w[j].get();
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    v[j][c] = NORM ? v[j][c] + value(xw, c) : silu(value(xw, c)) * v[j][c];
+            }
+        }
+    }
+    if constexpr (NORM) {
+        RowLoad<ANY> w[NV];
+        if (p.gamma) {                   // on its way during the sum
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                w[j].load(p.gamma, first + j * step, p.K);
+        }
+        if (p.h) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                store_bf16<ANY>(p.h + row * p.ldh, first + j * step, p.K, v[j]);
+        }
+        auto sum_of_squares = [&](float unit, float *buf) {
+            float s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    s = fmaf(v[j][c] * unit, v[j][c] * unit, s);
+            return row_sum<WARP>(s, buf);
+        };
+        const float rms = inverse_rms(sum_of_squares(1.0f, sums[0]), p.K, p.eps,
+                                      [&](float unit) { return sum_of_squares(unit, sums[1]); });
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const Raw8 g = w[j].get();
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                v[j][c] = p.gamma ? v[j][c] * rms * value(g, c) : v[j][c] * rms;
+        }
+        if (p.y) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                store_bf16<ANY>(p.y + row * p.K, first + j * step, p.K, v[j]);
+        }
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int e = first + j * step;
+        // (what lies beyond the row holds 0 * rms, which is NaN where rms is infinite)
+        if (!ANY ? e < p.K : e >= 0 && e + 8 <= p.K) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                m = max_nan(m, v[j][c]);
+        } else if (ANY) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                m = e + c >= 0 && e + c < p.K ? max_nan(m, v[j][c]) : m;
+        }
+    }
+    const RowScale r = row_scale(row_max<WARP>(abs_bits(m), maxima));
+    if (r.up != 1.0f || !r.finite) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                v[j][c] = r.finite ? v[j][c] * r.up : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        store_q8<ANY>(q, first + j * step, p.K, v[j], r);
+    if (t == 0)
+        p.scale[row] = r.scale;
+}
+
+// ------------------------------------------------------------------ longer rows
 template <bool NORM>
-__device__ __forceinline__ float row_value(const Q8RowParams &p, size_t row, int k, float rms)
+__device__ __forceinline__ float long_value(const Q8RowParams &p, size_t row, int k, float rms)
 {
     const float a = bf16_to_f32(p.x[row * p.ldx + k]);
     if (NORM) {
         const float h = p.second ? a + bf16_to_f32(p.second[row * p.ld2 + k]) : a;
-        return h * rms * (p.gamma ? bf16_to_f32(p.gamma[k]) : 1.0f);
+        return p.gamma ? h * rms * bf16_to_f32(p.gamma[k]) : h * rms;
     }
-    if (!p.second)
-        return a;
-    return silu(bf16_to_f32(p.second[row * p.ld2 + k])) * a;
-}
-
-__device__ __forceinline__ float sum_of_squares(const Q8RowParams &p, size_t row, float unit, float *sh)
-{
-    float s = 0.0f;
-    for (int k = threadIdx.x; k < p.K; k += kRowThreads) {
-        float h = bf16_to_f32(p.x[row * p.ldx + k]);
-        if (p.second)
-            h += bf16_to_f32(p.second[row * p.ld2 + k]);
-        h *= unit;
-        s += h * h;
-    }
-    return block_reduce<false>(s, sh);
+    return p.second ? silu(bf16_to_f32(p.second[row * p.ld2 + k])) * a : a;
 }
 
 template <bool NORM>
-__global__ void __launch_bounds__(kRowThreads) q8_rows_kernel(const Q8RowParams p)
+__global__ void __launch_bounds__(kLongThreads) q8_long_rows_kernel(const Q8RowParams p)
 {
-    __shared__ float sh[kRowThreads / 32];
+    __shared__ float sums[2][32];
+    __shared__ uint32_t maxima[32];
+    pdl_launch_dependents();
+    pdl_wait();
     const size_t row = blockIdx.x;
     float rms = 1.0f;
     if (NORM) {
-        float s = sum_of_squares(p, row, 1.0f, sh);
-        rms = rsqrtf(s / static_cast<float>(p.K) + p.eps);
-        if (!(s <= 3.402823466e38f)) {
-            // squares beyond fp32's range: the same with h taken 2^70 smaller
-            // (where h itself is not finite, so is this sum, and the row)
-            s = sum_of_squares(p, row, 0x1p-70f, sh);
-            rms = rsqrtf(s / static_cast<float>(p.K) + p.eps * 0x1p-140f) * 0x1p-70f;
-        }
+        auto sum_of_squares = [&](float unit, float *buf) {
+            float s = 0.0f;
+            for (int k = threadIdx.x; k < p.K; k += kLongThreads) {
+                const float h = long_value<true>(Q8RowParams{p.x, p.second, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                                             p.ldx, p.ld2, 0, 0, 0, 0.0f}, row, k, unit);
+                s = fmaf(h, h, s);
+            }
+            return row_sum<false>(s, buf);
+        };
+        rms = inverse_rms(sum_of_squares(1.0f, sums[0]), p.K, p.eps,
+                          [&](float unit) { return sum_of_squares(unit, sums[1]); });
     }
-    float amax = 0.0f;
-    int bad = 0;
-    for (int k = threadIdx.x; k < p.K; k += kRowThreads) {
-        const float v = row_value<NORM>(p, row, k, rms);
-        bad |= !(fabsf(v) <= 3.402823466e38f);
-        amax = fmaxf(amax, fabsf(v));
-    }
-    amax = block_reduce<true>(amax, sh);
-    const bool finite = !__syncthreads_or(bad);
-    const RowScale r = row_scale(amax, finite);
-    for (int k = threadIdx.x; k < p.K; k += kRowThreads) {
-        const float v = row_value<NORM>(p, row, k, rms);
-        if (NORM && p.h)
+    uint32_t m = 0;
+    for (int k = threadIdx.x; k < p.K; k += kLongThreads)
+        m = max(m, abs_bits(long_value<NORM>(p, row, k, rms)));
+    const RowScale r = row_scale(row_max<false>(m, maxima));
+    for (int k = threadIdx.x; k < p.K; k += kLongThreads) {
+        const float v = long_value<NORM>(p, row, k, rms);
+        if (NORM && p.h)                 // may be the residual itself: read by this thread, above
             p.h[row * p.ldh + k] = f32_to_bf16(bf16_to_f32(p.x[row * p.ldx + k]) + bf16_to_f32(p.second[row * p.ld2 + k]));
         if (NORM && p.y)
             p.y[row * p.K + k] = f32_to_bf16(v);
-        p.q[row * p.K + k] = to_q8(v, r, finite);
+        p.q[row * p.K + k] = static_cast<int8_t>(to_q8(r.finite ? v * r.up : 0.0f, r));
     }
     if (threadIdx.x == 0)
         p.scale[row] = r.scale;
 }
 
+template <class... A>
+cudaError_t launch(void (*kernel)(A...), unsigned grid, unsigned threads, const Q8RowParams &p, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// Threads and values a thread for rows of K.  A warp a row up to 1024 (1017
+// where the eights may stick out).  Beyond, few rows want many threads
+// (latency); many rows want as many values a thread as registers allow (32, or
+// 16 where every eight takes two blocks): fewer warps at each barrier, more
+// bytes in flight.  At 8192 x 7168 the norm with residual takes 63 us at 32, 92
+// at 16 and 83 at 8.
+template <bool NORM, bool ANY>
+cudaError_t launch_rows_as(const Q8RowParams &p, cudaStream_t s)
+{
+    const int eights = (p.K + (ANY ? 7 : 0) + 7) / 8;
+    auto threads = [&](int values) { return static_cast<unsigned>((eights + 4 * values - 1) / (4 * values) * 32); };
+    if (eights <= 128) {
+        const unsigned grid = static_cast<unsigned>((p.M + kWarpRows - 1) / kWarpRows);
+        if (eights <= 32)
+            return launch(q8_rows_kernel<NORM, ANY, 8, true>, grid, 32 * kWarpRows, p, s);
+        if (eights <= 64)
+            return launch(q8_rows_kernel<NORM, ANY, 16, true>, grid, 32 * kWarpRows, p, s);
+        return launch(q8_rows_kernel<NORM, ANY, 32, true>, grid, 32 * kWarpRows, p, s);
+    }
+    const bool few = p.M <= 2 * 152;
+    if (few && eights <= 1024)
+        return launch(q8_rows_kernel<NORM, ANY, 8, false>, p.M, threads(8), p, s);
+    if constexpr (!ANY) {
+        if (!few)
+            return launch(q8_rows_kernel<NORM, false, 32, false>, p.M, threads(32), p, s);
+    }
+    return launch(q8_rows_kernel<NORM, ANY, 16, false>, p.M, threads(16), p, s);
+}
+
+bool multiple(const void *ptr, size_t bytes) { return reinterpret_cast<uintptr_t>(ptr) % bytes == 0; }
+
+template <bool NORM>
+cudaError_t launch_rows(const Q8RowParams &p, cudaStream_t s)
+{
+    // null tensors are aligned
+    const bool aligned = p.K % 8 == 0 && p.ldx % 8 == 0 && (!p.second || p.ld2 % 8 == 0) && (!p.h || p.ldh % 8 == 0) &&
+                         multiple(p.x, 16) && multiple(p.second, 16) && multiple(p.gamma, 16) && multiple(p.h, 16) &&
+                         multiple(p.y, 16) && multiple(p.q, 8);
+    if (aligned ? p.K > kMaxRow : p.K > kMaxRow - 7)
+        return launch(q8_long_rows_kernel<NORM>, p.M, kLongThreads, p, s);
+    return aligned ? launch_rows_as<NORM, false>(p, s) : launch_rows_as<NORM, true>(p, s);
+}
+
 } // namespace
 
-cudaError_t launch_q8_norm(const Q8RowParams &p, cudaStream_t s)
-{
-    q8_rows_kernel<true><<<p.M, kRowThreads, 0, s>>>(p);
-    return cudaGetLastError();
-}
+cudaError_t launch_q8_norm(const Q8RowParams &p, cudaStream_t s) { return launch_rows<true>(p, s); }
 
-cudaError_t launch_q8_quantize(const Q8RowParams &p, cudaStream_t s)
-{
-    q8_rows_kernel<false><<<p.M, kRowThreads, 0, s>>>(p);
-    return cudaGetLastError();
-}
+cudaError_t launch_q8_quantize(const Q8RowParams &p, cudaStream_t s) { return launch_rows<false>(p, s); }
 
 } // namespace skg
