@@ -54,7 +54,6 @@ skg_status launched(cudaError_t e, const char *who)
 constexpr int kQ8Band = 8;            // token tiles per band of the tile order
 constexpr int kQ8BlockK = 128;        // k per unit of the tcgen05 kernels
 constexpr int kStreamMaxM = 16;
-constexpr int kSplitMaxM = 64;
 
 int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
@@ -65,27 +64,36 @@ int choose_split(int tiles, int nkb, int slots)
     return std::max(1, std::min({8, nkb, slots / std::max(1, tiles)}));
 }
 
-// Tokens per tile of the wide kernel: 128 or 192, whichever takes less time in
-// waves (a wave's time grows with the tile; 24 tokens' worth is fixed).
-int choose_wide_tile(int M, int n_pairs, int pairs)
+// The split or the wide kernel, by their times as measured (us): a CTA of the
+// split kernel takes 0.93 a unit of 128 k (0.69 with tiles of 32 tokens) and 4
+// for its ends, in as many waves as its grid needs; the wide one 0.40 a unit of
+// a tile and 7, x's widening among them.  Measured against this rule, split
+// then wide: 64 x 28672 x 8192 73 and 66, 128 x 384 x 7168 7.6 and 25, 128 x
+// 7168 x 7168 29.9 and 28.6, 256 x 4096 x 4096 18.9 and 20, 1000 x 4096 x 4096
+// 60 and 34.
+bool prefer_split(const skg_q8_plan_desc &d, int num_sms)
 {
-    long long best = 0;
-    int tile = 0;
-    for (const int t : {192, 128}) {
-        const long long waves = (static_cast<long long>(n_pairs) * ceil_div(M, t) + pairs - 1) / pairs;
-        const long long cost = waves * (t + 24);
-        if (!tile || cost < best) {
-            best = cost;
-            tile = t;
-        }
-    }
-    return tile;
+    const int m_tile = d.M <= 32 ? 32 : 64, nkb = ceil_div(d.K, kQ8BlockK), n_tiles = ceil_div(d.N, kTileN);
+    const long long slots = 2ll * num_sms, pairs = std::max(1, num_sms / 2);
+    const long long st = static_cast<long long>(n_tiles) * ceil_div(d.M, m_tile);
+    const long long wt = static_cast<long long>(ceil_div(n_tiles, 2)) * ceil_div(d.M, q8_wide_shape().m_tile);
+    const int split = st > slots ? 1 : choose_split(static_cast<int>(st), nkb, static_cast<int>(slots));
+    const double units = static_cast<double>((st * split + slots - 1) / slots) * ceil_div(nkb, split);
+    return 4.0 + (m_tile == 32 ? 0.69 : 0.93) * units <= 7.0 + 0.40 * static_cast<double>((wt + pairs - 1) / pairs) * nkb;
+}
+
+// Accumulations of 1024 k that a CTA of the split kernel puts away: all but two.
+int carried(const skg_q8_plan_desc &d)
+{
+    const int units = ceil_div(ceil_div(d.K, kQ8BlockK), d.split_k);
+    return std::max(0, ceil_div(units * kQ8BlockK, 1024) - 2);
 }
 
 skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int split, int num_sms, const char *who)
 {
     if (!kind)
-        kind = d->M <= kStreamMaxM ? SKG_Q8_KERNEL_STREAM : (d->M <= kSplitMaxM ? SKG_Q8_KERNEL_SPLIT : SKG_Q8_KERNEL_WIDE);
+        kind = d->M <= kStreamMaxM ? SKG_Q8_KERNEL_STREAM
+                                   : (prefer_split(*d, num_sms) ? SKG_Q8_KERNEL_SPLIT : SKG_Q8_KERNEL_WIDE);
     d->kernel_kind = kind;
     d->split_k = 1;
     d->smem_bytes = d->stages = 0;
@@ -102,17 +110,17 @@ skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int split, int
         d->ctas_per_sm = sh.ctas_per_sm;
         return SKG_OK;
     }
-    const int nkb = ceil_div(d->K, kQ8BlockK), n_tiles = ceil_div(d->N, kTileN);
+    const int nkb = ceil_div(d->K, kQ8BlockK);
     const bool wide = kind == SKG_Q8_KERNEL_WIDE;
     d->n_tile = wide ? 2 * kTileN : kTileN;
     if (!m_tile)
-        m_tile = wide ? choose_wide_tile(d->M, ceil_div(n_tiles, 2), std::max(1, num_sms / 2)) : (d->M <= 32 ? 32 : 64);
+        m_tile = wide ? q8_wide_shape().m_tile : (d->M <= 32 ? 32 : 64);
     d->m_tile = m_tile;
     const long long tiles = static_cast<long long>(ceil_div(d->N, d->n_tile)) * ceil_div(d->M, m_tile);
     if (tiles > (1ll << 27))
         return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^27 tiles", who);
     d->tiles = static_cast<int>(tiles);
-    const Q8TcShape sh = wide ? q8_wide_shape(m_tile) : q8_split_shape(m_tile);
+    const Q8TcShape sh = wide ? q8_wide_shape() : q8_split_shape(m_tile);
     d->threads = sh.threads;
     d->smem_bytes = sh.smem_bytes;
     d->stages = sh.stages;
@@ -124,8 +132,7 @@ skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int split, int
     }
     d->split_k = split ? std::min(split, nkb) : choose_split(d->tiles, nkb, num_sms * sh.ctas_per_sm);
     d->grid = d->tiles * d->split_k;
-    if (ceil_div(nkb, d->split_k) * kQ8BlockK > 2048)
-        d->workspace_bytes = static_cast<size_t>(d->grid) * m_tile * kTileN * 4;
+    d->workspace_bytes = static_cast<size_t>(d->grid) * carried(*d) * m_tile * kTileN * 4;
     return SKG_OK;
 }
 
@@ -282,7 +289,7 @@ skg_status skg_q8_plan_force(skg_q8_plan_t p, int kind, int m_tile, int split_k)
     skg_q8_plan_desc d = p->d;
     const int k = kind ? kind : d.kernel_kind;
     const bool tile_ok = m_tile == 0 || (k == SKG_Q8_KERNEL_SPLIT && (m_tile == 32 || m_tile == 64)) ||
-                         (k == SKG_Q8_KERNEL_WIDE && (m_tile == 128 || m_tile == 192));
+                         (k == SKG_Q8_KERNEL_WIDE && m_tile == q8_wide_shape().m_tile);
     if (!tile_ok)
         return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile %d is none of this kernel's", who, m_tile);
     if (split_k < 0 || split_k > 8 || (split_k && k != SKG_Q8_KERNEL_SPLIT))
@@ -355,6 +362,7 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
         Q8SplitParams t = {};
         t.g = g;
         t.carry = static_cast<int *>(p->ws);
+        t.carried = carried(d);
         t.err = p->err_dev;
         t.nkb = nkb;
         t.m_tiles = m_tiles;
@@ -380,7 +388,7 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
     t.timeout_ns = kDefaultTimeoutNs;
     cudaError_t e = launch_q8_widen(g.x, p->ws, static_cast<size_t>(d.M) * d.K, p->num_sms, s);
     if (e == cudaSuccess)
-        e = launch_q8_wide(tmW, tmX, t, d.m_tile, d.grid, s);
+        e = launch_q8_wide(tmW, tmX, t, d.grid, s);
     return launched(e, who);
 }
 

@@ -41,7 +41,8 @@ struct Q8LinearParams {
 // x m_tile tokens each, K cut over the cluster in units of 128.
 struct Q8SplitParams {
     Q8LinearParams g;
-    int *carry;               // [grid][m_tile][128] int32, where a CTA has more than 2048 k; else null
+    int *carry;               // [grid][carried][m_tile][128] int32
+    int carried;              // accumulations a CTA puts away: those of 1024 k beyond 2048
     unsigned *err;
     int nkb, m_tiles, split, static_w;
     int vec4;                 // N a multiple of 4, w_scale, residual and y aligned for four channels at a time
@@ -58,14 +59,14 @@ struct Q8WideParams {
 };
 
 struct Q8TcShape {
-    int ctas_per_sm, smem_bytes, threads, stages;
+    int m_tile, ctas_per_sm, smem_bytes, threads, stages;
 };
 
 Q8TcShape q8_split_shape(int m_tile);
-Q8TcShape q8_wide_shape(int m_tile);
+Q8TcShape q8_wide_shape();
 cudaError_t launch_q8_split(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8SplitParams &p, int m_tile, int grid,
                             cudaStream_t s);
-cudaError_t launch_q8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8WideParams &p, int m_tile, int grid,
+cudaError_t launch_q8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8WideParams &p, int grid,
                            cudaStream_t s);
 cudaError_t launch_q8_widen(const int8_t *x, void *out, size_t elements, int num_sms, cudaStream_t s);
 

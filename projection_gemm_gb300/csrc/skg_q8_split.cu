@@ -11,12 +11,14 @@
 // S CTAs computes one tile; CTA r takes the r-th part of K in units of 128.
 // What bounds it is W from HBM: two CTAs of an SM hold 2 x 3 units (MT = 64) in
 // flight.  Roles of a CTA:
-//   8 warps   widen, two sets of 4 on alternate units: a thread reads its W
+//   8 warps   widen W, two sets of 4 on alternate units: a thread reads its W
 //             row's 128 bytes from the TMA ring and writes them as fp16 to its
-//             TMEM lane (the MMA's A operand); the same warps widen the x tile
-//             into shared memory (the B operand)
-//   4 or 8    epilogue: accumulators to integers
+//             TMEM lane (the MMA's A operand)
+//   4 or 8    widen x into shared memory (the B operand), two sets as well; every
+//             2048 k and at the end, epilogue: accumulators to integers
 //   1 + 1     TMA; TMEM and MMA issue
+// (With x widened by the warps that widen W, a unit took a CTA 0.8 us at MT = 64;
+// HBM delivers one every 0.7.)
 // Then the cluster's CTAs leave their sums in their own shared memory and each
 // adds up and stores 1/S of the tile's tokens, read from its peers.  Through
 // global memory instead (partial sums, an arrival counter, the last CTA adds
@@ -41,10 +43,11 @@ namespace {
 template <int MT>
 struct SplitShape {
     static constexpr int kEpiWarps = MT / 8;
+    static constexpr int kXWarps = kEpiWarps / 2;            // a set that widens x: two, on alternate units
     static constexpr int kCols = MT * 4 / kEpiWarps;         // accumulator columns of an epilogue thread: 32
     static constexpr int kThreads = 32 * (kWidenWarps + kEpiWarps + 2);
-    static constexpr int kTmaWarp = kWidenWarps + kEpiWarps;
-    static constexpr int kMmaWarp = kTmaWarp + 1;
+    // The MMA warp first: the oldest warp of a scheduler goes before the others
+    static constexpr int kMmaWarp = 0, kTmaWarp = 1, kFirstWiden = 2, kFirstEpi = kFirstWiden + kWidenWarps;
     static constexpr int kStages = MT == 32 ? 4 : 3;         // ring of W and int8 x
     static constexpr int kOps = MT == 32 ? 3 : 2;            // widened operand buffers
     static_assert(kStages >= kOps && kOps >= kWidenSets, "the widen warps' waits need this");
@@ -160,10 +163,10 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         tma_prefetch_desc(&tmX);
         for (int i = 0; i < S; ++i) {
             mbar_init(&wfull[i], 1);
-            mbar_init(&wempty[i], 4);
+            mbar_init(&wempty[i], 4 + Sh::kXWarps);
         }
         for (int i = 0; i < OPS; ++i) {
-            mbar_init(&opfull[i], 4);
+            mbar_init(&opfull[i], 4 + Sh::kXWarps);
             mbar_init(&opempty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -185,7 +188,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         tc_fence_before();
         asm volatile("bar.sync 2, %0;" :: "n"(Sh::kThreads - 32) : "memory");
         tc_fence_after();
-        tmem_base = *tmem_slot;
+        tmem_base = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
     }
 
     if (warp == Sh::kTmaWarp) {
@@ -229,33 +232,38 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         // ---------------------------------------------------------- MMA issuer
         {
             const bool leader = elect_one();
+            const uint64_t x0 = smem_desc_kmajor_sw128(smem_u32(sX16));
             bool ok = true;
-            for (int j = 0; j < blocks; ++j) {
-                const int chunk = j / kExactBlocks, in_chunk = j % kExactBlocks, t = chunk & 1, b = j % OPS;
-                if (in_chunk == 0)
-                    ok = mbar_wait(&aempty[t], ((chunk >> 1) & 1) ^ 1, p.timeout_ns, &flags[0]);
-                ok = ok && mbar_wait(&opfull[b], (j / OPS) & 1, p.timeout_ns, &flags[0]);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) {
-                    q8_fail(p.err, &flags[0], kErrTimeoutMma);
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t bx = smem_u32(sX16 + b * Sh::kX16);
-                const uint32_t d = tmem_base + static_cast<uint32_t>(t * MT);
-                const uint32_t a = tmem_base + static_cast<uint32_t>(2 * MT + b * 64);
-                const uint64_t b0 = smem_desc_kmajor_sw128(bx), b1 = smem_desc_kmajor_sw128(bx + MT * 128);
-                if (leader) {
+            // A round of the operand buffers at a time, unrolled, so that their
+            // addresses and descriptors are constants.
+            for (int j0 = 0; ok && j0 < blocks; j0 += OPS) {
 #pragma unroll
-                    for (int kk = 0; kk < kQ8BlockK / 16; ++kk)
-                        tc_mma_f16_ts(d, a + 8 * kk, (kk < 4 ? b0 : b1) + 2 * (kk & 3), Sh::kIdesc,
-                                      (in_chunk > 0 || kk > 0) ? 1u : 0u);
-                    tc_commit(&opempty[b]);
-                    if (in_chunk == kExactBlocks - 1 || j + 1 == blocks)
-                        tc_commit(&afull[t]);
+                for (int b = 0; b < OPS; ++b) {
+                    const int j = j0 + b, chunk = j / kExactBlocks, in_chunk = j % kExactBlocks, t = chunk & 1;
+                    if (!ok || j >= blocks)
+                        break;
+                    if (in_chunk == 0)
+                        ok = mbar_wait(&aempty[t], ((chunk >> 1) & 1) ^ 1, p.timeout_ns, &flags[0]);
+                    ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(&opfull[b], (j / OPS) & 1, p.timeout_ns, &flags[0]));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t d = tmem_base + static_cast<uint32_t>(t * MT), a = tmem_base + 2 * MT + b * 64;
+                        const uint64_t bx = x0 + static_cast<uint64_t>(b * (Sh::kX16 / 16));
+#pragma unroll
+                        for (int kk = 0; kk < kQ8BlockK / 16; ++kk)
+                            tc_mma_f16_ts(d, a + 8 * kk, bx + (kk >= 4) * (MT * 128 / 16) + 2 * (kk & 3), Sh::kIdesc,
+                                          (in_chunk > 0 || kk > 0) ? 1u : 0u);
+                        tc_commit(&opempty[b]);
+                        if (in_chunk == kExactBlocks - 1 || j + 1 == blocks)
+                            tc_commit(&afull[t]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
+            if (!ok)
+                q8_fail(p.err, &flags[0], kErrTimeoutMma);
             if (!ok) {                   // abort: wait for the MMAs already issued before TMEM is freed
                 if (leader)
                     tc_commit(drain);
@@ -263,15 +271,15 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 mbar_wait(drain, 0, kDefaultTimeoutNs, &never);
             }
         }
-    } else if (warp < kWidenWarps) {
+    } else if (warp < Sh::kFirstEpi) {
         // --------------------------------------------------------------- widen
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * MT;
-        for (int j = warp >> 2; j < blocks; j += kWidenSets) {
+        for (int j = (warp - Sh::kFirstWiden) >> 2; j < blocks; j += kWidenSets) {
             const int sl = j % S, b = j % OPS;
             // The operand buffer first: once the MMA of unit j - OPS is done, unit
             // j - S <= j - OPS has been widened, so the ring slot's barrier is at
-            // most one phase behind and its parity says which.  (The sets run
+            // most one phase behind and its parity says which.  (The warps run
             // apart: by the parity alone, a slot still waiting for unit j - S
             // looks like one that holds unit j.)
             const bool ok = mbar_wait(&opempty[b], ((j / OPS) & 1) ^ 1, p.timeout_ns, &flags[0]) &&
@@ -282,18 +290,6 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             }
             tc_fence_after();
             widen_row<8>(sW + sl * kQ8WBytes, row, 0, lane_base + b * 64);
-            const uint8_t *xs = sXraw + sl * Sh::kRawX;
-            uint8_t *xd = sX16 + b * Sh::kX16;
-#pragma unroll 2
-            for (int i = 0; i < MT / 16; ++i) {
-                const int c = lane & 7, m = i * 16 + quarter * 4 + (lane >> 3), cc = (c & 3) * 2;
-                uint32_t r[8];
-                widen16(*reinterpret_cast<const uint4 *>(xs + m * 128 + ((c ^ (m & 7)) << 4)), r);
-                uint8_t *dst = xd + (c >> 2) * (MT * 128) + m * 128;
-                *reinterpret_cast<uint4 *>(dst + ((cc ^ (m & 7)) << 4)) = make_uint4(r[0], r[1], r[2], r[3]);
-                *reinterpret_cast<uint4 *>(dst + (((cc + 1) ^ (m & 7)) << 4)) = make_uint4(r[4], r[5], r[6], r[7]);
-            }
-            fence_proxy_async_smem();
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -303,68 +299,126 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             }
         }
     } else {
-        // ------------------------------------------------------------ epilogue
+        // ------------------------------------------- widen x, and the epilogue
         constexpr int NC = Sh::kCols;
         pdl_wait();                      // scales, residual, workspace and y only from here on
-        const int ew = warp - kWidenWarps;
+        const int ew = warp - Sh::kFirstEpi;
         const int row = (warp & 3) * 32 + lane;
         const int col0 = (ew >> 2) * NC, valid = p.g.M - m0 - col0;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(col0);
-        // Accumulations leave TMEM in pairs, both buffers at once.  More than
-        // one pair (2048 k) is carried in global memory: registers and shared
-        // memory are taken, and it is read back long after.
-        int *carry = p.carry + static_cast<size_t>(blockIdx.x) * (MT * kTileN) + col0 * kTileN + row;
+        // The last two accumulations stay in TMEM until the end; earlier ones
+        // (K parts of more than 2048) are put into global memory, a slot each,
+        // while the MMAs fill the other buffer: registers and shared memory are
+        // taken.
+        const int chunks = (blocks + kExactBlocks - 1) / kExactBlocks;
+        const size_t slot = MT * kTileN;
+        int *carry = p.carry + blockIdx.x * p.carried * slot + col0 * kTileN + row;
         int *sums = reinterpret_cast<int *>(smem) + col0 * kTileN + row;
-        int chunk = 0;
-        for (int j = 0; j < blocks; j += 2 * kExactBlocks) {
-            const bool pair = j + kExactBlocks < blocks, end = j + 2 * kExactBlocks >= blocks;
-            const uint32_t ph = (chunk >> 1) & 1;
-            bool ok = mbar_wait(&afull[0], ph, p.timeout_ns, &flags[0]) &&
-                      (!pair || mbar_wait(&afull[1], ph, p.timeout_ns, &flags[0]));
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
-                q8_fail(p.err, &flags[0], kErrTimeoutEpilogue);
-                break;
-            }
+        // This thread's pieces of an x tile: piece c of token m, where 8 pieces
+        // make a token's 128 bytes (swizzled), in fp16 half a row of each half.
+        const int c = lane & 7, m = ew % Sh::kXWarps * 4 + (lane >> 3), cc = (c & 3) * 2;
+        constexpr int kStep = Sh::kXWarps * 4 * 128;     // tokens a whole number of swizzle periods apart
+        static_assert(Sh::kXWarps * 4 % 8 == 0, "the swizzle repeats every 8 rows");
+        const int from = m * 128 + ((c ^ (m & 7)) << 4);
+        const int to0 = (c >> 2) * (MT * 128) + m * 128 + ((cc ^ (m & 7)) << 4), to1 = to0 ^ 16;
+        bool ok = true;
+        int put = 0;                     // accumulations put away
+        auto put_away = [&] {
+            const int t = put & 1;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&afull[t], (put >> 1) & 1, p.timeout_ns, &flags[0]));
+            if (!ok)
+                return;
             tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < NC; c0 += 16) {
-                int v[16], u[16];
-                load_sums(lane_base + static_cast<uint32_t>(c0), v);
-                if (pair) {
-                    load_sums(lane_base + static_cast<uint32_t>(MT + c0), u);
+                int v[16];
+                load_sums(lane_base + static_cast<uint32_t>(t * MT + c0), v);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        v[c] += u[c];
-                }
-                if (j > 0) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        u[c] = c0 + c < valid ? __ldcg(carry + (c0 + c) * kTileN) : 0;
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        v[c] += u[c];
-                }
-                if (!end) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (c0 + c < valid)
-                            __stcg(carry + (c0 + c) * kTileN, v[c]);
-                } else if (p.split == 1) {
-                    store_columns<16>(p.g, m0 + col0 + c0, n0 + row, v);
-                } else {
-                    // the ring is done with: the last MMA has read its operands
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        sums[(c0 + c) * kTileN] = v[c];
-                }
+                for (int i = 0; i < 16; ++i)
+                    if (c0 + i < valid)
+                        __stcg(carry + put * slot + (c0 + i) * kTileN, v[i]);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&aempty[0]);
-                mbar_arrive(&aempty[1]);
+            if (lane == 0)
+                mbar_arrive(&aempty[t]);
+            ++put;
+        };
+        for (int u = ew / Sh::kXWarps; u < blocks; u += 2) {
+            const int sl = u % S, b = u % OPS;
+            // the operand buffer first, as above
+            ok = mbar_wait(&opempty[b], ((u / OPS) & 1) ^ 1, p.timeout_ns, &flags[0]) &&
+                 mbar_wait(&wfull[sl], (u / S) & 1, p.timeout_ns, &flags[0]);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok)
+                break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {            // 4 pieces of 16 bytes a thread
+                uint32_t r[8];
+                widen16(*reinterpret_cast<const uint4 *>(sXraw + sl * Sh::kRawX + from + i * kStep), r);
+                uint8_t *dst = sX16 + b * Sh::kX16 + i * kStep;
+                *reinterpret_cast<uint4 *>(dst + to0) = make_uint4(r[0], r[1], r[2], r[3]);
+                *reinterpret_cast<uint4 *>(dst + to1) = make_uint4(r[4], r[5], r[6], r[7]);
             }
-            chunk += 2;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&opfull[b]);
+                mbar_arrive(&wempty[sl]);
+            }
+            // an accumulation is done once the unit two after it has been widened, or nearly
+            if (put + 2 < chunks && u >= (put + 1) * kExactBlocks + 2) {
+                put_away();
+                if (!ok)
+                    break;
+            }
+        }
+        while (ok && put + 2 < chunks)
+            put_away();
+        // The end: what was put away (fetched while the last MMAs run), and the
+        // one or two accumulations in TMEM.
+        int acc[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            acc[i] = 0;
+        for (int k = 0; k < put; ++k) {
+            int v[NC];
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                v[i] = i < valid ? __ldcg(carry + k * slot + i * kTileN) : 0;
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                acc[i] += v[i];
+        }
+        const int last = chunks - 1;
+        const bool pair = chunks > 1;
+        ok = ok && (!pair || mbar_wait(&afull[(last - 1) & 1], ((last - 1) >> 1) & 1, p.timeout_ns, &flags[0])) &&
+             mbar_wait(&afull[last & 1], (last >> 1) & 1, p.timeout_ns, &flags[0]);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok)
+            q8_fail(p.err, &flags[0], kErrTimeoutEpilogue);
+        tc_fence_after();
+#pragma unroll
+        for (int c0 = 0; c0 < NC && ok; c0 += 8) {
+            int v[8];
+            load_sums(lane_base + static_cast<uint32_t>((last & 1) * MT + c0), v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                acc[c0 + i] += v[i];
+            if (pair) {
+                load_sums(lane_base + static_cast<uint32_t>(((last - 1) & 1) * MT + c0), v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[c0 + i] += v[i];
+            }
+        }
+        if (ok && p.split == 1) {
+            store_columns<NC>(p.g, m0 + col0, n0 + row, acc);
+        } else if (ok) {
+            // in the ring's place: the last MMA has read its operands
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                sums[i * kTileN] = acc[i];
         }
     }
 
@@ -450,7 +504,7 @@ cudaError_t launch_shape(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q
 template <int MT>
 Q8TcShape shape_of()
 {
-    return {2, SplitShape<MT>::kSmem, SplitShape<MT>::kThreads, SplitShape<MT>::kStages};
+    return {MT, 2, SplitShape<MT>::kSmem, SplitShape<MT>::kThreads, SplitShape<MT>::kStages};
 }
 
 } // namespace

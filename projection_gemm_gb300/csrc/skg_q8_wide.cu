@@ -43,17 +43,17 @@ namespace {
 
 constexpr int kPair = 2;                             // CTAs of a cluster
 
-template <int MT>
+constexpr int MT = 128;                              // tokens of a tile: the MMA's N
+
 struct WideShape {
     static constexpr int kEpiWarps = 16;
     static constexpr int kCols = MT * 4 / kEpiWarps;         // accumulator columns of an epilogue thread
     static constexpr int kThreads = 32 * (kWidenWarps + kEpiWarps + 4);
-    static constexpr int kTmaWarp = kWidenWarps + kEpiWarps;
-    static constexpr int kMmaWarp = kTmaWarp + 1;
-    static constexpr int kWatchWarp = kMmaWarp + 1;
-    static constexpr int kXWarp = kWatchWarp + 1;
+    // The MMA warp first: the oldest warp of a scheduler goes before the others
+    static constexpr int kMmaWarp = 0, kTmaWarp = 1, kXWarp = 2, kWatchWarp = 3;
+    static constexpr int kFirstWiden = 4, kFirstEpi = kFirstWiden + kWidenWarps;
     static constexpr int kStages = 4;                        // ring of W
-    static constexpr int kXStages = MT > 128 ? 6 : 8;        // ring of fp16 x
+    static constexpr int kXStages = 8;                       // ring of fp16 x
     static constexpr int kOps = (512 - 2 * MT) / 64;         // widened W in TMEM
     static_assert(kStages >= kOps && kXStages >= kOps && kOps >= kWidenSets, "the waits need this");
     static constexpr uint32_t kX16 = MT * kQ8BlockK;         // this CTA's half of a unit's fp16 x: two 64-wide halves
@@ -75,11 +75,10 @@ __device__ __forceinline__ void tile_at(const Q8WideParams &p, int tile, int &np
     mt = b * p.band + r - np * wide;
 }
 
-template <int MT>
-__global__ void __launch_bounds__(WideShape<MT>::kThreads, 1) __cluster_dims__(kPair, 1, 1)
+__global__ void __launch_bounds__(WideShape::kThreads, 1) __cluster_dims__(kPair, 1, 1)
 q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Q8WideParams p)
 {
-    using Sh = WideShape<MT>;
+    using Sh = WideShape;
     constexpr int S = Sh::kStages, SX = Sh::kXStages, OPS = Sh::kOps;
     constexpr uint16_t kBoth = (1 << kPair) - 1;
 
@@ -219,47 +218,58 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         // ---------------------------------------------------------- MMA issuer
         if (rank == 0) {
             const bool leader = elect_one();
-            int chunk = 0, kb = 0;
-            bool ok = mbar_wait(&opfull[0], 0, p.timeout_ns, &flags[0]);
-            for (int j = 0; j < units; ++j) {
-                const int in_chunk = kb % kExactBlocks, t = chunk & 1, b = j % OPS, sx = j % SX;
-                if (in_chunk == 0)
-                    ok = ok && mbar_wait(&aempty[t], ((chunk >> 1) & 1) ^ 1, p.timeout_ns, &flags[0]);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) {
-                    q8_fail(p.err, &flags[0], kErrTimeoutMma);
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(t * MT);
-                const uint32_t a = tmem_base + static_cast<uint32_t>(2 * MT + b * 64);
-                const uint32_t bx = smem_u32(sX + sx * Sh::kX16);
-                const uint64_t b0 = smem_desc_kmajor_sw128(bx), b1 = smem_desc_kmajor_sw128(bx + Sh::kX16 / 2);
-                const bool end = ++kb == p.nkb || in_chunk == kExactBlocks - 1;
-                if (leader) {
+            const uint64_t x0 = smem_desc_kmajor_sw128(smem_u32(sX));
+            int kb = 0, in_chunk = 0, chunk = 0;
+            bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&opfull[0], 0, p.timeout_ns, &flags[0]));
+            // A round of the ring at a time, unrolled: the slots' addresses,
+            // descriptors and phases are then constants (worked out in a loop
+            // over single units they took longer than the MMAs).
+            for (int j0 = 0; ok && j0 < units; j0 += SX) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_f16_ts_pair(d, a + 8 * kk, b0 + 2 * kk, Sh::kIdesc, (in_chunk > 0 || kk > 0) ? 1u : 0u);
-                }
-                __syncwarp();
-                uint64_t *next = &opfull[(j + 1) % OPS];
-                const uint32_t next_phase = ((j + 1) / OPS) & 1;
-                const bool ready = j + 1 == units || mbar_try_wait(next, next_phase);
-                if (leader) {
+                for (int u = 0; u < SX; ++u) {
+                    if (!ok || j0 + u >= units)
+                        break;
+                    constexpr int kHalf = Sh::kX16 / 2 / 16;             // the second 64 k, in descriptor units
+                    const uint64_t bx = x0 + static_cast<uint64_t>(u * (Sh::kX16 / 16));
+                    const uint32_t a = tmem_base + 2 * MT + (u % OPS) * 64;
+                    const int t = chunk & 1;
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(t * MT);
+                    if (in_chunk == 0)
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&aempty[t], ((chunk >> 1) & 1) ^ 1, p.timeout_ns, &flags[0]));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_f16_ts_pair(d, a + 32 + 8 * kk, b1 + 2 * kk, Sh::kIdesc, 1u);
-                    // nobody waits for the last units, and the peer may be gone by then
-                    if (j + OPS < units)
-                        tc_commit_pair_multicast(&done[sx], kBoth);
-                    if (end)
-                        tc_commit_pair_multicast(&afull[t], kBoth);
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_f16_ts_pair(d, a + 8 * kk, bx + 2 * kk, Sh::kIdesc, (kk > 0 || in_chunk > 0) ? 1u : 0u);
+                    }
+                    const bool last = j0 + u + 1 == units;
+                    uint64_t *next = &opfull[(u + 1) % OPS];
+                    constexpr int kRounds = SX / OPS;                    // of the operand buffers, in one of the ring
+                    static_assert(SX % OPS == 0 && kRounds % 2 == 0, "phases repeat with the ring");
+                    const uint32_t next_phase = ((u + 1) / OPS) & 1;
+                    const bool ready = __all_sync(0xFFFFFFFFu, last || mbar_try_wait(next, next_phase));
+                    const bool end = ++kb == p.nkb || in_chunk == kExactBlocks - 1;
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_f16_ts_pair(d, a + 32 + 8 * kk, bx + kHalf + 2 * kk, Sh::kIdesc, 1u);
+                        // nobody waits for the last units, and the peer may be gone by then
+                        if (j0 + u + OPS < units)
+                            tc_commit_pair_multicast(&done[u], kBoth);
+                        if (end)
+                            tc_commit_pair_multicast(&afull[t], kBoth);
+                    }
+                    in_chunk = end ? 0 : in_chunk + 1;
+                    chunk += end;
+                    kb = kb == p.nkb ? 0 : kb;
+                    if (!ready)
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(next, next_phase, p.timeout_ns, &flags[0]));
                 }
-                __syncwarp();
-                chunk += end;
-                kb = kb == p.nkb ? 0 : kb;
-                ok = ready || mbar_wait(next, next_phase, p.timeout_ns, &flags[0]);
             }
+            if (!ok)
+                q8_fail(p.err, &flags[0], kErrTimeoutMma);
             if (!ok) {                   // abort: wait for the MMAs already issued before TMEM is freed
                 if (leader)
                     tc_commit_pair(drain);
@@ -267,12 +277,12 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 mbar_wait(drain, 0, kDefaultTimeoutNs, &never);
             }
         }
-    } else if (warp == Sh::kWatchWarp || warp < kWidenWarps) {
+    } else if (warp == Sh::kWatchWarp || warp < Sh::kFirstEpi) {
         // --------------------------------------------- widen, and watch over x
         const bool watch = warp == Sh::kWatchWarp;
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * MT;
-        for (int j = watch ? 0 : warp >> 2; j < units; j += watch ? 1 : kWidenSets) {
+        for (int j = watch ? 0 : (warp - Sh::kFirstWiden) >> 2; j < units; j += watch ? 1 : kWidenSets) {
             const int b = j % OPS, before = j - OPS;
             // The operand buffer first: once unit j - OPS is done, the units a
             // ring ago have been consumed, so the ring slots' barriers are at
@@ -304,7 +314,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         constexpr int NC = Sh::kCols;
         pdl_wait();                      // scales, residual and y only from here on
         const int row = (warp & 3) * 32 + lane;
-        const int col0 = ((warp - kWidenWarps) >> 2) * NC;
+        const int col0 = ((warp - Sh::kFirstEpi) >> 2) * NC;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(col0);
         int chunk = 0;
         bool ok = true;
@@ -377,10 +387,16 @@ cudaError_t launch_pdl(const void *f, unsigned grid, unsigned threads, size_t sm
     return cudaLaunchKernelExC(&cfg, f, args);
 }
 
-template <int MT>
-cudaError_t launch_shape(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8WideParams &p, int grid, cudaStream_t s)
+} // namespace
+
+Q8TcShape q8_wide_shape()
 {
-    using Sh = WideShape<MT>;
+    return {MT, 1, WideShape::kSmem, WideShape::kThreads, WideShape::kStages};
+}
+
+cudaError_t launch_q8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8WideParams &p, int grid,
+                           cudaStream_t s)
+{
     static int attr_set[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -388,31 +404,15 @@ cudaError_t launch_shape(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q
         return e;
     if (dev >= kMaxDevices)
         return cudaErrorInvalidDevice;
-    const void *f = reinterpret_cast<const void *>(&q8_wide_kernel<MT>);
+    const void *f = reinterpret_cast<const void *>(&q8_wide_kernel);
     if (__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE) == 0) {
-        e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+        e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, WideShape::kSmem);
         if (e != cudaSuccess)
             return e;
         __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
     }
     void *args[] = {const_cast<CUtensorMap *>(&tmW), const_cast<CUtensorMap *>(&tmX), const_cast<Q8WideParams *>(&p)};
-    return launch_pdl(f, static_cast<unsigned>(grid), Sh::kThreads, Sh::kSmem, args, s);
-}
-
-template <int MT>
-Q8TcShape shape_of()
-{
-    return {1, WideShape<MT>::kSmem, WideShape<MT>::kThreads, WideShape<MT>::kStages};
-}
-
-} // namespace
-
-Q8TcShape q8_wide_shape(int m_tile) { return m_tile == 128 ? shape_of<128>() : shape_of<192>(); }
-
-cudaError_t launch_q8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8WideParams &p, int m_tile, int grid,
-                           cudaStream_t s)
-{
-    return m_tile == 128 ? launch_shape<128>(tmW, tmX, p, grid, s) : launch_shape<192>(tmW, tmX, p, grid, s);
+    return launch_pdl(f, static_cast<unsigned>(grid), WideShape::kThreads, WideShape::kSmem, args, s);
 }
 
 cudaError_t launch_q8_widen(const int8_t *x, void *out, size_t elements, int num_sms, cudaStream_t s)

@@ -4,11 +4,13 @@ for profilers (ncu captures of a single kernel launch).
 usage: python -m projection_gemm_gb300.profile_case M N K [epilogue] [launches]
                                                     [--kind gemv|tc] [--split S] [--stages D] [--burst B]
        python -m projection_gemm_gb300.profile_case M --chain-group [--independent] [launches]
+       python -m projection_gemm_gb300.profile_case --q8 linear M N K [epilogue] | norm M K | quant M K | gate M K
 The operands are the seeded synthetic tensors of `inputs.py` (seed 11); the
 default plan is used unless --kind (skg_plan_force_kernel) or --split /
 --stages / --burst (skg_plan_force) force a configuration.  --chain-group runs the five decode-layer chain
 projections at M as one group launch (skg_group, each projection ordered
-after the previous one, or with --independent in no order) instead.  The
+after the previous one, or with --independent in no order) instead.  --q8
+runs one operator of the 8-bit path three times on normal rows.  The
 process exits non-zero on any library error.
 """
 import argparse
@@ -39,7 +41,50 @@ def chain_group(M, launches, ordered=True):
     print("ok")
 
 
+def q8(op, *sizes):
+    g = torch.Generator(device="cuda").manual_seed(11)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    def rows(M, K):
+        q, s = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+        skg.skg_quantize_q8(normal(M, K), None, q, s)
+        return q, s
+
+    if op == "linear":
+        M, N, K = (int(v) for v in sizes[:3])
+        epi = sizes[3] if len(sizes) > 3 else "bf16"
+        (x, xs), (W, ws) = rows(M, K), rows(N, K)
+        res = normal(M, N) if epi == "bf16_residual" else None
+        y = torch.empty(M, N, dtype=torch.float32 if epi == "fp32" else torch.bfloat16, device="cuda")
+        plan = skg.Q8Plan(M, N, K, epi)
+        print(plan.info())
+        for _ in range(3):
+            plan.run(x, xs, W, ws, res, y)
+        plan.check()
+        plan.close()
+    else:
+        M, K = (int(v) for v in sizes)
+        x, other, gamma = normal(M, K), normal(M, K), normal(K)
+        q, s = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+        h = torch.empty_like(x)
+        for _ in range(3):
+            if op == "norm":
+                skg.skg_rmsnorm_q8(x, other, gamma, 1e-6, h, q, s)
+            else:
+                skg.skg_quantize_q8(x, other if op == "gate" else None, q, s)
+    torch.cuda.synchronize()
+    print("ok")
+
+
 def main(argv):
+    if argv and argv[0] == "--q8":
+        build.build()
+        skg.load()
+        torch.cuda.set_device(0)
+        q8(*argv[1:])
+        return
     if "--chain-group" in argv:
         rest = [a for a in argv if a not in ("--chain-group", "--independent")]
         build.build()

@@ -108,7 +108,7 @@ def test_binding_refuses_host_tensors():
 def test_query_describes_a_launch_that_covers_every_tile(M, N, K):
     d = skg.skg_q8_plan_query(M, N, K, "bf16", SMS)
     assert d["grid"] >= 1 and d["threads"] % 32 == 0
-    assert d["kernel"] == ("q8_stream" if M <= 16 else "q8_split" if M <= 64 else "q8_wide")
+    assert (d["kernel"] == "q8_stream") == (M <= 16)
     assert d["tiles"] == -(-N // d["n_tile"]) * -(-M // d["m_tile"])
     if d["kernel"] == "q8_stream":
         assert d["workspace_bytes"] == 0 and d["grid"] == d["tiles"] and M <= d["m_tile"]
@@ -116,10 +116,10 @@ def test_query_describes_a_launch_that_covers_every_tile(M, N, K):
     nkb = -(-K // 128)
     assert d["smem_bytes"] * d["ctas_per_sm"] <= 227 * 1024
     if d["kernel"] == "q8_split":
-        assert M <= d["m_tile"] and 1 <= d["split_k"] <= min(8, nkb) and d["grid"] == d["tiles"] * d["split_k"]
+        assert d["m_tile"] == (32 if M <= 32 else 64) and 1 <= d["split_k"] <= min(8, nkb) and d["grid"] == d["tiles"] * d["split_k"]
         assert d["split_k"] == 1 or d["grid"] <= SMS * d["ctas_per_sm"]
-        carried = -(-nkb // d["split_k"]) > 16
-        assert d["workspace_bytes"] == (d["grid"] * d["m_tile"] * 512 if carried else 0)
+        put_away = max(0, -(-(-(-nkb // d["split_k"])) // 8) - 2)
+        assert d["workspace_bytes"] == d["grid"] * put_away * d["m_tile"] * 512
     else:
         assert d["split_k"] == 1 and d["grid"] == 2 * min(d["tiles"], SMS // 2)
         assert d["workspace_bytes"] == 2 * M * K
@@ -137,7 +137,10 @@ def test_streaming_launch_fills_as_few_slots_as_hold_it(M, N):
     assert d["threads"] * d["ctas_per_sm"] <= 1024
 
 
-@pytest.mark.parametrize("M,N,tile", [(65, 7168, 128), (192, 7168, 128), (256, 7168, 128), (1024, 7168, 128),
-                                      (4096, 12288, 192), (333, 5001, 128)])
-def test_wide_tile_takes_the_fewer_waves(M, N, tile):
-    assert skg.skg_q8_plan_query(M, N, 7168, "bf16", SMS)["m_tile"] == tile
+@pytest.mark.parametrize("M,N,K,kernel", [
+    (17, 7168, 7168, "q8_split"), (64, 7168, 16384, "q8_split"), (64, 28672, 8192, "q8_wide"), (128, 384, 7168, "q8_split"),
+    (128, 7168, 7168, "q8_wide"), (256, 4096, 4096, "q8_split"), (333, 5001, 4112, "q8_wide"), (1000, 4096, 4096, "q8_wide"),
+    (4096, 12288, 7168, "q8_wide")])
+def test_batches_take_the_kernel_measured_faster(M, N, K, kernel):
+    """Few tiles: K split over clusters; many: whole tiles."""
+    assert skg.skg_q8_plan_query(M, N, K, "bf16", SMS)["kernel"] == kernel
