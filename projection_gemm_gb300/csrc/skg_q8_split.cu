@@ -413,7 +413,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             }
         }
         if (ok && p.split == 1) {
-            store_columns<NC>(p.g, m0 + col0, n0 + row, acc);
+            store_columns(p.g, m0 + col0, n0 + row, load_scales(p.g, m0 + col0, n0 + row), acc);
         } else if (ok) {
             // in the ring's place: the last MMA has read its operands
 #pragma unroll

@@ -40,54 +40,58 @@ __device__ __forceinline__ void widen_row(const uint8_t *tile, int row, int firs
     }
 }
 
-// NC outputs (tokens m0...) of one channel n from their sums, 4 at a time so
-// that their loads are in flight together and few registers hold them.
-template <int EPI, int NC>
-__device__ __forceinline__ void store_columns_as(const Q8LinearParams &g, int m0, int n, const int (&acc)[NC])
+// What a warp's 32 channels x 32 tokens need besides their sums, fetched before
+// those are complete: a thread holds the scale of its channel n and of token
+// m0 + lane.
+struct Scales {
+    float w, x;
+};
+
+__device__ __forceinline__ Scales load_scales(const Q8LinearParams &g, int m0, int n)
 {
-    const int valid = g.M - m0;
-    const float ws = __ldcg(g.w_scale + n);
-    const float *xsp = g.x_scale + m0;
+    const int m = m0 + (threadIdx.x & 31);
+    return {n < g.N ? __ldcg(g.w_scale + n) : 0.0f, m < g.M ? __ldcg(g.x_scale + m) : 0.0f};
+}
+
+// 32 outputs (tokens m0...) of one channel n from their sums; the residual's
+// loads 8 at a time.  Called by whole warps.
+template <int EPI>
+__device__ __forceinline__ void store_columns_as(const Q8LinearParams &g, int m0, int n, const Scales &sc, const int (&acc)[32])
+{
+    const int valid = n < g.N ? g.M - m0 : 0;
     size_t at = static_cast<size_t>(m0) * g.N + n;
 #pragma unroll
-    for (int c0 = 0; c0 < NC; c0 += 4) {
-        float v[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            v[c] = c0 + c < valid ? q8_scaled(acc[c0 + c], __ldcg(xsp + c0 + c), ws) : 0.0f;
+    for (int c0 = 0; c0 < 32; c0 += 8) {
+        uint16_t b[8];
         if (EPI == SKG_EPI_BF16_RESIDUAL) {
             const uint16_t *r = g.res + at;
-            uint16_t b[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c, r += g.N)
+            for (int c = 0; c < 8; ++c, r += g.N)
                 b[c] = c0 + c < valid ? __ldcg(r) : 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                v[c] = __fadd_rn(v[c], bf16_to_f32(b[c]));
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c, at += g.N) {
+        for (int c = 0; c < 8; ++c, at += g.N) {
+            float v = q8_scaled(acc[c0 + c], __shfl_sync(0xFFFFFFFFu, sc.x, c0 + c), sc.w);
+            if (EPI == SKG_EPI_BF16_RESIDUAL)
+                v = __fadd_rn(v, bf16_to_f32(b[c]));
             if (c0 + c < valid) {
                 if (EPI == SKG_EPI_FP32)
-                    static_cast<float *>(g.y)[at] = v[c];
+                    static_cast<float *>(g.y)[at] = v;
                 else
-                    static_cast<uint16_t *>(g.y)[at] = f32_to_bf16(v[c]);
+                    static_cast<uint16_t *>(g.y)[at] = f32_to_bf16(v);
             }
         }
     }
 }
 
-template <int NC>
-__device__ __forceinline__ void store_columns(const Q8LinearParams &g, int m0, int n, const int (&acc)[NC])
+__device__ __forceinline__ void store_columns(const Q8LinearParams &g, int m0, int n, const Scales &sc, const int (&acc)[32])
 {
-    if (n >= g.N || m0 >= g.M)
-        return;
     if (g.epilogue == SKG_EPI_FP32)
-        store_columns_as<SKG_EPI_FP32>(g, m0, n, acc);
+        store_columns_as<SKG_EPI_FP32>(g, m0, n, sc, acc);
     else if (g.epilogue == SKG_EPI_BF16_RESIDUAL)
-        store_columns_as<SKG_EPI_BF16_RESIDUAL>(g, m0, n, acc);
+        store_columns_as<SKG_EPI_BF16_RESIDUAL>(g, m0, n, sc, acc);
     else
-        store_columns_as<SKG_EPI_BF16>(g, m0, n, acc);
+        store_columns_as<SKG_EPI_BF16>(g, m0, n, sc, acc);
 }
 
 // NC accumulator columns of this thread's TMEM lane as integers (they are

@@ -48,6 +48,7 @@ constexpr int MT = 128;                              // tokens of a tile: the MM
 struct WideShape {
     static constexpr int kEpiWarps = 16;
     static constexpr int kCols = MT * 4 / kEpiWarps;         // accumulator columns of an epilogue thread
+    static_assert(kCols == 32, "a lane holds the scale of a token");
     static constexpr int kThreads = 32 * (kWidenWarps + kEpiWarps + 4);
     // The MMA warp first: the oldest warp of a scheduler goes before the others
     static constexpr int kMmaWarp = 0, kTmaWarp = 1, kXWarp = 2, kWatchWarp = 3;
@@ -319,6 +320,10 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         int chunk = 0;
         bool ok = true;
         for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
+            int np, mt;
+            tile_at(p, tile, np, mt);
+            const int n = (np * kPair + rank) * kTileN + row;
+            const Scales sc = load_scales(p.g, mt * MT + col0, n);
             int acc[NC];
             for (int kb = 0; kb < p.nkb; kb += kExactBlocks, ++chunk) {
                 const int t = chunk & 1;
@@ -341,11 +346,8 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 if (lane == 0)
                     mbar_arrive_cluster(map_shared_rank(smem_u32(&aempty[t]), 0));
             }
-            if (ok) {
-                int np, mt;
-                tile_at(p, tile, np, mt);
-                store_columns<NC>(p.g, mt * MT + col0, (np * kPair + rank) * kTileN + row, acc);
-            }
+            if (ok)
+                store_columns(p.g, mt * MT + col0, n, sc, acc);
         }
     }
 
