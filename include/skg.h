@@ -481,7 +481,7 @@ typedef struct skg_q8_plan_desc {
     int tiles;                  /* output tiles */
     int split_k;                /* SPLIT: CTAs of a cluster, sharing a tile's K (1..8); else 1 */
     int grid, threads, smem_bytes, stages, ctas_per_sm;
-    size_t workspace_bytes;     /* SPLIT: sums put away where a CTA has more than 2048 k; WIDE: x as fp16 */
+    size_t workspace_bytes;     /* SPLIT: sums put away where a CTA has more than 2048 k; else 0 */
 } skg_q8_plan_desc;
 
 typedef struct skg_q8_plan_s *skg_q8_plan_t;

@@ -17,7 +17,7 @@ using namespace skg;
 struct skg_q8_plan_s {
     skg_q8_plan_desc d;
     int num_sms = 0;
-    void *ws = nullptr;               // carried sums (split) or x as fp16 (wide)
+    void *ws = nullptr;               // sums put away by the split kernel
     size_t ws_cap = 0;
     std::vector<void *> retired;      // outgrown workspaces: a captured graph may still use them
     unsigned int *err_host = nullptr; // mapped pinned word
@@ -67,10 +67,10 @@ int choose_split(int tiles, int nkb, int slots)
 // The split or the wide kernel, by their times as measured (us): a CTA of the
 // split kernel takes 0.93 a unit of 128 k (0.69 with tiles of 32 tokens) and 4
 // for its ends, in as many waves as its grid needs; the wide one 0.40 a unit of
-// a tile and 7, x's widening among them.  Measured against this rule, split
-// then wide: 64 x 28672 x 8192 73 and 66, 128 x 384 x 7168 7.6 and 25, 128 x
-// 7168 x 7168 29.9 and 28.6, 256 x 4096 x 4096 18.9 and 20, 1000 x 4096 x 4096
-// 60 and 34.
+// a tile and 5.  Measured against this rule, split then wide: 24 x 28672 x 8192
+// 46 and 57, 64 x 28672 x 8192 59 and 58, 128 x 384 x 7168 7.6 and 26, 128 x
+// 7168 x 7168 29.8 and 27.3, 256 x 4096 x 4096 18.7 and 17.8, 1000 x 4096 x 4096
+// 58 and 32; it is furthest off at 1000 x 1024 x 1024, 9.6 and 8.4.
 bool prefer_split(const skg_q8_plan_desc &d, int num_sms)
 {
     const int m_tile = d.M <= 32 ? 32 : 64, nkb = ceil_div(d.K, kQ8BlockK), n_tiles = ceil_div(d.N, kTileN);
@@ -79,7 +79,7 @@ bool prefer_split(const skg_q8_plan_desc &d, int num_sms)
     const long long wt = static_cast<long long>(ceil_div(n_tiles, 2)) * ceil_div(d.M, q8_wide_shape().m_tile);
     const int split = st > slots ? 1 : choose_split(static_cast<int>(st), nkb, static_cast<int>(slots));
     const double units = static_cast<double>((st * split + slots - 1) / slots) * ceil_div(nkb, split);
-    return 4.0 + (m_tile == 32 ? 0.69 : 0.93) * units <= 7.0 + 0.40 * static_cast<double>((wt + pairs - 1) / pairs) * nkb;
+    return 4.0 + (m_tile == 32 ? 0.69 : 0.93) * units <= 5.0 + 0.40 * static_cast<double>((wt + pairs - 1) / pairs) * nkb;
 }
 
 // Accumulations of 1024 k that a CTA of the split kernel puts away: all but two.
@@ -127,7 +127,6 @@ skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int split, int
     d->ctas_per_sm = sh.ctas_per_sm;
     if (wide) {
         d->grid = 2 * std::min(d->tiles, std::max(1, num_sms / 2));
-        d->workspace_bytes = static_cast<size_t>(d->M) * d->K * 2;
         return SKG_OK;
     }
     d->split_k = split ? std::min(split, nkb) : choose_split(d->tiles, nkb, num_sms * sh.ctas_per_sm);
@@ -373,7 +372,7 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
         t.timeout_ns = kDefaultTimeoutNs;
         return launched(launch_q8_split(tmW, tmX, t, d.m_tile, d.grid, s), who);
     }
-    st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p->ws, d.M, d.K, d.m_tile / 2);
+    st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, d.M, d.K, d.m_tile / 2);
     if (st != SKG_OK)
         return st;
     Q8WideParams t = {};
@@ -386,10 +385,7 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
     t.band = kQ8Band;
     t.static_w = d.static_weights;
     t.timeout_ns = kDefaultTimeoutNs;
-    cudaError_t e = launch_q8_widen(g.x, p->ws, static_cast<size_t>(d.M) * d.K, p->num_sms, s);
-    if (e == cudaSuccess)
-        e = launch_q8_wide(tmW, tmX, t, d.grid, s);
-    return launched(e, who);
+    return launched(launch_q8_wide(tmW, tmX, t, d.grid, s), who);
 }
 
 skg_status skg_q8_plan_check(skg_q8_plan_t p)

@@ -68,7 +68,6 @@ cudaError_t launch_q8_split(const CUtensorMap &tmW, const CUtensorMap &tmX, cons
                             cudaStream_t s);
 cudaError_t launch_q8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const Q8WideParams &p, int grid,
                            cudaStream_t s);
-cudaError_t launch_q8_widen(const int8_t *x, void *out, size_t elements, int num_sms, cudaStream_t s);
 
 cudaError_t launch_q8_norm(const Q8RowParams &p, cudaStream_t s);
 cudaError_t launch_q8_quantize(const Q8RowParams &p, cudaStream_t s);

@@ -289,7 +289,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 break;
             }
             tc_fence_after();
-            widen_row<8>(sW + sl * kQ8WBytes, row, 0, lane_base + b * 64);
+            widen_row(sW + sl * kQ8WBytes, row, lane_base + b * 64);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -314,13 +314,9 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         const size_t slot = MT * kTileN;
         int *carry = p.carry + blockIdx.x * p.carried * slot + col0 * kTileN + row;
         int *sums = reinterpret_cast<int *>(smem) + col0 * kTileN + row;
-        // This thread's pieces of an x tile: piece c of token m, where 8 pieces
-        // make a token's 128 bytes (swizzled), in fp16 half a row of each half.
-        const int c = lane & 7, m = ew % Sh::kXWarps * 4 + (lane >> 3), cc = (c & 3) * 2;
-        constexpr int kStep = Sh::kXWarps * 4 * 128;     // tokens a whole number of swizzle periods apart
-        static_assert(Sh::kXWarps * 4 % 8 == 0, "the swizzle repeats every 8 rows");
-        const int from = m * 128 + ((c ^ (m & 7)) << 4);
-        const int to0 = (c >> 2) * (MT * 128) + m * 128 + ((cc ^ (m & 7)) << 4), to1 = to0 ^ 16;
+        constexpr int kStep = Sh::kXWarps * 4;           // tokens that a set takes at a time
+        static_assert(kStep % 8 == 0, "the swizzle repeats every 8 rows");
+        const XPiece piece(ew % Sh::kXWarps * 4 + (lane >> 3), lane & 7, MT);
         bool ok = true;
         int put = 0;                     // accumulations put away
         auto put_away = [&] {
@@ -352,14 +348,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok)
                 break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {            // 4 pieces of 16 bytes a thread
-                uint32_t r[8];
-                widen16(*reinterpret_cast<const uint4 *>(sXraw + sl * Sh::kRawX + from + i * kStep), r);
-                uint8_t *dst = sX16 + b * Sh::kX16 + i * kStep;
-                *reinterpret_cast<uint4 *>(dst + to0) = make_uint4(r[0], r[1], r[2], r[3]);
-                *reinterpret_cast<uint4 *>(dst + to1) = make_uint4(r[4], r[5], r[6], r[7]);
-            }
+            piece.widen<MT / kStep>(sXraw + sl * Sh::kRawX, sX16 + b * Sh::kX16, kStep);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {

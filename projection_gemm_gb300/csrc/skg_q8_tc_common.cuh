@@ -23,22 +23,48 @@ __device__ __forceinline__ void widen16(const uint4 &v, uint32_t *r)
     widen4(v.w, r[6], r[7]);
 }
 
-// CHUNKS 16-byte pieces, from `first` on, of W row `row` of a unit (a tile of
-// 128-byte rows, 128-byte swizzle) as fp16 into this thread's TMEM lane: 8
-// columns a piece.
-template <int CHUNKS>
-__device__ __forceinline__ void widen_row(const uint8_t *tile, int row, int first, uint32_t taddr)
+// A W row's 128 bytes of a unit (a tile of 128-byte rows, 128-byte swizzle) as
+// fp16 into this thread's TMEM lane: 64 columns.
+__device__ __forceinline__ void widen_row(const uint8_t *tile, int row, uint32_t taddr)
 {
     const uint8_t *src = tile + row * kQ8BlockK;
 #pragma unroll
-    for (int i = 0; i < CHUNKS / 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
         uint32_t r[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            widen16(*reinterpret_cast<const uint4 *>(src + (((first + 2 * i + h) ^ (row & 7)) << 4)), r + 8 * h);
+            widen16(*reinterpret_cast<const uint4 *>(src + (((2 * i + h) ^ (row & 7)) << 4)), r + 8 * h);
         tmem_st_x16(taddr + 16 * i, r);
     }
 }
+
+// A thread's 16-byte pieces of an x tile (128 bytes a token, 128-byte swizzle):
+// piece c of token m and of every `step`-th token after it.  In fp16 a token is
+// 128 bytes of each of two 64-wide halves, swizzled too.
+struct XPiece {
+    int from, to0, to1;
+
+    __device__ __forceinline__ XPiece(int m, int c, int tokens)
+    {
+        const int cc = (c & 3) * 2;
+        from = m * 128 + ((c ^ (m & 7)) << 4);
+        to0 = (c >> 2) * (tokens * 128) + m * 128 + ((cc ^ (m & 7)) << 4);
+        to1 = to0 ^ 16;
+    }
+
+    template <int N>
+    __device__ __forceinline__ void widen(const uint8_t *raw, uint8_t *x16, int step) const      // step: of whole swizzle periods
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint32_t r[8];
+            widen16(*reinterpret_cast<const uint4 *>(raw + from + i * step * 128), r);
+            uint8_t *dst = x16 + i * step * 128;
+            *reinterpret_cast<uint4 *>(dst + to0) = make_uint4(r[0], r[1], r[2], r[3]);
+            *reinterpret_cast<uint4 *>(dst + to1) = make_uint4(r[4], r[5], r[6], r[7]);
+        }
+    }
+};
 
 // What a warp's 32 channels x 32 tokens need besides their sums, fetched before
 // those are complete: a thread holds the scale of its channel n and of token

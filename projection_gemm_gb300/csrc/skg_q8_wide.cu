@@ -1,27 +1,22 @@
 // skg_q8_wide.cu -- the 8-bit projection for many tokens: tcgen05 over whole
-// tiles, pairs of CTAs sharing x.
+// tiles, by pairs of CTAs.
 //
-// The arithmetic is that of skg_q8_split.cu: integers widened to fp16, products
-// summed by kind::f16 MMAs from a fresh fp32 accumulator every 1024 k, and the
-// accumulators added as int32, so the sums are exact.  What bounds it is the
-// tensor core, if x can be had in time: a unit of 128 k needs 16 KB of W and 256
-// bytes of x (in fp16; x is widened once, before this kernel, into the plan's
-// workspace, since every CTA would repeat it) for each of its tokens, and what
-// is in flight is bounded by shared memory.  So two CTAs work as one
-// (cta_group::2): 256 channels x MT tokens, each CTA with its 128 rows of W in
-// its own TMEM (A) and half of x in its own shared memory (B).  With one CTA a
-// tile and x multicast to both the ring held 3 units of MT = 192 and the loop
-// took 1290 cycles a unit, where the MMAs take 768.
+// The arithmetic is that of skg_q8_split.cu: integers widened to fp16 on chip,
+// products summed by kind::f16 MMAs from a fresh fp32 accumulator every 1024 k,
+// and the accumulators added as int32, so the sums are exact.  What bounds it is
+// the tensor core, if its operands can be had in time.  Two CTAs work as one
+// (cta_group::2): 256 channels x 128 tokens, each CTA with its 128 rows of W in
+// its own TMEM (A) and half of x in its own shared memory (B), so a unit of 128
+// k costs a CTA 16 KB of W and 8 of x from the L2 and the MMAs 512 cycles.
 //
 // Roles of a CTA (one per SM, pairs persistent over tiles):
-//   8 warps    widen, two sets of 4 on alternate units: W from the TMA ring
-//              into TMEM
+//   1          TMEM; in the first CTA of the pair, MMA issue for both
+//   1          TMA
+//   8 warps    widen, two sets of 4 on alternate units: W into TMEM, x into
+//              shared memory
 //   16         epilogue: accumulators into int32 registers; at a tile's end
 //              scales, residual, rounding and the store, while the next tile's
 //              MMAs go on in the other accumulator
-//   1 + 1      TMA of W, of x
-//   1          TMEM; in the first CTA of the pair, MMA issue for both
-//   1          watches the x ring and tells the MMA issuer
 // The MMA issuer is what the rest is arranged around.  About three MMAs queue up
 // behind the one that runs, and one wait on a barrier, even one already past,
 // takes as long as one or two of them; so it waits once a unit, for a barrier at
@@ -29,8 +24,6 @@
 // this one is still to issue, and commits once a unit.
 //
 // Every wait is bounded as in skg_q8_split.cu.
-#include <algorithm>
-
 #include "skg_internal.h"
 #include "skg_ptx.cuh"
 #include "skg_q8_common.cuh"
@@ -42,29 +35,27 @@ namespace {
 #include "skg_q8_tc_common.cuh"
 
 constexpr int kPair = 2;                             // CTAs of a cluster
-
 constexpr int MT = 128;                              // tokens of a tile: the MMA's N
+constexpr int kHalfTokens = MT / kPair;              // of which a CTA holds these
 
 struct WideShape {
     static constexpr int kEpiWarps = 16;
     static constexpr int kCols = MT * 4 / kEpiWarps;         // accumulator columns of an epilogue thread
     static_assert(kCols == 32, "a lane holds the scale of a token");
-    static constexpr int kThreads = 32 * (kWidenWarps + kEpiWarps + 4);
-    // The MMA warp first: the oldest warp of a scheduler goes before the others
-    static constexpr int kMmaWarp = 0, kTmaWarp = 1, kXWarp = 2, kWatchWarp = 3;
-    static constexpr int kFirstWiden = 4, kFirstEpi = kFirstWiden + kWidenWarps;
-    static constexpr int kStages = 4;                        // ring of W
-    static constexpr int kXStages = 8;                       // ring of fp16 x
-    static constexpr int kOps = (512 - 2 * MT) / 64;         // widened W in TMEM
-    static_assert(kStages >= kOps && kXStages >= kOps && kOps >= kWidenSets, "the waits need this");
-    static constexpr uint32_t kX16 = MT * kQ8BlockK;         // this CTA's half of a unit's fp16 x: two 64-wide halves
+    static constexpr int kThreads = 32 * (2 + kWidenWarps + kEpiWarps);
+    static constexpr int kMmaWarp = 0, kTmaWarp = 1, kFirstWiden = 2, kFirstEpi = kFirstWiden + kWidenWarps;
+    static constexpr int kStages = 6;                        // ring of W and int8 x
+    static constexpr int kOps = (512 - 2 * MT) / 64;         // widened operand buffers: 4
+    static_assert(kStages >= kOps && kOps >= kWidenSets, "the widen warps' waits need this");
+    static constexpr uint32_t kRawX = kHalfTokens * kQ8BlockK;
+    static constexpr uint32_t kX16 = 2 * kRawX;              // two 64-wide halves
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kIdesc = idesc_f16_f32(2 * kTileN, MT);
-    static constexpr int kBars = 2 * kStages + 2 * kXStages + kOps + 5;
-    static constexpr int kSmem = 1024 + kStages * kQ8WBytes + kXStages * kX16 + kBars * 8 + 16;
+    static constexpr int kBars = 2 * kStages + 2 * kOps + 5;
+    static constexpr int kSmem = 1024 + kStages * (kQ8WBytes + kRawX) + kOps * kX16 + kBars * 8 + 16;
 };
 
-// Tiles (pairs of 128 channels x MT tokens) in bands of p.band token tiles:
+// Tiles (pairs of 128 channels x 128 tokens) in bands of p.band token tiles:
 // within a band, token tiles fastest, so that the CTAs of a wave share a
 // compact block of x and W in L2.
 __device__ __forceinline__ void tile_at(const Q8WideParams &p, int tile, int &np, int &mt)
@@ -80,24 +71,24 @@ __global__ void __launch_bounds__(WideShape::kThreads, 1) __cluster_dims__(kPair
 q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Q8WideParams p)
 {
     using Sh = WideShape;
-    constexpr int S = Sh::kStages, SX = Sh::kXStages, OPS = Sh::kOps;
+    constexpr int S = Sh::kStages, OPS = Sh::kOps;
     constexpr uint16_t kBoth = (1 << kPair) - 1;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sW = smem;
-    uint8_t *sX = sW + S * kQ8WBytes;
-    uint64_t *wfull = reinterpret_cast<uint64_t *>(sX + SX * Sh::kX16);
+    uint8_t *sXraw = sW + S * kQ8WBytes;
+    uint8_t *sX16 = sXraw + S * Sh::kRawX;
+    uint64_t *wfull = reinterpret_cast<uint64_t *>(sX16 + OPS * Sh::kX16);
     uint64_t *wempty = wfull + S;
     uint64_t *opfull = wempty + S;
-    uint64_t *afull = opfull + OPS;      // [2] accumulators
+    uint64_t *opempty = opfull + OPS;
+    uint64_t *afull = opempty + OPS;     // [2] accumulators
     uint64_t *aempty = afull + 2;        // [2]
     uint64_t *drain = aempty + 2;        // [1]
-    uint64_t *xfull = drain + 1;         // [SX]
-    uint64_t *done = xfull + SX;         // [SX]: unit j's MMAs are done, at [j % SX]
     // opfull and aempty are those of the first CTA, with arrivals from both;
-    // the MMA's commits arrive at both CTAs' done and afull
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + SX);
+    // the MMA's commits arrive at both CTAs' opempty and afull
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *flags = reinterpret_cast<volatile int *>(tmem_slot + 1);  // [0] abort
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -113,15 +104,13 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             mbar_init(&wfull[i], 1);
             mbar_init(&wempty[i], 4);
         }
-        for (int i = 0; i < OPS; ++i)
-            mbar_init(&opfull[i], kPair * (4 + 1));
+        for (int i = 0; i < OPS; ++i) {
+            mbar_init(&opfull[i], kPair * 4);
+            mbar_init(&opempty[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&afull[i], 1);
             mbar_init(&aempty[i], kPair * Sh::kEpiWarps);
-        }
-        for (int i = 0; i < SX; ++i) {
-            mbar_init(&xfull[i], 1);
-            mbar_init(&done[i], 1);
         }
         mbar_init(drain, 1);
         flags[0] = 0;
@@ -141,97 +130,66 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     constexpr uint32_t tmem_base = 0;
 
     if (warp == Sh::kTmaWarp) {
-        // ------------------------------------------------------------ TMA of W
+        // -------------------------------------------------------- TMA producer
         const bool leader = elect_one();
         const uint64_t pol = policy_evict_normal();
         int np, mt;
-        int ahead = 0, issued = 0;
         auto load_w = [&](int j, int kb) {
             if (leader) {
-                mbar_arrive_expect_tx(&wfull[j % S], kQ8WBytes);
+                mbar_arrive_expect_tx(&wfull[j % S], kQ8WBytes + Sh::kRawX);
                 tma_load_2d(sW + j % S * kQ8WBytes, &tmW, &wfull[j % S], kb * kQ8BlockK, (np * kPair + rank) * kTileN, pol);
             }
             __syncwarp();
         };
-        if (p.static_w) {                // weights may be requested before the wait for the previous kernel
-            tile_at(p, cluster, np, mt);
-            for (; ahead < S && ahead < p.nkb; ++ahead)
-                load_w(ahead, ahead);
-            issued = ahead;
-        } else {
-            pdl_wait();
-        }
+        auto load_x = [&](int j, int kb) {       // this CTA's half of the tokens
+            if (leader)
+                tma_load_2d(sXraw + j % S * Sh::kRawX, &tmX, &wfull[j % S], kb * kQ8BlockK, mt * MT + rank * kHalfTokens, pol);
+            __syncwarp();
+        };
+        tile_at(p, cluster, np, mt);
+        const int ahead = p.static_w ? min(S, p.nkb) : 0;
+        for (int j = 0; j < ahead; ++j)  // weights may be requested before the wait for the previous kernel
+            load_w(j, j);
+        pdl_wait();
         bool ok = true;
-        int j = 0;
+        int j = 0, issued = ahead;
         for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
             tile_at(p, tile, np, mt);
             for (int kb = 0; kb < p.nkb; ++kb, ++j) {
-                if (j < ahead)
-                    continue;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&wempty[j % S], ((j / S) & 1) ^ 1, p.timeout_ns, &flags[0]));
-                if (!ok) {
-                    q8_fail(p.err, &flags[0], kErrTimeoutProducer);
-                    break;
+                if (j >= ahead) {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&wempty[j % S], ((j / S) & 1) ^ 1, p.timeout_ns, &flags[0]));
+                    if (!ok)
+                        break;
+                    load_w(j, kb);
+                    issued = j + 1;
                 }
-                load_w(j, kb);
-                issued = j + 1;
+                load_x(j, kb);
             }
         }
+        if (!ok)
+            q8_fail(p.err, &flags[0], kErrTimeoutProducer);
         if (flags[0]) {                  // abort: let every copy land before exit
             volatile int never = 0;
             for (int k = 0; k < S && k < issued; ++k)
                 mbar_wait(&wfull[k], ((issued - 1 - k) / S) & 1, kDefaultTimeoutNs, &never);
         }
-    } else if (warp == Sh::kXWarp) {
-        // ------------------------------------------------------------ TMA of x
-        const bool leader = elect_one();
-        const uint64_t pol = policy_evict_normal();
-        pdl_wait();
-        int issued = 0;
-        bool ok = true;
-        for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
-            int np, mt;
-            tile_at(p, tile, np, mt);
-            const int m = mt * MT + rank * (MT / kPair);      // this CTA's half of the tokens
-            for (int kb = 0; kb < p.nkb; ++kb) {
-                const int sx = issued % SX;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&done[sx], ((issued / SX) & 1) ^ 1, p.timeout_ns, &flags[0]));
-                if (!ok) {
-                    q8_fail(p.err, &flags[0], kErrTimeoutProducer);
-                    break;
-                }
-                if (leader) {
-                    mbar_arrive_expect_tx(&xfull[sx], Sh::kX16);
-                    uint8_t *dst = sX + sx * Sh::kX16;
-                    tma_load_2d(dst, &tmX, &xfull[sx], kb * kQ8BlockK, m, pol);
-                    tma_load_2d(dst + Sh::kX16 / 2, &tmX, &xfull[sx], kb * kQ8BlockK + 64, m, pol);
-                }
-                __syncwarp();
-                ++issued;
-            }
-        }
-        if (flags[0]) {                  // abort: let every copy land before exit
-            volatile int never = 0;
-            for (int k = 0; k < SX && k < issued; ++k)
-                mbar_wait(&xfull[k], ((issued - 1 - k) / SX) & 1, kDefaultTimeoutNs, &never);
-        }
     } else if (warp == Sh::kMmaWarp) {
         // ---------------------------------------------------------- MMA issuer
         if (rank == 0) {
             const bool leader = elect_one();
-            const uint64_t x0 = smem_desc_kmajor_sw128(smem_u32(sX));
+            const uint64_t x0 = smem_desc_kmajor_sw128(smem_u32(sX16));
             int kb = 0, in_chunk = 0, chunk = 0;
             bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&opfull[0], 0, p.timeout_ns, &flags[0]));
-            // A round of the ring at a time, unrolled: the slots' addresses,
-            // descriptors and phases are then constants (worked out in a loop
-            // over single units they took longer than the MMAs).
-            for (int j0 = 0; ok && j0 < units; j0 += SX) {
+            // Two rounds of the operand buffers at a time, unrolled: their
+            // addresses, descriptors and phases are then constants (worked out in
+            // a loop over single units they took longer than the MMAs).
+            for (int j0 = 0; ok && j0 < units; j0 += 2 * OPS) {
 #pragma unroll
-                for (int u = 0; u < SX; ++u) {
+                for (int u = 0; u < 2 * OPS; ++u) {
                     if (!ok || j0 + u >= units)
                         break;
                     constexpr int kHalf = Sh::kX16 / 2 / 16;             // the second 64 k, in descriptor units
-                    const uint64_t bx = x0 + static_cast<uint64_t>(u * (Sh::kX16 / 16));
+                    const uint64_t bx = x0 + static_cast<uint64_t>((u % OPS) * (Sh::kX16 / 16));
                     const uint32_t a = tmem_base + 2 * MT + (u % OPS) * 64;
                     const int t = chunk & 1;
                     const uint32_t d = tmem_base + static_cast<uint32_t>(t * MT);
@@ -247,8 +205,6 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     }
                     const bool last = j0 + u + 1 == units;
                     uint64_t *next = &opfull[(u + 1) % OPS];
-                    constexpr int kRounds = SX / OPS;                    // of the operand buffers, in one of the ring
-                    static_assert(SX % OPS == 0 && kRounds % 2 == 0, "phases repeat with the ring");
                     const uint32_t next_phase = ((u + 1) / OPS) & 1;
                     const bool ready = __all_sync(0xFFFFFFFFu, last || mbar_try_wait(next, next_phase));
                     const bool end = ++kb == p.nkb || in_chunk == kExactBlocks - 1;
@@ -258,7 +214,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                             tc_mma_f16_ts_pair(d, a + 32 + 8 * kk, bx + kHalf + 2 * kk, Sh::kIdesc, 1u);
                         // nobody waits for the last units, and the peer may be gone by then
                         if (j0 + u + OPS < units)
-                            tc_commit_pair_multicast(&done[u], kBoth);
+                            tc_commit_pair_multicast(&opempty[u % OPS], kBoth);
                         if (end)
                             tc_commit_pair_multicast(&afull[t], kBoth);
                     }
@@ -278,37 +234,31 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 mbar_wait(drain, 0, kDefaultTimeoutNs, &never);
             }
         }
-    } else if (warp == Sh::kWatchWarp || warp < Sh::kFirstEpi) {
-        // --------------------------------------------- widen, and watch over x
-        const bool watch = warp == Sh::kWatchWarp;
+    } else if (warp < Sh::kFirstEpi) {
+        // --------------------------------------------------------------- widen
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * MT;
-        for (int j = watch ? 0 : (warp - Sh::kFirstWiden) >> 2; j < units; j += watch ? 1 : kWidenSets) {
-            const int b = j % OPS, before = j - OPS;
-            // The operand buffer first: once unit j - OPS is done, the units a
-            // ring ago have been consumed, so the ring slots' barriers are at
-            // most one phase behind and their parity says which.  (The warps run
-            // apart: by the parity alone, a slot still waiting for unit j - S
-            // looks like one that holds unit j.)
-            bool ok = before < 0 || mbar_wait(&done[before % SX], (before / SX) & 1, p.timeout_ns, &flags[0]);
-            ok = ok && (watch ? mbar_wait(&xfull[j % SX], (j / SX) & 1, p.timeout_ns, &flags[0])
-                              : mbar_wait(&wfull[j % S], (j / S) & 1, p.timeout_ns, &flags[0]));
+        const XPiece piece(quarter * 4 + (lane >> 3), lane & 7, kHalfTokens);
+        for (int j = (warp - Sh::kFirstWiden) >> 2; j < units; j += kWidenSets) {
+            const int sl = j % S, b = j % OPS;
+            // The operand buffer first: see skg_q8_split.cu
+            const bool ok = mbar_wait(&opempty[b], ((j / OPS) & 1) ^ 1, p.timeout_ns, &flags[0]) &&
+                            mbar_wait(&wfull[sl], (j / S) & 1, p.timeout_ns, &flags[0]);
             if (!__all_sync(0xFFFFFFFFu, ok)) {      // the whole warp goes on, or none of it
                 q8_fail(p.err, &flags[0], kErrTimeoutWiden);
                 break;
             }
-            if (!watch) {
-                tc_fence_after();
-                widen_row<8>(sW + j % S * kQ8WBytes, row, 0, lane_base + b * 64);
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&wempty[j % S]);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-            }
-            if (lane == 0)
+            tc_fence_after();
+            widen_row(sW + sl * kQ8WBytes, row, lane_base + b * 64);
+            piece.widen<kHalfTokens / 16>(sXraw + sl * Sh::kRawX, sX16 + b * Sh::kX16, 16);
+            fence_proxy_async_smem();
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&wempty[sl]);
                 mbar_arrive_cluster(map_shared_rank(smem_u32(&opfull[b]), 0));
+            }
         }
     } else {
         // ------------------------------------------------------------ epilogue
@@ -360,35 +310,6 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     }
 }
 
-// x as fp16, for the MMA's B operand.
-__global__ void __launch_bounds__(256) q8_widen_kernel(const uint4 *x, uint4 *out, size_t vectors)
-{
-    pdl_launch_dependents();
-    pdl_wait();
-    for (size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < vectors;
-         i += static_cast<size_t>(gridDim.x) * 256) {
-        uint32_t r[8];
-        widen16(__ldcg(x + i), r);
-        out[2 * i] = make_uint4(r[0], r[1], r[2], r[3]);
-        out[2 * i + 1] = make_uint4(r[4], r[5], r[6], r[7]);
-    }
-}
-
-cudaError_t launch_pdl(const void *f, unsigned grid, unsigned threads, size_t smem, void **args, cudaStream_t s)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelExC(&cfg, f, args);
-}
-
 } // namespace
 
 Q8TcShape q8_wide_shape()
@@ -406,26 +327,23 @@ cudaError_t launch_q8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const
         return e;
     if (dev >= kMaxDevices)
         return cudaErrorInvalidDevice;
-    const void *f = reinterpret_cast<const void *>(&q8_wide_kernel);
     if (__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE) == 0) {
-        e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, WideShape::kSmem);
+        e = cudaFuncSetAttribute(q8_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WideShape::kSmem);
         if (e != cudaSuccess)
             return e;
         __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
     }
-    void *args[] = {const_cast<CUtensorMap *>(&tmW), const_cast<CUtensorMap *>(&tmX), const_cast<Q8WideParams *>(&p)};
-    return launch_pdl(f, static_cast<unsigned>(grid), WideShape::kThreads, WideShape::kSmem, args, s);
-}
-
-cudaError_t launch_q8_widen(const int8_t *x, void *out, size_t elements, int num_sms, cudaStream_t s)
-{
-    const uint4 *src = reinterpret_cast<const uint4 *>(x);
-    uint4 *dst = static_cast<uint4 *>(out);
-    size_t vectors = elements / 16;
-    const size_t blocks = (vectors + 255) / 256;
-    const unsigned grid = static_cast<unsigned>(std::min<size_t>(blocks, static_cast<size_t>(num_sms) * 8));
-    void *args[] = {&src, &dst, &vectors};
-    return launch_pdl(reinterpret_cast<const void *>(&q8_widen_kernel), grid, 256, 0, args, s);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(WideShape::kThreads);
+    cfg.dynamicSmemBytes = WideShape::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, q8_wide_kernel, tmW, tmX, p);
 }
 
 } // namespace skg

@@ -122,7 +122,7 @@ def test_query_describes_a_launch_that_covers_every_tile(M, N, K):
         assert d["workspace_bytes"] == d["grid"] * put_away * d["m_tile"] * 512
     else:
         assert d["split_k"] == 1 and d["grid"] == 2 * min(d["tiles"], SMS // 2)
-        assert d["workspace_bytes"] == 2 * M * K
+        assert d["workspace_bytes"] == 0
 
 
 @pytest.mark.parametrize("M", [1, 8, 9, 16])
@@ -139,7 +139,7 @@ def test_streaming_launch_fills_as_few_slots_as_hold_it(M, N):
 
 @pytest.mark.parametrize("M,N,K,kernel", [
     (17, 7168, 7168, "q8_split"), (64, 7168, 16384, "q8_split"), (64, 28672, 8192, "q8_wide"), (128, 384, 7168, "q8_split"),
-    (128, 7168, 7168, "q8_wide"), (256, 4096, 4096, "q8_split"), (333, 5001, 4112, "q8_wide"), (1000, 4096, 4096, "q8_wide"),
+    (128, 7168, 7168, "q8_wide"), (256, 4096, 4096, "q8_wide"), (128, 4096, 4096, "q8_split"), (333, 5001, 4112, "q8_wide"), (1000, 4096, 4096, "q8_wide"),
     (4096, 12288, 7168, "q8_wide")])
 def test_batches_take_the_kernel_measured_faster(M, N, K, kernel):
     """Few tiles: K split over clusters; many: whole tiles."""
