@@ -257,8 +257,8 @@ q8_rows_kernel(const Q8RowParams p)
     constexpr int NV = VALUES / 8;
     __shared__ float sums[2][32];
     __shared__ uint32_t maxima[32];
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const size_t row = WARP ? static_cast<size_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     if (WARP && row >= static_cast<size_t>(p.M))
         return;
@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(kLongThreads) q8_long_rows_kernel(const Q8RowP
 {
     __shared__ float sums[2][32];
     __shared__ uint32_t maxima[32];
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const size_t row = blockIdx.x;
     float rms = 1.0f;
     if (NORM) {

@@ -178,7 +178,6 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         fence_mbar_init();
     }
     __syncthreads();
-    pdl_launch_dependents();
     uint32_t tmem_base = 0;
     if (warp != Sh::kTmaWarp) {          // the TMA warp needs no TMEM: its first copies leave at once
         if (warp == Sh::kMmaWarp) {
@@ -211,6 +210,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 load_w(j);
             if (p.static_w)              // weights may be requested before the wait for the previous kernel
                 pdl_wait();
+            pdl_launch_dependents();     // not sooner: see skg_q8_stream.cu
             for (int j = 0; j < first; ++j)
                 load_x(j);
             int j = first;

@@ -64,7 +64,6 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) q8_stream_kernel(const Q8Lin
     static_assert(kFlush % DEPTH == 0, "the fp32 sums are moved at whole rounds");
     __shared__ int part[WARPS][RG * 16][NT * 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    pdl_launch_dependents();
     const int n0 = static_cast<int>(blockIdx.x) * (16 * RG);
     const int steps = (p.K + kStepK - 1) / kStepK;
     const int s0 = warp * steps / WARPS, s1 = (warp + 1) * steps / WARPS;
@@ -104,6 +103,9 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) q8_stream_kernel(const Q8Lin
         load_w(s0 + d, d);
     if (static_w)
         pdl_wait();                      // x, scales, residual and y only from here on
+    // The next kernel may start once the one before this is done, not sooner: a
+    // chain of kernels that all start early fills the SMs with waiting CTAs.
+    pdl_launch_dependents();
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
         load_x(s0 + d, d);

@@ -117,7 +117,6 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         fence_mbar_init();
     }
     __syncthreads();
-    pdl_launch_dependents();
     if (warp == Sh::kMmaWarp) {
         tmem_alloc_pair(tmem_slot, Sh::kTmemCols);
         tmem_relinquish_pair();
@@ -151,6 +150,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         for (int j = 0; j < ahead; ++j)  // weights may be requested before the wait for the previous kernel
             load_w(j, j);
         pdl_wait();
+        pdl_launch_dependents();         // not sooner: see skg_q8_stream.cu
         bool ok = true;
         int j = 0, issued = ahead;
         for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {

@@ -528,3 +528,37 @@ def test_bounded_wait_is_reported_and_the_plan_recovers():
     assert R.same_bits(c.y, want)
     plan.check()
     plan.close()
+
+
+@pytest.mark.parametrize("M", [1, 20, 100])
+def test_mlp_block(M):
+    """The block of q8_block.py, each stage from what the one before left."""
+    from projection_gemm_gb300.q8_block import Q8MLP
+    H, F, E = 512, 768, 48
+    g = rng(15, M)
+    x, r, gamma = normal(g, M, H).cuda(), normal(g, M, H).cuda(), (normal(g, H, std=0.2) + 1).cuda()
+    W1, W2 = normal(g, 2 * F, H, std=H ** -0.5).cuda(), normal(g, H, F, std=F ** -0.5).cuda()
+    Wr = normal(g, E, H, std=H ** -0.5).cuda() if M <= 64 else None
+    b = Q8MLP(M, gamma, W1, W2, Wr)
+    R.check_rows(W1.double(), b.gate_up, b.gate_up_scale, R.row_error(H))
+    R.check_rows(W2.double(), b.down, b.down_scale, R.row_error(F))
+    out, scores = b.run(x, r)
+    b.check()
+    v, _ = R.norm_rows(x, r, gamma, 1e-6)
+    R.check_rows(v, b.q, b.scale, R.row_error(H))
+    assert torch.equal(b.h, (x.float() + r.float()).to(torch.bfloat16))
+    assert R.same_bits(b.u, R.linear(b.q, b.scale, b.gate_up, b.gate_up_scale, None, "bf16"))
+    R.check_rows(R.gated_rows(b.u[:, F:], b.u[:, :F]), b.a, b.a_scale, R.row_error(F, b.u[:, :F]))
+    assert R.same_bits(out, R.linear(b.a, b.a_scale, b.down, b.down_scale, b.h, "bf16_residual"))
+    if Wr is not None:
+        want = b.v.double() @ Wr.double().t()
+        s1 = b.v.double().abs() @ Wr.double().abs().t()
+        assert bool(((scores.double() - want).abs() <= 2.0 ** -16 * s1 + 2.0 ** -23 * want.abs()).all())
+    # And the whole against the unquantised block.  Rounding to a step of max / 127 is off by step / sqrt(12):
+    # for normal rows (max 4 rms) 0.9% of the rms, for a's (products of two, max 12 rms) 2.7%.  W1 and v give u
+    # 1.3%, which enters a about twice; with a's and W2's own that is 3.4%; half as much again is allowed.
+    u = (v @ W1.double().t())
+    ref = (u[:, F:] * u[:, :F] / (1 + torch.exp(-u[:, :F]))) @ W2.double().t()
+    off = (out.double() - (x.double() + r.double()) - ref).norm() / ref.norm()
+    assert float(off) < 0.05
+    b.close()
