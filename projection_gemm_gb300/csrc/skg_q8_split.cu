@@ -316,7 +316,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         int *sums = reinterpret_cast<int *>(smem) + col0 * kTileN + row;
         constexpr int kStep = Sh::kXWarps * 4;           // tokens that a set takes at a time
         static_assert(kStep % 8 == 0, "the swizzle repeats every 8 rows");
-        const XPiece piece(ew % Sh::kXWarps * 4 + (lane >> 3), lane & 7, MT);
+        const XPiece piece(ew % Sh::kXWarps * 4, lane, MT);
         bool ok = true;
         int put = 0;                     // accumulations put away
         auto put_away = [&] {

@@ -238,7 +238,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         // --------------------------------------------------------------- widen
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * MT;
-        const XPiece piece(quarter * 4 + (lane >> 3), lane & 7, kHalfTokens);
+        const XPiece piece(quarter * 4, lane, kHalfTokens);
         for (int j = (warp - Sh::kFirstWiden) >> 2; j < units; j += kWidenSets) {
             const int sl = j % S, b = j % OPS;
             // The operand buffer first: see skg_q8_split.cu
