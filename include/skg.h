@@ -468,7 +468,8 @@ typedef enum skg_q8_kernel_kind {
     SKG_Q8_KERNEL_STREAM = 1,   /* M <= 16: W streams into registers, warp-level fp16 MMA, exact */
     SKG_Q8_KERNEL_SPLIT = 2,    /* M > 16, few tiles: TMA + tcgen05 on integers widened to fp16, exact; K split
                                    over the CTAs of a cluster, joined in shared memory */
-    SKG_Q8_KERNEL_WIDE = 3      /* M > 16, many tiles: the same arithmetic over whole tiles, by pairs of CTAs */
+    SKG_Q8_KERNEL_WIDE = 3      /* M > 16, many tiles: the same arithmetic by pairs of CTAs, over whole tiles or
+                                   with K split over the pairs of a cluster */
 } skg_q8_kernel_kind;
 
 /* What an 8-bit plan will launch. */
@@ -479,7 +480,7 @@ typedef struct skg_q8_plan_desc {
     int m_tile;                 /* tokens per tile (STREAM: 8 or 16; SPLIT: 32 or 64; WIDE: 128) */
     int n_tile;                 /* output channels per tile (STREAM: 16, 32 or 48; SPLIT: 128; WIDE: 256, a pair's) */
     int tiles;                  /* output tiles */
-    int split_k;                /* SPLIT: CTAs of a cluster, sharing a tile's K (1..8); else 1 */
+    int split_k;                /* parts of a tile's K: CTAs of a cluster (SPLIT: 1..8) or pairs of them (WIDE: 1..4); STREAM: 1 */
     int grid, threads, smem_bytes, stages, ctas_per_sm;
     size_t workspace_bytes;     /* SPLIT: sums put away where a CTA has more than 2048 k; else 0 */
 } skg_q8_plan_desc;
@@ -528,8 +529,8 @@ SKG_API skg_status skg_q8_run(skg_q8_plan_t plan, const void *x, const float *x_
 /*
  * skg_q8_plan_force -- override of the kernel choice (tests and measurements):
  * kind (an skg_q8_kernel_kind, 0 keeps; STREAM: M <= 16), m_tile (SPLIT: 32, 64;
- * WIDE: 128; 0 = chosen) and split_k (SPLIT: 1..8, no finer than K / 128;
- * 0 = chosen).  Results do not change.  A larger workspace is allocated where
+ * WIDE: 128; 0 = chosen) and split_k (SPLIT: 1..8, WIDE: 1..4, no finer than
+ * K / 128; 0 = chosen).  Results do not change.  A larger workspace is allocated where
  * needed and the old one kept until the plan is destroyed, as by skg_plan_force.
  * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_CUDA.
  */

@@ -57,29 +57,66 @@ constexpr int kStreamMaxM = 16;
 
 int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
+// Clusters resident at once on 152 SMs, by what a cluster's tile has its K
+// split into (cudaOccupancyMaxActiveClusters; a cluster stays within one GPC):
+// CTAs of the split kernel, two to an SM; pairs of the wide kernel, one CTA to
+// an SM.  43 tiles split in 7 are 301 CTAs, but 38 clusters at a time.
+constexpr int kSplitResident[] = {0, 304, 152, 97, 74, 58, 46, 38, 36};
+constexpr int kWideResident[] = {0, 76, 36, 23, 15};
+static_assert(sizeof(kWideResident) / sizeof(int) == kQ8WideMaxSplit + 1, "a count for each split");
+
+long long resident(int on_152, int num_sms) { return std::max(1ll, static_cast<long long>(on_152) * num_sms / 152); }
+
 // CTAs of a cluster of the split kernel: as many as one wave holds (at most the
 // portable 8), none without a unit of K.
-int choose_split(int tiles, int nkb, int slots)
+int choose_split(long long tiles, int nkb, int num_sms)
 {
-    return std::max(1, std::min({8, nkb, slots / std::max(1, tiles)}));
+    int s = std::min(8, nkb);
+    while (s > 1 && tiles > resident(kSplitResident[s], num_sms))
+        --s;
+    return s;
 }
 
-// The split or the wide kernel, by their times as measured (us): a CTA of the
-// split kernel takes 0.93 a unit of 128 k (0.69 with tiles of 32 tokens) and 4
-// for its ends, in as many waves as its grid needs; the wide one 0.40 a unit of
-// a tile and 5.  Measured against this rule, split then wide: 24 x 28672 x 8192
-// 46 and 57, 64 x 28672 x 8192 59 and 58, 128 x 384 x 7168 7.6 and 26, 128 x
-// 7168 x 7168 29.8 and 27.3, 256 x 4096 x 4096 18.7 and 17.8, 1000 x 4096 x 4096
+// The kernels' times (us) as measured: a CTA of the split kernel takes 0.93 a
+// unit of 128 k (0.69 with tiles of 32 tokens) and 4 for its ends, in as many
+// waves as its grid needs; a pair of the wide one 0.39 a unit and 5, or 8.5
+// where K is split and the cluster's pairs join their sums.
+double split_us(long long tiles, int nkb, int m_tile, int split, int num_sms)
+{
+    const long long slots = resident(kSplitResident[split], num_sms);
+    return 4.0 + (m_tile == 32 ? 0.69 : 0.93) * static_cast<double>((tiles + slots - 1) / slots * ceil_div(nkb, split));
+}
+
+double wide_us(long long tiles, int nkb, int split, int num_sms)
+{
+    const long long slots = resident(kWideResident[split], num_sms);
+    return (split > 1 ? 8.5 : 5.0) + 0.39 * static_cast<double>((tiles + slots - 1) / slots * ceil_div(nkb, split));
+}
+
+// Pairs that share a tile's K in the wide kernel: where one wave holds them
+// all, the fastest.  Measured with 1, 2, 3 and 4: 128 x 7168 x 7168 26.3, 19.7,
+// 30.6, 29.8; 65 x 7168 x 16384 53, 31.9, 47, 41; 128 x 2048 x 4096 17.1, 12.8,
+// 10.9, 11.3; 100 x 8192 x 2048 11.8, 11.9, 20.3, 29.2.
+int choose_wide_split(long long tiles, int nkb, int num_sms)
+{
+    int best = 1;
+    for (int s = 2; s <= std::min(kQ8WideMaxSplit, nkb); ++s)
+        if (tiles <= resident(kWideResident[s], num_sms) && wide_us(tiles, nkb, s, num_sms) < wide_us(tiles, nkb, best, num_sms))
+            best = s;
+    return best;
+}
+
+// The split or the wide kernel.  Measured, split then wide: 24 x 28672 x 8192
+// 46 and 57, 64 x 28672 x 8192 59 and 58, 128 x 1024 x 7168 9.8 and 12.3, 128 x
+// 7168 x 7168 26.9 and 19.7, 256 x 4096 x 4096 17.4 and 15.3, 1000 x 4096 x 4096
 // 58 and 32; it is furthest off at 1000 x 1024 x 1024, 9.6 and 8.4.
 bool prefer_split(const skg_q8_plan_desc &d, int num_sms)
 {
     const int m_tile = d.M <= 32 ? 32 : 64, nkb = ceil_div(d.K, kQ8BlockK), n_tiles = ceil_div(d.N, kTileN);
-    const long long slots = 2ll * num_sms, pairs = std::max(1, num_sms / 2);
     const long long st = static_cast<long long>(n_tiles) * ceil_div(d.M, m_tile);
     const long long wt = static_cast<long long>(ceil_div(n_tiles, 2)) * ceil_div(d.M, q8_wide_shape().m_tile);
-    const int split = st > slots ? 1 : choose_split(static_cast<int>(st), nkb, static_cast<int>(slots));
-    const double units = static_cast<double>((st * split + slots - 1) / slots) * ceil_div(nkb, split);
-    return 4.0 + (m_tile == 32 ? 0.69 : 0.93) * units <= 5.0 + 0.40 * static_cast<double>((wt + pairs - 1) / pairs) * nkb;
+    return split_us(st, nkb, m_tile, choose_split(st, nkb, num_sms), num_sms) <=
+           wide_us(wt, nkb, choose_wide_split(wt, nkb, num_sms), num_sms);
 }
 
 // Accumulations of 1024 k that a CTA of the split kernel puts away: all but two.
@@ -126,10 +163,11 @@ skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int split, int
     d->stages = sh.stages;
     d->ctas_per_sm = sh.ctas_per_sm;
     if (wide) {
-        d->grid = 2 * std::min(d->tiles, std::max(1, num_sms / 2));
+        d->split_k = split ? std::min(split, nkb) : choose_wide_split(tiles, nkb, num_sms);
+        d->grid = 2 * d->split_k * (d->split_k > 1 ? d->tiles : std::min(d->tiles, std::max(1, num_sms / 2)));
         return SKG_OK;
     }
-    d->split_k = split ? std::min(split, nkb) : choose_split(d->tiles, nkb, num_sms * sh.ctas_per_sm);
+    d->split_k = split ? std::min(split, nkb) : choose_split(d->tiles, nkb, num_sms);
     d->grid = d->tiles * d->split_k;
     d->workspace_bytes = static_cast<size_t>(d->grid) * carried(*d) * m_tile * kTileN * 4;
     return SKG_OK;
@@ -291,9 +329,9 @@ skg_status skg_q8_plan_force(skg_q8_plan_t p, int kind, int m_tile, int split_k)
                          (k == SKG_Q8_KERNEL_WIDE && m_tile == q8_wide_shape().m_tile);
     if (!tile_ok)
         return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile %d is none of this kernel's", who, m_tile);
-    if (split_k < 0 || split_k > 8 || (split_k && k != SKG_Q8_KERNEL_SPLIT))
-        return set_error(SKG_ERR_INVALID_ARG, "%s: split_k must be in [1, 8], for the split kernel alone (got %d)", who,
-                         split_k);
+    const int most = k == SKG_Q8_KERNEL_SPLIT ? 8 : k == SKG_Q8_KERNEL_WIDE ? kQ8WideMaxSplit : 0;
+    if (split_k < 0 || split_k > most)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: this kernel takes a split_k of at most %d (got %d)", who, most, split_k);
     skg_status st = fill_launch(&d, k, m_tile, split_k, p->num_sms, who);
     if (st != SKG_OK)
         return st;
@@ -350,6 +388,8 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
         return launched(launch_q8_stream(g, {d.n_tile / 16, d.threads / 32, d.ctas_per_sm}, d.static_weights != 0, s), who);
 
     const int nkb = ceil_div(d.K, kQ8BlockK), m_tiles = ceil_div(d.M, d.m_tile);
+    const int vec4 = d.N % 4 == 0 && aligned(w_scale, 16) && aligned(residual, 8) &&
+                     aligned(y, d.epilogue == SKG_EPI_FP32 ? 16 : 8);
     CUtensorMap tmW, tmX;
     skg_status st = encode_tiled_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, d.N, d.K, kTileN);
     if (st != SKG_OK)
@@ -367,8 +407,7 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
         t.m_tiles = m_tiles;
         t.split = d.split_k;
         t.static_w = d.static_weights;
-        t.vec4 = d.N % 4 == 0 && aligned(w_scale, 16) && aligned(residual, 8) &&
-                 aligned(y, d.epilogue == SKG_EPI_FP32 ? 16 : 8);
+        t.vec4 = vec4;
         t.timeout_ns = kDefaultTimeoutNs;
         return launched(launch_q8_split(tmW, tmX, t, d.m_tile, d.grid, s), who);
     }
@@ -383,6 +422,8 @@ skg_status skg_q8_run(skg_q8_plan_t p, const void *x, const float *x_scale, cons
     t.m_tiles = m_tiles;
     t.tiles = d.tiles;
     t.band = kQ8Band;
+    t.split = d.split_k;
+    t.vec4 = vec4;
     t.static_w = d.static_weights;
     t.timeout_ns = kDefaultTimeoutNs;
     return launched(launch_q8_wide(tmW, tmX, t, d.grid, s), who);

@@ -50,11 +50,13 @@ struct Q8SplitParams {
 };
 
 // The wide kernel's launch: tiles of 2 x 128 channels x m_tile tokens, one per
-// pair of CTAs at a time.
+// cluster of `split` pairs of CTAs at a time, each pair with its part of K.
+constexpr int kQ8WideMaxSplit = 4;         // 8 CTAs, the portable cluster size
 struct Q8WideParams {
     Q8LinearParams g;
     unsigned *err;
-    int nkb, n_pairs, m_tiles, tiles, band, static_w;
+    int nkb, n_pairs, m_tiles, tiles, band, split, static_w;
+    int vec4;                 // as in Q8SplitParams
     unsigned long long timeout_ns;
 };
 

@@ -1,5 +1,6 @@
 // skg_q8_tc_common.cuh -- device code shared by the 8-bit path's tcgen05 kernels:
-// widening, the epilogue's reading of accumulators and its stores.  Included inside namespace skg's anonymous namespace.
+// widening, the epilogue's reading of accumulators, its stores, and the join of a
+// split K.  Included inside namespace skg's anonymous namespace.
 #pragma once
 
 constexpr int kQ8BlockK = 128;                       // k of one unit: 128 bytes of a W row
@@ -141,4 +142,112 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, int (&v)[NC])
         asm volatile("" : "+r"(r[c >> 3][c & 7]));
         v[c] = __float2int_rn(__uint_as_float(r[c >> 3][c & 7]));
     }
+}
+
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr)
+{
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// What four neighbouring outputs (channels n.., token m) need besides their sums.
+struct Four {
+    float xs, ws[4];
+    uint16_t res[4];
+};
+
+__device__ __forceinline__ Four load_four(const Q8LinearParams &g, int m, int n, bool vec4)
+{
+    Four f;
+    f.xs = __ldcg(g.x_scale + m);
+    const size_t o = static_cast<size_t>(m) * g.N + n;
+    const bool res = g.epilogue == SKG_EPI_BF16_RESIDUAL;
+    if (vec4) {                          // n is a multiple of 4 and N too
+        const float4 w = n < g.N ? __ldcg(reinterpret_cast<const float4 *>(g.w_scale + n)) : make_float4(0, 0, 0, 0);
+        f.ws[0] = w.x, f.ws[1] = w.y, f.ws[2] = w.z, f.ws[3] = w.w;
+        const uint2 r = res && n < g.N ? __ldcg(reinterpret_cast<const uint2 *>(g.res + o)) : make_uint2(0, 0);
+        f.res[0] = r.x & 0xFFFF, f.res[1] = r.x >> 16, f.res[2] = r.y & 0xFFFF, f.res[3] = r.y >> 16;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f.ws[i] = n + i < g.N ? __ldcg(g.w_scale + n + i) : 0.0f;
+            f.res[i] = res && n + i < g.N ? __ldcg(g.res + o + i) : 0;
+        }
+    }
+    return f;
+}
+
+__device__ __forceinline__ void store_four(const Q8LinearParams &g, int m, int n, bool vec4, const Four &f, const int4 &sum)
+{
+    const int s[4] = {sum.x, sum.y, sum.z, sum.w};
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = q8_scaled(s[i], f.xs, f.ws[i]);
+        if (g.epilogue == SKG_EPI_BF16_RESIDUAL)
+            v[i] = __fadd_rn(v[i], bf16_to_f32(f.res[i]));
+    }
+    const size_t o = static_cast<size_t>(m) * g.N + n;
+    if (g.epilogue == SKG_EPI_FP32) {
+        float *y = static_cast<float *>(g.y) + o;
+        if (vec4 && n < g.N) {
+            *reinterpret_cast<float4 *>(y) = make_float4(v[0], v[1], v[2], v[3]);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < g.N)
+                y[i] = v[i];
+        return;
+    }
+    uint16_t *y = static_cast<uint16_t *>(g.y) + o;
+    if (vec4 && n < g.N) {
+        *reinterpret_cast<uint2 *>(y) = make_uint2(f32_to_bf16(v[0]) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16,
+                                                   f32_to_bf16(v[2]) | static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < g.N)
+            y[i] = f32_to_bf16(v[i]);
+}
+
+// The end of a tile whose K is split over `split` CTAs of the cluster, the
+// ranks first, first + step, ...: each has left its sums [token][128 channels]
+// as int32 at `smem`; this CTA, the part-th of them, adds up and stores its
+// share of the tokens, four channels a thread.  Called by whole CTAs, all of
+// the cluster's.
+template <int MAX_SPLIT, int THREADS>
+__device__ __forceinline__ void join_and_store(const Q8LinearParams &g, uint32_t smem, int m0, int n0, int tokens, int split,
+                                               int part, int step, int first, bool vec4)
+{
+    const int t1 = (part + 1) * tokens / split, n = n0 + (static_cast<int>(threadIdx.x) & 31) * 4;
+    int m = part * tokens / split + static_cast<int>(threadIdx.x >> 5);
+    Four f = {};
+    pdl_wait();
+    if (m < t1)
+        f = load_four(g, m0 + m, n, vec4);           // on its way while the cluster meets
+    cluster_sync();
+    const uint32_t base = smem + (threadIdx.x & 31) * 16;
+    while (m < t1) {
+        int4 sum = make_int4(0, 0, 0, 0);
+        int4 v[MAX_SPLIT];
+#pragma unroll
+        for (int r = 0; r < MAX_SPLIT; ++r)
+            v[r] = r < split ? ld_cluster_v4(map_shared_rank(base + m * (kTileN * 4), first + r * step)) : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < MAX_SPLIT; ++r) {
+            sum.x += v[r].x;
+            sum.y += v[r].y;
+            sum.z += v[r].z;
+            sum.w += v[r].w;
+        }
+        store_four(g, m0 + m, n, vec4, f, sum);
+        m += THREADS / 32;
+        if (m < t1)
+            f = load_four(g, m0 + m, n, vec4);
+    }
+    cluster_sync();                      // no CTA leaves while a peer reads its sums
 }

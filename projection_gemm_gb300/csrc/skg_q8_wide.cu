@@ -34,7 +34,7 @@ namespace {
 
 #include "skg_q8_tc_common.cuh"
 
-constexpr int kPair = 2;                             // CTAs of a cluster
+constexpr int kPair = 2;                             // CTAs that work as one
 constexpr int MT = 128;                              // tokens of a tile: the MMA's N
 constexpr int kHalfTokens = MT / kPair;              // of which a CTA holds these
 
@@ -51,6 +51,7 @@ struct WideShape {
     static constexpr uint32_t kX16 = 2 * kRawX;              // two 64-wide halves
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kIdesc = idesc_f16_f32(2 * kTileN, MT);
+    static_assert(kStages * kQ8WBytes >= MT * kTileN * 4, "the sums take the ring's place");
     static constexpr int kBars = 2 * kStages + 2 * kOps + 5;
     static constexpr int kSmem = 1024 + kStages * (kQ8WBytes + kRawX) + kOps * kX16 + kBars * 8 + 16;
 };
@@ -67,12 +68,11 @@ __device__ __forceinline__ void tile_at(const Q8WideParams &p, int tile, int &np
     mt = b * p.band + r - np * wide;
 }
 
-__global__ void __launch_bounds__(WideShape::kThreads, 1) __cluster_dims__(kPair, 1, 1)
+__global__ void __launch_bounds__(WideShape::kThreads, 1)
 q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Q8WideParams p)
 {
     using Sh = WideShape;
     constexpr int S = Sh::kStages, OPS = Sh::kOps;
-    constexpr uint16_t kBoth = (1 << kPair) - 1;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -92,10 +92,15 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     volatile int *flags = reinterpret_cast<volatile int *>(tmem_slot + 1);  // [0] abort
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(blockIdx.x) % kPair, cluster = static_cast<int>(blockIdx.x) / kPair;
-    const int clusters = static_cast<int>(gridDim.x) / kPair;
+    // A cluster is p.split pairs, each with its part of K.  With more than one
+    // there are as many clusters as tiles.
+    const int rank = static_cast<int>(blockIdx.x) % kPair, pair = static_cast<int>(blockIdx.x) / kPair;
+    const int part = pair % p.split, cluster = pair / p.split, first = part * kPair;
+    const int clusters = static_cast<int>(gridDim.x) / (kPair * p.split);
+    const uint16_t both = static_cast<uint16_t>(((1 << kPair) - 1) << first);        // the pair's ranks in the cluster
     const int my_tiles = (p.tiles - cluster + clusters - 1) / clusters;
-    const int units = my_tiles * p.nkb;
+    const int kb0 = part * p.nkb / p.split, nkb = (part + 1) * p.nkb / p.split - kb0;
+    const int units = my_tiles * nkb;
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tmW);
@@ -136,17 +141,17 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         auto load_w = [&](int j, int kb) {
             if (leader) {
                 mbar_arrive_expect_tx(&wfull[j % S], kQ8WBytes + Sh::kRawX);
-                tma_load_2d(sW + j % S * kQ8WBytes, &tmW, &wfull[j % S], kb * kQ8BlockK, (np * kPair + rank) * kTileN, pol);
+                tma_load_2d(sW + j % S * kQ8WBytes, &tmW, &wfull[j % S], (kb0 + kb) * kQ8BlockK, (np * kPair + rank) * kTileN, pol);
             }
             __syncwarp();
         };
         auto load_x = [&](int j, int kb) {       // this CTA's half of the tokens
             if (leader)
-                tma_load_2d(sXraw + j % S * Sh::kRawX, &tmX, &wfull[j % S], kb * kQ8BlockK, mt * MT + rank * kHalfTokens, pol);
+                tma_load_2d(sXraw + j % S * Sh::kRawX, &tmX, &wfull[j % S], (kb0 + kb) * kQ8BlockK, mt * MT + rank * kHalfTokens, pol);
             __syncwarp();
         };
         tile_at(p, cluster, np, mt);
-        const int ahead = p.static_w ? min(S, p.nkb) : 0;
+        const int ahead = p.static_w ? min(S, nkb) : 0;
         for (int j = 0; j < ahead; ++j)  // weights may be requested before the wait for the previous kernel
             load_w(j, j);
         pdl_wait();
@@ -155,7 +160,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         int j = 0, issued = ahead;
         for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
             tile_at(p, tile, np, mt);
-            for (int kb = 0; kb < p.nkb; ++kb, ++j) {
+            for (int kb = 0; kb < nkb; ++kb, ++j) {
                 if (j >= ahead) {
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&wempty[j % S], ((j / S) & 1) ^ 1, p.timeout_ns, &flags[0]));
                     if (!ok)
@@ -207,20 +212,20 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     uint64_t *next = &opfull[(u + 1) % OPS];
                     const uint32_t next_phase = ((u + 1) / OPS) & 1;
                     const bool ready = __all_sync(0xFFFFFFFFu, last || mbar_try_wait(next, next_phase));
-                    const bool end = ++kb == p.nkb || in_chunk == kExactBlocks - 1;
+                    const bool end = ++kb == nkb || in_chunk == kExactBlocks - 1;
                     if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             tc_mma_f16_ts_pair(d, a + 32 + 8 * kk, bx + kHalf + 2 * kk, Sh::kIdesc, 1u);
                         // nobody waits for the last units, and the peer may be gone by then
                         if (j0 + u + OPS < units)
-                            tc_commit_pair_multicast(&opempty[u % OPS], kBoth);
+                            tc_commit_pair_multicast(&opempty[u % OPS], both);
                         if (end)
-                            tc_commit_pair_multicast(&afull[t], kBoth);
+                            tc_commit_pair_multicast(&afull[t], both);
                     }
                     in_chunk = end ? 0 : in_chunk + 1;
                     chunk += end;
-                    kb = kb == p.nkb ? 0 : kb;
+                    kb = kb == nkb ? 0 : kb;
                     if (!ready)
                         ok = __all_sync(0xFFFFFFFFu, mbar_wait(next, next_phase, p.timeout_ns, &flags[0]));
                 }
@@ -257,7 +262,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&wempty[sl]);
-                mbar_arrive_cluster(map_shared_rank(smem_u32(&opfull[b]), 0));
+                mbar_arrive_cluster(map_shared_rank(smem_u32(&opfull[b]), first));
             }
         }
     } else {
@@ -275,7 +280,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             const int n = (np * kPair + rank) * kTileN + row;
             const Scales sc = load_scales(p.g, mt * MT + col0, n);
             int acc[NC];
-            for (int kb = 0; kb < p.nkb; kb += kExactBlocks, ++chunk) {
+            for (int kb = 0; kb < nkb; kb += kExactBlocks, ++chunk) {
                 const int t = chunk & 1;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(&afull[t], (chunk >> 1) & 1, p.timeout_ns, &flags[0]));
                 if (!ok) {
@@ -294,16 +299,29 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(map_shared_rank(smem_u32(&aempty[t]), 0));
+                    mbar_arrive_cluster(map_shared_rank(smem_u32(&aempty[t]), first));
             }
-            if (ok)
+            if (ok && p.split == 1) {
                 store_columns(p.g, mt * MT + col0, n, sc, acc);
+            } else if (ok) {
+                // in the ring's place: the last MMA has read its operands
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    reinterpret_cast<int *>(smem)[(col0 + c) * kTileN + row] = acc[c];
+            }
         }
     }
 
     __syncwarp();
     tc_fence_before();
-    cluster_sync();                      // no CTA leaves while its peer may still send to it
+    if (p.split == 1) {
+        cluster_sync();                  // no CTA leaves while its peer may still send to it
+    } else {
+        int np, mt;
+        tile_at(p, cluster, np, mt);
+        join_and_store<kQ8WideMaxSplit, Sh::kThreads>(p.g, smem_u32(smem), mt * MT, (np * kPair + rank) * kTileN,
+                                                      min(MT, p.g.M - mt * MT), p.split, part, kPair, rank, p.vec4 != 0);
+    }
     if (warp == Sh::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, Sh::kTmemCols);
@@ -338,11 +356,14 @@ cudaError_t launch_q8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const
     cfg.blockDim = dim3(WideShape::kThreads);
     cfg.dynamicSmemBytes = WideShape::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(kPair * p.split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, q8_wide_kernel, tmW, tmX, p);
 }
 

@@ -121,7 +121,9 @@ def test_query_describes_a_launch_that_covers_every_tile(M, N, K):
         put_away = max(0, -(-(-(-nkb // d["split_k"])) // 8) - 2)
         assert d["workspace_bytes"] == d["grid"] * put_away * d["m_tile"] * 512
     else:
-        assert d["split_k"] == 1 and d["grid"] == 2 * min(d["tiles"], SMS // 2)
+        assert 1 <= d["split_k"] <= min(4, nkb)
+        assert d["grid"] == 2 * (min(d["tiles"], SMS // 2) if d["split_k"] == 1 else d["split_k"] * d["tiles"])
+        assert d["grid"] <= SMS
         assert d["workspace_bytes"] == 0
 
 
@@ -140,7 +142,17 @@ def test_streaming_launch_fills_as_few_slots_as_hold_it(M, N):
 @pytest.mark.parametrize("M,N,K,kernel", [
     (17, 7168, 7168, "q8_split"), (64, 7168, 16384, "q8_split"), (64, 28672, 8192, "q8_wide"), (128, 384, 7168, "q8_split"),
     (128, 7168, 7168, "q8_wide"), (256, 4096, 4096, "q8_wide"), (128, 4096, 4096, "q8_split"), (333, 5001, 4112, "q8_wide"), (1000, 4096, 4096, "q8_wide"),
-    (4096, 12288, 7168, "q8_wide")])
+    (65, 7168, 16384, "q8_wide"), (4096, 12288, 7168, "q8_wide")])
 def test_batches_take_the_kernel_measured_faster(M, N, K, kernel):
     """Few tiles: K split over clusters; many: whole tiles."""
     assert skg.skg_q8_plan_query(M, N, K, "bf16", SMS)["kernel"] == kernel
+
+
+@pytest.mark.parametrize("M,N,K,kernel,split", [
+    (32, 128 * 36, 7168, "q8_split", 8), (32, 128 * 38, 7168, "q8_split", 7), (32, 128 * 43, 7168, "q8_split", 6),
+    (64, 128 * 46, 7168, "q8_split", 6), (64, 128 * 56, 7168, "q8_split", 5), (64, 128 * 59, 2048, "q8_split", 4),
+    (128, 256 * 28, 7168, "q8_wide", 2), (128, 256 * 36, 7168, "q8_wide", 2), (128, 256 * 37, 7168, "q8_wide", 1),
+    (128, 256 * 23, 16384, "q8_wide", 3), (128, 256 * 24, 16384, "q8_wide", 2), (128, 256 * 32, 2048, "q8_wide", 1)])
+def test_clusters_of_a_split_k_are_resident_at_once(M, N, K, kernel, split):
+    d = skg.skg_q8_plan_query(M, N, K, "bf16", SMS)
+    assert (d["kernel"], d["split_k"]) == (kernel, split)

@@ -415,7 +415,8 @@ def test_binding_refuses_wrong_tensors():
 
 
 # ------------------------------------------------------------------------- every kernel at every shape
-SHAPES = [(skg.SKG_Q8_KERNEL_SPLIT, t, k) for t in (32, 64) for k in range(1, 9)] + [(skg.SKG_Q8_KERNEL_WIDE, 128, 0)]
+SHAPES = [(skg.SKG_Q8_KERNEL_SPLIT, t, k) for t in (32, 64) for k in range(1, 9)] + \
+         [(skg.SKG_Q8_KERNEL_WIDE, 128, k) for k in range(1, 5)]
 
 
 @pytest.mark.parametrize("kind,m_tile,split", SHAPES)
