@@ -466,9 +466,9 @@ SKG_API skg_status skg_quantize_q8(int M, int K, const void *x, size_t ldx, cons
 
 typedef enum skg_q8_kernel_kind {
     SKG_Q8_KERNEL_STREAM = 1,   /* M <= 16: W streams into registers, warp-level fp16 MMA, exact */
-    SKG_Q8_KERNEL_SPLIT = 2,    /* M > 16, few tiles: TMA + tcgen05 on integers widened to fp16, exact; K split
+    SKG_Q8_KERNEL_SPLIT = 2,    /* M > 8, few tiles: TMA + tcgen05 on integers widened to fp16, exact; K split
                                    over the CTAs of a cluster, joined in shared memory */
-    SKG_Q8_KERNEL_WIDE = 3      /* M > 16, many tiles: the same arithmetic by pairs of CTAs, over whole tiles or
+    SKG_Q8_KERNEL_WIDE = 3      /* M > 8, many tiles: the same arithmetic by pairs of CTAs, over whole tiles or
                                    with K split over the pairs of a cluster */
 } skg_q8_kernel_kind;
 
@@ -478,7 +478,7 @@ typedef struct skg_q8_plan_desc {
     int M, N, K, epilogue;
     int static_weights;         /* see skg_q8_plan */
     int m_tile;                 /* tokens per tile (STREAM: 8 or 16; SPLIT: 32 or 64; WIDE: 128) */
-    int n_tile;                 /* output channels per tile (STREAM: 16, 32 or 48; SPLIT: 128; WIDE: 256, a pair's) */
+    int n_tile;                 /* output channels per tile (STREAM: 16 or 32; SPLIT: 128; WIDE: 256, a pair's) */
     int tiles;                  /* output tiles */
     int split_k;                /* parts of a tile's K: CTAs of a cluster (SPLIT: 1..8) or pairs of them (WIDE: 1..4); STREAM: 1 */
     int grid, threads, smem_bytes, stages, ctas_per_sm;

@@ -106,6 +106,17 @@ int choose_wide_split(long long tiles, int nkb, int num_sms)
     return best;
 }
 
+// The streaming kernel up to 8 tokens, and up to 16 while its CTAs fit in one
+// wave (three to an SM) or W is so small that the split kernel's ends weigh more.  Measured, stream then split: 8 x 12288 x 7168 16.9 and
+// 19.0, 8 x 28672 x 8192 39.6 and 45; 16 x 2432 x 7168 6.1 and 7.9, 16 x 7296 x
+// 7168 11.9 and 12.5, 9 x 5000 x 4112 7.9 and 8.4; beyond, 16 x 9216 x 4096 14.0
+// and 9.9, 9 x 16384 x 7168 29 and 24, 16 x 16384 x 2048 11.5 and 9.3, but 16 x
+// 12288 x 1024 6.1 and 6.8.  It is furthest off at 16 x 4096 x 16384, 16.9 and 15.0.
+bool prefer_stream(const skg_q8_plan_desc &d, int num_sms)
+{
+    return d.M <= 8 || (d.M <= kStreamMaxM && (ceil_div(d.N, 16) <= 3 * num_sms || static_cast<long long>(d.N) * d.K <= (16 << 20)));
+}
+
 // The split or the wide kernel.  Measured, split then wide: 24 x 28672 x 8192
 // 46 and 57, 64 x 28672 x 8192 59 and 58, 128 x 1024 x 7168 9.8 and 12.3, 128 x
 // 7168 x 7168 26.9 and 19.7, 256 x 4096 x 4096 17.4 and 15.3, 1000 x 4096 x 4096
@@ -129,8 +140,9 @@ int carried(const skg_q8_plan_desc &d)
 skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int split, int num_sms, const char *who)
 {
     if (!kind)
-        kind = d->M <= kStreamMaxM ? SKG_Q8_KERNEL_STREAM
-                                   : (prefer_split(*d, num_sms) ? SKG_Q8_KERNEL_SPLIT : SKG_Q8_KERNEL_WIDE);
+        kind = prefer_stream(*d, num_sms)  ? SKG_Q8_KERNEL_STREAM
+               : prefer_split(*d, num_sms) ? SKG_Q8_KERNEL_SPLIT
+                                           : SKG_Q8_KERNEL_WIDE;
     d->kernel_kind = kind;
     d->split_k = 1;
     d->smem_bytes = d->stages = 0;

@@ -206,7 +206,8 @@ cudaError_t launch_as(const Q8LinearParams &p, bool static_w, cudaStream_t s)
 // hold the grid in one wave (M = 1: N = 2048 16 warps 5.0 us, 8 warps 8.5 us;
 // N = 4096 two CTAs of 16 warps 4.2, three of 8 5.5; N = 7168 three of 8 9.6,
 // two of 16 11.2).  Beyond one wave of 16-channel CTAs, 32 (M <= 8: N = 12288
-// 16.0 us against 17.4) or 48 channels (M > 8: 21.3 against 22.7).
+// 16.0 us against 17.4).  (With M > 8 such a grid is the split kernel's, but for
+// small W: 12288 x 1024 with M = 16 5.9 us, 48 channels a CTA 7.3.)
 Q8StreamShape q8_stream_shape(int M, int N, int num_sms)
 {
     const long long groups = (static_cast<long long>(N) + 15) / 16;
@@ -217,7 +218,7 @@ Q8StreamShape q8_stream_shape(int M, int N, int num_sms)
         return two ? Q8StreamShape{1, 8, 2} : Q8StreamShape{1, 16, 2};
     if (groups <= 3ll * num_sms)
         return {1, 8, 3};
-    return two ? Q8StreamShape{3, 8, 2} : Q8StreamShape{2, 8, 3};
+    return two ? Q8StreamShape{1, 8, 3} : Q8StreamShape{2, 8, 3};
 }
 
 cudaError_t launch_q8_stream(const Q8LinearParams &p, const Q8StreamShape &sh, bool static_w, cudaStream_t s)
@@ -230,8 +231,6 @@ cudaError_t launch_q8_stream(const Q8LinearParams &p, const Q8StreamShape &sh, b
         return sh.ctas_per_sm == 1 ? launch_as<1, 1, 16, 1, 1>(p, static_w, s)
                                    : launch_as<1, 1, 16, 2, 1>(p, static_w, s);
     }
-    if (sh.groups == 3)
-        return launch_as<2, 3, 8, 2, 2>(p, static_w, s);
     if (sh.warps == 16)
         return launch_as<2, 1, 16, 1, 1>(p, static_w, s);
     return sh.ctas_per_sm == 2 ? launch_as<2, 1, 8, 2, 2>(p, static_w, s) : launch_as<2, 1, 8, 3, 1>(p, static_w, s);

@@ -108,7 +108,7 @@ def test_binding_refuses_host_tensors():
 def test_query_describes_a_launch_that_covers_every_tile(M, N, K):
     d = skg.skg_q8_plan_query(M, N, K, "bf16", SMS)
     assert d["grid"] >= 1 and d["threads"] % 32 == 0
-    assert (d["kernel"] == "q8_stream") == (M <= 16)
+    assert (d["kernel"] == "q8_stream") == (M <= 8 or M <= 16 and (-(-N // 16) <= 3 * SMS or N * K <= 1 << 24))
     assert d["tiles"] == -(-N // d["n_tile"]) * -(-M // d["m_tile"])
     if d["kernel"] == "q8_stream":
         assert d["workspace_bytes"] == 0 and d["grid"] == d["tiles"] and M <= d["m_tile"]
@@ -130,17 +130,19 @@ def test_query_describes_a_launch_that_covers_every_tile(M, N, K):
 @pytest.mark.parametrize("M", [1, 8, 9, 16])
 @pytest.mark.parametrize("N", [1, 384, 16 * SMS, 16 * SMS + 1, 32 * SMS, 32 * SMS + 1, 48 * SMS, 48 * SMS + 1, 12288, 200000])
 def test_streaming_launch_fills_as_few_slots_as_hold_it(M, N):
-    d = skg.skg_q8_plan_query(M, N, 1024, "bf16", SMS)
+    d = skg.skg_q8_plan_query(M, N, 7168, "bf16", SMS)
     groups = -(-N // 16)
     if groups <= 3 * SMS:
-        assert d["n_tile"] == 16 and d["ctas_per_sm"] == -(-groups // SMS)
+        assert d["kernel"] == "q8_stream" and d["n_tile"] == 16 and d["ctas_per_sm"] == -(-groups // SMS)
+    elif M <= 8:
+        assert d["kernel"] == "q8_stream" and d["n_tile"] == 32
     else:
-        assert d["n_tile"] == (32 if M <= 8 else 48)
+        assert d["kernel"] != "q8_stream"
     assert d["threads"] * d["ctas_per_sm"] <= 1024
 
 
 @pytest.mark.parametrize("M,N,K,kernel", [
-    (17, 7168, 7168, "q8_split"), (64, 7168, 16384, "q8_split"), (64, 28672, 8192, "q8_wide"), (128, 384, 7168, "q8_split"),
+    (16, 7168, 7168, "q8_stream"), (16, 12288, 7168, "q8_split"), (16, 12288, 1024, "q8_stream"), (8, 28672, 8192, "q8_stream"), (17, 7168, 7168, "q8_split"), (64, 7168, 16384, "q8_split"), (64, 28672, 8192, "q8_wide"), (128, 384, 7168, "q8_split"),
     (128, 7168, 7168, "q8_wide"), (256, 4096, 4096, "q8_wide"), (128, 4096, 4096, "q8_split"), (333, 5001, 4112, "q8_wide"), (1000, 4096, 4096, "q8_wide"),
     (65, 7168, 16384, "q8_wide"), (4096, 12288, 7168, "q8_wide")])
 def test_batches_take_the_kernel_measured_faster(M, N, K, kernel):

@@ -465,7 +465,7 @@ def test_output_addresses(M, N, epilogue):
 def test_streaming_kernel_at_every_launch_shape(M, N, K):
     c = Linear(M, N, K, "bf16_residual", 7)
     plan = skg.Q8Plan(M, N, K, "bf16_residual", static_weights=(N + K) % 2 == 0)
-    assert plan.info()["kernel"] == "q8_stream"
+    plan.force(skg.SKG_Q8_KERNEL_STREAM)
     assert R.same_bits(c.run(plan), c.want())
     plan.close()
 
