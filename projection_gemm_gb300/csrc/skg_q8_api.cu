@@ -67,42 +67,75 @@ static_assert(sizeof(kWideResident) / sizeof(int) == kQ8WideMaxSplit + 1, "a cou
 
 long long resident(int on_152, int num_sms) { return std::max(1ll, static_cast<long long>(on_152) * num_sms / 152); }
 
-// CTAs of a cluster of the split kernel: as many as one wave holds (at most the
-// portable 8), none without a unit of K.
-int choose_split(long long tiles, int nkb, int num_sms)
-{
-    int s = std::min(8, nkb);
-    while (s > 1 && tiles > resident(kSplitResident[s], num_sms))
-        --s;
-    return s;
-}
-
-// The kernels' times (us) as measured: a CTA of the split kernel takes 0.93 a
-// unit of 128 k (0.69 with tiles of 32 tokens) and 4 for its ends, in as many
-// waves as its grid needs; a pair of the wide one 0.39 a unit and 5, or 8.5
-// where K is split and the cluster's pairs join their sums.
+// The tcgen05 kernels' times (us) as measured.  A CTA of the split kernel takes
+// 0.93 a unit of 128 k, 0.52 if it has the SM to itself (0.69 and 0.40 with
+// tiles of 32 tokens), and 2.8 for its ends, 2.2 more to join a split K.
 double split_us(long long tiles, int nkb, int m_tile, int split, int num_sms)
 {
-    const long long slots = resident(kSplitResident[split], num_sms);
-    return 4.0 + (m_tile == 32 ? 0.69 : 0.93) * static_cast<double>((tiles + slots - 1) / slots * ceil_div(nkb, split));
+    const long long slots = resident(kSplitResident[split], num_sms), waves = (tiles + slots - 1) / slots;
+    const bool alone = tiles * split <= num_sms;
+    const double unit = m_tile == 32 ? (alone ? 0.40 : 0.69) : (alone ? 0.52 : 0.93);
+    return static_cast<double>(waves) * ((split > 1 ? 5.0 : 2.8) + unit * ceil_div(nkb, split));
 }
 
+// A pair of the wide kernel takes 0.39 a unit and 0.9 a tile, but no less than
+// its epilogue's 2.6, and 4.1 for its ends, 3.5 more to join a split K.
 double wide_us(long long tiles, int nkb, int split, int num_sms)
 {
-    const long long slots = resident(kWideResident[split], num_sms);
-    return (split > 1 ? 8.5 : 5.0) + 0.39 * static_cast<double>((tiles + slots - 1) / slots * ceil_div(nkb, split));
+    const long long slots = resident(kWideResident[split], num_sms), waves = (tiles + slots - 1) / slots;
+    return (split > 1 ? 7.6 : 4.1) + static_cast<double>(waves) * std::max(2.6, 0.9 + 0.39 * ceil_div(nkb, split));
 }
 
-// Pairs that share a tile's K in the wide kernel: where one wave holds them
-// all, the fastest.  Measured with 1, 2, 3 and 4: 128 x 7168 x 7168 26.3, 19.7,
-// 30.6, 29.8; 65 x 7168 x 16384 53, 31.9, 47, 41; 128 x 2048 x 4096 17.1, 12.8,
-// 10.9, 11.3; 100 x 8192 x 2048 11.8, 11.9, 20.3, 29.2.
-int choose_wide_split(long long tiles, int nkb, int num_sms)
+struct TcChoice {
+    int m_tile, split;
+    double us;
+};
+
+long long tiles_of(const skg_q8_plan_desc &d, int n_tile, int m_tile)
 {
-    int best = 1;
-    for (int s = 2; s <= std::min(kQ8WideMaxSplit, nkb); ++s)
-        if (tiles <= resident(kWideResident[s], num_sms) && wide_us(tiles, nkb, s, num_sms) < wide_us(tiles, nkb, best, num_sms))
-            best = s;
+    return static_cast<long long>(ceil_div(d.N, n_tile)) * ceil_div(d.M, m_tile);
+}
+
+// The split kernel's tile and the CTAs that share its K, given either or none
+// (0): the fastest of those whose clusters are resident at once.  Measured, with
+// 1 ... CTAs of 64-token tiles, then of 32: 428 x 1560 x 976 6.7, 8.2, 9.1 and
+// 7.4, 13.6; 204 x 120 x 10800 44, 26, 19, 14.8, (8) 9.4 and 34, 19.9, (4) 10.9,
+// (8) 7.2; 64 x 7168 x 7168 31, 20.1, 20.6, (5) 15.3.
+TcChoice choose_split(const skg_q8_plan_desc &d, int m_tile, int split, int num_sms)
+{
+    const int nkb = ceil_div(d.K, kQ8BlockK);
+    TcChoice best = {0, 0, 0.0};
+    for (int mt = 64; mt >= 32; mt -= 32) {
+        if (m_tile ? mt != m_tile : mt == 64 && d.M <= 32)
+            continue;
+        const long long tiles = tiles_of(d, kTileN, mt);
+        for (int s = 1; s <= std::min(8, nkb); ++s) {
+            if (split ? s != std::min(split, nkb) : s > 1 && tiles > resident(kSplitResident[s], num_sms))
+                continue;
+            const double us = split_us(tiles, nkb, mt, s, num_sms);
+            if (!best.split || us < best.us)
+                best = {mt, s, us};
+        }
+    }
+    return best;
+}
+
+// Pairs that share a tile's K in the wide kernel, in the same way.  Measured
+// with 1, 2, 3 and 4: 128 x 7168 x 7168 26.3, 19.7, 30.6, 29.8; 65 x 7168 x 16384
+// 53, 31.9, 47, 41; 128 x 2048 x 4096 17.1, 12.8, 10.9, 11.3; 100 x 8192 x 2048
+// 11.8, 11.9, 20.3, 29.2.
+TcChoice choose_wide(const skg_q8_plan_desc &d, int split, int num_sms)
+{
+    const int nkb = ceil_div(d.K, kQ8BlockK), mt = q8_wide_shape().m_tile;
+    const long long tiles = tiles_of(d, 2 * kTileN, mt);
+    TcChoice best = {0, 0, 0.0};
+    for (int s = 1; s <= std::min(kQ8WideMaxSplit, nkb); ++s) {
+        if (split ? s != std::min(split, nkb) : s > 1 && tiles > resident(kWideResident[s], num_sms))
+            continue;
+        const double us = wide_us(tiles, nkb, s, num_sms);
+        if (!best.split || us < best.us)
+            best = {mt, s, us};
+    }
     return best;
 }
 
@@ -119,15 +152,11 @@ bool prefer_stream(const skg_q8_plan_desc &d, int num_sms)
 
 // The split or the wide kernel.  Measured, split then wide: 24 x 28672 x 8192
 // 46 and 57, 64 x 28672 x 8192 59 and 58, 128 x 1024 x 7168 9.8 and 12.3, 128 x
-// 7168 x 7168 26.9 and 19.7, 256 x 4096 x 4096 17.4 and 15.3, 1000 x 4096 x 4096
-// 58 and 32; it is furthest off at 1000 x 1024 x 1024, 9.6 and 8.4.
+// 7168 x 7168 26.9 and 19.7, 256 x 4096 x 4096 17.4 and 15.3, 1849 x 680 x 320
+// 5.7 and 8.0, 1000 x 4096 x 4096 58 and 32.
 bool prefer_split(const skg_q8_plan_desc &d, int num_sms)
 {
-    const int m_tile = d.M <= 32 ? 32 : 64, nkb = ceil_div(d.K, kQ8BlockK), n_tiles = ceil_div(d.N, kTileN);
-    const long long st = static_cast<long long>(n_tiles) * ceil_div(d.M, m_tile);
-    const long long wt = static_cast<long long>(ceil_div(n_tiles, 2)) * ceil_div(d.M, q8_wide_shape().m_tile);
-    return split_us(st, nkb, m_tile, choose_split(st, nkb, num_sms), num_sms) <=
-           wide_us(wt, nkb, choose_wide_split(wt, nkb, num_sms), num_sms);
+    return choose_split(d, 0, 0, num_sms).us <= choose_wide(d, 0, num_sms).us;
 }
 
 // Accumulations of 1024 k that a CTA of the split kernel puts away: all but two.
@@ -159,29 +188,26 @@ skg_status fill_launch(skg_q8_plan_desc *d, int kind, int m_tile, int split, int
         d->ctas_per_sm = sh.ctas_per_sm;
         return SKG_OK;
     }
-    const int nkb = ceil_div(d->K, kQ8BlockK);
     const bool wide = kind == SKG_Q8_KERNEL_WIDE;
+    const TcChoice c = wide ? choose_wide(*d, split, num_sms) : choose_split(*d, m_tile, split, num_sms);
+    d->m_tile = c.m_tile;
+    d->split_k = c.split;
     d->n_tile = wide ? 2 * kTileN : kTileN;
-    if (!m_tile)
-        m_tile = wide ? q8_wide_shape().m_tile : (d->M <= 32 ? 32 : 64);
-    d->m_tile = m_tile;
-    const long long tiles = static_cast<long long>(ceil_div(d->N, d->n_tile)) * ceil_div(d->M, m_tile);
+    const long long tiles = tiles_of(*d, d->n_tile, d->m_tile);
     if (tiles > (1ll << 27))
         return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^27 tiles", who);
     d->tiles = static_cast<int>(tiles);
-    const Q8TcShape sh = wide ? q8_wide_shape() : q8_split_shape(m_tile);
+    const Q8TcShape sh = wide ? q8_wide_shape() : q8_split_shape(d->m_tile);
     d->threads = sh.threads;
     d->smem_bytes = sh.smem_bytes;
     d->stages = sh.stages;
     d->ctas_per_sm = sh.ctas_per_sm;
     if (wide) {
-        d->split_k = split ? std::min(split, nkb) : choose_wide_split(tiles, nkb, num_sms);
         d->grid = 2 * d->split_k * (d->split_k > 1 ? d->tiles : std::min(d->tiles, std::max(1, num_sms / 2)));
         return SKG_OK;
     }
-    d->split_k = split ? std::min(split, nkb) : choose_split(d->tiles, nkb, num_sms);
     d->grid = d->tiles * d->split_k;
-    d->workspace_bytes = static_cast<size_t>(d->grid) * carried(*d) * m_tile * kTileN * 4;
+    d->workspace_bytes = static_cast<size_t>(d->grid) * carried(*d) * d->m_tile * kTileN * 4;
     return SKG_OK;
 }
 

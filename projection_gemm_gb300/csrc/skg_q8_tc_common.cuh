@@ -152,7 +152,22 @@ __device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr)
     return v;
 }
 
-// What four neighbouring outputs (channels n.., token m) need besides their sums.
+// Four 32-bit words of a CTA of the cluster: 16 neighbouring bytes, or words 128
+// bytes apart.
+__device__ __forceinline__ int4 ld_cluster_four(uint32_t addr, bool vec4)
+{
+    if (vec4)
+        return ld_cluster_v4(addr);
+    int v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[i]) : "r"(addr + 128 * i) : "memory");
+    return make_int4(v[0], v[1], v[2], v[3]);
+}
+
+// What four outputs of a token (channels n, n + 1, ... with vec4, else n, n + 32,
+// ..., so that a warp's loads and stores cover neighbouring channels) need
+// besides their sums.
 struct Four {
     float xs, ws[4];
     uint16_t res[4];
@@ -172,8 +187,8 @@ __device__ __forceinline__ Four load_four(const Q8LinearParams &g, int m, int n,
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            f.ws[i] = n + i < g.N ? __ldcg(g.w_scale + n + i) : 0.0f;
-            f.res[i] = res && n + i < g.N ? __ldcg(g.res + o + i) : 0;
+            f.ws[i] = n + 32 * i < g.N ? __ldcg(g.w_scale + n + 32 * i) : 0.0f;
+            f.res[i] = res && n + 32 * i < g.N ? __ldcg(g.res + o + 32 * i) : 0;
         }
     }
     return f;
@@ -198,8 +213,8 @@ __device__ __forceinline__ void store_four(const Q8LinearParams &g, int m, int n
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (n + i < g.N)
-                y[i] = v[i];
+            if (n + 32 * i < g.N)
+                y[32 * i] = v[i];
         return;
     }
     uint16_t *y = static_cast<uint16_t *>(g.y) + o;
@@ -210,8 +225,8 @@ __device__ __forceinline__ void store_four(const Q8LinearParams &g, int m, int n
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (n + i < g.N)
-            y[i] = f32_to_bf16(v[i]);
+        if (n + 32 * i < g.N)
+            y[32 * i] = f32_to_bf16(v[i]);
 }
 
 // The end of a tile whose K is split over `split` CTAs of the cluster, the
@@ -223,20 +238,21 @@ template <int MAX_SPLIT, int THREADS>
 __device__ __forceinline__ void join_and_store(const Q8LinearParams &g, uint32_t smem, int m0, int n0, int tokens, int split,
                                                int part, int step, int first, bool vec4)
 {
-    const int t1 = (part + 1) * tokens / split, n = n0 + (static_cast<int>(threadIdx.x) & 31) * 4;
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const int t1 = (part + 1) * tokens / split, n = n0 + (vec4 ? 4 * lane : lane);
     int m = part * tokens / split + static_cast<int>(threadIdx.x >> 5);
     Four f = {};
     pdl_wait();
     if (m < t1)
         f = load_four(g, m0 + m, n, vec4);           // on its way while the cluster meets
     cluster_sync();
-    const uint32_t base = smem + (threadIdx.x & 31) * 16;
+    const uint32_t base = smem + (vec4 ? 16 * lane : 4 * lane);
     while (m < t1) {
         int4 sum = make_int4(0, 0, 0, 0);
         int4 v[MAX_SPLIT];
 #pragma unroll
         for (int r = 0; r < MAX_SPLIT; ++r)
-            v[r] = r < split ? ld_cluster_v4(map_shared_rank(base + m * (kTileN * 4), first + r * step)) : make_int4(0, 0, 0, 0);
+            v[r] = r < split ? ld_cluster_four(map_shared_rank(base + m * (kTileN * 4), first + r * step), vec4) : make_int4(0, 0, 0, 0);
 #pragma unroll
         for (int r = 0; r < MAX_SPLIT; ++r) {
             sum.x += v[r].x;
