@@ -9,21 +9,31 @@
 //
 // Tile (swap-AB): 128 rows of W are the MMA's M, MT tokens its N.  A cluster of
 // S CTAs computes one tile; CTA r takes the r-th part of K in units of 128.
-// What bounds it is W from HBM: two CTAs of an SM hold 2 x 3 units (MT = 64) in
-// flight.  Roles of a CTA:
+// Two CTAs an SM hold 2 x 3 units (MT = 64) in flight.  Roles of a CTA:
 //   8 warps   widen W, two sets of 4 on alternate units: a thread reads its W
 //             row's 128 bytes from the TMA ring and writes them as fp16 to its
 //             TMEM lane (the MMA's A operand)
 //   4 or 8    widen x into shared memory (the B operand), two sets as well; every
 //             2048 k and at the end, epilogue: accumulators to integers
 //   1 + 1     TMA; TMEM and MMA issue
-// (With x widened by the warps that widen W, a unit took a CTA 0.8 us at MT = 64;
-// HBM delivers one every 0.7.)
-// Then the cluster's CTAs leave their sums in their own shared memory and each
+// Sets of warps on alternate units rather than all on each: what a unit costs a
+// warp besides the widening (two waits, fences, two arrivals) is as much again
+// as half of it, and all 8 on every unit took 31.2 us at 64 x 7168 x 16384.
+// The cluster's CTAs then leave their sums in their own shared memory and each
 // adds up and stores 1/S of the tile's tokens, read from its peers.  Through
 // global memory instead (partial sums, an arrival counter, the last CTA adds
 // up) the same step took 6 us at M = 32 and 10 at M = 64: each round trip waits
 // 1 to 1.7 us behind the next launch's weights.
+//
+// Measured, back to back with weights from HBM (6.70 TB/s copy peak): 32 x 7168 x
+// 7168 12.7 us (4.1 TB/s), 64 x 7168 x 7168 15.3 us (3.4), 64 x 7168 x 16384 29.0
+// us (4.1), 64 x 384 x 7168 6.5 us.  What bounds the deep one: 4.8 us are the
+// launch's ends and the join; then a unit takes the SM's two CTAs 0.93 us.
+// Without any widening it takes 0.92 with W from HBM, and 0.76 with widening but
+// W from the L2, 0.58 with neither (the MMAs: at N = 64 they run at half rate), so
+// the memory's latency and the widening bound it together.  A fourth stage for W,
+// units requested in pairs, or another start in K for each tile changed nothing
+// (28.8, 29.3, 28.2 us).
 //
 // Every wait is bounded; on expiry a thread records the timeout in the plan's
 // error word, raises the CTA's abort flag, waits for its own copies and MMAs,

@@ -14,9 +14,12 @@
 // feeds them to four MMAs, and x follows the same order.
 //
 // Measured, back to back with weights from HBM (GB300, 6.70 TB/s copy peak):
-// 1 x 12288 x 7168 16.0 us (5.5 TB/s), 1 x 7168 x 16384 20.8 us (5.6 TB/s),
-// 8 x 7168 x 7168 9.8 us (5.2 TB/s), 1 x 1024 x 1024 1.6 us.  With the int8 MMA
-// (no widening) 16 tokens take 14.0 us at 7168 x 7168 against 12.2 us.
+// 1 x 12288 x 7168 16.0-16.4 us (5.4 TB/s), 1 x 7168 x 16384 21.0 us (5.6 TB/s),
+// 8 x 7168 x 7168 9.9 us (5.2 TB/s), 16 x 7168 x 7168 11.9 us (4.3 TB/s), 1 x
+// 1024 x 1024 1.8 us.  Up to 8 tokens HBM and the launch's ends bound it; with 16
+// the widening of x weighs as much as that of W (instructions issue in 58% of
+// the cycles, the ALU pipe is at 51%).  With the int8 MMA (no widening) 16 tokens
+// take 14.0 us at 7168 x 7168.
 #include "skg_internal.h"
 #include "skg_ptx.cuh"
 #include "skg_q8_common.cuh"

@@ -23,6 +23,22 @@
 // which everything the unit needs arrives, looks for the next one while half of
 // this one is still to issue, and commits once a unit.
 //
+// Where the tiles leave SMs idle, K is split over the up to 4 pairs of a cluster,
+// which leave their sums in shared memory and add them up as the split kernel's
+// CTAs do.
+//
+// Measured, weights from HBM: 4096 x 12288 x 7168 463-500 us (1.44-1.56 PFLOP/s of
+// the 1.96 that cuBLAS reaches; it draws 1.34 kW and the clock falls to 1.8 GHz
+// if it runs for seconds), 1024 x 7168 x 7168 72 us (1.46), 333 x 5001 x 4112 20.4
+// us, 256 x 4096 x 4096 15.3 us (17.4 unsplit), 128 x 7168 x 7168 19.6 us (26.3
+// unsplit).  A unit takes 0.39 us, where its MMAs take 0.27.  What bounds it is
+// the widening: without that of W 4096 tokens take 368 us, without that of x 424,
+// without the epilogue's sums 440.  Instructions issue in 60% of the cycles and
+// shared memory moves 87 KB a unit.  Three sets of widening warps (460 us) or 8
+// epilogue warps instead of 16 (547: registers spill) are no better; with all 8
+// warps on every unit it takes 550.  x widened by a kernel before took 475 us
+// where this took 500, but 22.7 for 333 x 5001 x 4112 and a workspace.
+//
 // Every wait is bounded as in skg_q8_split.cu.
 #include "skg_internal.h"
 #include "skg_ptx.cuh"
