@@ -51,11 +51,19 @@ constexpr int kLongThreads = 1024;
 // or 254 times a power of two and the quotient exact.)  Rounded to nearest, the
 // quotient is below 127 / max half of the time, and such a value goes to 63: 0.07%
 // of the elements of normal rows.  Every other value is further from half way
-// than the quotient's rounding takes it.
+// than the quotient's rounding takes it.  (The quotient to nearest, raised by a
+// unit where its product with the maximum falls short: __fdiv_ru does the same
+// and costs a warp-bound row kernel 3 to 10%, 131072 x 256 24.9 and 27.6 us.)
 struct RowScale {
     float scale, up, factor;
     bool finite;
 };
+
+__device__ __forceinline__ float quotient_up(float a, float b)
+{
+    const float f = a / b;
+    return fmaf(f, b, -a) < 0.0f ? __uint_as_float(__float_as_uint(f) + 1) : f;
+}
 
 __device__ __forceinline__ RowScale row_scale(uint32_t max_bits)
 {
@@ -63,7 +71,7 @@ __device__ __forceinline__ RowScale row_scale(uint32_t max_bits)
     const float amax = __uint_as_float(max_bits);
     r.finite = max_bits < 0x7F800000u;
     r.up = amax < 1e-30f ? 0x1p100f : 1.0f;
-    r.factor = amax > 0.0f && r.finite ? __fdiv_ru(127.0f, amax * r.up) : 0.0f;
+    r.factor = amax > 0.0f && r.finite ? quotient_up(127.0f, amax * r.up) : 0.0f;
     r.scale = r.finite ? amax / 127.0f : __int_as_float(0x7FC00000);
     return r;
 }
