@@ -436,6 +436,9 @@ SKG_API skg_status skg_group_destroy(skg_group_t group);
  * skg_rmsnorm_q8 -- residual addition, root-mean-square norm and quantisation
  * of M >= 0 rows of any length K >= 1, in one kernel on `stream`:
  *     h = x + residual (or x);   v = h / sqrt(mean(h^2) + eps) * gamma
+ * h and v are fp32; where they are within its range the norm is right whatever
+ * their squares are, for any eps >= 0.  (With eps = 0 a row of zeros is 0 / 0: scale
+ * NaN, q = 0.)
  *   x        bf16 [M, K], row stride ldx >= K elements; read-only
  *   residual bf16 [M, K], row stride ldr >= K, or NULL
  *   gamma    bf16 [K], or NULL for ones

@@ -32,7 +32,6 @@
 namespace skg {
 namespace {
 
-constexpr float kMaxFinite = 3.402823466e38f;
 constexpr int kWarpRows = 8;              // rows of a CTA where a warp takes a row
 constexpr int kMaxRow = 16384;            // longest row held in registers
 constexpr int kLongThreads = 1024;
@@ -93,17 +92,38 @@ __device__ __forceinline__ float max_nan(float m, float v)
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// 1 / sqrt(mean + eps) from the sum of squares of h; where that has left fp32's
-// range, `again` gives the sum with h taken 2^70 smaller (where h itself is not
-// finite, so is that sum, and the row).
-template <class F>
-__device__ __forceinline__ float inverse_rms(float sum, int K, float eps, F &&again)
-{
-    if (sum <= kMaxFinite)
-        return rsqrtf(sum / static_cast<float>(K) + eps);
-    sum = again(0x1p-70f);
-    return rsqrtf(sum / static_cast<float>(K) + eps * 0x1p-140f) * 0x1p-70f;
-}
+// The norm's factor, 1 / sqrt(mean(h^2) + eps), is had from the sum of squares in
+// fp32.  Where that has left, or is about to leave, the range in which fp32 holds
+// the sum and the mean to their precision (`plain` is false), it is taken again with
+// h scaled by a power of two:
+//   sum > 2^100: by 2^-80.  The largest h are below 2^48 then, and no row's sum
+//     (K < 2^31) overflows; the mean was above 2^69, so it stays above 2^-91.  The
+//     factor, scaled back, is 2^-128 at the least.
+//   mean + eps < 2^-100: by 2^90, exactly, and the norm goes on from the scaled h.
+//     All of h was below 2^-34, so the sum stays below 2^111; bf16's smallest
+//     value becomes 2^-43.
+// A value that is not finite makes the sum infinite or NaN, and the row's maximum
+// NaN.  A row of zeros with eps = 0 is 0 / 0.
+struct RowNorm {
+    float mean, n, eps;
+    bool plain, large;
+
+    __device__ __forceinline__ RowNorm(float sum, int K, float e) : n(static_cast<float>(K)), eps(e)
+    {
+        mean = sum / n + e;
+        large = !(sum <= 0x1p100f);
+        plain = !large && mean >= 0x1p-100f;
+    }
+
+    __device__ __forceinline__ float unit() const { return large ? 0x1p-80f : 0x1p90f; }
+    __device__ __forceinline__ float factor() const { return rsqrtf(mean); }
+
+    // From the sum with h scaled by unit(): the factor of h itself if large, else of the scaled h.
+    __device__ __forceinline__ float scaled_factor(float sum) const
+    {
+        return rsqrtf(sum / n + eps * unit() * unit()) * (large ? unit() : 1.0f);
+    }
+};
 
 // ------------------------------------------------------------ rows in registers
 // Eight elements as loaded.  (Not by the read-only path: the kernel may have
@@ -338,8 +358,18 @@ q8_rows_kernel(const Q8RowParams p)
                     s = fmaf(v[j][c] * unit, v[j][c] * unit, s);
             return row_sum<WARP>(s, buf);
         };
-        const float rms = inverse_rms(sum_of_squares(1.0f, sums[0]), p.K, p.eps,
-                                      [&](float unit) { return sum_of_squares(unit, sums[1]); });
+        const RowNorm norm(sum_of_squares(1.0f, sums[0]), p.K, p.eps);
+        float rms = norm.factor();
+        if (!norm.plain) {
+            if (!norm.large) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        v[j][c] *= norm.unit();
+            }
+            rms = norm.scaled_factor(sum_of_squares(norm.large ? norm.unit() : 1.0f, sums[1]));
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const Raw8 g = w[j].get();
@@ -357,7 +387,7 @@ q8_rows_kernel(const Q8RowParams p)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int e = first + j * step;
-        // (what lies beyond the row holds 0 * rms, which is NaN where rms is infinite)
+        // (what lies beyond the row holds 0 * rms, which is NaN where that factor is infinite)
         if (!ANY ? e < p.K : e >= 0 && e + 8 <= p.K) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
@@ -384,15 +414,44 @@ q8_rows_kernel(const Q8RowParams p)
 }
 
 // ------------------------------------------------------------------ longer rows
-template <bool NORM>
-__device__ __forceinline__ float long_value(const Q8RowParams &p, size_t row, int k, float rms)
+// The sum that the norm goes on from, scaled where TINY.
+template <bool TINY>
+__device__ __forceinline__ float long_sum(const Q8RowParams &p, size_t row, int k)
 {
     const float a = bf16_to_f32(p.x[row * p.ldx + k]);
+    const float h = p.second ? a + bf16_to_f32(p.second[row * p.ld2 + k]) : a;
+    return TINY ? h * 0x1p90f : h;
+}
+
+template <bool NORM, bool TINY>
+__device__ __forceinline__ float long_value(const Q8RowParams &p, size_t row, int k, float rms)
+{
     if (NORM) {
-        const float h = p.second ? a + bf16_to_f32(p.second[row * p.ld2 + k]) : a;
+        const float h = long_sum<TINY>(p, row, k);
         return p.gamma ? h * rms * bf16_to_f32(p.gamma[k]) : h * rms;
     }
+    const float a = bf16_to_f32(p.x[row * p.ldx + k]);
     return p.second ? silu(bf16_to_f32(p.second[row * p.ld2 + k])) * a : a;
+}
+
+// The maximum and the integers of a row.
+template <bool NORM, bool TINY>
+__device__ __forceinline__ void long_row(const Q8RowParams &p, size_t row, float rms, uint32_t *maxima)
+{
+    uint32_t m = 0;
+    for (int k = threadIdx.x; k < p.K; k += kLongThreads)
+        m = max(m, abs_bits(long_value<NORM, TINY>(p, row, k, rms)));
+    const RowScale r = row_scale(row_max<false>(m, maxima));
+    for (int k = threadIdx.x; k < p.K; k += kLongThreads) {
+        const float v = long_value<NORM, TINY>(p, row, k, rms);
+        if (NORM && p.h)                 // may be the residual itself: read by this thread, above
+            p.h[row * p.ldh + k] = f32_to_bf16(long_sum<false>(p, row, k));
+        if (NORM && p.y)
+            p.y[row * p.K + k] = f32_to_bf16(v);
+        p.q[row * p.K + k] = static_cast<int8_t>(to_q8(r.finite ? v * r.up : 0.0f, r));
+    }
+    if (threadIdx.x == 0)
+        p.scale[row] = r.scale;
 }
 
 template <bool NORM>
@@ -408,29 +467,22 @@ __global__ void __launch_bounds__(kLongThreads) q8_long_rows_kernel(const Q8RowP
         auto sum_of_squares = [&](float unit, float *buf) {
             float s = 0.0f;
             for (int k = threadIdx.x; k < p.K; k += kLongThreads) {
-                const float h = long_value<true>(Q8RowParams{p.x, p.second, nullptr, nullptr, nullptr, nullptr, nullptr,
-                                                             p.ldx, p.ld2, 0, 0, 0, 0.0f}, row, k, unit);
+                const float h = long_sum<false>(p, row, k) * unit;
                 s = fmaf(h, h, s);
             }
             return row_sum<false>(s, buf);
         };
-        rms = inverse_rms(sum_of_squares(1.0f, sums[0]), p.K, p.eps,
-                          [&](float unit) { return sum_of_squares(unit, sums[1]); });
+        const RowNorm norm(sum_of_squares(1.0f, sums[0]), p.K, p.eps);
+        rms = norm.factor();
+        if (!norm.plain) {
+            rms = norm.scaled_factor(sum_of_squares(norm.unit(), sums[1]));
+            if (!norm.large) {
+                long_row<true, true>(p, row, rms, maxima);
+                return;
+            }
+        }
     }
-    uint32_t m = 0;
-    for (int k = threadIdx.x; k < p.K; k += kLongThreads)
-        m = max(m, abs_bits(long_value<NORM>(p, row, k, rms)));
-    const RowScale r = row_scale(row_max<false>(m, maxima));
-    for (int k = threadIdx.x; k < p.K; k += kLongThreads) {
-        const float v = long_value<NORM>(p, row, k, rms);
-        if (NORM && p.h)                 // may be the residual itself: read by this thread, above
-            p.h[row * p.ldh + k] = f32_to_bf16(bf16_to_f32(p.x[row * p.ldx + k]) + bf16_to_f32(p.second[row * p.ld2 + k]));
-        if (NORM && p.y)
-            p.y[row * p.K + k] = f32_to_bf16(v);
-        p.q[row * p.K + k] = static_cast<int8_t>(to_q8(r.finite ? v * r.up : 0.0f, r));
-    }
-    if (threadIdx.x == 0)
-        p.scale[row] = r.scale;
+    long_row<NORM, false>(p, row, rms, maxima);
 }
 
 template <class... A>

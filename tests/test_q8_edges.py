@@ -48,3 +48,61 @@ def test_every_integer_of_a_bf16_row_is_the_nearest_half_to_even(K, scale):
     want, ties = nearest_even(v)
     assert ties >= 256
     assert int((q.long() != want).sum()) == 0
+
+
+# ------------------------------------------------------------------------------------------------- norm
+LENGTHS = [8, 256, 1000, 1024, 5001, 7168, 16384, 20001]          # every form of the row kernels
+
+
+def check_norm(x, residual, gamma, eps):
+    eps = float(np.float32(eps))
+    M, K = x.shape
+    q, s = rows_out(M, K)
+    y = torch.empty_like(x)
+    skg.skg_rmsnorm_q8(x, residual, gamma, eps, None, q, s, y)
+    v, _ = R.norm_rows(x, residual, gamma, eps)
+    e = R.row_error(K)
+    R.check_rows(v, q, s, e, f"{M}x{K} eps={eps}")
+    assert bool(((y.double() - v).abs() <= (2.0 ** -8 + e) * v.abs() + 2.0 ** -133).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", LENGTHS)
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 3e38])
+def test_norm_of_the_largest_values(K, eps):
+    """The sum of squares leaves fp32's range, by up to K 2^128; one small value among them stays what it is."""
+    g = rng(31, K)
+    x = torch.from_numpy(g.choice([-1.0, 1.0], size=(5, K))).float() * 3.38e38
+    x[1] *= torch.from_numpy(g.uniform(0, 1, K)).float()
+    x[2] *= 1e-17
+    x[3] *= 2.0 ** -20
+    x[4, 1:] = 1e-30
+    x = x.to(torch.bfloat16).cuda()
+    check_norm(x, None, (normal(g, K, std=0.2) + 1).cuda(), eps)
+    check_norm(x[2:], normal(g, 3, K).cuda(), None, eps)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", LENGTHS)
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-36, 1e-30])
+def test_norm_of_the_smallest_values(K, eps):
+    """Squares below fp32's range, which eps does not cover."""
+    g = rng(32, K)
+    sizes = [1e-8, 1e-15, 1e-18, 1e-20, 1e-21, 1e-22, 5e-23, 1e-23, 1e-30, 1e-37, 1e-39]
+    x = torch.stack([normal(g, K).float() * v for v in sizes]).to(torch.bfloat16)
+    x[:, 0] = torch.tensor(sizes).to(torch.bfloat16)
+    x[-1, 1:] = 0                                       # one value alone
+    x = x.cuda()
+    check_norm(x, None, (normal(g, K, std=0.2) + 1).cuda(), eps)
+    check_norm(x, x.flip(0).contiguous(), None, eps)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [8, 1001, 20001])
+def test_norm_of_zeros(K):
+    """0 with eps; 0 / 0 without."""
+    x = torch.zeros(2, K, dtype=torch.bfloat16, device="cuda")
+    for eps in (1e-6, 0.0):
+        q, s = rows_out(2, K)
+        skg.skg_rmsnorm_q8(x, None, None, eps, None, q, s)
+        assert bool((q == 0).all()) and bool((s == 0).all() if eps else s.isnan().all())
