@@ -386,13 +386,42 @@ __device__ __forceinline__ uint32_t map_shared_rank(uint32_t saddr, uint32_t ran
     return r;
 }
 
-// Arrive on the barrier at this (mapped) address of a CTA of the cluster.  What
-// it announces is in tensor memory (ordered by tcgen05.fence) or was written by
-// copies that this thread has waited for: no ordering of plain memory at cluster
-// scope is asked for, which would wait for all of the thread's stores.
+// Arrive on the barrier at this (mapped) address of a CTA of the cluster.  Relaxed:
+// for what is ordered by tcgen05.fence alone, contents of tensor memory.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
 {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+}
+
+// The same, after all that this thread wrote or has seen written to memory.  It
+// waits for those writes: about 0.65 us, one at a time on an SM.
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+}
+
+// mbar_try_wait and mbar_wait on a barrier of this CTA at which threads of other
+// CTAs of the cluster arrive.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, uint64_t timeout_ns, volatile int *abort)
+{
+    if (mbar_try_wait_cluster(bar, parity))
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!*abort && globaltimer_ns() - t0 <= timeout_ns) {
+        if (mbar_try_wait_cluster(bar, parity))
+            return true;
+    }
+    return false;
 }
 
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr)

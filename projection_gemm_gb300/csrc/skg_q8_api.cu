@@ -78,12 +78,12 @@ double split_us(long long tiles, int nkb, int m_tile, int split, int num_sms)
     return static_cast<double>(waves) * ((split > 1 ? 5.0 : 2.8) + unit * ceil_div(nkb, split));
 }
 
-// A pair of the wide kernel takes 0.39 a unit and 0.9 a tile, but no less than
-// its epilogue's 2.6, and 4.1 for its ends, 3.5 more to join a split K.
+// A pair of the wide kernel takes 0.42 a unit and 0.9 a tile, but no less than
+// its epilogue's 2.6, and 5.4 for its ends, 3.5 more to join a split K.
 double wide_us(long long tiles, int nkb, int split, int num_sms)
 {
     const long long slots = resident(kWideResident[split], num_sms), waves = (tiles + slots - 1) / slots;
-    return (split > 1 ? 7.6 : 4.1) + static_cast<double>(waves) * std::max(2.6, 0.9 + 0.39 * ceil_div(nkb, split));
+    return (split > 1 ? 8.9 : 5.4) + static_cast<double>(waves) * std::max(2.6, 0.9 + 0.42 * ceil_div(nkb, split));
 }
 
 struct TcChoice {

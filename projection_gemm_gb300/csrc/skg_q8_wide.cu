@@ -10,34 +10,46 @@
 // k costs a CTA 16 KB of W and 8 of x from the L2 and the MMAs 512 cycles.
 //
 // Roles of a CTA (one per SM, pairs persistent over tiles):
-//   1          TMEM; in the first CTA of the pair, MMA issue for both
-//   1          TMA
+//   1          TMEM; in the first CTA of the pair MMA issue for both, in the second
+//              a relay
+//   1 + 1      TMA of W, TMA of x
 //   8 warps    widen, two sets of 4 on alternate units: W into TMEM, x into
 //              shared memory
 //   16         epilogue: accumulators into int32 registers; at a tile's end
 //              scales, residual, rounding and the store, while the next tile's
 //              MMAs go on in the other accumulator
+//   1          in the second CTA, the other relay
 // The MMA issuer is what the rest is arranged around.  About three MMAs queue up
 // behind the one that runs, and one wait on a barrier, even one already past,
 // takes as long as one or two of them; so it waits once a unit, for a barrier at
 // which everything the unit needs arrives, looks for the next one while half of
 // this one is still to issue, and commits once a unit.
 //
+// What the second CTA's warps announce to the issuer in the first.  W is in TMEM:
+// tcgen05.fence orders it, and the arrival is relaxed.  x is written with plain
+// stores, which only a release at cluster scope orders before what a thread of
+// another CTA does, and that release takes 0.7 to 1.2 us.  In the widening warps
+// it took 1024 x 7168 x 7168 from 72 to 118 us.  So x is widened kAhead units
+// before W, the widening warps arrive at a barrier of their own CTA, and two other
+// warps in turn pass that on, with the release, for two units at a time: 76 us,
+// as long as without the release.  (One relay 88 us; x two units ahead 87.)
+//
 // Where the tiles leave SMs idle, K is split over the up to 4 pairs of a cluster,
 // which leave their sums in shared memory and add them up as the split kernel's
 // CTAs do.
 //
-// Measured, weights from HBM: 4096 x 12288 x 7168 463-500 us (1.44-1.56 PFLOP/s of
+// Measured, weights from HBM: 4096 x 12288 x 7168 483-500 us (1.44-1.49 PFLOP/s of
 // the 1.96 that cuBLAS reaches; it draws 1.34 kW and the clock falls to 1.8 GHz
-// if it runs for seconds), 1024 x 7168 x 7168 72 us (1.46), 333 x 5001 x 4112 20.4
-// us, 256 x 4096 x 4096 15.3 us (17.4 unsplit), 128 x 7168 x 7168 19.6 us (26.3
-// unsplit).  A unit takes 0.39 us, where its MMAs take 0.27.  What bounds it is
-// the widening: without that of W 4096 tokens take 368 us, without that of x 424,
-// without the epilogue's sums 440.  Instructions issue in 60% of the cycles and
-// shared memory moves 87 KB a unit.  Three sets of widening warps (460 us) or 8
-// epilogue warps instead of 16 (547: registers spill) are no better; with all 8
-// warps on every unit it takes 550.  x widened by a kernel before took 475 us
-// where this took 500, but 22.7 for 333 x 5001 x 4112 and a workspace.
+// if it runs for seconds), 1024 x 7168 x 7168 76 us (1.38), 333 x 5001 x 4112 22.5
+// us, 256 x 4096 x 4096 16.8 us, 128 x 7168 x 7168 22.1 us.  A unit takes 0.41 us,
+// where its MMAs take 0.27.  What bounds it is the widening, and how soon the ring
+// is filled again: an iteration of a set of widening warps works for 1030 cycles and
+// waits for 500, a load takes 2200 until it has arrived, and with the producers'
+// work in one warp 1024 tokens take 83 us.  (x read by the widening warps from
+// global memory instead, with 6 stages of W: 88 us; the ring's bytes taken into
+// registers before the wait for the operand buffer: 86.)  Three sets of widening
+// warps or 8 epilogue warps instead of 16 are no better; with all 8 widening warps
+// on every unit 4096 tokens take 550 us.
 //
 // Every wait is bounded as in skg_q8_split.cu.
 #include "skg_internal.h"
@@ -58,18 +70,24 @@ struct WideShape {
     static constexpr int kEpiWarps = 16;
     static constexpr int kCols = MT * 4 / kEpiWarps;         // accumulator columns of an epilogue thread
     static_assert(kCols == 32, "a lane holds the scale of a token");
-    static constexpr int kThreads = 32 * (2 + kWidenWarps + kEpiWarps);
-    static constexpr int kMmaWarp = 0, kTmaWarp = 1, kFirstWiden = 2, kFirstEpi = kFirstWiden + kWidenWarps;
-    static constexpr int kStages = 6;                        // ring of W and int8 x
-    static constexpr int kOps = (512 - 2 * MT) / 64;         // widened operand buffers: 4
-    static_assert(kStages >= kOps && kOps >= kWidenSets, "the widen warps' waits need this");
+    static constexpr int kThreads = 32 * (4 + kWidenWarps + kEpiWarps);
+    static constexpr int kMmaWarp = 0, kTmaWarp = 1, kFirstWiden = 2, kFirstEpi = kFirstWiden + kWidenWarps,
+                         kTmaXWarp = kFirstEpi + kEpiWarps, kRelayWarp = kTmaXWarp + 1;
+    static constexpr int kStages = 4;                        // ring of int8: W of a unit, x of one kAhead later
+    static constexpr int kOps = (512 - 2 * MT) / 64;         // widened W, in TMEM: 4
+    static constexpr int kAhead = 4;                         // units by which x is widened before W
+    static constexpr int kXOps = kOps + kAhead;              // widened x: 8
+    static_assert(kStages % kWidenSets == 0 && kOps % kWidenSets == 0 && kAhead == 2 * kWidenSets && kXOps % kOps == 0 &&
+                      kAhead <= kStages,
+                  "a buffer is always the same set's; the prologue's and the issuer's order");
     static constexpr uint32_t kRawX = kHalfTokens * kQ8BlockK;
     static constexpr uint32_t kX16 = 2 * kRawX;              // two 64-wide halves
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kIdesc = idesc_f16_f32(2 * kTileN, MT);
     static_assert(kStages * kQ8WBytes >= MT * kTileN * 4, "the sums take the ring's place");
-    static constexpr int kBars = 2 * kStages + 2 * kOps + 5;
-    static constexpr int kSmem = 1024 + kStages * (kQ8WBytes + kRawX) + kOps * kX16 + kBars * 8 + 16;
+    static constexpr int kBars = kStages + kOps + 2 * kXOps + 7;
+    static constexpr int kSmem = 1024 + kStages * (kQ8WBytes + kRawX) + kXOps * kX16 + kBars * 8 + 16;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
 // Tiles (pairs of 128 channels x 128 tokens) in bands of p.band token tiles:
@@ -88,22 +106,28 @@ __global__ void __launch_bounds__(WideShape::kThreads, 1)
 q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Q8WideParams p)
 {
     using Sh = WideShape;
-    constexpr int S = Sh::kStages, OPS = Sh::kOps;
+    constexpr uint32_t S = Sh::kStages, OPS = Sh::kOps, XOPS = Sh::kXOps, AHEAD = Sh::kAhead;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sW = smem;
     uint8_t *sXraw = sW + S * kQ8WBytes;
     uint8_t *sX16 = sXraw + S * Sh::kRawX;
-    uint64_t *wfull = reinterpret_cast<uint64_t *>(sX16 + OPS * Sh::kX16);
-    uint64_t *wempty = wfull + S;
-    uint64_t *opfull = wempty + S;
-    uint64_t *opempty = opfull + OPS;
-    uint64_t *afull = opempty + OPS;     // [2] accumulators
+    // int8 x of the first kAhead units: those of a set in the buffer where the set
+    // widens x of its unit after them.  A warp reads and writes the same tokens,
+    // which lie in the same rows.
+    uint8_t *sX0 = sX16 + AHEAD * Sh::kX16;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sX16 + XOPS * Sh::kX16);
+    uint64_t *widened = full + S;        // [XOPS] this CTA's W of a unit, and x of the one AHEAD of it
+    uint64_t *opfull = widened + XOPS;   // [XOPS] operands of a unit, both CTAs'
+    uint64_t *done = opfull + XOPS;      // [OPS] MMAs of a unit
+    uint64_t *afull = done + OPS;        // [2] accumulators
     uint64_t *aempty = afull + 2;        // [2]
-    uint64_t *drain = aempty + 2;        // [1]
+    uint64_t *x0full = aempty + 2;       // [1] int8 x of the first AHEAD units
+    uint64_t *x0done = x0full + 1;       // [1] widened
+    uint64_t *drain = x0done + 1;        // [1]
     // opfull and aempty are those of the first CTA, with arrivals from both;
-    // the MMA's commits arrive at both CTAs' opempty and afull
+    // the MMA's commits arrive at both CTAs' done and afull
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *flags = reinterpret_cast<volatile int *>(tmem_slot + 1);  // [0] abort
 
@@ -121,14 +145,17 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmX);
-        for (int i = 0; i < S; ++i) {
-            mbar_init(&wfull[i], 1);
-            mbar_init(&wempty[i], 4);
+        for (int i = 0; i < S; ++i)
+            mbar_init(&full[i], 2);      // W's producer and x's
+        for (int i = 0; i < XOPS; ++i) {
+            mbar_init(&widened[i], 4);
+            // W of both CTAs, which in the first stands for its x too; the first unit of two: the second CTA's x of both
+            mbar_init(&opfull[i], kPair * 4 + (i % kWidenSets == 0 ? 1 : 0));
         }
-        for (int i = 0; i < OPS; ++i) {
-            mbar_init(&opfull[i], kPair * 4);
-            mbar_init(&opempty[i], 1);
-        }
+        for (int i = 0; i < OPS; ++i)
+            mbar_init(&done[i], 1);
+        mbar_init(x0full, 1);
+        mbar_init(x0done, kWidenWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&afull[i], 1);
             mbar_init(&aempty[i], kPair * Sh::kEpiWarps);
@@ -149,73 +176,135 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     // the MMA's addresses in uniform registers
     constexpr uint32_t tmem_base = 0;
 
+    // Unit u - S has left the ring: its W has been widened, and the x that came with it.
+    auto wait_widened = [&](uint32_t u) {
+        return u < S || __all_sync(0xFFFFFFFFu, mbar_wait(&widened[(u - S) % XOPS], (u - S) / XOPS & 1, p.timeout_ns, &flags[0]));
+    };
+    // A producer's end: on an abort, every copy of its first u units lands before it exits.
+    auto drain_ring = [&](bool ok, uint32_t u) {
+        if (!ok)
+            q8_fail(p.err, &flags[0], kErrTimeoutProducer);
+        if (flags[0]) {
+            volatile int never = 0;
+            for (uint32_t k = 0; k < S && k < u; ++k)
+                mbar_wait(&full[k], (u - 1 - k) / S & 1, kDefaultTimeoutNs, &never);
+        }
+    };
+    // x of the second CTA's pairs of units r, r + 2, ... has been widened: passed on to the issuer.
+    auto relay = [&](int r) {
+        bool ok = true;
+        for (uint32_t u = r * kWidenSets; ok && u < static_cast<uint32_t>(units); u += 2 * kWidenSets) {
+            if (u < AHEAD)
+                ok = mbar_wait(x0done, 0, p.timeout_ns, &flags[0]);
+            for (uint32_t v = u; ok && u >= AHEAD && v < u + kWidenSets && v < static_cast<uint32_t>(units); ++v)
+                ok = mbar_wait(&widened[(v - AHEAD) % XOPS], (v - AHEAD) / XOPS & 1, p.timeout_ns, &flags[0]);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok && lane == 0)
+                mbar_arrive_cluster_release(map_shared_rank(smem_u32(&opfull[u % XOPS]), first));
+            __syncwarp();
+        }
+        if (!ok)
+            q8_fail(p.err, &flags[0], kErrTimeoutWiden);
+    };
     if (warp == Sh::kTmaWarp) {
-        // -------------------------------------------------------- TMA producer
+        // ------------------------------------------------------ TMA producer of W
         const bool leader = elect_one();
         const uint64_t pol = policy_evict_normal();
         int np, mt;
-        auto load_w = [&](int j, int kb) {
+        auto load = [&](uint32_t u, int kb) {
             if (leader) {
-                mbar_arrive_expect_tx(&wfull[j % S], kQ8WBytes + Sh::kRawX);
-                tma_load_2d(sW + j % S * kQ8WBytes, &tmW, &wfull[j % S], (kb0 + kb) * kQ8BlockK, (np * kPair + rank) * kTileN, pol);
+                mbar_arrive_expect_tx(&full[u % S], kQ8WBytes);
+                tma_load_2d(sW + u % S * kQ8WBytes, &tmW, &full[u % S], (kb0 + kb) * kQ8BlockK, (np * kPair + rank) * kTileN, pol);
             }
-            __syncwarp();
-        };
-        auto load_x = [&](int j, int kb) {       // this CTA's half of the tokens
-            if (leader)
-                tma_load_2d(sXraw + j % S * Sh::kRawX, &tmX, &wfull[j % S], (kb0 + kb) * kQ8BlockK, mt * MT + rank * kHalfTokens, pol);
             __syncwarp();
         };
         tile_at(p, cluster, np, mt);
-        const int ahead = p.static_w ? min(S, nkb) : 0;
-        for (int j = 0; j < ahead; ++j)  // weights may be requested before the wait for the previous kernel
-            load_w(j, j);
+        const uint32_t ahead = p.static_w ? min(S, nkb) : 0;
+        for (uint32_t u = 0; u < ahead; ++u)     // weights may be requested before the wait for the previous kernel
+            load(u, u);
         pdl_wait();
         pdl_launch_dependents();         // not sooner: see skg_q8_stream.cu
         bool ok = true;
-        int j = 0, issued = ahead;
+        uint32_t u = 0;
         for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
             tile_at(p, tile, np, mt);
-            for (int kb = 0; kb < nkb; ++kb, ++j) {
-                if (j >= ahead) {
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&wempty[j % S], ((j / S) & 1) ^ 1, p.timeout_ns, &flags[0]));
-                    if (!ok)
-                        break;
-                    load_w(j, kb);
-                    issued = j + 1;
-                }
-                load_x(j, kb);
+            for (int kb = 0; kb < nkb; ++kb, ++u) {
+                if (u < ahead)
+                    continue;
+                ok = wait_widened(u);
+                if (!ok)
+                    break;
+                load(u, kb);
             }
         }
-        if (!ok)
-            q8_fail(p.err, &flags[0], kErrTimeoutProducer);
-        if (flags[0]) {                  // abort: let every copy land before exit
-            volatile int never = 0;
-            for (int k = 0; k < S && k < issued; ++k)
-                mbar_wait(&wfull[k], ((issued - 1 - k) / S) & 1, kDefaultTimeoutNs, &never);
+        drain_ring(ok, max(u, ahead));
+    } else if (warp == Sh::kTmaXWarp) {
+        // ------------------------------------------------------ TMA producer of x
+        const bool leader = elect_one();
+        const uint64_t pol = policy_evict_normal();
+        pdl_wait();
+        if (leader)
+            mbar_arrive_expect_tx(x0full, min(units, AHEAD) * Sh::kRawX);
+        __syncwarp();
+        bool ok = true;
+        uint32_t v = 0;
+        for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
+            int np, mt;
+            tile_at(p, tile, np, mt);
+            for (int kb = 0; kb < nkb; ++kb, ++v) {
+                const uint32_t u = v - AHEAD;            // with W of this unit
+                uint8_t *to = sX0 + v % kWidenSets * Sh::kX16 + v / kWidenSets * Sh::kRawX;
+                uint64_t *bar = x0full;
+                if (v >= AHEAD) {
+                    ok = wait_widened(u);
+                    if (!ok)
+                        break;
+                    to = sXraw + u % S * Sh::kRawX;
+                    bar = &full[u % S];
+                }
+                if (leader) {
+                    if (v >= AHEAD)
+                        mbar_arrive_expect_tx(bar, Sh::kRawX);
+                    tma_load_2d(to, &tmX, bar, (kb0 + kb) * kQ8BlockK, mt * MT + rank * kHalfTokens, pol);
+                }
+                __syncwarp();
+            }
         }
+        const uint32_t issued = v > AHEAD ? v - AHEAD : 0;
+        for (uint32_t u = issued; ok && u < static_cast<uint32_t>(units); ++u) {
+            ok = wait_widened(u);        // no x comes with the last units' W
+            if (ok && leader)
+                mbar_arrive(&full[u % S]);
+            __syncwarp();
+        }
+        if (flags[0]) {
+            volatile int never = 0;
+            mbar_wait(x0full, 0, kDefaultTimeoutNs, &never);
+        }
+        drain_ring(ok, issued);
     } else if (warp == Sh::kMmaWarp) {
         // ---------------------------------------------------------- MMA issuer
         if (rank == 0) {
             const bool leader = elect_one();
             const uint64_t x0 = smem_desc_kmajor_sw128(smem_u32(sX16));
             int kb = 0, in_chunk = 0, chunk = 0;
-            bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&opfull[0], 0, p.timeout_ns, &flags[0]));
-            // Two rounds of the operand buffers at a time, unrolled: their
-            // addresses, descriptors and phases are then constants (worked out in
-            // a loop over single units they took longer than the MMAs).
-            for (int j0 = 0; ok && j0 < units; j0 += 2 * OPS) {
+            bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&opfull[0], 0, p.timeout_ns, &flags[0]));
+            // A round of the operand buffers at a time, unrolled: their addresses and
+            // descriptors are then constants (worked out in a loop over single units
+            // they took longer than the MMAs).
+            uint32_t round = 0;
+            for (int j0 = 0; ok && j0 < units; j0 += XOPS, round ^= 1) {
 #pragma unroll
-                for (int u = 0; u < 2 * OPS; ++u) {
+                for (int u = 0; u < XOPS; ++u) {
                     if (!ok || j0 + u >= units)
                         break;
                     constexpr int kHalf = Sh::kX16 / 2 / 16;             // the second 64 k, in descriptor units
-                    const uint64_t bx = x0 + static_cast<uint64_t>((u % OPS) * (Sh::kX16 / 16));
+                    const uint64_t bx = x0 + static_cast<uint64_t>(u * (Sh::kX16 / 16));
                     const uint32_t a = tmem_base + 2 * MT + (u % OPS) * 64;
                     const int t = chunk & 1;
                     const uint32_t d = tmem_base + static_cast<uint32_t>(t * MT);
                     if (in_chunk == 0)
-                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&aempty[t], ((chunk >> 1) & 1) ^ 1, p.timeout_ns, &flags[0]));
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&aempty[t], ((chunk >> 1) & 1) ^ 1, p.timeout_ns, &flags[0]));
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -225,9 +314,9 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                             tc_mma_f16_ts_pair(d, a + 8 * kk, bx + 2 * kk, Sh::kIdesc, (kk > 0 || in_chunk > 0) ? 1u : 0u);
                     }
                     const bool last = j0 + u + 1 == units;
-                    uint64_t *next = &opfull[(u + 1) % OPS];
-                    const uint32_t next_phase = ((u + 1) / OPS) & 1;
-                    const bool ready = __all_sync(0xFFFFFFFFu, last || mbar_try_wait(next, next_phase));
+                    uint64_t *next = &opfull[(u + 1) % XOPS];
+                    const uint32_t next_phase = u + 1 < XOPS ? round : round ^ 1;
+                    const bool ready = __all_sync(0xFFFFFFFFu, last || mbar_try_wait_cluster(next, next_phase));
                     const bool end = ++kb == nkb || in_chunk == kExactBlocks - 1;
                     if (leader) {
 #pragma unroll
@@ -235,7 +324,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                             tc_mma_f16_ts_pair(d, a + 32 + 8 * kk, bx + kHalf + 2 * kk, Sh::kIdesc, 1u);
                         // nobody waits for the last units, and the peer may be gone by then
                         if (j0 + u + OPS < units)
-                            tc_commit_pair_multicast(&opempty[u % OPS], both);
+                            tc_commit_pair_multicast(&done[u % OPS], both);
                         if (end)
                             tc_commit_pair_multicast(&afull[t], both);
                     }
@@ -243,7 +332,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     chunk += end;
                     kb = kb == nkb ? 0 : kb;
                     if (!ready)
-                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(next, next_phase, p.timeout_ns, &flags[0]));
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(next, next_phase, p.timeout_ns, &flags[0]));
                 }
             }
             if (!ok)
@@ -254,33 +343,54 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 volatile int never = 0;
                 mbar_wait(drain, 0, kDefaultTimeoutNs, &never);
             }
+        } else {
+            relay(0);
         }
+    } else if (warp == Sh::kRelayWarp) {
+        if (rank != 0)
+            relay(1);
     } else if (warp < Sh::kFirstEpi) {
         // --------------------------------------------------------------- widen
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * MT;
         const XPiece piece(quarter * 4, lane, kHalfTokens);
-        for (int j = (warp - Sh::kFirstWiden) >> 2; j < units; j += kWidenSets) {
-            const int sl = j % S, b = j % OPS;
-            // The operand buffer first: see skg_q8_split.cu
-            const bool ok = mbar_wait(&opempty[b], ((j / OPS) & 1) ^ 1, p.timeout_ns, &flags[0]) &&
-                            mbar_wait(&wfull[sl], (j / S) & 1, p.timeout_ns, &flags[0]);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {      // the whole warp goes on, or none of it
-                q8_fail(p.err, &flags[0], kErrTimeoutWiden);
+        const uint32_t set = (warp - Sh::kFirstWiden) >> 2;
+        const uint32_t opfull_there = map_shared_rank(smem_u32(opfull), first);
+        bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(x0full, 0, p.timeout_ns, &flags[0]));
+        for (uint32_t u = set; ok && u < AHEAD; u += kWidenSets) {
+            piece.widen<kHalfTokens / 16>(sX0 + set * Sh::kX16 + u / kWidenSets * Sh::kRawX, sX16 + u * Sh::kX16, 16);
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
+        if (ok && lane == 0)
+            mbar_arrive(x0done);
+        for (uint32_t u = set; ok && u < static_cast<uint32_t>(units); u += kWidenSets) {
+            // Unit u - OPS is done, so W has its place in TMEM, and x of unit u + AHEAD =
+            // u - OPS + XOPS its buffer.
+            const uint32_t sl = u % S;
+            ok = mbar_wait_cluster(&done[u % OPS], ((u / OPS) & 1) ^ 1, p.timeout_ns, &flags[0]) &&
+                 mbar_wait(&full[sl], (u / S) & 1, p.timeout_ns, &flags[0]);
+            ok = __all_sync(0xFFFFFFFFu, ok);            // the whole warp goes on, or none of it
+            if (!ok)
                 break;
-            }
             tc_fence_after();
-            widen_row(sW + sl * kQ8WBytes, row, lane_base + b * 64);
-            piece.widen<kHalfTokens / 16>(sXraw + sl * Sh::kRawX, sX16 + b * Sh::kX16, 16);
+            widen_row(sW + sl * kQ8WBytes, row, lane_base + u % OPS * 64);
+            // (beyond the last unit: what is left in the ring, into a buffer that is not read)
+            piece.widen<kHalfTokens / 16>(sXraw + sl * Sh::kRawX, sX16 + (u + AHEAD) % XOPS * Sh::kX16, 16);
             fence_proxy_async_smem();
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&wempty[sl]);
-                mbar_arrive_cluster(map_shared_rank(smem_u32(&opfull[b]), first));
+                mbar_arrive(&widened[u % XOPS]);
+                if (rank == 0)
+                    mbar_arrive(&opfull[u % XOPS]);      // W of this unit, and its x, widened before
+                else
+                    mbar_arrive_cluster(opfull_there + u % XOPS * 8);
             }
         }
+        if (!ok)
+            q8_fail(p.err, &flags[0], kErrTimeoutWiden);
     } else {
         // ------------------------------------------------------------ epilogue
         constexpr int NC = Sh::kCols;
@@ -298,7 +408,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             int acc[NC];
             for (int kb = 0; kb < nkb; kb += kExactBlocks, ++chunk) {
                 const int t = chunk & 1;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&afull[t], (chunk >> 1) & 1, p.timeout_ns, &flags[0]));
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&afull[t], (chunk >> 1) & 1, p.timeout_ns, &flags[0]));
                 if (!ok) {
                     q8_fail(p.err, &flags[0], kErrTimeoutEpilogue);
                     break;
