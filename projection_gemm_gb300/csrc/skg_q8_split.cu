@@ -150,7 +150,6 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 load_w(j);
             if (p.static_w)              // weights may be requested before the wait for the previous kernel
                 pdl_wait();
-            pdl_launch_dependents();     // not sooner: see skg_q8_stream.cu
             for (int j = 0; j < first; ++j)
                 load_x(j);
             int j = first;
@@ -242,6 +241,9 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         // ------------------------------------------- widen x, and the epilogue
         constexpr int NC = Sh::kCols;
         pdl_wait();                      // scales, residual, workspace and y only from here on
+        // Not sooner (see skg_q8_stream.cu), and after this CTA's TMEM is allocated: the
+        // dependents' CTAs may take the rest of an SM's, and they wait for this one.
+        pdl_launch_dependents();
         const int ew = warp - Sh::kFirstEpi;
         const int row = (warp & 3) * 32 + lane;
         const int col0 = (ew >> 2) * NC, valid = p.g.M - m0 - col0;
