@@ -13,11 +13,24 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_floa
 __device__ __forceinline__ uint16_t f32_to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
 // silu(g) = g / (1 + exp(-g)), from exp(-|g|) so that neither side overflows
-// (at g = -89 exp(-g) has left fp32 while the quotient has not).
+// (at g = -89 exp(-g) has left fp32 while the quotient has not).  The fast
+// exponential, off by up to 2 + |g| units in the last place: of 67 million gated
+// values 5.8e-7 get another integer than in 64 bits, with expf 5.7e-7, in plain
+// 32-bit operations 4.2e-7; expf takes 8 to 30% longer.
 __device__ __forceinline__ float silu(float g)
 {
     const float e = __expf(-fabsf(g));
     return g * __fdividef(g < 0.0f ? e : 1.0f, 1.0f + e);
+}
+
+// silu(g) x far below 0, where exp(g) nears or leaves the end of fp32's range, 1 +
+// exp(g) is 1, and x may be large: by quarters of the exponential, each in range.
+constexpr float kFarGate = -80.0f;
+
+__device__ __forceinline__ float far_gated(float g, float x)
+{
+    const float e = __expf(0.25f * g);
+    return x * e * e * g * e * e;
 }
 
 // Four int8 of a word as four fp16: with the sign bit flipped a byte b is

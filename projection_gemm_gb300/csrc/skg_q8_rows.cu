@@ -17,11 +17,11 @@
 // three passes over memory.
 //
 // Measured, with the bytes that have to move (6.70 TB/s copy peak): norm with
-// residual 8192 x 7168 61.7 us (6.66 TB/s), 4096 x 2048 8.0 us (from the L2), 1 x
-// 7168 2.5 us; gated quantiser 4096 x 16384 60.6 us (5.5 TB/s: exp, the quotient
+// residual 8192 x 7168 63.5 us (6.47 TB/s), 4096 x 2048 8.2 us (from the L2), 1 x
+// 7168 2.5 us; gated quantiser 4096 x 16384 56.8 us (5.9 TB/s: exp, the quotient
 // and the conversions issue in 64% of the cycles); quantiser 8192 x 7168 30-35
 // us; rows of odd length cost twice the instructions: norm 8191 x 7169 121 us
-// (3.4 TB/s), quantiser 1023 x 5001 5.0 us; norm 2048 x 20000, three passes, 114.
+// (3.4 TB/s), quantiser 1023 x 5001 5.1 us; norm 2048 x 20000, three passes, 109.
 #include <algorithm>
 
 #include "skg_internal.h"
@@ -140,6 +140,22 @@ __device__ __forceinline__ void load_block(const uint16_t *p, uint32_t *w)
 __device__ __forceinline__ float value(const Raw8 &r, int i)
 {
     return i & 1 ? bf16hi(r.w[i >> 1]) : bf16lo(r.w[i >> 1]);
+}
+
+// The larger of two bf16 in each half of a word, as unsigned integers: of negative
+// gates the lowest.
+__device__ __forceinline__ uint32_t lowest_gate(uint32_t m, const Raw8 &r)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = __vmaxu2(m, r.w[i]);
+    return m;
+}
+
+__device__ __forceinline__ bool far_gate(uint32_t m)
+{
+    constexpr uint32_t kFarBits = 0xC2A0;            // kFarGate
+    return (m & 0xFFFF) > kFarBits || (m >> 16) > kFarBits;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -315,6 +331,7 @@ q8_rows_kernel(const Q8RowParams p)
     float v[NV][8];
     {
         RowLoad<ANY> a[NV], w[NV];
+        uint32_t far = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             a[j].load(x, first + j * step, p.K);
@@ -334,6 +351,28 @@ q8_rows_kernel(const Q8RowParams p)
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     v[j][c] = NORM ? v[j][c] + value(xw, c) : silu(value(xw, c)) * v[j][c];
+                if constexpr (!NORM && WARP) {
+                    if (far_gate(lowest_gate(0, xw))) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            v[j][c] = value(xw, c) < kFarGate ? far_gated(value(xw, c), value(xa, c)) : v[j][c];
+                    }
+                } else if (!NORM) {
+                    far = lowest_gate(far, xw);
+                }
+            }
+        }
+        if (!NORM && !WARP && far_gate(far)) {       // rare: fetched again
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                RowLoad<ANY> b;
+                b.load(x, first + j * step, p.K);
+                const Raw8 xa = b.get();
+                b.load(second, first + j * step, p.K);
+                const Raw8 xw = b.get();
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    v[j][c] = value(xw, c) < kFarGate ? far_gated(value(xw, c), value(xa, c)) : v[j][c];
             }
         }
     }
@@ -414,36 +453,48 @@ q8_rows_kernel(const Q8RowParams p)
 }
 
 // ------------------------------------------------------------------ longer rows
-// The sum that the norm goes on from, scaled where TINY.
-template <bool TINY>
+// EDGE: the norm goes on from the scaled sum, and the gate has values below kFarGate.
+template <bool EDGE>
 __device__ __forceinline__ float long_sum(const Q8RowParams &p, size_t row, int k)
 {
     const float a = bf16_to_f32(p.x[row * p.ldx + k]);
     const float h = p.second ? a + bf16_to_f32(p.second[row * p.ld2 + k]) : a;
-    return TINY ? h * 0x1p90f : h;
+    return EDGE ? h * 0x1p90f : h;
 }
 
-template <bool NORM, bool TINY>
-__device__ __forceinline__ float long_value(const Q8RowParams &p, size_t row, int k, float rms)
+template <bool NORM, bool EDGE>
+__device__ __forceinline__ float long_value(const Q8RowParams &p, size_t row, int k, float rms, float &gate)
 {
     if (NORM) {
-        const float h = long_sum<TINY>(p, row, k);
+        const float h = long_sum<EDGE>(p, row, k);
         return p.gamma ? h * rms * bf16_to_f32(p.gamma[k]) : h * rms;
     }
     const float a = bf16_to_f32(p.x[row * p.ldx + k]);
-    return p.second ? silu(bf16_to_f32(p.second[row * p.ld2 + k])) * a : a;
+    if (!p.second)
+        return a;
+    gate = bf16_to_f32(p.second[row * p.ld2 + k]);
+    return EDGE && gate < kFarGate ? far_gated(gate, a) : silu(gate) * a;
 }
 
 // The maximum and the integers of a row.
-template <bool NORM, bool TINY>
+template <bool NORM, bool EDGE>
 __device__ __forceinline__ void long_row(const Q8RowParams &p, size_t row, float rms, uint32_t *maxima)
 {
     uint32_t m = 0;
-    for (int k = threadIdx.x; k < p.K; k += kLongThreads)
-        m = max(m, abs_bits(long_value<NORM, TINY>(p, row, k, rms)));
+    float gate = 0.0f, lowest = 0.0f;
+    for (int k = threadIdx.x; k < p.K; k += kLongThreads) {
+        m = max(m, abs_bits(long_value<NORM, EDGE>(p, row, k, rms, gate)));
+        lowest = fminf(lowest, gate);
+    }
+    if constexpr (!NORM && !EDGE) {
+        if (__syncthreads_or(lowest < kFarGate)) {
+            long_row<false, true>(p, row, rms, maxima);
+            return;
+        }
+    }
     const RowScale r = row_scale(row_max<false>(m, maxima));
     for (int k = threadIdx.x; k < p.K; k += kLongThreads) {
-        const float v = long_value<NORM, TINY>(p, row, k, rms);
+        const float v = long_value<NORM, EDGE>(p, row, k, rms, gate);
         if (NORM && p.h)                 // may be the residual itself: read by this thread, above
             p.h[row * p.ldh + k] = f32_to_bf16(long_sum<false>(p, row, k));
         if (NORM && p.y)

@@ -106,3 +106,17 @@ def test_norm_of_zeros(K):
         q, s = rows_out(2, K)
         skg.skg_rmsnorm_q8(x, None, None, eps, None, q, s)
         assert bool((q == 0).all()) and bool((s == 0).all() if eps else s.isnan().all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", LENGTHS)
+@pytest.mark.parametrize("lo,hi,size", [(-104, -88, 1e2), (-120, -100, 1e20), (-200, -150, 3e38), (-130, -86, 1e30)])
+def test_quantize_rows_of_large_negative_gates(K, lo, hi, size):
+    """exp(g) below fp32's range, its product with x within: the row has the values of the formula."""
+    g = rng(33, K, -lo)
+    gate = torch.from_numpy(g.uniform(lo, hi, size=(6, K))).to(torch.bfloat16).cuda()
+    x = torch.from_numpy(g.uniform(0.25, 1, size=(6, K)) * size * g.choice([-1.0, 1.0], size=(6, K))).to(torch.bfloat16).cuda()
+    v = R.gated_rows(x, gate)
+    q, s = rows_out(6, K)
+    skg.skg_quantize_q8(x, gate, q, s)
+    R.check_rows(v, q, s, R.row_error(K, gate))
