@@ -17,7 +17,7 @@
 // three passes over memory.
 //
 // Measured, with the bytes that have to move (6.70 TB/s copy peak): norm with
-// residual 8192 x 7168 63.5 us (6.47 TB/s), 4096 x 2048 8.2 us (from the L2), 1 x
+// residual 8192 x 7168 61.2 us (6.72 TB/s), 4096 x 2048 8.2 us (from the L2), 1 x
 // 7168 2.5 us; gated quantiser 4096 x 16384 56.8 us (5.9 TB/s: exp, the quotient
 // and the conversions issue in 64% of the cycles); quantiser 8192 x 7168 30-35
 // us; rows of odd length cost twice the instructions: norm 8191 x 7169 121 us
@@ -378,15 +378,15 @@ q8_rows_kernel(const Q8RowParams p)
     }
     if constexpr (NORM) {
         RowLoad<ANY> w[NV];
-        if (p.gamma) {                   // on its way during the sum
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                w[j].load(p.gamma, first + j * step, p.K);
-        }
         if (p.h) {
 #pragma unroll
             for (int j = 0; j < NV; ++j)
                 store_bf16<ANY>(p.h + row * p.ldh, first + j * step, p.K, v[j]);
+        }
+        if (p.gamma) {                   // on its way during the sum; after h's stores, whose registers it takes
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                w[j].load(p.gamma, first + j * step, p.K);
         }
         auto sum_of_squares = [&](float unit, float *buf) {
             float s = 0.0f;
