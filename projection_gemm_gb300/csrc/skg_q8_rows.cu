@@ -453,9 +453,10 @@ q8_rows_kernel(const Q8RowParams p)
 }
 
 // ------------------------------------------------------------------ longer rows
+// (K up to 2^31 - 1: the index passes it.)
 // EDGE: the norm goes on from the scaled sum, and the gate has values below kFarGate.
 template <bool EDGE>
-__device__ __forceinline__ float long_sum(const Q8RowParams &p, size_t row, int k)
+__device__ __forceinline__ float long_sum(const Q8RowParams &p, size_t row, unsigned k)
 {
     const float a = bf16_to_f32(p.x[row * p.ldx + k]);
     const float h = p.second ? a + bf16_to_f32(p.second[row * p.ld2 + k]) : a;
@@ -463,7 +464,7 @@ __device__ __forceinline__ float long_sum(const Q8RowParams &p, size_t row, int 
 }
 
 template <bool NORM, bool EDGE>
-__device__ __forceinline__ float long_value(const Q8RowParams &p, size_t row, int k, float rms, float &gate)
+__device__ __forceinline__ float long_value(const Q8RowParams &p, size_t row, unsigned k, float rms, float &gate)
 {
     if (NORM) {
         const float h = long_sum<EDGE>(p, row, k);
@@ -482,7 +483,7 @@ __device__ __forceinline__ void long_row(const Q8RowParams &p, size_t row, float
 {
     uint32_t m = 0;
     float gate = 0.0f, lowest = 0.0f;
-    for (int k = threadIdx.x; k < p.K; k += kLongThreads) {
+    for (unsigned k = threadIdx.x; k < static_cast<unsigned>(p.K); k += kLongThreads) {
         m = max(m, abs_bits(long_value<NORM, EDGE>(p, row, k, rms, gate)));
         lowest = fminf(lowest, gate);
     }
@@ -493,7 +494,7 @@ __device__ __forceinline__ void long_row(const Q8RowParams &p, size_t row, float
         }
     }
     const RowScale r = row_scale(row_max<false>(m, maxima));
-    for (int k = threadIdx.x; k < p.K; k += kLongThreads) {
+    for (unsigned k = threadIdx.x; k < static_cast<unsigned>(p.K); k += kLongThreads) {
         const float v = long_value<NORM, EDGE>(p, row, k, rms, gate);
         if (NORM && p.h)                 // may be the residual itself: read by this thread, above
             p.h[row * p.ldh + k] = f32_to_bf16(long_sum<false>(p, row, k));
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kLongThreads) q8_long_rows_kernel(const Q8RowP
     if (NORM) {
         auto sum_of_squares = [&](float unit, float *buf) {
             float s = 0.0f;
-            for (int k = threadIdx.x; k < p.K; k += kLongThreads) {
+            for (unsigned k = threadIdx.x; k < static_cast<unsigned>(p.K); k += kLongThreads) {
                 const float h = long_sum<false>(p, row, k) * unit;
                 s = fmaf(h, h, s);
             }
@@ -563,7 +564,7 @@ cudaError_t launch_rows_as(const Q8RowParams &p, cudaStream_t s)
     const int eights = (p.K + (ANY ? 7 : 0) + 7) / 8;
     auto threads = [&](int values) { return static_cast<unsigned>((eights + 4 * values - 1) / (4 * values) * 32); };
     if (eights <= 128) {
-        const unsigned grid = static_cast<unsigned>((p.M + kWarpRows - 1) / kWarpRows);
+        const unsigned grid = (static_cast<unsigned>(p.M) + kWarpRows - 1) / kWarpRows;
         if (eights <= 32)
             return launch(q8_rows_kernel<NORM, ANY, 8, true>, grid, 32 * kWarpRows, p, s);
         if (eights <= 64)

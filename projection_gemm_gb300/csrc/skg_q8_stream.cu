@@ -190,7 +190,7 @@ template <int NT, int RG, int WARPS, int CTAS, int DEPTH>
 cudaError_t launch_as(const Q8LinearParams &p, bool static_w, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.N + 16 * RG - 1) / (16 * RG)));
+    cfg.gridDim = dim3((static_cast<unsigned>(p.N) + 16 * RG - 1) / (16 * RG));      // N up to 2^31 - 1
     cfg.blockDim = dim3(WARPS * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -120,3 +120,52 @@ def test_quantize_rows_of_large_negative_gates(K, lo, hi, size):
     q, s = rows_out(6, K)
     skg.skg_quantize_q8(x, gate, q, s)
     R.check_rows(v, q, s, R.row_error(K, gate))
+
+
+# -------------------------------------------------------------------------------- the ends of the sizes
+LARGEST = 2 ** 31 - 1
+
+
+@pytest.mark.gpu
+def test_the_longest_row():
+    x = torch.zeros(1, LARGEST, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1023, 1024, 2 ** 30, LARGEST - 1025, LARGEST - 1024, LARGEST - 1], device="cuda")
+    x[0, at] = normal(rng(34), len(at)).cuda()
+    q, s = rows_out(1, LARGEST)
+    skg.skg_quantize_q8(x, None, q, s)
+    want, _ = nearest_even(x[:, at])
+    assert torch.equal(q[:, at].long(), want) and int(torch.count_nonzero(q)) == int((want != 0).sum())
+    assert s[0] == (x[:, at].abs().amax().double() / 127).float()
+
+
+@pytest.mark.gpu
+def test_the_most_rows():
+    """One element each: its integer is -127, 0 or 127."""
+    x = torch.zeros(LARGEST, 1, dtype=torch.bfloat16, device="cuda")
+    x[::3] = 2.0
+    x[1::3] = -0.5
+    x[LARGEST - 1] = 3.0
+    q, s = rows_out(LARGEST, 1)
+    skg.skg_quantize_q8(x, None, q, s)
+    assert q[LARGEST - 1].item() == 127 and s[LARGEST - 1] == torch.tensor(3.0) / 127
+    for first, integer, size in ((0, 127, 2.0), (1, -127, 0.5), (2, 0, 0.0)):
+        end = LARGEST - 1
+        assert bool((q[first:end:3] == integer).all()) and bool((s[first:end:3] == torch.tensor(size) / 127).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 8])
+def test_the_most_channels(M):
+    N, K = LARGEST, 16
+    W = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda", generator=torch.Generator("cuda").manual_seed(35))
+    x, xs = R.integers(rng(35), M, K).cuda(), torch.full((M,), 0.5, device="cuda")
+    ws = torch.ones(N, device="cuda")
+    y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    plan = skg.Q8Plan(M, N, K, "bf16", static_weights=True)
+    plan.run(x, xs, W, ws, None, y)
+    for a in range(0, N, N // 7):
+        b = min(a + 1_000_000, N)
+        assert R.same_bits(y[:, a:b], R.linear(x, xs, W[a:b], ws[a:b], None, "bf16"))
+    assert R.same_bits(y[:, N - 1000:], R.linear(x, xs, W[N - 1000:], ws[N - 1000:], None, "bf16"))
+    assert not bool(y.isnan().any())
+    plan.close()
