@@ -395,6 +395,13 @@ def _bad(what: str):
     raise SkgError(SKG_ERR_INVALID_ARG, what)
 
 
+def _int(v, name) -> int:
+    """A size or selector for the C ABI, whose int ctypes would otherwise cut to 32 bits."""
+    if not -2**31 <= v < 2**31:
+        _bad(f"{name} = {v} does not fit 32 bits")
+    return v
+
+
 def _rows(t, name, shape, dtype) -> int:
     """Row stride of a tensor of `shape` [M, K] whose rows are contiguous."""
     if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
@@ -429,7 +436,7 @@ def skg_rmsnorm_q8(x, residual, gamma, eps: float, h, q, scale, y=None, stream=N
     bf16, shape = torch.bfloat16, x.shape
     if len(shape) != 2:
         _bad("x must be [M, K]")
-    M, K = shape
+    M, K = _int(shape[0], "M"), _int(shape[1], "K")
     ldx = _rows(x, "x", shape, bf16)
     ldr = 0 if residual is None else _rows(residual, "residual", shape, bf16)
     ldh = 0 if h is None else _rows(h, "h", shape, bf16)
@@ -446,7 +453,7 @@ def skg_quantize_q8(x, gate, q, scale, stream=None):
     shape = x.shape
     if len(shape) != 2:
         _bad("x must be [M, K]")
-    M, K = shape
+    M, K = _int(shape[0], "M"), _int(shape[1], "K")
     ldx = _rows(x, "x", shape, torch.bfloat16)
     ldg = 0 if gate is None else _rows(gate, "gate", shape, torch.bfloat16)
     _check(load().skg_quantize_q8(
@@ -456,13 +463,15 @@ def skg_quantize_q8(x, gate, q, scale, stream=None):
 
 def skg_q8_plan_query(M: int, N: int, K: int, epilogue, num_sms: int) -> dict:
     d = skg_q8_plan_desc()
-    _check(load().skg_q8_plan_query(M, N, K, _epi(epilogue), num_sms, ctypes.byref(d)))
+    _check(load().skg_q8_plan_query(_int(M, "M"), _int(N, "N"), _int(K, "K"), _int(_epi(epilogue), "epilogue"),
+                                    _int(num_sms, "num_sms"), ctypes.byref(d)))
     return d.as_dict()
 
 
 def skg_q8_plan(M: int, N: int, K: int, epilogue, static_weights: bool = False) -> int:
     h = ctypes.c_void_p()
-    _check(load().skg_q8_plan(M, N, K, _epi(epilogue), 1 if static_weights else 0, ctypes.byref(h)))
+    _check(load().skg_q8_plan(_int(M, "M"), _int(N, "N"), _int(K, "K"), _int(_epi(epilogue), "epilogue"),
+                              1 if static_weights else 0, ctypes.byref(h)))
     return h.value
 
 
@@ -472,7 +481,7 @@ def skg_q8_run(plan: int, x, x_scale, W, w_scale, residual, y, stream=None):
 
 
 def skg_q8_plan_force(plan: int, kind: int = 0, m_tile: int = 0, split_k: int = 0):
-    _check(load().skg_q8_plan_force(plan, kind, m_tile, split_k))
+    _check(load().skg_q8_plan_force(plan, _int(kind, "kind"), _int(m_tile, "m_tile"), _int(split_k, "split_k")))
 
 
 def skg_q8_plan_info(plan: int) -> dict:

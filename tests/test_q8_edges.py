@@ -169,3 +169,42 @@ def test_the_most_channels(M):
     assert R.same_bits(y[:, N - 1000:], R.linear(x, xs, W[N - 1000:], ws[N - 1000:], None, "bf16"))
     assert not bool(y.isnan().any())
     plan.close()
+
+
+@pytest.mark.parametrize("call", [
+    lambda v: skg.skg_q8_plan_query(v, 128, 128, "bf16", 152), lambda v: skg.skg_q8_plan_query(4, v, 128, "bf16", 152),
+    lambda v: skg.skg_q8_plan_query(4, 128, v, "bf16", 152), lambda v: skg.skg_q8_plan_query(4, 128, 128, v, 152),
+    lambda v: skg.skg_q8_plan_query(4, 128, 128, "bf16", v), lambda v: skg.skg_q8_plan(v, 128, 128, "bf16"),
+    lambda v: skg.skg_q8_plan(4, v, 128, "bf16"), lambda v: skg.skg_q8_plan(4, 128, v, "bf16"),
+    lambda v: skg.skg_q8_plan_force(None, v), lambda v: skg.skg_q8_plan_force(None, 0, 0, v)])
+def test_sizes_beyond_32_bits_are_refused_not_cut(call):
+    for v in (2 ** 32 + 16, 2 ** 33 + 128, 2 ** 31, -2 ** 32 + 16):
+        with pytest.raises(skg.SkgError) as e:
+            call(v)
+        assert e.value.status == skg.SKG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("shape", [(2 ** 32 + 5, 1), (1, 2 ** 32 + 8), (2 ** 31, 1)])
+def test_rows_beyond_32_bits_are_refused_not_cut(shape):
+    """A tensor as the binding sees one: shape, type, strides, place."""
+    class Huge:
+        dtype, is_cuda = torch.bfloat16, True
+
+        def __init__(self, shape, dtype=torch.bfloat16):
+            self.shape, self.dtype = torch.Size(shape), dtype
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 1 << 20
+
+        def get_device(self):
+            return 0
+
+    x, q, s = Huge(shape), Huge(shape, torch.int8), Huge(shape[:1], torch.float32)
+    for call in (lambda: skg.skg_rmsnorm_q8(x, None, None, 1e-6, None, q, s, stream=0),
+                 lambda: skg.skg_quantize_q8(x, None, q, s, stream=0)):
+        with pytest.raises(skg.SkgError) as e:
+            call()
+        assert e.value.status == skg.SKG_ERR_INVALID_ARG
