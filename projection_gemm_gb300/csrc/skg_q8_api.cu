@@ -216,12 +216,17 @@ skg_status ensure_workspace(skg_q8_plan_s *p, const char *who)
     const size_t need = p->d.workspace_bytes;
     if (need <= p->ws_cap)
         return SKG_OK;
+    try {                             // the only allocation that could throw, out of a C entry
+        p->retired.reserve(p->retired.size() + 1);
+    } catch (const std::bad_alloc &) {
+        return set_error(SKG_ERR_CUDA, "%s: out of host memory", who);
+    }
     void *ws = nullptr;
     const cudaError_t e = cudaMalloc(&ws, need);
     if (e != cudaSuccess)
         return launched(e, who);
     if (p->ws)
-        p->retired.push_back(p->ws);
+        p->retired.push_back(p->ws);  // has its place
     p->ws = ws;
     p->ws_cap = need;
     return SKG_OK;
