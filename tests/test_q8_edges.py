@@ -6,7 +6,7 @@ import torch
 
 from projection_gemm_gb300 import skg
 from tests import q8_reference as R
-from tests.test_q8_gpu import normal, rng, rows_out
+from tests.test_q8_gpu import Linear, normal, rng, rows_out
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -208,3 +208,138 @@ def test_rows_beyond_32_bits_are_refused_not_cut(shape):
         with pytest.raises(skg.SkgError) as e:
             call()
         assert e.value.status == skg.SKG_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------------------------------- projection
+def cancelling(g, M, N, K):
+    """Operands whose sums over the first half of K are near 127^2 K / 2 and over all of it small: what an addition
+    of large partial sums loses shows in every bit of the result."""
+    half = K // 2
+    x, W = R.integers(g, M, K, 100, 127), R.integers(g, N, K, 100, 127)
+    x[:, half:] = x[:, :half]
+    W[:, half:] = -W[:, :half]
+    at = torch.from_numpy(g.choice(K, size=40, replace=False))
+    x[:, at] = R.integers(g, M, 40)
+    W[:, at] = R.integers(g, N, 40)
+    return x.cuda(), W.cuda()
+
+
+STREAM = (skg.SKG_Q8_KERNEL_STREAM, 0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,m_tile,split", [STREAM] + [(skg.SKG_Q8_KERNEL_SPLIT, t, k) for t in (32, 64) for k in range(1, 9)] +
+                         [(skg.SKG_Q8_KERNEL_WIDE, 128, k) for k in range(1, 5)])
+def test_large_partial_sums_that_cancel(kind, m_tile, split):
+    for M, N, K in [(16, 260, 16400), (70, 130, 8192)]:
+        if kind == skg.SKG_Q8_KERNEL_STREAM and M > 16:
+            continue
+        x, W = cancelling(rng(36, M, K), M, N, K)
+        sums = x.double() @ W.double().t()
+        half = (x[:, :K // 2].double() @ W[:, :K // 2].double().t()).abs().max()
+        assert float(half) > 2 ** 25 and float(sums.abs().max()) < 2 ** 24
+        one = torch.ones(max(M, N), device="cuda")
+        y = torch.empty(M, N, dtype=torch.float32, device="cuda")
+        plan = skg.Q8Plan(M, N, K, "fp32")
+        plan.force(kind, m_tile, split)
+        plan.run(x, one[:M], W, one[:N], None, y)
+        assert torch.equal(y.double(), sums)
+        plan.close()
+
+
+def with_workspace(M, N, K):
+    """A plan that puts sums away: K of one CTA."""
+    plan = skg.Q8Plan(M, N, K, "fp32", static_weights=True)
+    plan.force(skg.SKG_Q8_KERNEL_SPLIT, 64 if M > 32 else 32, 1)
+    assert plan.info()["workspace_bytes"] > 0
+    return plan
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(48, 2000, 8192), (20, 300, 16400), (200, 640, 5120)])
+def test_workspaces_of_two_plans_at_once(M, N, K):
+    cs = [Linear(M, N, K, "fp32", 40 + i) for i in range(2)]
+    plans, streams = [with_workspace(M, N, K) for _ in cs], [torch.cuda.Stream() for _ in cs]
+    want = [c.want() for c in cs]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for c, p, s in zip(cs, plans, streams):
+            c.run(p, s)
+    for c, p, w in zip(cs, plans, want):
+        p.check()
+        assert R.same_bits(c.y, w)
+        p.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("M,N,K", [(48, 2000, 8192), (20, 300, 16400), (64, 7168, 7168), (200, 640, 5120)])
+def test_runs_of_one_plan_follow_each_other_with_nothing_between(M, N, K, graph):
+    """Alternating inputs, an output each: a run's sums in the workspace are not the next one's."""
+    cs = [Linear(M, N, K, "fp32", 50 + i) for i in range(2)]
+    want = [c.want() for c in cs]
+    ys = [torch.full((M, N), float("nan"), device="cuda") for _ in range(12)]
+    plan = with_workspace(M, N, K)
+
+    def runs():
+        for i, y in enumerate(ys):
+            c = cs[i % 2]
+            plan.run(c.x, c.xs, c.W, c.ws, None, y)
+
+    torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            runs()
+        g.replay()
+    else:
+        runs()
+    plan.check()
+    torch.cuda.synchronize()
+    for i, y in enumerate(ys):
+        assert R.same_bits(y, want[i % 2]), i
+    plan.close()
+
+
+@pytest.mark.gpu
+def test_a_graph_of_a_plan_forced_to_other_workspaces():
+    """Runs captured with a workspace that the plan then outgrows keep their own."""
+    M, N, K = 40, 640, 16384
+    c = Linear(M, N, K, "fp32", 60)
+    want = c.want()
+    plan = skg.Q8Plan(M, N, K, "fp32")
+    graphs = []
+    for split in (8, 4, 2, 1):
+        plan.force(skg.SKG_Q8_KERNEL_SPLIT, 64, split)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(plan)
+        graphs.append(g)
+    assert plan.info()["workspace_bytes"] > 0
+    for g in graphs + graphs[::-1]:
+        c.y.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert R.same_bits(c.y, want)
+    plan.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(300, 10000, 1280), (130, 2000, 528), (1500, 2300, 2064), (129, 257, 128), (4096, 3000, 384)])
+def test_wide_runs_follow_each_other_with_nothing_between(M, N, K):
+    """The widened operands of one launch's last units and of the next one's first."""
+    cs = [Linear(M, N, K, "fp32", 70 + i) for i in range(2)]
+    want = [c.want() for c in cs]
+    ys = [torch.full((M, N), float("nan"), device="cuda") for _ in range(10)]
+    for split in (1, 2):
+        plan = skg.Q8Plan(M, N, K, "fp32", static_weights=split == 1)
+        plan.force(skg.SKG_Q8_KERNEL_WIDE, 128, split)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for i, y in enumerate(ys):
+                c = cs[i % 2]
+                plan.run(c.x, c.xs, c.W, c.ws, None, y)
+        plan.check()
+        for i, y in enumerate(ys):
+            assert R.same_bits(y, want[i % 2]), (split, i)
+        plan.close()
