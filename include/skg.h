@@ -432,6 +432,8 @@ SKG_API skg_status skg_group_destroy(skg_group_t group);
  * the nearest integer, half to even.  A row of zeros has scale 0 and q = 0.  A
  * row with a value that is not finite (NaN, infinity) has scale NaN and q = 0:
  * a projection of that row is NaN, and no other row is affected.
+ * Rows of any length can be quantised; a projection takes K in multiples of 16, so
+ * rows that are to be projected are made that long, with zeros, before.
  *
  * skg_rmsnorm_q8 -- residual addition, root-mean-square norm and quantisation
  * of M >= 0 rows of any length K >= 1, in one kernel on `stream`:

@@ -60,7 +60,9 @@ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 // Clusters resident at once on 152 SMs, by what a cluster's tile has its K
 // split into (cudaOccupancyMaxActiveClusters; a cluster stays within one GPC):
 // CTAs of the split kernel, two to an SM; pairs of the wide kernel, one CTA to
-// an SM.  43 tiles split in 7 are 301 CTAs, but 38 clusters at a time.
+// an SM.  43 tiles split in 7 are 301 CTAs, but 38 clusters at a time.  (With
+// another number of SMs the counts are scaled, which clusters need not follow; a
+// launch that does not fit takes longer and gives the same result.)
 constexpr int kSplitResident[] = {0, 304, 152, 97, 74, 58, 46, 38, 36};
 constexpr int kWideResident[] = {0, 76, 36, 23, 15};
 static_assert(sizeof(kWideResident) / sizeof(int) == kQ8WideMaxSplit + 1, "a count for each split");
@@ -121,9 +123,9 @@ TcChoice choose_split(const skg_q8_plan_desc &d, int m_tile, int split, int num_
 }
 
 // Pairs that share a tile's K in the wide kernel, in the same way.  Measured
-// with 1, 2, 3 and 4: 128 x 7168 x 7168 26.3, 19.7, 30.6, 29.8; 65 x 7168 x 16384
-// 53, 31.9, 47, 41; 128 x 2048 x 4096 17.1, 12.8, 10.9, 11.3; 100 x 8192 x 2048
-// 11.8, 11.9, 20.3, 29.2.
+// with 1, 2, 3 and 4: 128 x 7168 x 7168 29.4, 22.0, 34.7, 32.9; 65 x 7168 x 16384
+// 58, 36.1, 53, 46; 128 x 2048 x 4096 19.0, 14.6, 12.7, 12.8; 100 x 8192 x 2048
+// 13.7, 13.0, 22.8, 32.7.
 TcChoice choose_wide(const skg_q8_plan_desc &d, int split, int num_sms)
 {
     const int nkb = ceil_div(d.K, kQ8BlockK), mt = q8_wide_shape().m_tile;
@@ -151,9 +153,10 @@ bool prefer_stream(const skg_q8_plan_desc &d, int num_sms)
 }
 
 // The split or the wide kernel.  Measured, split then wide: 24 x 28672 x 8192
-// 46 and 57, 64 x 28672 x 8192 59 and 58, 128 x 1024 x 7168 9.8 and 12.3, 128 x
-// 7168 x 7168 26.9 and 19.7, 256 x 4096 x 4096 17.4 and 15.3, 1849 x 680 x 320
-// 5.7 and 8.0, 1000 x 4096 x 4096 58 and 32.
+// 47 and 63, 128 x 1024 x 7168 10.0 and 13.9, 128 x 7168 x 7168 26.5 and 21.9,
+// 256 x 4096 x 4096 18.5 and 16.7, 1849 x 680 x 320 5.5 and 8.7, 1000 x 4096 x
+// 4096 52 and 33.6.  It is furthest off at 64 x 28672 x 8192, 55.6 and 63.5, where
+// the wide kernel is taken.
 bool prefer_split(const skg_q8_plan_desc &d, int num_sms)
 {
     return choose_split(d, 0, 0, num_sms).us <= choose_wide(d, 0, num_sms).us;

@@ -571,7 +571,7 @@ cudaError_t launch_rows_as(const Q8RowParams &p, cudaStream_t s)
             return launch(q8_rows_kernel<NORM, ANY, 16, true>, grid, 32 * kWarpRows, p, s);
         return launch(q8_rows_kernel<NORM, ANY, 32, true>, grid, 32 * kWarpRows, p, s);
     }
-    const bool few = p.M <= 2 * 152;
+    const bool few = p.M <= 2 * 152;     // two rows for each of a GB300's SMs
     if (few && eights <= 1024)
         return launch(q8_rows_kernel<NORM, ANY, 8, false>, p.M, threads(8), p, s);
     if constexpr (!ANY) {

@@ -38,10 +38,11 @@
 // which leave their sums in shared memory and add them up as the split kernel's
 // CTAs do.
 //
-// Measured, weights from HBM: 4096 x 12288 x 7168 483-500 us (1.44-1.49 PFLOP/s of
+// Measured, weights from HBM: 4096 x 12288 x 7168 483-513 us (1.41-1.49 PFLOP/s of
 // the 1.96 that cuBLAS reaches; it draws 1.34 kW and the clock falls to 1.8 GHz
-// if it runs for seconds), 1024 x 7168 x 7168 76 us (1.38), 333 x 5001 x 4112 22.5
-// us, 256 x 4096 x 4096 16.8 us, 128 x 7168 x 7168 22.1 us.  A unit takes 0.41 us,
+// if it runs for seconds), 1024 x 7168 x 7168 76 us (1.38; 82 right after the
+// former), 333 x 5001 x 4112 22.4 us, 256 x 4096 x 4096 16.7 us (19.3 unsplit), 128 x
+// 7168 x 7168 22.0 us (29.4 unsplit).  A unit takes 0.41 us,
 // where its MMAs take 0.27.  What bounds it is the widening, and how soon the ring
 // is filled again: an iteration of a set of widening warps works for 1030 cycles and
 // waits for 500, a load takes 2200 until it has arrived, and with the producers'
