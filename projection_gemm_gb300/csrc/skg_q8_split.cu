@@ -128,6 +128,10 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         asm volatile("bar.sync 2, %0;" :: "n"(Sh::kThreads - 32) : "memory");
         tc_fence_after();
         tmem_base = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+        // Without x there is nothing to do before the previous kernel's end, and the
+        // bounded waits do not count its time.  Scales, residual, workspace and y are
+        // touched only from here on.
+        pdl_wait();
     }
 
     if (warp == Sh::kTmaWarp) {
@@ -240,7 +244,6 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     } else {
         // ------------------------------------------- widen x, and the epilogue
         constexpr int NC = Sh::kCols;
-        pdl_wait();                      // scales, residual, workspace and y only from here on
         // Not sooner (see skg_q8_stream.cu), and after this CTA's TMEM is allocated: the
         // dependents' CTAs may take the rest of an SM's, and they wait for this one.
         pdl_launch_dependents();

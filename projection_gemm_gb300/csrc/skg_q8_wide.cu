@@ -130,7 +130,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     // opfull and aempty are those of the first CTA, with arrivals from both;
     // the MMA's commits arrive at both CTAs' done and afull
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
-    volatile int *flags = reinterpret_cast<volatile int *>(tmem_slot + 1);  // [0] abort
+    volatile int *flags = reinterpret_cast<volatile int *>(tmem_slot + 1);  // [0] abort, [1] the previous kernel has ended
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // A cluster is p.split pairs, each with its part of K.  With more than one
@@ -162,7 +162,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             mbar_init(&aempty[i], kPair * Sh::kEpiWarps);
         }
         mbar_init(drain, 1);
-        flags[0] = 0;
+        flags[0] = flags[1] = 0;
         fence_mbar_init();
     }
     __syncthreads();
@@ -177,6 +177,19 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     // the MMA's addresses in uniform registers
     constexpr uint32_t tmem_base = 0;
 
+    // A warp's first wait, for what comes of x: its limit does not count the previous
+    // kernel's time.  (pdl_wait in these warps does the same, and a block of 64 tokens
+    // took 77 us instead of 72, one of 1024 283 instead of 278.)
+    auto first_wait = [&](uint64_t *bar) {
+        uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait_cluster(bar, 0)) {
+            if (flags[1] == 0)
+                t0 = globaltimer_ns();
+            if (flags[0] || globaltimer_ns() - t0 > p.timeout_ns)
+                return false;
+        }
+        return true;
+    };
     // Unit u - S has left the ring: its W has been widened, and the x that came with it.
     auto wait_widened = [&](uint32_t u) {
         return u < S || __all_sync(0xFFFFFFFFu, mbar_wait(&widened[(u - S) % XOPS], (u - S) / XOPS & 1, p.timeout_ns, &flags[0]));
@@ -196,7 +209,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         bool ok = true;
         for (uint32_t u = r * kWidenSets; ok && u < static_cast<uint32_t>(units); u += 2 * kWidenSets) {
             if (u < AHEAD)
-                ok = mbar_wait(x0done, 0, p.timeout_ns, &flags[0]);
+                ok = first_wait(x0done);
             for (uint32_t v = u; ok && u >= AHEAD && v < u + kWidenSets && v < static_cast<uint32_t>(units); ++v)
                 ok = mbar_wait(&widened[(v - AHEAD) % XOPS], (v - AHEAD) / XOPS & 1, p.timeout_ns, &flags[0]);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -224,6 +237,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         for (uint32_t u = 0; u < ahead; ++u)     // weights may be requested before the wait for the previous kernel
             load(u, u);
         pdl_wait();
+        flags[1] = 1;
         pdl_launch_dependents();         // not sooner: see skg_q8_stream.cu
         bool ok = true;
         uint32_t u = 0;
@@ -289,7 +303,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             const bool leader = elect_one();
             const uint64_t x0 = smem_desc_kmajor_sw128(smem_u32(sX16));
             int kb = 0, in_chunk = 0, chunk = 0;
-            bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&opfull[0], 0, p.timeout_ns, &flags[0]));
+            bool ok = __all_sync(0xFFFFFFFFu, first_wait(&opfull[0]));
             // A round of the operand buffers at a time, unrolled: their addresses and
             // descriptors are then constants (worked out in a loop over single units
             // they took longer than the MMAs).
@@ -357,7 +371,7 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         const XPiece piece(quarter * 4, lane, kHalfTokens);
         const uint32_t set = (warp - Sh::kFirstWiden) >> 2;
         const uint32_t opfull_there = map_shared_rank(smem_u32(opfull), first);
-        bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(x0full, 0, p.timeout_ns, &flags[0]));
+        bool ok = __all_sync(0xFFFFFFFFu, first_wait(x0full));
         for (uint32_t u = set; ok && u < AHEAD; u += kWidenSets) {
             piece.widen<kHalfTokens / 16>(sX0 + set * Sh::kX16 + u / kWidenSets * Sh::kRawX, sX16 + u * Sh::kX16, 16);
             fence_proxy_async_smem();

@@ -343,3 +343,26 @@ def test_wide_runs_follow_each_other_with_nothing_between(M, N, K):
         for i, y in enumerate(ys):
             assert R.same_bits(y, want[i % 2]), (split, i)
         plan.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [20, 200])
+def test_a_projection_after_a_kernel_that_takes_long(M):
+    """The bounded waits of a launch that starts early do not count what the kernel before it takes."""
+    x = torch.zeros(1, LARGEST, dtype=torch.bfloat16, device="cuda")
+    x[0, -1] = 2.0 ** -90                               # with eps = 0 the sum is taken twice: longer than the limit
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    q, s = rows_out(1, LARGEST)
+    c = Linear(M, 500, 1024, "bf16", 80)
+    want = c.want()
+    plan = skg.Q8Plan(M, 500, 1024, "bf16", static_weights=True)
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    a.record()
+    skg.skg_rmsnorm_q8(x, x, x[0], 0.0, h, q, s, y)
+    c.run(plan)
+    b.record()
+    plan.check()
+    assert R.same_bits(c.y, want) and q[0, -1] == 127
+    assert a.elapsed_time(b) > 1000
+    plan.close()
