@@ -555,6 +555,182 @@ SKG_API skg_status skg_q8_debug_wait_timeout(skg_q8_plan_t plan, unsigned long l
 /* Free the plan (after its work finished). */
 SKG_API skg_status skg_q8_plan_destroy(skg_q8_plan_t plan);
 
+/*
+ * The 8-bit floating point path -- projections of e4m3 numbers with an fp32 scale
+ * for each block of 128: for tokens and weights whose range one scale a row does
+ * not serve, of one weight or of the experts that the tokens go to.
+ *
+ *   activations:  q[m,k] e4m3, scale[m, k / 128]:          q * scale is the value
+ *   weights:      q[n,k] e4m3, scale[n / 128, k / 128]
+ *   projection:   y[m,n] = sum_b x_scale[m,b] w_scale[n / 128, b]
+ *                          sum_(k in block b) x[m,k] W[n,k]   (+ residual[m,n])
+ *
+ * (Divisions of indexes round down; the last block of a row or column is short
+ * where 128 does not divide it.)  These are serving operators: no gradients.
+ *
+ * Quantising a block of values v (fp32): scale = max|v| / 448, q = e4m3(v * f) with
+ * f = 448 / max|v|, each operation rounded to fp32 and the product to e4m3, half
+ * to even.  A block of zeros has scale 0 and q = 0.  A block with a value that is
+ * not finite has scale NaN and q = 0: a projection that reads it is NaN.
+ *
+ * skg_quantize_f8 -- M >= 0 rows of any K >= 1: of x, or of silu(gate) * x with
+ * silu(g) = g / (1 + exp(-g)); or row i of the output from row rows[i] of those.
+ *   x, gate  bf16 rows of K, row strides ldx, ldg >= K; gate may be NULL.  Both may
+ *            be halves of one [M, 2K] tensor
+ *   rows     int32 [M], or NULL.  With rows, x and gate have x_rows >= 0 rows, and
+ *            an index outside [0, x_rows) gives a row of q = 0, scale = 0.  Without,
+ *            they have M, and x_rows is not read
+ *   q, scale e4m3 [M, K] and fp32 [M, ceil(K / 128)], dense
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_quantize_f8(int M, int K, const void *x, size_t ldx, const void *gate, size_t ldg, const int *rows,
+                                   int x_rows, void *q, float *scale, void *stream);
+
+/*
+ * skg_quantize_f8_weights -- weights W bf16 [experts, N, K] (experts = 1 for one
+ * weight), dense, to q e4m3 of the same shape and scale fp32 [experts,
+ * ceil(N / 128), ceil(K / 128)].
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_ALIGNMENT, SKG_ERR_UNSUPPORTED (more than
+ * 2^31 - 1 blocks), SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_quantize_f8_weights(int experts, int N, int K, const void *W, void *q, float *scale, void *stream);
+
+typedef enum skg_f8_kernel_kind {
+    SKG_F8_KERNEL_SPLIT = 1,    /* few tokens (of each expert): 128 channels x m_tile tokens, K split over the CTAs of
+                                   a cluster, joined in shared memory */
+    SKG_F8_KERNEL_WIDE = 2      /* many: 256 tokens x 256 channels by pairs of CTAs */
+} skg_f8_kernel_kind;
+
+/* What a plan of the 8-bit floating point path will launch. */
+typedef struct skg_f8_plan_desc {
+    int kernel_kind;            /* skg_f8_kernel_kind */
+    int M, N, K, epilogue;
+    int experts;                /* 0: one weight */
+    int static_weights;         /* see skg_f8_plan */
+    int m_tile, n_tile;         /* tokens and channels of a tile */
+    int tiles;                  /* output tiles; with experts the most that offsets can ask for */
+    int split_k;                /* SPLIT: CTAs that share a tile's K, 1..8; WIDE: 1 */
+    int grid, threads, smem_bytes, stages, ctas_per_sm;
+} skg_f8_plan_desc;
+
+typedef struct skg_f8_plan_s *skg_f8_plan_t;
+
+/*
+ * skg_f8_plan_query -- the launch of a projection on a GPU with num_sms SMs,
+ * without touching any GPU.  1 <= M <= 2^20 rows, N >= 1, K a multiple of 16 in
+ * [16, 131072], epilogue as for skg_plan, experts in [0, 1024].
+ * Errors: SKG_ERR_INVALID_ARG (M, N, num_sms, experts, epilogue, NULL),
+ * SKG_ERR_UNSUPPORTED (K, M or experts above the limits, more than 2^31 - 256
+ * channels of all experts, or more than 2^27 tiles).
+ */
+SKG_API skg_status skg_f8_plan_query(int M, int N, int K, int epilogue, int experts, int num_sms, skg_f8_plan_desc *out);
+
+/*
+ * skg_f8_plan -- build a plan on the current device.  experts = 0: every row by one
+ * weight.  experts = E > 0: rows sorted by expert, rows offsets[e] to
+ * offsets[e + 1] by weight e.  static_weights as for skg_q8_plan (with experts it
+ * changes nothing: which weight comes first is known from offsets).  Allocates a
+ * mapped host word for device-side error reports and no device memory; free the
+ * plan with skg_f8_plan_destroy.
+ * Errors: as skg_f8_plan_query, plus SKG_ERR_CUDA.  *out is NULL on failure.
+ */
+SKG_API skg_status skg_f8_plan(int M, int N, int K, int epilogue, int experts, int static_weights, skg_f8_plan_t *out);
+
+/*
+ * skg_f8_run -- the projection on `stream`.
+ *   x        e4m3 [M,K] dense, 16-byte aligned; x_scale fp32 [M, ceil(K / 128)]
+ *   W        e4m3 [N,K], or [E,N,K], dense, 16-byte aligned; w_scale fp32
+ *            [ceil(N / 128), ceil(K / 128)], or [E, ...] of that
+ *   residual bf16 [M,N], non-NULL iff the epilogue is SKG_EPI_BF16_RESIDUAL
+ *   offsets  int32 [E + 1] on the device, ascending within [0, M], non-NULL iff the
+ *            plan has experts (as skg_experts_sort writes them).  Rows before the
+ *            first and behind the last of them are left as they were in y.  Other
+ *            numbers are taken as the nearest that are allowed, in order
+ *   y        [M,N] bf16 (fp32 for SKG_EPI_FP32); must not overlap the inputs
+ * Sums of products and over blocks are fp32, the residual is added in fp32, and the
+ * result is rounded once.  The order of the sum over blocks depends on the launch
+ * shape: a plan gives the same bits each time, and a row's result does not depend
+ * on the other rows.
+ * Allocates nothing and keeps no workspace: runs of a plan may be in flight at the
+ * same time.  The plan's device must be the current one.
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_ALIGNMENT, SKG_ERR_DEVICE_TIMEOUT
+ * (reported by an earlier launch of this plan), SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_f8_run(skg_f8_plan_t plan, const void *x, const float *x_scale, const void *W, const float *w_scale,
+                              const void *residual, const int *offsets, void *y, void *stream);
+
+/*
+ * skg_f8_plan_force -- override of the kernel choice (tests and measurements):
+ * kind (an skg_f8_kernel_kind, 0 keeps), m_tile (SPLIT: 16, 32, 64, 128; WIDE: 256;
+ * 0 = chosen) and split_k (SPLIT: 1..8, no finer than K / 128; 0 = chosen).
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED.
+ */
+SKG_API skg_status skg_f8_plan_force(skg_f8_plan_t plan, int kind, int m_tile, int split_k);
+
+/* Copy the plan's launch description into *out. */
+SKG_API skg_status skg_f8_plan_info(skg_f8_plan_t plan, skg_f8_plan_desc *out);
+
+/* As skg_q8_plan_check. */
+SKG_API skg_status skg_f8_plan_check(skg_f8_plan_t plan);
+
+/* skg_debug_wait_timeout with the word of this plan. */
+SKG_API skg_status skg_f8_debug_wait_timeout(skg_f8_plan_t plan, unsigned long long timeout_ns, void *stream);
+
+/* Free the plan (after its work finished). */
+SKG_API skg_status skg_f8_plan_destroy(skg_f8_plan_t plan);
+
+/*
+ * Tokens to their experts and back.  T tokens choose k experts each; the T * k
+ * choices become R = T * k rows, sorted by expert.
+ *
+ * skg_experts_sort -- from expert int32 [T, k]:
+ *   offsets  int32 [experts + 1]: expert e has the sorted rows offsets[e] to offsets[e + 1]
+ *   rows     int32 [T * k]: the token of each sorted row; -1 behind the last
+ *   pos      int32 [T, k]: the sorted row of each choice; -1 where expert[t, j] is
+ *            outside [0, experts), a choice that goes nowhere
+ * Rows of an expert are in the order of their choices (t, then j).  The same expert
+ * twice makes two rows.  One launch.  T >= 0, k >= 1, 1 <= experts <= 1024, T * k
+ * <= 2^24.
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_experts_sort(int T, int k, int experts, const int *expert, int *offsets, int *rows, int *pos,
+                                    void *stream);
+
+/*
+ * skg_experts_gather -- out[p] = x[rows[p]] for R >= 0 rows, zeros where rows[p] is
+ * outside [0, T).  Its gradient is skg_experts_combine without weights.
+ *   x bf16 [T, N], row stride ldx >= N; rows int32 [R]; out bf16 [R, N] dense; N <= 2^30
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_experts_gather(int R, int T, int N, const void *x, size_t ldx, const int *rows, void *out, void *stream);
+
+/*
+ * skg_experts_combine -- out[t] = residual[t] + sum_j weight[t,j] y[pos[t,j]], in
+ * fp32 in the order of j, rounded once.  A choice whose pos is outside [0, R) is
+ * left out, whatever its weight; a token without any has its residual, or zeros.
+ *   y bf16 [R, N], row stride ldy >= N; pos int32 [T, k]; weight fp32 [T, k], or
+ *   NULL for ones; residual bf16 [T, N] dense, or NULL; out bf16 [T, N] dense, which
+ *   may be the residual.  N <= 2^30, T * k < 2^31
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_experts_combine(int T, int k, int R, int N, const void *y, size_t ldy, const int *pos,
+                                       const float *weight, const void *residual, void *out, void *stream);
+
+/*
+ * skg_experts_combine_grad -- gradients of skg_experts_combine with weights:
+ *   grad_y[pos[t,j]] = weight[t,j] grad_out[t], rounded once; rows that no choice
+ *                    goes to are left as they were.  bf16 [R, N] dense
+ *   grad_weight[t,j] = <grad_out[t], y[pos[t,j]]>, fp32, 0 where a choice was left out
+ *   grad_out bf16 [T, N] dense; the others as for skg_experts_combine.  (The
+ *   residual's gradient is grad_out itself.)
+ * A sorted row belongs to one choice: where pos has the same row twice, grad_y has
+ * one of the two.
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
+ */
+SKG_API skg_status skg_experts_combine_grad(int T, int k, int R, int N, const void *grad_out, const void *y, size_t ldy,
+                                            const int *pos, const float *weight, void *grad_y, float *grad_weight,
+                                            void *stream);
+
 #ifdef __cplusplus
 }
 #endif

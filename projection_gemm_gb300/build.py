@@ -23,7 +23,8 @@ LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libskg.so")
 
 SOURCES = ["skg_api.cu", "skg_gemv.cu", "skg_splitk_tc.cu", "skg_group_tc.cu", "skg_prefetch.cu", "skg_rowpar.cu",
-           "skg_q8_api.cu", "skg_q8_rows.cu", "skg_q8_stream.cu", "skg_q8_split.cu", "skg_q8_wide.cu"]
+           "skg_q8_api.cu", "skg_q8_rows.cu", "skg_q8_stream.cu", "skg_q8_split.cu", "skg_q8_wide.cu",
+           "skg_f8_api.cu", "skg_f8_rows.cu", "skg_f8_split.cu", "skg_f8_wide.cu", "skg_experts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

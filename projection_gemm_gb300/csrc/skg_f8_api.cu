@@ -1,0 +1,372 @@
+// skg_f8_api.cu -- host side of the 8-bit floating point path of include/skg.h:
+// argument checks, plans and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <new>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "skg.h"
+#include "skg_f8_internal.h"
+#include "skg_internal.h"
+
+using namespace skg;
+
+struct skg_f8_plan_s {
+    skg_f8_plan_desc d;
+    int device = 0, num_sms = 0;
+    unsigned int *err_host = nullptr; // mapped pinned word
+    unsigned int *err_dev = nullptr;
+    cudaStream_t last_stream = nullptr;
+};
+
+namespace {
+
+constexpr int kF8MaxK = 131072;
+constexpr int kF8MaxM = 1 << 20;
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }      // null is aligned
+
+skg_status launched(cudaError_t e, const char *who)
+{
+    return e == cudaSuccess ? SKG_OK
+                            : set_error(SKG_ERR_CUDA, "%s: %s (%s)", who, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+
+// Clusters of the split kernel resident at once on 152 SMs, by the CTAs of a
+// cluster, two to an SM (cudaOccupancyMaxActiveClusters; a cluster stays within
+// one GPC).  (With another number of SMs the counts are scaled; a launch that does
+// not fit takes longer and gives the same result.)
+constexpr int kSplitResident[] = {0, 304, 152, 97, 74, 58, 46, 38, 36};
+static_assert(sizeof(kSplitResident) / sizeof(int) == kF8SplitMax + 1, "a count for each split");
+
+long long resident(int on_152, int num_sms) { return std::max(1ll, static_cast<long long>(on_152) * num_sms / 152); }
+
+// Token tiles: of one weight exactly; of experts as many as they take about, for
+// the choice of a launch (`most` false), or at the most.
+double token_tiles(const skg_f8_plan_desc &d, int m_tile, bool most)
+{
+    if (!d.experts)
+        return ceil_div(d.M, m_tile);
+    if (most)
+        return std::min(d.experts, d.M) + d.M / m_tile;
+    const double taken = d.experts * (1.0 - std::pow(1.0 - 1.0 / d.experts, d.M)), rows = d.M / taken;
+    return taken * std::max(1.0, rows / m_tile + 0.5);
+}
+
+// The kernels' times (us) as measured.
+double split_us(const skg_f8_plan_desc &d, int m_tile, int split, int num_sms)
+{
+    const double tiles = token_tiles(d, m_tile, false) * ceil_div(d.N, kTileN);
+    const int units = ceil_div(ceil_div(d.K, kF8Block), split);
+    const double slots = static_cast<double>(resident(kSplitResident[split], num_sms));
+    const bool alone = tiles * split <= num_sms;
+    const double both = m_tile <= 32 ? 0.72 : m_tile == 64 ? 0.80 : 1.0;
+    const double unit = alone ? 0.6 * both : both;
+    return std::ceil(tiles / slots) * unit * units + (split > 1 ? 5.0 : 3.0);
+}
+
+double wide_us(const skg_f8_plan_desc &d, int num_sms)
+{
+    const double tiles = token_tiles(d, 256, false) * ceil_div(d.N, 256), slots = std::max(1, num_sms / 2);
+    return std::ceil(tiles / slots) * (0.34 * ceil_div(d.K, kF8Block) + 1.0) + 5.0;
+}
+
+struct Choice {
+    int m_tile, split;
+    double us;
+};
+
+// The split kernel's tile and the CTAs that share its K, given either or none (0).
+Choice choose_split(const skg_f8_plan_desc &d, int m_tile, int split, int num_sms)
+{
+    const int nkb = ceil_div(d.K, kF8Block);
+    Choice best = {0, 0, 0.0};
+    for (int mt = 16; mt <= 128; mt *= 2) {
+        if (m_tile && mt != m_tile)
+            continue;
+        for (int s = 1; s <= std::min(kF8SplitMax, nkb); ++s) {
+            const double tiles = token_tiles(d, mt, false) * ceil_div(d.N, kTileN);
+            if (split ? s != std::min(split, nkb) : s > 1 && tiles > resident(kSplitResident[s], num_sms))
+                continue;
+            const double us = split_us(d, mt, s, num_sms);
+            if (!best.split || us < best.us)
+                best = {mt, s, us};
+        }
+    }
+    return best;
+}
+
+skg_status fill_launch(skg_f8_plan_desc *d, int kind, int m_tile, int split, int num_sms, const char *who)
+{
+    const Choice c = choose_split(*d, m_tile, split, num_sms);
+    if (!kind)
+        kind = c.us <= wide_us(*d, num_sms) ? SKG_F8_KERNEL_SPLIT : SKG_F8_KERNEL_WIDE;
+    d->kernel_kind = kind;
+    const bool wide = kind == SKG_F8_KERNEL_WIDE;
+    const F8TcShape sh = wide ? f8_wide_shape(d->experts) : f8_split_shape(c.m_tile, d->experts);
+    d->m_tile = sh.m_tile;
+    d->n_tile = wide ? 2 * kTileN : kTileN;
+    d->split_k = wide ? 1 : c.split;
+    d->threads = sh.threads;
+    d->smem_bytes = sh.smem_bytes;
+    d->stages = sh.stages;
+    d->ctas_per_sm = sh.ctas_per_sm;
+    const double tiles = token_tiles(*d, d->m_tile, true) * ceil_div(d->N, d->n_tile);
+    if (tiles > (1 << 27))
+        return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^27 tiles", who);
+    d->tiles = static_cast<int>(tiles);
+    const int ctas = wide ? 2 : d->split_k, slots = std::max(1, num_sms * sh.ctas_per_sm / ctas);
+    d->grid = ctas * (d->split_k > 1 ? d->tiles : std::min(d->tiles, slots));
+    return SKG_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+skg_status skg_quantize_f8(int M, int K, const void *x, size_t ldx, const void *gate, size_t ldg, const int *rows, int x_rows,
+                           void *q, float *scale, void *stream)
+{
+    static const char who[] = "skg_quantize_f8";
+    if (M < 0 || K < 1 || (rows && x_rows < 0))
+        return set_error(SKG_ERR_INVALID_ARG, "%s: M and x_rows must be >= 0 and K >= 1 (got M=%d, x_rows=%d, K=%d)", who, M,
+                         x_rows, K);
+    if (M > 0 && ((!x && !(rows && x_rows == 0)) || !q || !scale))
+        return set_error(SKG_ERR_INVALID_ARG, "%s: x, q and scale must be non-NULL", who);
+    if (ldx < static_cast<size_t>(K) || (gate && ldg < static_cast<size_t>(K)))
+        return set_error(SKG_ERR_INVALID_ARG, "%s: a row stride of x / gate is below K = %d", who, K);
+    if (!aligned(x, 2) || !aligned(gate, 2) || !aligned(rows, 4) || !aligned(scale, 4))
+        return set_error(SKG_ERR_ALIGNMENT, "%s: x, gate, rows or scale misses its element alignment", who);
+    if (M == 0)
+        return SKG_OK;
+    F8RowParams p = {};
+    p.x = static_cast<const uint16_t *>(x);
+    p.gate = static_cast<const uint16_t *>(gate);
+    p.rows = rows;
+    p.q = static_cast<uint8_t *>(q);
+    p.scale = scale;
+    p.ldx = ldx;
+    p.ldg = ldg;
+    p.M = M;
+    p.K = K;
+    p.kb = ceil_div(K, kF8Block);
+    p.x_rows = x_rows;
+    return launched(launch_f8_quantize(p, static_cast<cudaStream_t>(stream)), who);
+}
+
+skg_status skg_quantize_f8_weights(int experts, int N, int K, const void *W, void *q, float *scale, void *stream)
+{
+    static const char who[] = "skg_quantize_f8_weights";
+    if (experts < 1 || N < 1 || K < 1)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: experts, N and K must be positive (got %d, %d, %d)", who, experts, N, K);
+    if (!W || !q || !scale)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: W, q and scale must be non-NULL", who);
+    if (!aligned(W, 2) || !aligned(scale, 4))
+        return set_error(SKG_ERR_ALIGNMENT, "%s: W or scale misses its element alignment", who);
+    F8WeightParams p = {static_cast<const uint16_t *>(W), static_cast<uint8_t *>(q), scale, experts, N, K,
+                        ceil_div(N, kF8Block), ceil_div(K, kF8Block)};
+    if (static_cast<double>(experts) * p.nb * p.kb > 2147483647.0)
+        return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 blocks", who);
+    return launched(launch_f8_quantize_weights(p, static_cast<cudaStream_t>(stream)), who);
+}
+
+skg_status skg_f8_plan_query(int M, int N, int K, int epilogue, int experts, int num_sms, skg_f8_plan_desc *out)
+{
+    static const char who[] = "skg_f8_plan_query";
+    if (!out)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: out is NULL", who);
+    if (M < 1 || N < 1 || num_sms < 1 || experts < 0)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: M, N and num_sms must be positive, experts >= 0 (got %d, %d, %d, %d)", who,
+                         M, N, num_sms, experts);
+    if (epilogue < SKG_EPI_BF16 || epilogue > SKG_EPI_FP32)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: unknown epilogue %d", who, epilogue);
+    if (K < 16 || K % 16 != 0 || K > kF8MaxK)
+        return set_error(SKG_ERR_UNSUPPORTED, "%s: K must be a multiple of 16 in [16, %d] (got %d)", who, kF8MaxK, K);
+    if (M > kF8MaxM || experts > kF8MaxExperts)
+        return set_error(SKG_ERR_UNSUPPORTED, "%s: M must be at most %d and experts %d (got %d, %d)", who, kF8MaxM,
+                         kF8MaxExperts, M, experts);
+    if (static_cast<long long>(std::max(1, experts)) * N > 0x7FFFFF00ll)
+        return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^31 - 256 channels in all (%d experts, N=%d)", who, experts, N);
+    skg_f8_plan_desc d = {};
+    d.M = M;
+    d.N = N;
+    d.K = K;
+    d.epilogue = epilogue;
+    d.experts = experts;
+    const skg_status st = fill_launch(&d, 0, 0, 0, num_sms, who);
+    if (st == SKG_OK)
+        *out = d;
+    return st;
+}
+
+skg_status skg_f8_plan(int M, int N, int K, int epilogue, int experts, int static_weights, skg_f8_plan_t *out)
+{
+    static const char who[] = "skg_f8_plan";
+    if (!out)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: out is NULL", who);
+    *out = nullptr;
+    skg_f8_plan_desc d;
+    skg_status st = skg_f8_plan_query(M, N, K, epilogue, experts, 1, &d);     // the arguments alone
+    if (st != SKG_OK)
+        return st;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return launched(e, who);
+    skg_f8_plan_s *p = new (std::nothrow) skg_f8_plan_s();
+    if (!p)
+        return set_error(SKG_ERR_CUDA, "%s: out of host memory", who);
+    p->d = d;
+    p->d.static_weights = static_weights != 0;
+    p->device = dev;
+    p->num_sms = sms;
+    st = fill_launch(&p->d, 0, 0, 0, sms, who);
+    if (st == SKG_OK)
+        st = launched(cudaHostAlloc(reinterpret_cast<void **>(&p->err_host), sizeof(unsigned int), cudaHostAllocMapped), who);
+    if (st == SKG_OK) {
+        *p->err_host = 0;
+        st = launched(cudaHostGetDevicePointer(reinterpret_cast<void **>(&p->err_dev), p->err_host, 0), who);
+    }
+    if (st != SKG_OK) {
+        skg_f8_plan_destroy(p);
+        return st;
+    }
+    *out = p;
+    return SKG_OK;
+}
+
+skg_status skg_f8_plan_force(skg_f8_plan_t p, int kind, int m_tile, int split_k)
+{
+    static const char who[] = "skg_f8_plan_force";
+    if (!p)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: plan is NULL", who);
+    if (kind < 0 || kind > SKG_F8_KERNEL_WIDE)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: unknown kernel kind %d", who, kind);
+    const int k = kind ? kind : p->d.kernel_kind;
+    const bool wide = k == SKG_F8_KERNEL_WIDE;
+    if (m_tile != 0 && !(wide ? m_tile == 256 : m_tile == 16 || m_tile == 32 || m_tile == 64 || m_tile == 128))
+        return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile %d is none of this kernel's", who, m_tile);
+    if (split_k < 0 || split_k > (wide ? 1 : kF8SplitMax))
+        return set_error(SKG_ERR_INVALID_ARG, "%s: this kernel takes a split_k of at most %d (got %d)", who,
+                         wide ? 1 : kF8SplitMax, split_k);
+    skg_f8_plan_desc d = p->d;
+    const skg_status st = fill_launch(&d, k, wide ? 0 : m_tile, split_k, p->num_sms, who);
+    if (st == SKG_OK)
+        p->d = d;
+    return st;
+}
+
+skg_status skg_f8_plan_info(skg_f8_plan_t p, skg_f8_plan_desc *out)
+{
+    if (!p || !out)
+        return set_error(SKG_ERR_INVALID_ARG, "skg_f8_plan_info: plan and out must be non-NULL");
+    *out = p->d;
+    return SKG_OK;
+}
+
+skg_status skg_f8_run(skg_f8_plan_t p, const void *x, const float *x_scale, const void *W, const float *w_scale,
+                      const void *residual, const int *offsets, void *y, void *stream)
+{
+    static const char who[] = "skg_f8_run";
+    if (!p)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: plan is NULL", who);
+    if (!x || !x_scale || !W || !w_scale || !y)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: x, x_scale, W, w_scale and y must be non-NULL", who);
+    const skg_f8_plan_desc &d = p->d;
+    const bool want = d.epilogue == SKG_EPI_BF16_RESIDUAL;
+    if (want != (residual != nullptr))
+        return set_error(SKG_ERR_INVALID_ARG, want ? "%s: this plan's epilogue needs a residual"
+                                                   : "%s: this plan's epilogue takes no residual", who);
+    if ((d.experts != 0) != (offsets != nullptr))
+        return set_error(SKG_ERR_INVALID_ARG, d.experts ? "%s: this plan's experts need offsets"
+                                                        : "%s: this plan has no experts and takes no offsets", who);
+    if (!aligned(x, 16) || !aligned(W, 16))
+        return set_error(SKG_ERR_ALIGNMENT, "%s: x and W must be 16-byte aligned", who);
+    if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(y, d.epilogue == SKG_EPI_FP32 ? 4 : 2) ||
+        !aligned(residual, 2) || !aligned(offsets, 4))
+        return set_error(SKG_ERR_ALIGNMENT, "%s: a scale, y, residual or offsets misses its element alignment", who);
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return launched(e, who);
+    if (dev != p->device)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: the plan is of device %d, the current one is %d", who, p->device, dev);
+    if (__atomic_exchange_n(p->err_host, 0u, __ATOMIC_ACQ_REL) != 0)
+        return set_error(SKG_ERR_DEVICE_TIMEOUT, "%s: an earlier launch of this plan ran out of a bounded wait", who);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    p->last_stream = s;
+    F8LinearParams g = {};
+    g.x_scale = x_scale;
+    g.w_scale = w_scale;
+    g.res = static_cast<const uint16_t *>(residual);
+    g.y = y;
+    g.offsets = offsets;
+    g.err = p->err_dev;
+    g.M = d.M;
+    g.N = d.N;
+    g.K = d.K;
+    g.epilogue = d.epilogue;
+    g.experts = d.experts;
+    g.nkb = ceil_div(d.K, kF8Block);
+    g.nb = ceil_div(d.N, kF8Block);
+    g.m_tiles = ceil_div(d.M, d.m_tile);
+    g.n_tiles = ceil_div(d.N, d.n_tile);
+    g.split = d.split_k;
+    g.static_w = d.static_weights;
+    g.vec4 = d.N % 4 == 0 && aligned(residual, 8) && aligned(y, d.epilogue == SKG_EPI_FP32 ? 16 : 8);
+    g.timeout_ns = kDefaultTimeoutNs;
+    const bool wide = d.kernel_kind == SKG_F8_KERNEL_WIDE;
+    CUtensorMap tmW, tmX;
+    skg_status st = encode_tiled_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, d.N * std::max(1, d.experts), d.K, kTileN);
+    if (st == SKG_OK)
+        st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, d.M, d.K, wide ? d.m_tile / 2 : d.m_tile);
+    if (st != SKG_OK)
+        return st;
+    return launched(wide ? launch_f8_wide(tmW, tmX, g, d.grid, s) : launch_f8_split(tmW, tmX, g, d.m_tile, d.grid, s), who);
+}
+
+skg_status skg_f8_plan_check(skg_f8_plan_t p)
+{
+    static const char who[] = "skg_f8_plan_check";
+    if (!p)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: plan is NULL", who);
+    cudaError_t e = p->last_stream ? cudaStreamSynchronize(p->last_stream) : cudaDeviceSynchronize();
+    if (e == cudaSuccess)
+        e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return launched(e, who);
+    const unsigned w = __atomic_exchange_n(p->err_host, 0u, __ATOMIC_ACQ_REL);
+    if (w != 0)
+        return set_error(SKG_ERR_DEVICE_TIMEOUT, "a kernel of this plan ran out of a bounded wait (bits 0x%x)", w);
+    return SKG_OK;
+}
+
+skg_status skg_f8_debug_wait_timeout(skg_f8_plan_t p, unsigned long long timeout_ns, void *stream)
+{
+    static const char who[] = "skg_f8_debug_wait_timeout";
+    if (!p)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: plan is NULL", who);
+    if (timeout_ns == 0 || timeout_ns > 10000000000ull)
+        return set_error(SKG_ERR_INVALID_ARG, "%s: timeout_ns must be in (0, 10 s]", who);
+    p->last_stream = static_cast<cudaStream_t>(stream);
+    return launched(launch_debug_wait(p->err_dev, timeout_ns, p->last_stream), who);
+}
+
+skg_status skg_f8_plan_destroy(skg_f8_plan_t p)
+{
+    if (!p)
+        return SKG_OK;
+    if (p->err_host)
+        cudaFreeHost(p->err_host);
+    delete p;
+    return SKG_OK;
+}
+
+} // extern "C"

@@ -1,0 +1,258 @@
+// skg_f8_rows.cu -- bf16 turned into e4m3 with one fp32 scale for each block of
+// 128 values of a row (activations), or of 128 x 128 (weights).
+//
+//   v = x, or silu(gate) * x;   scale = max|v| / 448;   q = e4m3(v * (448 / max|v|))
+//
+// v, the quotient and the product are fp32, and the product is rounded once, half
+// to even.  A block is read once: its values stay in registers through the
+// maximum.
+#include <algorithm>
+
+#include "skg_f8_internal.h"
+#include "skg_internal.h"
+#include "skg_ptx.cuh"
+#include "skg_q8_common.cuh"
+
+namespace skg {
+namespace {
+
+// A block's scale and the factor that takes a value to its e4m3 number, from the
+// bits of max|v| (|NaN| > infinity > every finite value, as integers).  A block of
+// zeros has scale 0.  One with a value that is not finite has scale NaN and
+// numbers 0, so that whatever it multiplies is NaN.  Below 1e-30 the quotient 448 /
+// max would leave fp32's range: both are raised by 2^100, which is exact.
+struct BlockScale {
+    float scale, up, factor;
+};
+
+__device__ __forceinline__ BlockScale block_scale(uint32_t max_bits)
+{
+    BlockScale b;
+    const float amax = __uint_as_float(max_bits);
+    const bool finite = max_bits < 0x7F800000u;
+    b.up = amax < 1e-30f ? 0x1p100f : 1.0f;
+    b.factor = amax > 0.0f && finite ? 448.0f / (amax * b.up) : 0.0f;
+    b.scale = finite ? amax / 448.0f : __int_as_float(0x7FC00000);
+    return b;
+}
+
+// Two values as e4m3 numbers, the first in the low byte.  (Beyond 448 by a
+// rounding: 448.)
+__device__ __forceinline__ uint32_t two_e4m3(float a, float b)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+struct Eight {
+    float v[8];
+};
+
+// max|v| as bits, larger than infinity's where a value is NaN.
+__device__ __forceinline__ uint32_t max_bits(const Eight &e)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = max(m, __float_as_uint(e.v[i]) & 0x7FFFFFFFu);
+    return m;
+}
+
+__device__ __forceinline__ uint2 to_e4m3(const Eight &e, const BlockScale &b)
+{
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)          // (a factor of 0 does not make a NaN or an infinity 0)
+        u[i] = b.factor == 0.0f ? 0.0f : e.v[i] * b.up * b.factor;
+    return make_uint2(two_e4m3(u[0], u[1]) | two_e4m3(u[2], u[3]) << 16, two_e4m3(u[4], u[5]) | two_e4m3(u[6], u[7]) << 16);
+}
+
+// Eight elements as loaded, zeros where the row ends.  ANY: of any alignment.
+template <bool ANY>
+__device__ __forceinline__ uint4 load8(const uint16_t *row, long long e, int K)
+{
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if constexpr (!ANY) {
+        if (e < K)
+            asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(row + e));
+    } else {
+    uint16_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        h[i] = 0;
+        if (e + i < K)
+            asm volatile("ld.global.u16 %0, [%1];" : "=h"(h[i]) : "l"(row + e + i));
+    }
+    r.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
+    r.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
+    r.z = h[4] | static_cast<uint32_t>(h[5]) << 16;
+    r.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
+    }
+    return r;
+}
+
+template <bool ANY>
+__device__ __forceinline__ void store8(uint8_t *row, long long e, int K, const uint2 &w)
+{
+    if constexpr (!ANY) {
+        if (e < K)
+            *reinterpret_cast<uint2 *>(row + e) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i < K)
+                row[e + i] = static_cast<uint8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+    }
+}
+
+__device__ __forceinline__ Eight widen8(const uint4 &w)
+{
+    return {{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y), bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)}};
+}
+
+__device__ __forceinline__ float gated(float g, float x) { return g < kFarGate ? far_gated(g, x) : silu(g) * x; }
+
+constexpr int kRowWarps = 8;
+
+// A warp takes 2 P blocks of a row, 16 lanes a block, 8 values a lane.
+template <bool ANY, bool GATE, int P>
+__global__ void __launch_bounds__(32 * kRowWarps) f8_rows_kernel(const F8RowParams p, int groups)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const long long unit = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    const long long row = unit / groups;
+    if (row >= p.M)
+        return;
+    const int b0 = static_cast<int>(unit - row * groups) * 2 * P, lane = threadIdx.x & 31, half = lane >> 4;
+    long long from = row;
+    bool live = true;
+    if (p.rows) {
+        const int r = __ldcg(p.rows + row);
+        live = r >= 0 && r < p.x_rows;
+        from = live ? r : 0;
+    }
+    const uint16_t *x = p.x + from * p.ldx;
+    const uint16_t *g = GATE ? p.gate + from * p.ldg : nullptr;
+    const long long e0 = (static_cast<long long>(b0) + half) * kF8Block + (lane & 15) * 8;
+    const int K = live ? p.K : 0;
+    uint4 a[P], c[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        a[i] = load8<ANY>(x, e0 + i * 2 * kF8Block, K);
+    if (GATE) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            c[i] = load8<ANY>(g, e0 + i * 2 * kF8Block, K);
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        Eight v = widen8(a[i]);
+        if (GATE) {
+            const Eight w = widen8(c[i]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v.v[k] = gated(w.v[k], v.v[k]);
+        }
+        uint32_t m = max_bits(v);
+#pragma unroll
+        for (int o = 8; o; o >>= 1)
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const BlockScale s = block_scale(m);
+        store8<ANY>(p.q + row * p.K, e0 + i * 2 * kF8Block, p.K, to_e4m3(v, s));
+        const int b = b0 + 2 * i + half;
+        if ((lane & 15) == 0 && b < p.kb)
+            p.scale[row * p.kb + b] = s.scale;
+    }
+}
+
+// A CTA takes a block of 128 x 128: 16 lanes a row, 16 rows at a time.
+template <bool ANY>
+__global__ void __launch_bounds__(256) f8_weights_kernel(const F8WeightParams p)
+{
+    __shared__ uint32_t maxima[8];
+    pdl_wait();
+    pdl_launch_dependents();
+    const long long block = blockIdx.x, en = block / p.kb;
+    const int b = static_cast<int>(block - en * p.kb), e = static_cast<int>(en / p.nb), nb = static_cast<int>(en - static_cast<long long>(e) * p.nb);
+    const int t = threadIdx.x, k = (t & 15) * 8;
+    uint4 a[8];
+    uint32_t m = 0;
+    const long long e0 = static_cast<long long>(b) * kF8Block + k;
+    auto at = [&](int i) {
+        return (static_cast<size_t>(e) * p.N + nb * kF8Block + (t >> 4) + 16 * i) * p.K;
+    };
+    auto inside = [&](int i) { return static_cast<long long>(nb) * kF8Block + (t >> 4) + 16 * i < p.N; };
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        a[i] = load8<ANY>(p.W + at(i), e0, inside(i) ? p.K : 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = max(m, max_bits(widen8(a[i])));
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((t & 31) == 0)
+        maxima[t >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = max(m, maxima[i]);
+    const BlockScale s = block_scale(m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        store8<ANY>(p.q + at(i), e0, inside(i) ? p.K : 0, to_e4m3(widen8(a[i]), s));
+    if (t == 0)
+        p.scale[block] = s.scale;
+}
+
+template <class P, class... A>
+cudaError_t launch(void (*kernel)(P, A...), long long grid, unsigned threads, cudaStream_t s, const P &p, A... a)
+{
+    if (grid > 0x7FFFFFFFll)
+        return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, a...);
+}
+
+bool multiple(const void *ptr, size_t bytes) { return reinterpret_cast<uintptr_t>(ptr) % bytes == 0; }
+
+template <bool ANY, bool GATE>
+cudaError_t launch_rows(const F8RowParams &p, cudaStream_t s)
+{
+    auto run = [&](auto kernel, int blocks) {
+        const int groups = (p.kb + blocks - 1) / blocks;
+        return launch(kernel, (static_cast<long long>(p.M) * groups + kRowWarps - 1) / kRowWarps, 32 * kRowWarps, s, p, groups);
+    };
+    // Many blocks of long rows: eight a warp, for bytes in flight.
+    if (p.kb >= 8 && static_cast<long long>(p.M) * p.kb >= 8 * 16 * 152)
+        return run(f8_rows_kernel<ANY, GATE, 4>, 8);
+    return run(f8_rows_kernel<ANY, GATE, 1>, 2);
+}
+
+} // namespace
+
+cudaError_t launch_f8_quantize(const F8RowParams &p, cudaStream_t s)
+{
+    const bool aligned = p.K % 8 == 0 && p.ldx % 8 == 0 && (!p.gate || p.ldg % 8 == 0) && multiple(p.x, 16) &&
+                         multiple(p.gate, 16) && multiple(p.q, 8);           // null is aligned
+    if (p.gate)
+        return aligned ? launch_rows<false, true>(p, s) : launch_rows<true, true>(p, s);
+    return aligned ? launch_rows<false, false>(p, s) : launch_rows<true, false>(p, s);
+}
+
+cudaError_t launch_f8_quantize_weights(const F8WeightParams &p, cudaStream_t s)
+{
+    const bool aligned = p.K % 8 == 0 && multiple(p.W, 16) && multiple(p.q, 8);
+    const long long grid = static_cast<long long>(p.E) * p.nb * p.kb;
+    return aligned ? launch(f8_weights_kernel<false>, grid, 256, s, p) : launch(f8_weights_kernel<true>, grid, 256, s, p);
+}
+
+} // namespace skg

@@ -39,6 +39,12 @@ SKG_Q8_KERNEL_WIDE = 3
 Q8_KERNEL_NAMES = {SKG_Q8_KERNEL_STREAM: "q8_stream", SKG_Q8_KERNEL_SPLIT: "q8_split",
                    SKG_Q8_KERNEL_WIDE: "q8_wide"}
 
+SKG_F8_KERNEL_SPLIT = 1
+SKG_F8_KERNEL_WIDE = 2
+F8_KERNEL_NAMES = {SKG_F8_KERNEL_SPLIT: "f8_split", SKG_F8_KERNEL_WIDE: "f8_wide"}
+
+F8_BLOCK = 128            # values that share a scale
+
 # Every symbol include/skg.h declares.
 EXPORTS = (
     "skg_plan_query", "skg_plan", "skg_plan_force", "skg_plan_force_kernel", "skg_plan_set_pdl", "skg_run",
@@ -49,6 +55,9 @@ EXPORTS = (
     "skg_group", "skg_group_run", "skg_group_info", "skg_group_check", "skg_group_destroy",
     "skg_rmsnorm_q8", "skg_quantize_q8", "skg_q8_plan_query", "skg_q8_plan", "skg_q8_run", "skg_q8_plan_destroy",
     "skg_q8_plan_force", "skg_q8_plan_info", "skg_q8_plan_check", "skg_q8_debug_wait_timeout",
+    "skg_quantize_f8", "skg_quantize_f8_weights", "skg_f8_plan_query", "skg_f8_plan", "skg_f8_run", "skg_f8_plan_destroy",
+    "skg_f8_plan_force", "skg_f8_plan_info", "skg_f8_plan_check", "skg_f8_debug_wait_timeout",
+    "skg_experts_sort", "skg_experts_gather", "skg_experts_combine", "skg_experts_combine_grad",
 )
 
 
@@ -87,6 +96,17 @@ class skg_q8_plan_desc(ctypes.Structure):
     def as_dict(self) -> dict:
         d = {f: getattr(self, f) for f, _ in self._fields_}
         d["kernel"] = Q8_KERNEL_NAMES.get(self.kernel_kind, "?")
+        return d
+
+
+class skg_f8_plan_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in (
+        "kernel_kind", "M", "N", "K", "epilogue", "experts", "static_weights", "m_tile", "n_tile", "tiles", "split_k",
+        "grid", "threads", "smem_bytes", "stages", "ctas_per_sm")]
+
+    def as_dict(self) -> dict:
+        d = {f: getattr(self, f) for f, _ in self._fields_}
+        d["kernel"] = F8_KERNEL_NAMES.get(self.kernel_kind, "?")
         return d
 
 
@@ -138,6 +158,20 @@ def load(path: str = LIB_PATH):
     lib.skg_q8_plan_info.argtypes = [vp, P(skg_q8_plan_desc)]
     lib.skg_q8_plan_check.argtypes = [vp]
     lib.skg_q8_debug_wait_timeout.argtypes = [vp, ctypes.c_ulonglong, vp]
+    lib.skg_quantize_f8.argtypes = [i, i, vp, sz, vp, sz, vp, i, vp, vp, vp]
+    lib.skg_quantize_f8_weights.argtypes = [i, i, i, vp, vp, vp, vp]
+    lib.skg_f8_plan_query.argtypes = [i, i, i, i, i, i, P(skg_f8_plan_desc)]
+    lib.skg_f8_plan.argtypes = [i, i, i, i, i, i, P(vp)]
+    lib.skg_f8_run.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.skg_f8_plan_destroy.argtypes = [vp]
+    lib.skg_f8_plan_force.argtypes = [vp, i, i, i]
+    lib.skg_f8_plan_info.argtypes = [vp, P(skg_f8_plan_desc)]
+    lib.skg_f8_plan_check.argtypes = [vp]
+    lib.skg_f8_debug_wait_timeout.argtypes = [vp, ctypes.c_ulonglong, vp]
+    lib.skg_experts_sort.argtypes = [i, i, i, vp, vp, vp, vp, vp]
+    lib.skg_experts_gather.argtypes = [i, i, i, vp, sz, vp, vp, vp]
+    lib.skg_experts_combine.argtypes = [i, i, i, i, vp, sz, vp, vp, vp, vp, vp]
+    lib.skg_experts_combine_grad.argtypes = [i, i, i, i, vp, vp, sz, vp, vp, vp, vp, vp]
     for name in EXPORTS:
         getattr(lib, name).restype = ctypes.c_int
     lib.skg_last_error.restype = ctypes.c_char_p
@@ -555,3 +589,195 @@ class Q8Plan:
             self.close()
         except Exception:
             pass
+
+
+# --------------------------------------------- the 8-bit floating point path
+def _blocks(n: int) -> int:
+    return -(-n // F8_BLOCK)
+
+
+def _indices(t, name, shape) -> int:
+    import torch
+    return _dense(t, name, shape, torch.int32)
+
+
+def skg_quantize_f8(x, gate, q, scale, rows=None, stream=None):
+    """x, gate: bf16 [T, K] (rows may be strided; gate may be None); rows int32 [M], the row of x of each row of q, or
+    None (M = T); q float8_e4m3fn [M, K]; scale fp32 [M, ceil(K / 128)]."""
+    import torch
+    shape = x.shape
+    if len(shape) != 2:
+        _bad("x must be [T, K]")
+    T, K = _int(shape[0], "T"), _int(shape[1], "K")
+    M = T if rows is None else _int(rows.numel(), "M")
+    ldx = _rows(x, "x", shape, torch.bfloat16)
+    ldg = 0 if gate is None else _rows(gate, "gate", shape, torch.bfloat16)
+    _check(load().skg_quantize_f8(
+        M, K, x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg,
+        None if rows is None or M == 0 else _indices(rows, "rows", (M,)), T,
+        _dense(q, "q", (M, K), torch.float8_e4m3fn), _dense(scale, "scale", (M, _blocks(K)), torch.float32),
+        _stream_of(stream, x)))
+
+
+def skg_quantize_f8_weights(W, q, scale, stream=None):
+    """W: bf16 [N, K], or [E, N, K] of E experts; q float8_e4m3fn of that shape; scale fp32 [ceil(N / 128),
+    ceil(K / 128)], or [E, ...] of that."""
+    import torch
+    shape = W.shape
+    if len(shape) not in (2, 3):
+        _bad("W must be [N, K] or [E, N, K]")
+    E, N, K = (_int(v, n) for v, n in zip((1, *shape)[-3:], ("E", "N", "K")))
+    _check(load().skg_quantize_f8_weights(
+        E, N, K, _dense(W, "W", shape, torch.bfloat16), _dense(q, "q", shape, torch.float8_e4m3fn),
+        _dense(scale, "scale", (*shape[:-2], _blocks(N), _blocks(K)), torch.float32), _stream_of(stream, W)))
+
+
+def skg_f8_plan_query(M: int, N: int, K: int, epilogue, experts: int, num_sms: int) -> dict:
+    d = skg_f8_plan_desc()
+    _check(load().skg_f8_plan_query(_int(M, "M"), _int(N, "N"), _int(K, "K"), _int(_epi(epilogue), "epilogue"),
+                                    _int(experts, "experts"), _int(num_sms, "num_sms"), ctypes.byref(d)))
+    return d.as_dict()
+
+
+def skg_f8_plan(M: int, N: int, K: int, epilogue, experts: int = 0, static_weights: bool = False) -> int:
+    h = ctypes.c_void_p()
+    _check(load().skg_f8_plan(_int(M, "M"), _int(N, "N"), _int(K, "K"), _int(_epi(epilogue), "epilogue"),
+                              _int(experts, "experts"), 1 if static_weights else 0, ctypes.byref(h)))
+    return h.value
+
+
+def skg_f8_run(plan: int, x, x_scale, W, w_scale, residual, y, offsets=None, stream=None):
+    _check(load().skg_f8_run(plan, _ptr(x), _ptr(x_scale), _ptr(W), _ptr(w_scale), _ptr(residual), _ptr(offsets), _ptr(y),
+                             _stream(stream)))
+
+
+def skg_f8_plan_force(plan: int, kind: int = 0, m_tile: int = 0, split_k: int = 0):
+    _check(load().skg_f8_plan_force(plan, _int(kind, "kind"), _int(m_tile, "m_tile"), _int(split_k, "split_k")))
+
+
+def skg_f8_plan_info(plan: int) -> dict:
+    d = skg_f8_plan_desc()
+    _check(load().skg_f8_plan_info(plan, ctypes.byref(d)))
+    return d.as_dict()
+
+
+def skg_f8_plan_check(plan: int):
+    _check(load().skg_f8_plan_check(plan))
+
+
+def skg_f8_debug_wait_timeout(plan: int, timeout_ns: int, stream=None):
+    _check(load().skg_f8_debug_wait_timeout(plan, int(timeout_ns), _stream(stream)))
+
+
+def skg_f8_plan_destroy(plan: int):
+    _check(load().skg_f8_plan_destroy(plan))
+
+
+class F8Plan:
+    """Owns one plan of the 8-bit floating point path: M rows by a weight [N, K], or, with experts, each by the weight
+    of its expert among [experts, N, K].  run checks the tensors against it."""
+
+    def __init__(self, M: int, N: int, K: int, epilogue="bf16", experts: int = 0, static_weights: bool = False):
+        import torch
+        self.M, self.N, self.K, self.experts = M, N, K, experts
+        self.epilogue = _epi(epilogue)
+        each = (experts,) if experts else ()
+        self._shapes = (M, K), (M, _blocks(K)), (*each, N, K), (*each, _blocks(N), _blocks(K)), (M, N)
+        self._types = (torch.float8_e4m3fn, torch.float32, torch.bfloat16,
+                       torch.float32 if self.epilogue == SKG_EPI_FP32 else torch.bfloat16)
+        self.handle = None
+        self.handle = skg_f8_plan(M, N, K, self.epilogue, experts, static_weights)
+
+    def run(self, x, x_scale, W, w_scale, residual, y, offsets=None, stream=None):
+        # one expression, as in Q8Plan.run
+        mk, mb, nk, nb, mn = self._shapes
+        f8, f32, bf16, out = self._types
+        if not (x.dtype is f8 and x.shape == mk and x.is_contiguous() and x.is_cuda and
+                W.dtype is f8 and W.shape == nk and W.is_contiguous() and W.is_cuda and
+                x_scale.dtype is f32 and x_scale.shape == mb and x_scale.is_contiguous() and x_scale.is_cuda and
+                w_scale.dtype is f32 and w_scale.shape == nb and w_scale.is_contiguous() and w_scale.is_cuda and
+                y.dtype is out and y.shape == mn and y.is_contiguous() and y.is_cuda):
+            for t, name, shape, dtype in ((x, "x", mk, f8), (x_scale, "x_scale", mb, f32), (W, "W", nk, f8),
+                                          (w_scale, "w_scale", nb, f32), (y, "y", mn, out)):
+                _dense(t, name, shape, dtype)
+        if residual is not None:
+            _dense(residual, "residual", mn, bf16)
+        if offsets is not None:
+            _indices(offsets, "offsets", (self.experts + 1,))
+        status = load().skg_f8_run(self.handle, x.data_ptr(), x_scale.data_ptr(), W.data_ptr(), w_scale.data_ptr(),
+                                   None if residual is None else residual.data_ptr(),
+                                   None if offsets is None else offsets.data_ptr(), y.data_ptr(), _stream_of(stream, x))
+        if status:
+            _check(status)
+
+    def force(self, kind: int = 0, m_tile: int = 0, split_k: int = 0):
+        skg_f8_plan_force(self.handle, kind, m_tile, split_k)
+
+    def info(self) -> dict:
+        return skg_f8_plan_info(self.handle)
+
+    def check(self):
+        skg_f8_plan_check(self.handle)
+
+    def close(self):
+        if self.handle:
+            skg_f8_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ------------------------------------------- tokens to their experts and back
+def skg_experts_sort(expert, offsets, rows, pos, stream=None):
+    """expert int32 [T, k]; offsets int32 [experts + 1]; rows int32 [T * k]; pos int32 [T, k]."""
+    shape = expert.shape
+    if len(shape) != 2 or len(offsets.shape) != 1:
+        _bad("expert must be [T, k] and offsets [experts + 1]")
+    T, k, E = _int(shape[0], "T"), _int(shape[1], "k"), _int(offsets.shape[0] - 1, "experts")
+    _check(load().skg_experts_sort(T, k, E, _indices(expert, "expert", shape), _indices(offsets, "offsets", (E + 1,)),
+                                   _indices(rows, "rows", (T * k,)), _indices(pos, "pos", shape), _stream_of(stream, expert)))
+
+
+def skg_experts_gather(x, rows, out, stream=None):
+    """x bf16 [T, N] (rows may be strided); rows int32 [R]; out bf16 [R, N]."""
+    import torch
+    if len(x.shape) != 2 or len(rows.shape) != 1:
+        _bad("x must be [T, N] and rows [R]")
+    T, N, R = _int(x.shape[0], "T"), _int(x.shape[1], "N"), _int(rows.shape[0], "R")
+    ldx = _rows(x, "x", x.shape, torch.bfloat16)
+    _check(load().skg_experts_gather(R, T, N, x.data_ptr(), ldx, _indices(rows, "rows", (R,)),
+                                     _dense(out, "out", (R, N), torch.bfloat16), _stream_of(stream, x)))
+
+
+def _choices(y, pos):
+    import torch
+    if len(y.shape) != 2 or len(pos.shape) != 2:
+        _bad("y must be [R, N] and pos [T, k]")
+    T, k, R, N = (_int(v, n) for v, n in zip((*pos.shape, *y.shape), ("T", "k", "R", "N")))
+    return T, k, R, N, _rows(y, "y", y.shape, torch.bfloat16), _indices(pos, "pos", pos.shape)
+
+
+def skg_experts_combine(y, pos, weight, residual, out, stream=None):
+    """y bf16 [R, N] (rows may be strided); pos int32 [T, k]; weight fp32 [T, k] or None; residual bf16 [T, N] or None;
+    out bf16 [T, N]."""
+    import torch
+    T, k, R, N, ldy, at = _choices(y, pos)
+    _check(load().skg_experts_combine(
+        T, k, R, N, y.data_ptr(), ldy, at, None if weight is None else _dense(weight, "weight", (T, k), torch.float32),
+        None if residual is None else _dense(residual, "residual", (T, N), torch.bfloat16),
+        _dense(out, "out", (T, N), torch.bfloat16), _stream_of(stream, y)))
+
+
+def skg_experts_combine_grad(grad_out, y, pos, weight, grad_y, grad_weight, stream=None):
+    """grad_out bf16 [T, N]; y bf16 [R, N] (rows may be strided); pos int32 [T, k]; weight, grad_weight fp32 [T, k];
+    grad_y bf16 [R, N]."""
+    import torch
+    T, k, R, N, ldy, at = _choices(y, pos)
+    _check(load().skg_experts_combine_grad(
+        T, k, R, N, _dense(grad_out, "grad_out", (T, N), torch.bfloat16), y.data_ptr(), ldy, at,
+        _dense(weight, "weight", (T, k), torch.float32), _dense(grad_y, "grad_y", (R, N), torch.bfloat16),
+        _dense(grad_weight, "grad_weight", (T, k), torch.float32), _stream_of(stream, y)))
