@@ -598,7 +598,7 @@ SKG_API skg_status skg_quantize_f8_weights(int experts, int N, int K, const void
 typedef enum skg_f8_kernel_kind {
     SKG_F8_KERNEL_SPLIT = 1,    /* few tokens (of each expert): 128 channels x m_tile tokens, K split over the CTAs of
                                    a cluster, joined in shared memory */
-    SKG_F8_KERNEL_WIDE = 2      /* many: 256 tokens x 256 channels by pairs of CTAs */
+    SKG_F8_KERNEL_WIDE = 2      /* many: 128 x 128, or 256 tokens x 256 channels by pairs of CTAs, K split in the same way */
 } skg_f8_kernel_kind;
 
 /* What a plan of the 8-bit floating point path will launch. */
@@ -609,7 +609,7 @@ typedef struct skg_f8_plan_desc {
     int static_weights;         /* see skg_f8_plan */
     int m_tile, n_tile;         /* tokens and channels of a tile */
     int tiles;                  /* output tiles; with experts the most that offsets can ask for */
-    int split_k;                /* SPLIT: CTAs that share a tile's K, 1..8; WIDE: 1 */
+    int split_k;                /* CTAs (or pairs of them) that share a tile's K: SPLIT 1..8, WIDE 1..4 */
     int grid, threads, smem_bytes, stages, ctas_per_sm;
 } skg_f8_plan_desc;
 
@@ -661,8 +661,9 @@ SKG_API skg_status skg_f8_run(skg_f8_plan_t plan, const void *x, const float *x_
 
 /*
  * skg_f8_plan_force -- override of the kernel choice (tests and measurements):
- * kind (an skg_f8_kernel_kind, 0 keeps), m_tile (SPLIT: 16, 32, 64, 128; WIDE: 256;
- * 0 = chosen) and split_k (SPLIT: 1..8, no finer than K / 128; 0 = chosen).
+ * kind (an skg_f8_kernel_kind, 0 keeps), m_tile (SPLIT: 16, 32, 64; WIDE: 128, 256;
+ * 0 = chosen) and split_k (SPLIT: 1..8, WIDE: 1..4, no finer than K / 128; 0 =
+ * chosen).
  * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED.
  */
 SKG_API skg_status skg_f8_plan_force(skg_f8_plan_t plan, int kind, int m_tile, int split_k);

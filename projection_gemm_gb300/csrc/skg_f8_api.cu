@@ -58,44 +58,58 @@ double token_tiles(const skg_f8_plan_desc &d, int m_tile, bool most)
     return taken * std::max(1.0, rows / m_tile + 0.5);
 }
 
-// The kernels' times (us) as measured.
-double split_us(const skg_f8_plan_desc &d, int m_tile, int split, int num_sms)
-{
-    const double tiles = token_tiles(d, m_tile, false) * ceil_div(d.N, kTileN);
-    const int units = ceil_div(ceil_div(d.K, kF8Block), split);
-    const double slots = static_cast<double>(resident(kSplitResident[split], num_sms));
-    const bool alone = tiles * split <= num_sms;
-    const double both = m_tile <= 32 ? 0.72 : m_tile == 64 ? 0.80 : 1.0;
-    const double unit = alone ? 0.6 * both : both;
-    return std::ceil(tiles / slots) * unit * units + (split > 1 ? 5.0 : 3.0);
-}
-
-double wide_us(const skg_f8_plan_desc &d, int num_sms)
-{
-    const double tiles = token_tiles(d, 256, false) * ceil_div(d.N, 256), slots = std::max(1, num_sms / 2);
-    return std::ceil(tiles / slots) * (0.34 * ceil_div(d.K, kF8Block) + 1.0) + 5.0;
-}
+// The same of the wide kernel, a CTA an SM: single CTAs (128 tokens) and pairs (256).
+constexpr int kWideResident1[] = {0, 152, 76, 48, 36};
+constexpr int kWideResident2[] = {0, 76, 36, 23, 15};
 
 struct Choice {
-    int m_tile, split;
+    int kind, m_tile, split;
     double us;
 };
 
-// The split kernel's tile and the CTAs that share its K, given either or none (0).
-Choice choose_split(const skg_f8_plan_desc &d, int m_tile, int split, int num_sms)
+int n_tile_of(int kind, int m_tile) { return kind == SKG_F8_KERNEL_WIDE ? m_tile : kTileN; }
+
+int max_split(int kind) { return kind == SKG_F8_KERNEL_WIDE ? kF8WideMaxSplit : kF8SplitMax; }
+
+long long slots_of(int kind, int m_tile, int split, int num_sms)
+{
+    const int *r = kind == SKG_F8_KERNEL_SPLIT ? kSplitResident : m_tile == 128 ? kWideResident1 : kWideResident2;
+    return resident(r[split], num_sms);
+}
+
+// The kernels' times (us) as measured: a unit of 128 k, a tile, a launch's ends.
+double launch_us(const skg_f8_plan_desc &d, int kind, int m_tile, int split, int num_sms)
+{
+    const double tiles = token_tiles(d, m_tile, false) * ceil_div(d.N, n_tile_of(kind, m_tile));
+    const int units = ceil_div(ceil_div(d.K, kF8Block), split);
+    const double waves = std::ceil(tiles / static_cast<double>(slots_of(kind, m_tile, split, num_sms)));
+    if (kind == SKG_F8_KERNEL_SPLIT) {
+        const bool alone = tiles * split <= num_sms;
+        const double both = m_tile <= 32 ? 0.72 : 0.80;
+        return waves * (alone ? 0.6 * both : both) * units + (split > 1 ? 5.0 : 3.0);
+    }
+    const double unit = m_tile == 128 ? 0.36 : 0.42;
+    return waves * (unit * units + 1.0) + (split > 1 ? 8.0 : 5.0);
+}
+
+// The launch that takes the least time, given a kernel, a tile and the CTAs that
+// share a tile's K, or none of them (0).  K is split only into clusters that are
+// resident at once.
+Choice choose(const skg_f8_plan_desc &d, int kind, int m_tile, int split, int num_sms)
 {
     const int nkb = ceil_div(d.K, kF8Block);
-    Choice best = {0, 0, 0.0};
-    for (int mt = 16; mt <= 128; mt *= 2) {
-        if (m_tile && mt != m_tile)
+    Choice best = {0, 0, 0, 0.0};
+    for (int mt = 16; mt <= 256; mt *= 2) {
+        const int k = mt <= 64 ? SKG_F8_KERNEL_SPLIT : SKG_F8_KERNEL_WIDE;
+        if ((kind && k != kind) || (m_tile && mt != m_tile))
             continue;
-        for (int s = 1; s <= std::min(kF8SplitMax, nkb); ++s) {
-            const double tiles = token_tiles(d, mt, false) * ceil_div(d.N, kTileN);
-            if (split ? s != std::min(split, nkb) : s > 1 && tiles > resident(kSplitResident[s], num_sms))
+        for (int s = 1; s <= std::min(max_split(k), nkb); ++s) {
+            const double tiles = token_tiles(d, mt, false) * ceil_div(d.N, n_tile_of(k, mt));
+            if (split ? s != std::min(split, nkb) : s > 1 && tiles > slots_of(k, mt, s, num_sms))
                 continue;
-            const double us = split_us(d, mt, s, num_sms);
-            if (!best.split || us < best.us)
-                best = {mt, s, us};
+            const double us = launch_us(d, k, mt, s, num_sms);
+            if (!best.kind || us < best.us)
+                best = {k, mt, s, us};
         }
     }
     return best;
@@ -103,15 +117,13 @@ Choice choose_split(const skg_f8_plan_desc &d, int m_tile, int split, int num_sm
 
 skg_status fill_launch(skg_f8_plan_desc *d, int kind, int m_tile, int split, int num_sms, const char *who)
 {
-    const Choice c = choose_split(*d, m_tile, split, num_sms);
-    if (!kind)
-        kind = c.us <= wide_us(*d, num_sms) ? SKG_F8_KERNEL_SPLIT : SKG_F8_KERNEL_WIDE;
-    d->kernel_kind = kind;
-    const bool wide = kind == SKG_F8_KERNEL_WIDE;
-    const F8TcShape sh = wide ? f8_wide_shape(d->experts) : f8_split_shape(c.m_tile, d->experts);
+    const Choice c = choose(*d, kind, m_tile, split, num_sms);
+    const bool wide = c.kind == SKG_F8_KERNEL_WIDE;
+    const F8TcShape sh = wide ? f8_wide_shape(c.m_tile, d->experts) : f8_split_shape(c.m_tile, d->experts);
+    d->kernel_kind = c.kind;
     d->m_tile = sh.m_tile;
-    d->n_tile = wide ? 2 * kTileN : kTileN;
-    d->split_k = wide ? 1 : c.split;
+    d->n_tile = n_tile_of(c.kind, c.m_tile);
+    d->split_k = c.split;
     d->threads = sh.threads;
     d->smem_bytes = sh.smem_bytes;
     d->stages = sh.stages;
@@ -120,8 +132,8 @@ skg_status fill_launch(skg_f8_plan_desc *d, int kind, int m_tile, int split, int
     if (tiles > (1 << 27))
         return set_error(SKG_ERR_UNSUPPORTED, "%s: more than 2^27 tiles", who);
     d->tiles = static_cast<int>(tiles);
-    const int ctas = wide ? 2 : d->split_k, slots = std::max(1, num_sms * sh.ctas_per_sm / ctas);
-    d->grid = ctas * (d->split_k > 1 ? d->tiles : std::min(d->tiles, slots));
+    const int ctas = (c.m_tile == 256 ? 2 : 1) * c.split, slots = std::max(1, num_sms * sh.ctas_per_sm / ctas);
+    d->grid = ctas * (c.split > 1 ? d->tiles : std::min(d->tiles, slots));
     return SKG_OK;
 }
 
@@ -251,13 +263,12 @@ skg_status skg_f8_plan_force(skg_f8_plan_t p, int kind, int m_tile, int split_k)
         return set_error(SKG_ERR_INVALID_ARG, "%s: unknown kernel kind %d", who, kind);
     const int k = kind ? kind : p->d.kernel_kind;
     const bool wide = k == SKG_F8_KERNEL_WIDE;
-    if (m_tile != 0 && !(wide ? m_tile == 256 : m_tile == 16 || m_tile == 32 || m_tile == 64 || m_tile == 128))
+    if (m_tile != 0 && !(wide ? m_tile == 128 || m_tile == 256 : m_tile == 16 || m_tile == 32 || m_tile == 64))
         return set_error(SKG_ERR_INVALID_ARG, "%s: m_tile %d is none of this kernel's", who, m_tile);
-    if (split_k < 0 || split_k > (wide ? 1 : kF8SplitMax))
-        return set_error(SKG_ERR_INVALID_ARG, "%s: this kernel takes a split_k of at most %d (got %d)", who,
-                         wide ? 1 : kF8SplitMax, split_k);
+    if (split_k < 0 || split_k > max_split(k))
+        return set_error(SKG_ERR_INVALID_ARG, "%s: this kernel takes a split_k of at most %d (got %d)", who, max_split(k), split_k);
     skg_f8_plan_desc d = p->d;
-    const skg_status st = fill_launch(&d, k, wide ? 0 : m_tile, split_k, p->num_sms, who);
+    const skg_status st = fill_launch(&d, k, m_tile, split_k, p->num_sms, who);
     if (st == SKG_OK)
         p->d = d;
     return st;
@@ -321,15 +332,16 @@ skg_status skg_f8_run(skg_f8_plan_t p, const void *x, const float *x_scale, cons
     g.split = d.split_k;
     g.static_w = d.static_weights;
     g.vec4 = d.N % 4 == 0 && aligned(residual, 8) && aligned(y, d.epilogue == SKG_EPI_FP32 ? 16 : 8);
+    g.vec = d.epilogue == SKG_EPI_BF16 ? d.N % 8 == 0 && aligned(y, 16) : g.vec4;
     g.timeout_ns = kDefaultTimeoutNs;
     const bool wide = d.kernel_kind == SKG_F8_KERNEL_WIDE;
     CUtensorMap tmW, tmX;
     skg_status st = encode_tiled_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, d.N * std::max(1, d.experts), d.K, kTileN);
     if (st == SKG_OK)
-        st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, d.M, d.K, wide ? d.m_tile / 2 : d.m_tile);
+        st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, d.M, d.K, wide ? 128 : d.m_tile);
     if (st != SKG_OK)
         return st;
-    return launched(wide ? launch_f8_wide(tmW, tmX, g, d.grid, s) : launch_f8_split(tmW, tmX, g, d.m_tile, d.grid, s), who);
+    return launched(wide ? launch_f8_wide(tmW, tmX, g, d.m_tile, d.grid, s) : launch_f8_split(tmW, tmX, g, d.m_tile, d.grid, s), who);
 }
 
 skg_status skg_f8_plan_check(skg_f8_plan_t p)

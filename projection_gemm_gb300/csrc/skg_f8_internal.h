@@ -50,6 +50,7 @@ struct F8LinearParams {
     int m_tiles, n_tiles;     // m_tiles: without experts
     int split, static_w;
     int vec4;                 // N a multiple of 4, residual and y aligned for four channels at a time
+    int vec;                  // the same for 16 bytes of sums, or of bf16 where no residual is added
     unsigned long long timeout_ns;
 };
 
@@ -59,9 +60,11 @@ struct F8TcShape {
 
 constexpr int kF8SplitMax = 8;             // CTAs of a cluster that share a tile's K
 F8TcShape f8_split_shape(int m_tile, int experts);
-F8TcShape f8_wide_shape(int experts);
+constexpr int kF8WideMaxSplit = 4;         // the same of the wide kernel, whose tiles of 256 tokens take two CTAs for one
+F8TcShape f8_wide_shape(int m_tile, int experts);
 cudaError_t launch_f8_split(const CUtensorMap &tmW, const CUtensorMap &tmX, const F8LinearParams &p, int m_tile, int grid,
                             cudaStream_t s);
-cudaError_t launch_f8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const F8LinearParams &p, int grid, cudaStream_t s);
+cudaError_t launch_f8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const F8LinearParams &p, int m_tile, int grid,
+                           cudaStream_t s);
 
 } // namespace skg

@@ -12,7 +12,7 @@
 // CTAs computes a tile, CTA r the r-th part of K; with S = 1 CTAs are persistent
 // over tiles.  Two CTAs an SM.  Roles of a CTA:
 //   1 + 1     TMA; TMEM and MMA issue
-//   4 or 8    accumulators into registers, and the tile's end: residual,
+//   4         accumulators into registers, and the tile's end: residual,
 //             rounding, store
 // With S > 1 the cluster's CTAs leave their sums in their own shared memory and
 // each adds up and stores 1/S of the tile's tokens, read from its peers in order
@@ -35,93 +35,23 @@ namespace {
 
 template <int MT>
 struct SplitShape {
-    static constexpr int kEpiWarps = MT == 128 ? 8 : 4;
+    static constexpr int kEpiWarps = 4;
     static constexpr int kCols = MT * 4 / kEpiWarps;         // accumulator columns of an epilogue thread
     static constexpr int kMmaWarp = 0, kTmaWarp = 1, kFirstEpi = 2;
     static constexpr int kThreads = 32 * (2 + kEpiWarps);
-    static constexpr int kStages = MT <= 32 ? 5 : MT == 64 ? 4 : 3;
-    static constexpr int kAcc = MT <= 64 ? 4 : 2;            // accumulators in flight
+    static constexpr int kStages = MT <= 32 ? 5 : 4;
+    static constexpr int kAcc = 4;                           // accumulators in flight
     static constexpr uint32_t kTmemCols = kAcc * MT;
     static_assert(kTmemCols <= 256, "two CTAs share the SM's tensor memory");
     static constexpr uint32_t kXBytes = MT * kF8Block;
     static constexpr uint32_t kStage = kF8TileBytes + kXBytes;
-    static_assert(kStages * kStage >= MT * kTileN * 4, "the sums take the ring's place");
+    static_assert(kStages * kStage >= MT * kTileN * 4 && kCols == MT, "the sums take the ring's place");
     static constexpr uint32_t kIdesc = idesc_e4m3_f32(kTileN, MT);
     static constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
     static constexpr int kScales = kEpiWarps * 2 * kCols * 4;        // a unit's scales, by warp, twice
     static constexpr int kSmem = 1024 + kStages * kStage + kScales + kBars * 8 + 16;
     static_assert(2 * (kSmem + f8_table_bytes(kF8MaxExperts) + 1024) <= 228 * 1024, "two CTAs an SM");
 };
-
-// One output; the residual is added in fp32, and the sum rounded once.
-__device__ __forceinline__ void f8_store(const F8LinearParams &p, int m, int n, float v)
-{
-    const size_t o = static_cast<size_t>(m) * p.N + n;
-    if (p.epilogue == SKG_EPI_FP32) {
-        static_cast<float *>(p.y)[o] = v;
-        return;
-    }
-    if (p.epilogue == SKG_EPI_BF16_RESIDUAL)
-        v += bf16_to_f32(__ldcg(p.res + o));
-    static_cast<uint16_t *>(p.y)[o] = f32_to_bf16(v);
-}
-
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
-// The end of a tile whose K is split over the cluster's CTAs: each has left its
-// sums [token][128 channels] at `smem`; this CTA adds up and stores its share of
-// the tokens, a warp a token.  Called by whole CTAs, all of the cluster's.
-template <int THREADS>
-__device__ __forceinline__ void join_and_store(const F8LinearParams &p, uint32_t smem, int m0, int n0, int tokens, int rank)
-{
-    const int lane = static_cast<int>(threadIdx.x) & 31;
-    cluster_sync();
-    const int t1 = (rank + 1) * tokens / p.split;
-    for (int m = rank * tokens / p.split + static_cast<int>(threadIdx.x >> 5); m < t1; m += THREADS / 32) {
-        const uint32_t at = smem + m * (kTileN * 4);
-        if (p.vec4) {
-            const int n = n0 + 4 * lane;
-            float4 v[kF8SplitMax];
-#pragma unroll
-            for (int r = 0; r < kF8SplitMax; ++r)
-                v[r] = r < p.split ? ld_cluster_f32x4(map_shared_rank(at + 16 * lane, r)) : make_float4(0, 0, 0, 0);
-            float4 s = v[0];
-#pragma unroll
-            for (int r = 1; r < kF8SplitMax; ++r)
-                s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
-            if (n < p.N) {
-                const size_t o = static_cast<size_t>(m0 + m) * p.N + n;
-                if (p.epilogue == SKG_EPI_FP32) {
-                    *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + o) = s;
-                } else {
-                    if (p.epilogue == SKG_EPI_BF16_RESIDUAL) {
-                        const uint2 b = __ldcg(reinterpret_cast<const uint2 *>(p.res + o));
-                        s.x += bf16lo(b.x), s.y += bf16hi(b.x), s.z += bf16lo(b.y), s.w += bf16hi(b.y);
-                    }
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + o) =
-                        make_uint2(f32_to_bf16(s.x) | static_cast<uint32_t>(f32_to_bf16(s.y)) << 16,
-                                   f32_to_bf16(s.z) | static_cast<uint32_t>(f32_to_bf16(s.w)) << 16);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float s = 0.0f;
-                for (int r = 0; r < p.split; ++r)
-                    s += ld_shared_cluster_f32(map_shared_rank(at + 4 * (lane + 32 * i), r));
-                if (n0 + lane + 32 * i < p.N)
-                    f8_store(p, m0 + m, n0 + lane + 32 * i, s);
-            }
-        }
-    }
-    cluster_sync();                      // no CTA leaves while a peer reads its sums
-}
 
 template <int MT>
 __global__ void __launch_bounds__(SplitShape<MT>::kThreads, 2)
@@ -271,19 +201,19 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         // Not sooner (see skg_q8_stream.cu), and after this CTA's TMEM is allocated.
         pdl_launch_dependents();
         const int ew = warp - Sh::kFirstEpi;
-        const int row = (warp & 3) * 32 + lane, col0 = (ew >> 2) * NC;
-        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(col0);
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         float *mine = scales + ew * 2 * NC;
         constexpr int CP = (NC + 31) / 32;               // tokens whose scales a lane fetches
-        constexpr int AHEAD = MT == 128 ? 2 : 4;         // units whose scales are on their way
-        constexpr int H = NC >= 32 && MT < 128 ? 2 : 1;  // 16 columns read at a time, or 32
+        constexpr int AHEAD = 4;                         // units whose scales are on their way
+        constexpr int H = NC >= 32 ? 2 : 1;              // 16 columns read at a time, or 32
         bool ok = true;
         int j = 0;
         for (int tile = first; ok && tile < tiles; tile += step) {
             const F8Tile t = f8_tile(p, MT, table, tile);
-            const int tokens = min(t.m1 - t.m0 - col0, NC);
+            const int tokens = min(t.m1 - t.m0, NC);
             const float *ws = p.w_scale + (static_cast<size_t>(t.e) * p.nb + t.nt) * p.nkb + kb0;
-            const float *xs = p.x_scale + static_cast<size_t>(t.m0 + col0 + lane) * p.nkb + kb0;
+            const float *xs = p.x_scale + static_cast<size_t>(t.m0 + lane) * p.nkb + kb0;
             float w[AHEAD], x[AHEAD][CP];
             auto fetch = [&](int kb, float &wv, float (&xv)[CP]) {
                 wv = kb < units ? __ldcg(ws + kb) : 0.0f;
@@ -351,13 +281,13 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
                         if (c < tokens)
-                            f8_store(p, t.m0 + col0 + c, n, acc[c]);
+                            f8_store(p, t.m0 + c, n, acc[c]);
                 }
             } else {
                 // in the ring's place: the last MMA has read its operands
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    reinterpret_cast<float *>(smem)[(col0 + c) * kTileN + row] = acc[c];
+                    *reinterpret_cast<float *>(smem + f8_sum_at(kTileN, c, row)) = acc[c];
             }
         }
         if (!ok)
@@ -368,7 +298,7 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     tc_fence_before();
     if (p.split > 1) {
         const F8Tile t = f8_tile(p, MT, table, first);
-        join_and_store<Sh::kThreads>(p, smem_u32(smem), t.m0, t.nt * kTileN, min(MT, t.m1 - t.m0), rank);
+        f8_join<kF8SplitMax, Sh::kThreads>(p, smem_u32(smem), kTileN, t.m0, t.nt * kTileN, min(MT, t.m1 - t.m0), rank, 0, 1);
     } else {
         __syncthreads();
     }
@@ -426,7 +356,7 @@ F8TcShape shape_of(int experts)
 F8TcShape f8_split_shape(int m_tile, int experts)
 {
     return m_tile == 16 ? shape_of<16>(experts) : m_tile == 32 ? shape_of<32>(experts)
-           : m_tile == 64 ? shape_of<64>(experts) : shape_of<128>(experts);
+                                                                        : shape_of<64>(experts);
 }
 
 cudaError_t launch_f8_split(const CUtensorMap &tmW, const CUtensorMap &tmX, const F8LinearParams &p, int m_tile, int grid,
@@ -434,8 +364,7 @@ cudaError_t launch_f8_split(const CUtensorMap &tmW, const CUtensorMap &tmX, cons
 {
     return m_tile == 16   ? launch_shape<16>(tmW, tmX, p, grid, s)
            : m_tile == 32 ? launch_shape<32>(tmW, tmX, p, grid, s)
-           : m_tile == 64 ? launch_shape<64>(tmW, tmX, p, grid, s)
-                          : launch_shape<128>(tmW, tmX, p, grid, s);
+                          : launch_shape<64>(tmW, tmX, p, grid, s);
 }
 
 } // namespace skg

@@ -32,76 +32,120 @@ namespace {
 
 #include "skg_f8_tc_common.cuh"
 
-constexpr int kPair = 2;
-constexpr int MT = 256, NT = 256;                    // tokens and channels of a pair's tile
 constexpr uint64_t kLandNs = 10000000;               // 10 ms: far longer than any copy takes
 
+template <int PAIR>
 struct WideShape {
+    static constexpr int MT = 128 * PAIR, NT = 128 * PAIR;   // tokens and channels of a tile
     static constexpr int kEpiWarps = 8;
-    static constexpr int kCols = NT * 4 / kEpiWarps;         // 128: one block of channels
-    static_assert(kCols == kF8Block, "one scale of W a thread");
-    static constexpr int kMmaWarp = 0, kTmaWarp = 1, kFirstEpi = 2;
-    static constexpr int kThreads = 32 * (2 + kEpiWarps);
-    static constexpr int kStages = 6;
-    static constexpr int kAcc = 2;
+    static constexpr int kCols = NT * 4 / kEpiWarps;         // accumulator columns of an epilogue thread
+    static_assert(kF8Block % kCols == 0, "one scale of W a thread");
+    static constexpr int kMmaWarp = 0, kTmaWarp = 1, kFirstEpi = 4;          // two warps of the first warpgroup are idle
+    static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+    // Registers: the launch has 3 warpgroups of 168 a thread.
+    static constexpr int kRegsFew = 72, kRegsMany = 216;
+    static_assert(kRegsFew + 2 * kRegsMany <= 3 * 168 && kThreads == 3 * 128, "no more than the launch has");
+    static constexpr int kStages = 5;
+    static constexpr int kAcc = 512 / NT;                    // accumulators in flight
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kStage = 2 * kF8TileBytes;     // a CTA's x and W of a unit
     static constexpr uint32_t kIdesc = idesc_e4m3_f32(MT, NT);
     static constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
-    static constexpr int kSmem = 1024 + kStages * kStage + kBars * 8 + 16;
+    static constexpr int kOut = 32 * 128;                    // a warp's part of the output on its way: 32 rows of 128 bytes
+    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kOut + kBars * 8 + 16;
+    static_assert(kStages * kStage >= 128 * NT * 4, "the sums take the ring's place");
     static_assert(kSmem + f8_table_bytes(kF8MaxExperts) <= 227 * 1024, "shared memory of a CTA");
 };
 
-// 16 outputs (channels n0 ...) of one token.
-template <int EPI>
-__device__ __forceinline__ void store_row(const F8LinearParams &p, int m, int n0, const float *v)
+// A warp's 32 rows (tokens m0 ... below m1, a lane each) of NC channels from n0,
+// by way of shared memory, so that a store's lanes cover rows: of 128 bytes at a
+// time, bf16 or, where more is to be added, fp32.  (Each lane storing its own row
+// in pieces of 8 bytes took 8 us a tile.)  16-byte pieces are swizzled by row.
+template <int EPI, int NC>
+__device__ __forceinline__ void store_tile(const F8LinearParams &p, int m0, int m1, int n0, const float (&acc)[NC],
+                                           uint8_t *out)
 {
-    const size_t o = static_cast<size_t>(m) * p.N + n0;
-    if (p.vec4) {
-#pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-            if (n0 + c >= p.N)
-                return;
-            float4 s = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-            if (EPI == SKG_EPI_FP32) {
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + o + c) = s;
-                continue;
-            }
-            if (EPI == SKG_EPI_BF16_RESIDUAL) {
-                const uint2 b = __ldcg(reinterpret_cast<const uint2 *>(p.res + o + c));
-                s.x += bf16lo(b.x), s.y += bf16hi(b.x), s.z += bf16lo(b.y), s.w += bf16hi(b.y);
-            }
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + o + c) =
-                make_uint2(f32_to_bf16(s.x) | static_cast<uint32_t>(f32_to_bf16(s.y)) << 16,
-                           f32_to_bf16(s.z) | static_cast<uint32_t>(f32_to_bf16(s.w)) << 16);
-        }
+    constexpr int W = EPI == SKG_EPI_BF16 ? 64 : 32;             // channels at a time
+    const int lane = static_cast<int>(threadIdx.x) & 31, rows = min(m1 - m0, 32);
+    if (rows <= 0)
         return;
-    }
+    auto piece = [&](int row, int c) { return out + row * 128 + ((c ^ (row & 7)) << 4); };
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        if (n0 + c >= p.N)
+    for (int c0 = 0; c0 < NC; c0 += W) {
+        const int n = n0 + c0, valid = p.N - n;
+        if (valid <= 0)
             return;
-        float s = v[c];
-        if (EPI == SKG_EPI_FP32) {
-            static_cast<float *>(p.y)[o + c] = s;
-            continue;
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (EPI == SKG_EPI_BF16) {
+                    w[i] = two_bf16(acc[c0 + 8 * c + 2 * i], acc[c0 + 8 * c + 2 * i + 1]);
+                } else {
+                    w[i] = __float_as_uint(acc[c0 + 4 * c + i]);
+                }
+            }
+            *reinterpret_cast<uint4 *>(piece(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (EPI == SKG_EPI_BF16_RESIDUAL)
-            s += bf16_to_f32(__ldcg(p.res + o + c));
-        static_cast<uint16_t *>(p.y)[o + c] = f32_to_bf16(s);
+        __syncwarp();
+        if (p.vec) {                     // pieces of the output are aligned, and N ends between two
+            const int c = lane & 7;
+            const bool in = c * (W / 8) < valid;
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 4) {
+                const int r = r0 + (lane >> 3);
+                const uint4 v = *reinterpret_cast<const uint4 *>(piece(r, c));
+                if (!in || r >= rows)
+                    continue;
+                const size_t o = static_cast<size_t>(m0 + r) * p.N + n + c * (W / 8);
+                if constexpr (EPI == SKG_EPI_BF16_RESIDUAL) {
+                    const uint2 b = __ldcg(reinterpret_cast<const uint2 *>(p.res + o));
+                    const float s0 = __uint_as_float(v.x) + bf16lo(b.x), s1 = __uint_as_float(v.y) + bf16hi(b.x);
+                    const float s2 = __uint_as_float(v.z) + bf16lo(b.y), s3 = __uint_as_float(v.w) + bf16hi(b.y);
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + o) =
+                        make_uint2(two_bf16(s0, s1), two_bf16(s2, s3));
+                } else if constexpr (EPI == SKG_EPI_FP32) {
+                    *reinterpret_cast<uint4 *>(static_cast<float *>(p.y) + o) = v;
+                } else {
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + o) = v;
+                }
+            }
+        } else {
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+#pragma unroll
+                for (int c = lane; c < W; c += 32) {
+                    if (c >= valid)
+                        continue;
+                    const size_t o = static_cast<size_t>(m0 + r) * p.N + n + c;
+                    if constexpr (EPI == SKG_EPI_BF16) {
+                        static_cast<uint16_t *>(p.y)[o] = *reinterpret_cast<const uint16_t *>(piece(r, c >> 3) + 2 * (c & 7));
+                    } else {
+                        float v = *reinterpret_cast<const float *>(piece(r, c >> 2) + 4 * (c & 3));
+                        if (EPI == SKG_EPI_BF16_RESIDUAL)
+                            static_cast<uint16_t *>(p.y)[o] = f32_to_bf16(v + bf16_to_f32(__ldcg(p.res + o)));
+                        else
+                            static_cast<float *>(p.y)[o] = v;
+                    }
+                }
+            }
+        }
     }
 }
 
-__global__ void __launch_bounds__(WideShape::kThreads, 1)
+template <int PAIR>
+__global__ void __launch_bounds__(WideShape<PAIR>::kThreads, 1)
 f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const F8LinearParams p)
 {
-    using Sh = WideShape;
-    constexpr int S = Sh::kStages, NA = Sh::kAcc, NC = Sh::kCols;
+    using Sh = WideShape<PAIR>;
+    constexpr int MT = Sh::MT, NT = Sh::NT, S = Sh::kStages, NA = Sh::kAcc, NC = Sh::kCols;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sX = smem, *sW = smem + S * kF8TileBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S * Sh::kStage);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S * Sh::kStage + Sh::kEpiWarps * Sh::kOut);
     uint64_t *empty = full + S;
     uint64_t *afull = empty + S;         // [NA] accumulators
     uint64_t *aempty = afull + NA;       // [NA]
@@ -115,9 +159,12 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     table.tile0 = table.row0 + p.experts + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(blockIdx.x) % kPair, first = static_cast<int>(blockIdx.x) / kPair;
-    const int step = static_cast<int>(gridDim.x) / kPair;
-    const int units = p.nkb;
+    // A cluster is p.split CTAs or pairs, each with its part of K.  With more than
+    // one there is a cluster for each tile.
+    const int rank = static_cast<int>(blockIdx.x) % PAIR, part = static_cast<int>(blockIdx.x) / PAIR % p.split;
+    const int first = static_cast<int>(blockIdx.x) / (PAIR * p.split), step = static_cast<int>(gridDim.x) / (PAIR * p.split);
+    const int lead = part * PAIR;        // the pair's first CTA, in the cluster
+    const int kb0 = part * p.nkb / p.split, units = (part + 1) * p.nkb / p.split - kb0;
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tmW);
@@ -128,7 +175,7 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         }
         for (int i = 0; i < NA; ++i) {
             mbar_init(&afull[i], 1);
-            mbar_init(&aempty[i], kPair * Sh::kEpiWarps);
+            mbar_init(&aempty[i], PAIR * Sh::kEpiWarps);
         }
         mbar_init(drain, 1);
         flags[0] = 0;
@@ -141,11 +188,16 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     }
     __syncthreads();
     const int tiles = f8_tiles(p, table);
-    if (first >= tiles)                  // both CTAs of the pair
+    if (first >= tiles)                  // all of the cluster's CTAs
         return;
     if (warp == Sh::kMmaWarp) {
-        tmem_alloc_pair(tmem_slot, Sh::kTmemCols);
-        tmem_relinquish_pair();
+        if constexpr (PAIR == 2) {
+            tmem_alloc_pair(tmem_slot, Sh::kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, Sh::kTmemCols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     cluster_sync();                      // the peer's barriers exist before anything is sent there
@@ -154,111 +206,133 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     if (warp != Sh::kTmaWarp)            // the bounded waits do not count the previous kernel's time
         pdl_wait();
 
-    if (warp == Sh::kTmaWarp) {
-        // -------------------------------------------------------- TMA producer
-        const bool leader = elect_one();
-        const uint64_t pol = policy_evict_normal();
-        const uint32_t full0 = map_shared_rank(smem_u32(full), 0);
-        auto load_w = [&](int u, const F8Tile &t, int kb) {
-            if (rank == 0)               // for both CTAs' copies, which may be counted before
-                mbar_arrive_expect_tx(&full[u % S], kPair * Sh::kStage);
-            tma_load_2d_pair(sW + u % S * kF8TileBytes, &tmW, full0 + u % S * 8, kb * kF8Block,
-                             t.e * p.N + t.nt * NT + rank * (NT / kPair), pol);
-        };
-        auto load_x = [&](int u, const F8Tile &t, int kb) {
-            tma_load_2d_pair(sX + u % S * kF8TileBytes, &tmX, full0 + u % S * 8, kb * kF8Block, t.m0 + rank * (MT / kPair), pol);
-        };
-        F8Tile t = f8_tile(p, MT, table, first);
-        const int ahead = p.static_w && !p.experts ? min(S, units) : 0;
-        if (leader)
-            for (int u = 0; u < ahead; ++u)
-                load_w(u, t, u);
-        pdl_wait();
-        if (leader)
-            for (int u = 0; u < ahead; ++u)
-                load_x(u, t, u);
-        bool ok = true;
-        int j = 0;
-        for (int tile = first; ok && tile < tiles; tile += step) {
-            if (tile != first)
-                t = f8_tile(p, MT, table, tile);
-            for (int kb = 0; kb < units; ++kb, ++j) {
-                if (j < ahead)
-                    continue;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&empty[j % S], ((j / S) & 1) ^ 1, p.timeout_ns, &flags[0]));
-                if (!ok)
-                    break;
-                if (leader) {
-                    load_w(j, t, kb);
-                    load_x(j, t, kb);
-                }
-                __syncwarp();
-            }
-        }
-        if (!ok)
-            f8_fail(p.err, &flags[0], kErrTimeoutProducer);
-        if (flags[0]) {                  // abort: let every copy land before exit, a few microseconds after its issue
-            const uint64_t t0 = globaltimer_ns();    // (the second CTA's are counted in the first)
-            while (globaltimer_ns() - t0 < kLandNs) {
-            }
-        }
-    } else if (warp == Sh::kMmaWarp) {
-        // ---------------------------------------------------------- MMA issuer
-        if (rank == 0) {
+    if (warp < Sh::kFirstEpi) {
+        regs_dec<Sh::kRegsFew>();
+        if (warp == Sh::kTmaWarp) {
+            // -------------------------------------------------------- TMA producer
             const bool leader = elect_one();
-            const uint64_t w0 = smem_desc_kmajor_sw128(smem_u32(sW)), x0 = smem_desc_kmajor_sw128(smem_u32(sX));
-            const int total = ((tiles - first + step - 1) / step) * units;
+            const uint64_t pol = policy_evict_normal();
+            const uint32_t full0 = map_shared_rank(smem_u32(full), lead);
+            auto load = [&](uint8_t *ring, int u, const CUtensorMap *m, int kb, int row) {
+                if constexpr (PAIR == 2)
+                    tma_load_2d_pair(ring + u % S * kF8TileBytes, m, full0 + u % S * 8, (kb0 + kb) * kF8Block, row, pol);
+                else
+                    tma_load_2d(ring + u % S * kF8TileBytes, m, &full[u % S], (kb0 + kb) * kF8Block, row, pol);
+            };
+            auto load_w = [&](int u, const F8Tile &t, int kb) {
+                if (rank == 0)           // for both CTAs' copies, which may be counted before
+                    mbar_arrive_expect_tx(&full[u % S], PAIR * Sh::kStage);
+                load(sW, u, &tmW, kb, t.e * p.N + t.nt * NT + rank * 128);
+            };
+            auto load_x = [&](int u, const F8Tile &t, int kb) { load(sX, u, &tmX, kb, t.m0 + rank * 128); };
+            F8Tile t = f8_tile(p, MT, table, first);
+            const int ahead = p.static_w && !p.experts ? min(S, units) : 0;
+            if (leader)
+                for (int u = 0; u < ahead; ++u)
+                    load_w(u, t, u);
+            pdl_wait();
+            if (leader)
+                for (int u = 0; u < ahead; ++u)
+                    load_x(u, t, u);
             bool ok = true;
-            int sl = 0, phase = 0;
-            for (int j = 0; j < total; ++j) {
-                const int t = j % NA;
-                ok = mbar_wait_cluster(&aempty[t], ((j / NA) & 1) ^ 1, p.timeout_ns, &flags[0]) &&
-                     mbar_wait_cluster(&full[sl], phase, p.timeout_ns, &flags[0]);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                if (leader) {
-                    const uint64_t a = x0 + static_cast<uint64_t>(sl * (kF8TileBytes / 16));
-                    const uint64_t b = w0 + static_cast<uint64_t>(sl * (kF8TileBytes / 16));
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_f8_pair(tmem_base + t * NT, a + 2 * kk, b + 2 * kk, Sh::kIdesc, kk > 0);
-                    // nobody waits for the last units' slots, and the peer's producer may be gone by then
-                    if (j + S < total)
-                        tc_commit_pair_multicast(&empty[sl], 3);
-                    tc_commit_pair_multicast(&afull[t], 3);
-                }
-                __syncwarp();
-                if (++sl == S) {
-                    sl = 0;
-                    phase ^= 1;
+            int j = 0;
+            for (int tile = first; ok && tile < tiles; tile += step) {
+                if (tile != first)
+                    t = f8_tile(p, MT, table, tile);
+                for (int kb = 0; kb < units; ++kb, ++j) {
+                    if (j < ahead)
+                        continue;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[j % S], ((j / S) & 1) ^ 1, p.timeout_ns, &flags[0]));
+                    if (!ok)
+                        break;
+                    if (leader) {
+                        load_w(j, t, kb);
+                        load_x(j, t, kb);
+                    }
+                    __syncwarp();
                 }
             }
-            if (!ok) {                   // abort: wait for the MMAs already issued before TMEM is freed
-                f8_fail(p.err, &flags[0], kErrTimeoutMma);
-                if (leader)
-                    tc_commit_pair(drain);
-                volatile int never = 0;
-                mbar_wait(drain, 0, kDefaultTimeoutNs, &never);
+            if (!ok)
+                f8_fail(p.err, &flags[0], kErrTimeoutProducer);
+            if (flags[0]) {                  // abort: let every copy land before exit, a few microseconds after its issue
+                const uint64_t t0 = globaltimer_ns();    // (the second CTA's are counted in the first)
+                while (globaltimer_ns() - t0 < kLandNs) {
+                }
+            }
+        } else if (warp == Sh::kMmaWarp) {
+            // ---------------------------------------------------------- MMA issuer
+            if (rank == 0) {
+                const bool leader = elect_one();
+                const uint64_t w0 = smem_desc_kmajor_sw128(smem_u32(sW)), x0 = smem_desc_kmajor_sw128(smem_u32(sX));
+                const int total = ((tiles - first + step - 1) / step) * units;
+                auto commit = [&](uint64_t *bar) {
+                    if constexpr (PAIR == 2)
+                        tc_commit_pair_multicast(bar, static_cast<uint16_t>(3 << lead));
+                    else
+                        tc_commit(bar);
+                };
+                bool ok = true;
+                int sl = 0, phase = 0;
+                for (int j = 0; j < total; ++j) {
+                    const int t = j % NA;
+                    ok = mbar_wait(&aempty[t], ((j / NA) & 1) ^ 1, p.timeout_ns, &flags[0]) &&
+                         mbar_wait(&full[sl], phase, p.timeout_ns, &flags[0]);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t a = x0 + static_cast<uint64_t>(sl * (kF8TileBytes / 16));
+                        const uint64_t b = w0 + static_cast<uint64_t>(sl * (kF8TileBytes / 16));
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if constexpr (PAIR == 2)
+                                tc_mma_f8_pair(tmem_base + t * NT, a + 2 * kk, b + 2 * kk, Sh::kIdesc, kk > 0);
+                            else
+                                tc_mma_f8(tmem_base + t * NT, a + 2 * kk, b + 2 * kk, Sh::kIdesc, kk > 0);
+                        }
+                        // nobody waits for the last units' slots, and the peer's producer may be gone by then
+                        if (j + S < total)
+                            commit(&empty[sl]);
+                        commit(&afull[t]);
+                    }
+                    __syncwarp();
+                    if (++sl == S) {
+                        sl = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) {                   // abort: wait for the MMAs already issued before TMEM is freed
+                    f8_fail(p.err, &flags[0], kErrTimeoutMma);
+                    if (leader) {
+                        if constexpr (PAIR == 2)
+                            tc_commit_pair(drain);
+                        else
+                            tc_commit(drain);
+                    }
+                    volatile int never = 0;
+                    mbar_wait(drain, 0, kDefaultTimeoutNs, &never);
+                }
             }
         }
     } else {
+        regs_inc<Sh::kRegsMany>();
         // ------------------------------------------------------------ epilogue
         pdl_launch_dependents();         // not sooner: see skg_q8_stream.cu
         const int ew = warp - Sh::kFirstEpi;
-        const int row = rank * (MT / kPair) + (warp & 3) * 32 + lane, col0 = (ew >> 2) * NC;
+        const int col0 = (ew >> 2) * NC, row0 = rank * 128 + (warp & 3) * 32;
+        uint8_t *out = smem + S * Sh::kStage + ew * Sh::kOut;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(col0);
-        const uint32_t aempty0 = map_shared_rank(smem_u32(aempty), 0);
-        constexpr int AHEAD = 4;
+        const uint32_t aempty0 = map_shared_rank(smem_u32(aempty), lead);
+        constexpr int AHEAD = 8;
         bool ok = true;
         int j = 0;
         for (int tile = first; ok && tile < tiles; tile += step) {
             const F8Tile t = f8_tile(p, MT, table, tile);
-            const int m = t.m0 + row, nb = t.nt * (NT / kF8Block) + (ew >> 2);
+            const int m = t.m0 + row0 + lane, nb = t.nt * (NT / kF8Block) + col0 / kF8Block;
             const bool live = m < t.m1 && nb < p.nb;
-            const float *ws = p.w_scale + (static_cast<size_t>(t.e) * p.nb + nb) * p.nkb;
-            const float *xs = p.x_scale + static_cast<size_t>(m) * p.nkb;
+            const float *ws = p.w_scale + (static_cast<size_t>(t.e) * p.nb + nb) * p.nkb + kb0;
+            const float *xs = p.x_scale + static_cast<size_t>(m) * p.nkb + kb0;
             float w[AHEAD], x[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
@@ -279,45 +353,34 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     w[i] = more ? __ldcg(ws + kb + i + AHEAD) : 0.0f;
                     x[i] = more ? __ldca(xs + kb + i + AHEAD) : 0.0f;
                     const int a = j % NA;
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&afull[a], (j / NA) & 1, p.timeout_ns, &flags[0]));
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&afull[a], (j / NA) & 1, p.timeout_ns, &flags[0]));
                     if (!ok)
                         break;
                     tc_fence_after();
-#pragma unroll
-                    for (int c0 = 0; c0 < NC; c0 += 32) {
-                        uint32_t r[2][16];
-                        tmem_ld_x16(lane_base + static_cast<uint32_t>(a * NT + c0), r[0]);
-                        tmem_ld_x16(lane_base + static_cast<uint32_t>(a * NT + c0 + 16), r[1]);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            f8_taken(r[h]);
-#pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                acc[c0 + 16 * h + c] = fmaf(__uint_as_float(r[h][c]), s, acc[c0 + 16 * h + c]);
-                        }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_cluster(aempty0 + a * 8);
+                    f8_add_unit(acc, lane_base + static_cast<uint32_t>(a * NT), s, [&] {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_cluster(aempty0 + a * 8);
+                    });
                     ++j;
                 }
             }
             if (!ok)
                 break;
-            if (live) {
-                const int n0 = t.nt * NT + col0;
+            const int n0 = t.nt * NT + col0;
+            if (p.split > 1) {
+                // in the ring's place: the last MMA has read its operands
 #pragma unroll
-                for (int c = 0; c < NC; c += 16) {
-                    if (p.epilogue == SKG_EPI_FP32)
-                        store_row<SKG_EPI_FP32>(p, m, n0 + c, acc + c);
-                    else if (p.epilogue == SKG_EPI_BF16_RESIDUAL)
-                        store_row<SKG_EPI_BF16_RESIDUAL>(p, m, n0 + c, acc + c);
-                    else
-                        store_row<SKG_EPI_BF16>(p, m, n0 + c, acc + c);
-                }
-            }
+                for (int c = 0; c < NC; c += 4)
+                    *reinterpret_cast<float4 *>(smem + f8_sum_at(NT, row0 - rank * 128 + lane, col0 + c)) =
+                        make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+            } else if (p.epilogue == SKG_EPI_FP32)
+                store_tile<SKG_EPI_FP32, NC>(p, t.m0 + row0, t.m1, n0, acc, out);
+            else if (p.epilogue == SKG_EPI_BF16_RESIDUAL)
+                store_tile<SKG_EPI_BF16_RESIDUAL, NC>(p, t.m0 + row0, t.m1, n0, acc, out);
+            else
+                store_tile<SKG_EPI_BF16, NC>(p, t.m0 + row0, t.m1, n0, acc, out);
         }
         if (!ok)
             f8_fail(p.err, &flags[0], kErrTimeoutEpilogue);
@@ -325,22 +388,28 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 
     __syncwarp();
     tc_fence_before();
-    cluster_sync();                      // no CTA leaves while its peer may still send to it
+    if (p.split > 1) {
+        const F8Tile t = f8_tile(p, MT, table, first);
+        f8_join<kF8WideMaxSplit, Sh::kThreads>(p, smem_u32(smem), NT, t.m0 + rank * 128, t.nt * NT, min(128, max(0, t.m1 - t.m0 - rank * 128)),
+                                               part, rank, PAIR);
+    } else if (PAIR == 2) {
+        cluster_sync();                  // no CTA leaves while its peer may still send to it
+    } else {
+        __syncthreads();
+    }
     if (warp == Sh::kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, Sh::kTmemCols);
+        if constexpr (PAIR == 2)
+            tmem_dealloc_pair(tmem_base, Sh::kTmemCols);
+        else
+            tmem_dealloc(tmem_base, Sh::kTmemCols);
     }
 }
 
-} // namespace
-
-F8TcShape f8_wide_shape(int experts)
+template <int PAIR>
+cudaError_t launch_shape(const CUtensorMap &tmW, const CUtensorMap &tmX, const F8LinearParams &p, int grid, cudaStream_t s)
 {
-    return {MT, 1, WideShape::kSmem + f8_table_bytes(experts), WideShape::kThreads, WideShape::kStages};
-}
-
-cudaError_t launch_f8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const F8LinearParams &p, int grid, cudaStream_t s)
-{
+    using Sh = WideShape<PAIR>;
     static int attr_set[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -349,26 +418,43 @@ cudaError_t launch_f8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const
     if (dev >= kMaxDevices)
         return cudaErrorInvalidDevice;
     if (__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE) == 0) {
-        e = cudaFuncSetAttribute(f8_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 WideShape::kSmem + f8_table_bytes(kF8MaxExperts));
+        e = cudaFuncSetAttribute(f8_wide_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Sh::kSmem + f8_table_bytes(kF8MaxExperts));
         if (e != cudaSuccess)
             return e;
         __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(WideShape::kThreads);
-    cfg.dynamicSmemBytes = WideShape::kSmem + f8_table_bytes(p.experts);
+    cfg.blockDim = dim3(Sh::kThreads);
+    cfg.dynamicSmemBytes = Sh::kSmem + f8_table_bytes(p.experts);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kPair;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(PAIR * p.split);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, f8_wide_kernel, tmW, tmX, p);
+    return cudaLaunchKernelEx(&cfg, f8_wide_kernel<PAIR>, tmW, tmX, p);
+}
+
+template <int PAIR>
+F8TcShape shape_of(int experts)
+{
+    using Sh = WideShape<PAIR>;
+    return {Sh::MT, 1, Sh::kSmem + f8_table_bytes(experts), Sh::kThreads, Sh::kStages};
+}
+
+} // namespace
+
+F8TcShape f8_wide_shape(int m_tile, int experts) { return m_tile == 256 ? shape_of<2>(experts) : shape_of<1>(experts); }
+
+cudaError_t launch_f8_wide(const CUtensorMap &tmW, const CUtensorMap &tmX, const F8LinearParams &p, int m_tile, int grid,
+                           cudaStream_t s)
+{
+    return m_tile == 256 ? launch_shape<2>(tmW, tmX, p, grid, s) : launch_shape<1>(tmW, tmX, p, grid, s);
 }
 
 } // namespace skg

@@ -44,6 +44,20 @@ __device__ __forceinline__ void pdl_launch_dependents()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The registers a thread of this warpgroup may have from here on: fewer, or more
+// out of those that other warpgroups have given up.
+template <int N>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+
 // ------------------------------------------------------------ L2 policies
 __device__ __forceinline__ uint64_t policy_evict_first()
 {

@@ -10,8 +10,8 @@ from tests import f8_reference as R
 
 pytestmark = pytest.mark.gpu
 
-SPLITS = [(skg.SKG_F8_KERNEL_SPLIT, mt, s) for mt in (16, 32, 64, 128) for s in (1, 2, 5, 8)]
-LAUNCHES = SPLITS + [(skg.SKG_F8_KERNEL_WIDE, 256, 1)]
+LAUNCHES = [(skg.SKG_F8_KERNEL_SPLIT, mt, s) for mt in (16, 32, 64) for s in (1, 2, 5, 8)] + \
+           [(skg.SKG_F8_KERNEL_WIDE, mt, s) for mt in (128, 256) for s in (1, 2, 3, 4)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -205,7 +205,7 @@ def test_experts_as_planned(counts, first, behind, epilogue):
     by_experts(counts, 136, 272, epilogue, first=first, behind=behind)
 
 
-@pytest.mark.parametrize("launch", [(1, 16, 1), (1, 32, 2), (1, 128, 1), (2, 256, 1)])
+@pytest.mark.parametrize("launch", [(1, 16, 1), (1, 32, 2), (2, 128, 1), (2, 256, 1)])
 @pytest.mark.parametrize("offsets", [[-5, 3, 2, 900, 20], [30, 20, 10, 0, -1], [0, 0, 0, 0, 2 ** 31 - 1],
                                      [-2 ** 31, -1, 5, 4, 40]])
 def test_offsets_that_are_out_of_order_or_range(offsets, launch):
@@ -229,7 +229,7 @@ def test_offsets_that_are_out_of_order_or_range(offsets, launch):
     assert bool((y[:at[0]] == -7).all()) and bool((y[at[4]:] == -7).all())
 
 
-@pytest.mark.parametrize("launch", [(1, 16, 4), (1, 64, 1), (2, 256, 1)])
+@pytest.mark.parametrize("launch", [(1, 16, 4), (1, 64, 1), (2, 128, 3), (2, 256, 1)])
 def test_scales_that_are_nan_or_zero_stay_in_their_rows_and_blocks(launch):
     g = gen(10)
     M, N, K = 40, 300, 512
