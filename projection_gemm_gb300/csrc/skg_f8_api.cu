@@ -46,6 +46,12 @@ static_assert(sizeof(kSplitResident) / sizeof(int) == kF8SplitMax + 1, "a count 
 
 long long resident(int on_152, int num_sms) { return std::max(1ll, static_cast<long long>(on_152) * num_sms / 152); }
 
+// Experts with a row, about: the rows' choices taken as even.
+double taken(const skg_f8_plan_desc &d)
+{
+    return d.experts ? d.experts * (1.0 - std::pow(1.0 - 1.0 / d.experts, d.M)) : 1.0;
+}
+
 // Token tiles: of one weight exactly; of experts as many as they take about, for
 // the choice of a launch (`most` false), or at the most.
 double token_tiles(const skg_f8_plan_desc &d, int m_tile, bool most)
@@ -54,8 +60,7 @@ double token_tiles(const skg_f8_plan_desc &d, int m_tile, bool most)
         return ceil_div(d.M, m_tile);
     if (most)
         return std::min(d.experts, d.M) + d.M / m_tile;
-    const double taken = d.experts * (1.0 - std::pow(1.0 - 1.0 / d.experts, d.M)), rows = d.M / taken;
-    return taken * std::max(1.0, rows / m_tile + 0.5);
+    return taken(d) * std::max(1.0, d.M / taken(d) / m_tile + 0.5);
 }
 
 // The same of the wide kernel, a CTA an SM: single CTAs (128 tokens) and pairs (256).
@@ -77,19 +82,42 @@ long long slots_of(int kind, int m_tile, int split, int num_sms)
     return resident(r[split], num_sms);
 }
 
-// The kernels' times (us) as measured: a unit of 128 k, a tile, a launch's ends.
+// The kernels' times (us) as measured: what a unit of 128 k takes a CTA's MMAs and
+// its epilogue, a tile's end, and a launch's ends.
+//
+//                     unit: one CTA an SM, two   tile   ends   with K split
+//   SPLIT 16 tokens         0.27  0.40           0.6    2.8    4.9
+//         32                0.30  0.46           0.8    2.8    4.9
+//         64                0.43  0.85           1.2    2.8    4.9
+//   WIDE 128                0.33  -              1.0    3.0    6.8
+//        256 (pairs)        0.39  -              2.0    4.0    7.8
+//
+// A tile of the wide kernel takes 2 more where rows of the output are not aligned.
+// The weights come from HBM at 6.3 TB/s at the most.  Where that is what bounds the
+// split kernel, its ends with K split are 8.3 less 0.0225 a CTA: few CTAs take longer until
+// enough of the weights is on its way.  With experts, clusters start 1.3 later.
 double launch_us(const skg_f8_plan_desc &d, int kind, int m_tile, int split, int num_sms)
 {
-    const double tiles = token_tiles(d, m_tile, false) * ceil_div(d.N, n_tile_of(kind, m_tile));
+    const double sms = num_sms, m_tiles = token_tiles(d, m_tile, false), tiles = m_tiles * ceil_div(d.N, n_tile_of(kind, m_tile));
     const int units = ceil_div(ceil_div(d.K, kF8Block), split);
-    const double waves = std::ceil(tiles / static_cast<double>(slots_of(kind, m_tile, split, num_sms)));
-    if (kind == SKG_F8_KERNEL_SPLIT) {
-        const bool alone = tiles * split <= num_sms;
-        const double both = m_tile <= 32 ? 0.72 : 0.80;
-        return waves * (alone ? 0.6 * both : both) * units + (split > 1 ? 5.0 : 3.0);
+    const double slots = static_cast<double>(slots_of(kind, m_tile, split, num_sms));
+    const double at_once = std::min(tiles, slots) * split;            // CTAs, or pairs of them
+    double waves = std::ceil(tiles / slots);
+    if (split == 1 && waves > 2.0)
+        waves = tiles / slots + 0.5;     // persistent: not all end together
+    const double hbm = taken(d) * d.N * d.K / 6.3e6;
+    double unit, tile, ends;
+    if (kind == SKG_F8_KERNEL_WIDE) {
+        unit = m_tile == 128 ? 0.33 : 0.39;
+        tile = (m_tile == 128 ? 1.0 : 2.0) + (d.N % 8 != 0 ? 2.0 : 0.0);
+        ends = (m_tile == 128 ? 3.0 : 4.0) + (split > 1 ? 3.8 : 0.0);
+    } else {
+        const bool two = at_once > sms;
+        unit = m_tile == 16 ? (two ? 0.40 : 0.27) : m_tile == 32 ? (two ? 0.46 : 0.30) : (two ? 0.85 : 0.43);
+        tile = m_tile == 16 ? 0.6 : m_tile == 32 ? 0.8 : 1.2;
+        ends = split == 1 ? 2.8 : waves * (unit * units + tile) > hbm ? 4.9 : std::max(2.0, 8.3 - 0.0225 * at_once * 152.0 / sms);
     }
-    const double unit = m_tile == 128 ? 0.36 : 0.42;
-    return waves * (unit * units + 1.0) + (split > 1 ? 8.0 : 5.0);
+    return std::max(hbm, waves * (unit * units + tile)) + ends + (d.experts && split > 1 ? 1.3 : 0.0);
 }
 
 // The launch that takes the least time, given a kernel, a tile and the CTAs that
@@ -335,10 +363,13 @@ skg_status skg_f8_run(skg_f8_plan_t p, const void *x, const float *x_scale, cons
     g.vec = d.epilogue == SKG_EPI_BF16 ? d.N % 8 == 0 && aligned(y, 16) : g.vec4;
     g.timeout_ns = kDefaultTimeoutNs;
     const bool wide = d.kernel_kind == SKG_F8_KERNEL_WIDE;
+    const int w_rows = d.N * std::max(1, d.experts);
+    g.w_box = std::min(kTileN, w_rows);
+    g.x_box = std::min(wide ? 128 : d.m_tile, d.M);
     CUtensorMap tmW, tmX;
-    skg_status st = encode_tiled_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, d.N * std::max(1, d.experts), d.K, kTileN);
+    skg_status st = encode_tiled_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, w_rows, d.K, g.w_box);
     if (st == SKG_OK)
-        st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, d.M, d.K, wide ? 128 : d.m_tile);
+        st = encode_tiled_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, d.M, d.K, g.x_box);
     if (st != SKG_OK)
         return st;
     return launched(wide ? launch_f8_wide(tmW, tmX, g, d.m_tile, d.grid, s) : launch_f8_split(tmW, tmX, g, d.m_tile, d.grid, s), who);

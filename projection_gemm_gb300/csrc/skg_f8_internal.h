@@ -48,6 +48,7 @@ struct F8LinearParams {
     int M, N, K, epilogue, experts;
     int nkb, nb;
     int m_tiles, n_tiles;     // m_tiles: without experts
+    int x_box, w_box;         // rows of x and of W that a copy takes: see f8_window
     int split, static_w;
     int vec4;                 // N a multiple of 4, residual and y aligned for four channels at a time
     int vec;                  // the same for 16 bytes of sums, or of bf16 where no residual is added

@@ -53,6 +53,37 @@ struct SplitShape {
     static_assert(2 * (kSmem + f8_table_bytes(kF8MaxExperts) + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
+// The outputs of one channel n from its sums of the tokens from m0 on: those of
+// columns lo to hi.
+template <int EPI, int NC>
+__device__ __forceinline__ void store_columns(const F8LinearParams &p, int m0, int n, int lo, int hi, const float (&acc)[NC])
+{
+    size_t at = static_cast<size_t>(m0) * p.N + n;
+#pragma unroll
+    for (int c0 = 0; c0 < NC; c0 += 8, at += static_cast<size_t>(8) * p.N) {
+        if (c0 >= hi)
+            return;
+        uint16_t b[8];
+        if (EPI == SKG_EPI_BF16_RESIDUAL) {
+            const uint16_t *r = p.res + at;
+#pragma unroll
+            for (int c = 0; c < 8; ++c, r += p.N)
+                b[c] = c0 + c >= lo && c0 + c < hi ? __ldcg(r) : 0;
+        }
+        size_t o = at;
+#pragma unroll
+        for (int c = 0; c < 8; ++c, o += p.N) {
+            const float v = EPI == SKG_EPI_BF16_RESIDUAL ? acc[c0 + c] + bf16_to_f32(b[c]) : acc[c0 + c];
+            if (c0 + c >= lo && c0 + c < hi) {
+                if (EPI == SKG_EPI_FP32)
+                    static_cast<float *>(p.y)[o] = v;
+                else
+                    static_cast<uint16_t *>(p.y)[o] = f32_to_bf16(v);
+            }
+        }
+    }
+}
+
 template <int MT>
 __global__ void __launch_bounds__(SplitShape<MT>::kThreads, 2)
 f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const F8LinearParams p)
@@ -127,11 +158,12 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             const uint64_t pol_x = policy_evict_last();
             int j = 0;
             auto load_w = [&](int u, const F8Tile &t, int kb) {
-                mbar_arrive_expect_tx(&full[u % S], Sh::kStage);
-                tma_load_2d(sW + u % S * kF8TileBytes, &tmW, &full[u % S], (kb0 + kb) * kF8Block, t.e * p.N + t.nt * kTileN, pol_w);
+                mbar_arrive_expect_tx(&full[u % S], (p.w_box + p.x_box) * kF8Block);
+                tma_load_2d(sW + u % S * kF8TileBytes, &tmW, &full[u % S], (kb0 + kb) * kF8Block,
+                            f8_w_window(p, t.e, t.nt * kTileN), pol_w);
             };
             auto load_x = [&](int u, const F8Tile &t, int kb) {
-                tma_load_2d(sX + u % S * Sh::kXBytes, &tmX, &full[u % S], (kb0 + kb) * kF8Block, t.m0, pol_x);
+                tma_load_2d(sX + u % S * Sh::kXBytes, &tmX, &full[u % S], (kb0 + kb) * kF8Block, f8_x_window(p, t.m0), pol_x);
             };
             F8Tile t = f8_tile(p, MT, table, first);
             // weights may be requested before the wait for the previous kernel
@@ -211,15 +243,16 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         int j = 0;
         for (int tile = first; ok && tile < tiles; tile += step) {
             const F8Tile t = f8_tile(p, MT, table, tile);
-            const int tokens = min(t.m1 - t.m0, NC);
+            // tokens m0 + lo to m0 + hi of the window, and this thread's channel of the other
+            const int m0 = f8_x_window(p, t.m0), lo = t.m0 - m0, hi = min(t.m1, t.m0 + MT) - m0;
             const float *ws = p.w_scale + (static_cast<size_t>(t.e) * p.nb + t.nt) * p.nkb + kb0;
-            const float *xs = p.x_scale + static_cast<size_t>(t.m0 + lane) * p.nkb + kb0;
+            const float *xs = p.x_scale + static_cast<size_t>(m0 + lane) * p.nkb + kb0;
             float w[AHEAD], x[AHEAD][CP];
             auto fetch = [&](int kb, float &wv, float (&xv)[CP]) {
                 wv = kb < units ? __ldcg(ws + kb) : 0.0f;
 #pragma unroll
                 for (int c = 0; c < CP; ++c)
-                    xv[c] = kb < units && lane + 32 * c < tokens ? __ldca(xs + static_cast<size_t>(32 * c) * p.nkb + kb) : 0.0f;
+                    xv[c] = kb < units && lane + 32 * c >= lo && lane + 32 * c < hi ? __ldca(xs + static_cast<size_t>(32 * c) * p.nkb + kb) : 0.0f;
             };
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i)
@@ -276,13 +309,15 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             if (!ok)
                 break;
             if (p.split == 1) {
-                const int n = t.nt * kTileN + row;
-                if (n < p.N) {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        if (c < tokens)
-                            f8_store(p, t.m0 + c, n, acc[c]);
-                }
+                const int n = f8_w_window(p, t.e, t.nt * kTileN) - t.e * p.N + row;
+                if (n < t.nt * kTileN || n >= p.N)
+                    continue;
+                if (p.epilogue == SKG_EPI_FP32)
+                    store_columns<SKG_EPI_FP32>(p, m0, n, lo, hi, acc);
+                else if (p.epilogue == SKG_EPI_BF16_RESIDUAL)
+                    store_columns<SKG_EPI_BF16_RESIDUAL>(p, m0, n, lo, hi, acc);
+                else
+                    store_columns<SKG_EPI_BF16>(p, m0, n, lo, hi, acc);
             } else {
                 // in the ring's place: the last MMA has read its operands
 #pragma unroll
@@ -298,7 +333,8 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     tc_fence_before();
     if (p.split > 1) {
         const F8Tile t = f8_tile(p, MT, table, first);
-        f8_join<kF8SplitMax, Sh::kThreads>(p, smem_u32(smem), kTileN, t.m0, t.nt * kTileN, min(MT, t.m1 - t.m0), rank, 0, 1);
+        const int n0[1] = {f8_w_window(p, t.e, t.nt * kTileN) - t.e * p.N}, na[1] = {t.nt * kTileN};
+        f8_join<kF8SplitMax, Sh::kThreads, 1>(p, smem_u32(smem), f8_x_window(p, t.m0), t.m0, min(t.m1, t.m0 + MT), n0, na, rank, 0, 1);
     } else {
         __syncthreads();
     }

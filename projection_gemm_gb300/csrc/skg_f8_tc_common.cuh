@@ -25,6 +25,7 @@ __host__ __device__ constexpr int f8_table_bytes(int experts) { return experts ?
 // out of range whatever they are.
 __device__ __forceinline__ void f8_build_table(const F8LinearParams &p, int m_tile, const F8Table &t)
 {
+    constexpr int PER = 4;               // experts a lane: the loads of 128 are on their way together
     const int lane = threadIdx.x & 31;
     auto read = [&](int e) { return e <= p.experts ? min(max(__ldcg(p.offsets + e), 0), p.M) : 0; };
     int row = read(0), tiles = 0;
@@ -32,29 +33,46 @@ __device__ __forceinline__ void f8_build_table(const F8LinearParams &p, int m_ti
         t.row0[0] = row;
         t.tile0[0] = 0;
     }
-    for (int e0 = 1; e0 <= p.experts; e0 += 32) {
-        int v = read(e0 + lane);
+    for (int e0 = 1; e0 <= p.experts; e0 += 32 * PER) {
+        const int e = e0 + lane * PER;
+        int end[PER], n[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            end[i] = read(e + i);
+#pragma unroll
+        for (int i = 1; i < PER; ++i)
+            end[i] = max(end[i], end[i - 1]);
+        int top = end[PER - 1];          // of the lanes up to this one
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-            v = lane >= o ? max(v, u) : v;
+            const int u = __shfl_up_sync(0xFFFFFFFFu, top, o);
+            top = lane >= o ? max(top, u) : top;
         }
-        v = max(v, row);
-        int before = __shfl_up_sync(0xFFFFFFFFu, v, 1);
-        before = lane ? before : row;
-        int n = (v - before + m_tile - 1) / m_tile;
+        int before = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+        before = lane ? max(before, row) : row;
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            end[i] = max(end[i], before);
+            sum += (end[i] - before + m_tile - 1) / m_tile;
+            n[i] = sum;
+            before = end[i];
+        }
+        int up = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xFFFFFFFFu, n, o);
-            n += lane >= o ? u : 0;
+            const int u = __shfl_up_sync(0xFFFFFFFFu, up, o);
+            up += lane >= o ? u : 0;
         }
-        n += tiles;
-        if (e0 + lane <= p.experts) {
-            t.row0[e0 + lane] = v;
-            t.tile0[e0 + lane] = n;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (e + i <= p.experts) {
+                t.row0[e + i] = end[i];
+                t.tile0[e + i] = tiles + up - sum + n[i];
+            }
         }
-        row = __shfl_sync(0xFFFFFFFFu, v, 31);
-        tiles = __shfl_sync(0xFFFFFFFFu, n, 31);
+        row = max(row, __shfl_sync(0xFFFFFFFFu, top, 31));
+        tiles += __shfl_sync(0xFFFFFFFFu, up, 31);
     }
 }
 
@@ -97,6 +115,21 @@ __device__ __forceinline__ F8Tile f8_tile(const F8LinearParams &p, int m_tile, c
     r.nt = i / wide;
     r.m0 += (b * kF8Band + i - r.nt * wide) * m_tile;
     return r;
+}
+
+// Where a copy of `box` rows begins that is to have the rows from `row` on (of
+// `rows` in all): there, or sooner, so that it ends with the last row.  A copy most of
+// whose rows lie beyond the tensor's end takes far longer than one that has them
+// all: 32 units of 128 rows of which 26, or 40, were there 65 us, or 21.  The rows
+// before `row` that come with it are computed and left out.
+__device__ __forceinline__ int f8_window(int row, int rows, int box) { return min(row, rows - box); }
+
+__device__ __forceinline__ int f8_x_window(const F8LinearParams &p, int m0) { return f8_window(m0, p.M, p.x_box); }
+
+// Of the channels from n0 on of expert e: in rows of all experts' weights.
+__device__ __forceinline__ int f8_w_window(const F8LinearParams &p, int e, int n0)
+{
+    return f8_window(e * p.N + n0, max(1, p.experts) * p.N, p.w_box);
 }
 
 // 16 accumulator columns of this thread's TMEM lane, on their way until
@@ -174,39 +207,41 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
 }
 
 // The end of a tile whose K is split over p.split CTAs of the cluster, the ranks
-// first, first + rank_step, ...: each has left its sums at `smem`; this CTA, the part-th of
-// them, adds up and stores its share of the tokens, a warp a token and 128
-// channels, always in the order of the parts.  Called by whole CTAs, all of the
-// cluster's.
-template <int MAX_SPLIT, int THREADS>
-__device__ __forceinline__ void f8_join(const F8LinearParams &p, uint32_t smem, int channels, int m0, int n0, int tokens, int part,
-                                        int first, int rank_step)
+// first, first + rank_step, ...: each has left its sums at `smem`, tokens from m0 on
+// and blocks of 128 channels from n[0], n[1] on (windows); the outputs are those of
+// tokens ma to mb and channels na[b] to p.N.  This CTA, the part-th of them, adds up and
+// stores its share of the tokens, a warp a token and block, always in the order of
+// the parts.  Called by whole CTAs, all of the cluster's.
+template <int MAX_SPLIT, int THREADS, int BLOCKS>
+__device__ __forceinline__ void f8_join(const F8LinearParams &p, uint32_t smem, int m0, int ma, int mb, const int (&n0)[BLOCKS],
+                                        const int (&na)[BLOCKS], int part, int first, int rank_step)
 {
+    constexpr int channels = BLOCKS * kF8Block;
     const int lane = static_cast<int>(threadIdx.x) & 31;
     cluster_sync();
-    const int t1 = (part + 1) * tokens / p.split, blocks = channels / kF8Block;
-    const int t0 = part * tokens / p.split;
-    for (int i = static_cast<int>(threadIdx.x >> 5); i < (t1 - t0) * blocks; i += THREADS / 32) {
-        const int m = t0 + i / blocks, c0 = i % blocks * kF8Block;
+    const int tokens = max(0, mb - ma), t0 = part * tokens / p.split, t1 = (part + 1) * tokens / p.split;
+    for (int i = static_cast<int>(threadIdx.x >> 5); i < (t1 - t0) * BLOCKS; i += THREADS / 32) {
+        const int m = ma + t0 + i / BLOCKS, b = i % BLOCKS;
+        const int first_n = BLOCKS == 1 || b == 0 ? n0[0] : n0[BLOCKS - 1], least = BLOCKS == 1 || b == 0 ? na[0] : na[BLOCKS - 1];
         if (p.vec4) {
-            const int c = c0 + 4 * lane, n = n0 + c;
+            const int c = b * kF8Block + 4 * lane, n = first_n + 4 * lane;
             float4 v[MAX_SPLIT];
 #pragma unroll
             for (int r = 0; r < MAX_SPLIT; ++r)
-                v[r] = r < p.split ? ld_cluster_f32x4(map_shared_rank(smem + f8_sum_at(channels, m, c), first + r * rank_step))
+                v[r] = r < p.split ? ld_cluster_f32x4(map_shared_rank(smem + f8_sum_at(channels, m - m0, c), first + r * rank_step))
                                    : make_float4(0, 0, 0, 0);
             float4 s = v[0];
 #pragma unroll
             for (int r = 1; r < MAX_SPLIT; ++r)
                 s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
-            if (n < p.N) {
-                const size_t o = static_cast<size_t>(m0 + m) * p.N + n;
+            if (n >= least && n < p.N) {
+                const size_t o = static_cast<size_t>(m) * p.N + n;
                 if (p.epilogue == SKG_EPI_FP32) {
                     *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + o) = s;
                 } else {
                     if (p.epilogue == SKG_EPI_BF16_RESIDUAL) {
-                        const uint2 b = __ldcg(reinterpret_cast<const uint2 *>(p.res + o));
-                        s.x += bf16lo(b.x), s.y += bf16hi(b.x), s.z += bf16lo(b.y), s.w += bf16hi(b.y);
+                        const uint2 r = __ldcg(reinterpret_cast<const uint2 *>(p.res + o));
+                        s.x += bf16lo(r.x), s.y += bf16hi(r.x), s.z += bf16lo(r.y), s.w += bf16hi(r.y);
                     }
                     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + o) = make_uint2(two_bf16(s.x, s.y), two_bf16(s.z, s.w));
                 }
@@ -214,12 +249,12 @@ __device__ __forceinline__ void f8_join(const F8LinearParams &p, uint32_t smem, 
         } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int c = c0 + lane + 32 * k;
+                const int c = b * kF8Block + lane + 32 * k, n = first_n + lane + 32 * k;
                 float s = 0.0f;
                 for (int r = 0; r < p.split; ++r)
-                    s += ld_shared_cluster_f32(map_shared_rank(smem + f8_sum_at(channels, m, c), first + r * rank_step));
-                if (n0 + c < p.N)
-                    f8_store(p, m0 + m, n0 + c, s);
+                    s += ld_shared_cluster_f32(map_shared_rank(smem + f8_sum_at(channels, m - m0, c), first + r * rank_step));
+                if (n >= least && n < p.N)
+                    f8_store(p, m, n, s);
             }
         }
     }

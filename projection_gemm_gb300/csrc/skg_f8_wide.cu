@@ -43,7 +43,7 @@ struct WideShape {
     static constexpr int kMmaWarp = 0, kTmaWarp = 1, kFirstEpi = 4;          // two warps of the first warpgroup are idle
     static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
     // Registers: the launch has 3 warpgroups of 168 a thread.
-    static constexpr int kRegsFew = 72, kRegsMany = 216;
+    static constexpr int kRegsFew = 56, kRegsMany = 224;
     static_assert(kRegsFew + 2 * kRegsMany <= 3 * 168 && kThreads == 3 * 128, "no more than the launch has");
     static constexpr int kStages = 5;
     static constexpr int kAcc = 512 / NT;                    // accumulators in flight
@@ -57,24 +57,25 @@ struct WideShape {
     static_assert(kSmem + f8_table_bytes(kF8MaxExperts) <= 227 * 1024, "shared memory of a CTA");
 };
 
-// A warp's 32 rows (tokens m0 ... below m1, a lane each) of NC channels from n0,
-// by way of shared memory, so that a store's lanes cover rows: of 128 bytes at a
-// time, bf16 or, where more is to be added, fp32.  (Each lane storing its own row
-// in pieces of 8 bytes took 8 us a tile.)  16-byte pieces are swizzled by row.
+// A warp's 32 rows (tokens from m0 on, a lane each; the outputs are those of lanes lo
+// to hi) of NC channels from n0 (the outputs are those from na on), by way of shared
+// memory, so that a store's lanes cover rows: of 128 bytes at a time, bf16 or,
+// where more is to be added, fp32.  (Each lane storing its own row in pieces of 8
+// bytes took 8 us a tile.)  16-byte pieces are swizzled by row.
 template <int EPI, int NC>
-__device__ __forceinline__ void store_tile(const F8LinearParams &p, int m0, int m1, int n0, const float (&acc)[NC],
+__device__ __forceinline__ void store_tile(const F8LinearParams &p, int m0, int lo, int hi, int n0, int na, const float (&acc)[NC],
                                            uint8_t *out)
 {
     constexpr int W = EPI == SKG_EPI_BF16 ? 64 : 32;             // channels at a time
-    const int lane = static_cast<int>(threadIdx.x) & 31, rows = min(m1 - m0, 32);
-    if (rows <= 0)
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    if (hi <= 0 || lo >= 32)
         return;
     auto piece = [&](int row, int c) { return out + row * 128 + ((c ^ (row & 7)) << 4); };
 #pragma unroll
     for (int c0 = 0; c0 < NC; c0 += W) {
-        const int n = n0 + c0, valid = p.N - n;
-        if (valid <= 0)
-            return;
+        const int n = n0 + c0, least = na - n, valid = p.N - n;  // channels n + least to n + valid
+        if (valid <= 0 || least >= W)
+            continue;
         __syncwarp();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -92,12 +93,12 @@ __device__ __forceinline__ void store_tile(const F8LinearParams &p, int m0, int 
         __syncwarp();
         if (p.vec) {                     // pieces of the output are aligned, and N ends between two
             const int c = lane & 7;
-            const bool in = c * (W / 8) < valid;
+            const bool in = c * (W / 8) >= least && c * (W / 8) < valid;
 #pragma unroll
             for (int r0 = 0; r0 < 32; r0 += 4) {
                 const int r = r0 + (lane >> 3);
                 const uint4 v = *reinterpret_cast<const uint4 *>(piece(r, c));
-                if (!in || r >= rows)
+                if (!in || r < lo || r >= hi)
                     continue;
                 const size_t o = static_cast<size_t>(m0 + r) * p.N + n + c * (W / 8);
                 if constexpr (EPI == SKG_EPI_BF16_RESIDUAL) {
@@ -114,10 +115,10 @@ __device__ __forceinline__ void store_tile(const F8LinearParams &p, int m0, int 
             }
         } else {
 #pragma unroll 4
-            for (int r = 0; r < rows; ++r) {
+            for (int r = max(lo, 0); r < min(hi, 32); ++r) {
 #pragma unroll
                 for (int c = lane; c < W; c += 32) {
-                    if (c >= valid)
+                    if (c < least || c >= valid)
                         continue;
                     const size_t o = static_cast<size_t>(m0 + r) * p.N + n + c;
                     if constexpr (EPI == SKG_EPI_BF16) {
@@ -221,10 +222,10 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             };
             auto load_w = [&](int u, const F8Tile &t, int kb) {
                 if (rank == 0)           // for both CTAs' copies, which may be counted before
-                    mbar_arrive_expect_tx(&full[u % S], PAIR * Sh::kStage);
-                load(sW, u, &tmW, kb, t.e * p.N + t.nt * NT + rank * 128);
+                    mbar_arrive_expect_tx(&full[u % S], PAIR * (p.w_box + p.x_box) * kF8Block);
+                load(sW, u, &tmW, kb, f8_w_window(p, t.e, t.nt * NT + rank * 128));
             };
-            auto load_x = [&](int u, const F8Tile &t, int kb) { load(sX, u, &tmX, kb, t.m0 + rank * 128); };
+            auto load_x = [&](int u, const F8Tile &t, int kb) { load(sX, u, &tmX, kb, f8_x_window(p, t.m0 + rank * 128)); };
             F8Tile t = f8_tile(p, MT, table, first);
             const int ahead = p.static_w && !p.experts ? min(S, units) : 0;
             if (leader)
@@ -320,17 +321,19 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         // ------------------------------------------------------------ epilogue
         pdl_launch_dependents();         // not sooner: see skg_q8_stream.cu
         const int ew = warp - Sh::kFirstEpi;
-        const int col0 = (ew >> 2) * NC, row0 = rank * 128 + (warp & 3) * 32;
+        const int col0 = (ew >> 2) * NC, row0 = (warp & 3) * 32;
         uint8_t *out = smem + S * Sh::kStage + ew * Sh::kOut;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(col0);
         const uint32_t aempty0 = map_shared_rank(smem_u32(aempty), lead);
-        constexpr int AHEAD = 8;
+        constexpr int AHEAD = 6;
         bool ok = true;
         int j = 0;
         for (int tile = first; ok && tile < tiles; tile += step) {
             const F8Tile t = f8_tile(p, MT, table, tile);
-            const int m = t.m0 + row0 + lane, nb = t.nt * (NT / kF8Block) + col0 / kF8Block;
-            const bool live = m < t.m1 && nb < p.nb;
+            // this CTA's tokens are ma to mb, the window's from m0 on
+            const int ma = t.m0 + rank * 128, mb = min(t.m1, ma + 128), m0 = f8_x_window(p, ma);
+            const int m = m0 + row0 + lane, nb = t.nt * (NT / kF8Block) + col0 / kF8Block;
+            const bool live = m >= ma && m < mb && nb < p.nb;
             const float *ws = p.w_scale + (static_cast<size_t>(t.e) * p.nb + nb) * p.nkb + kb0;
             const float *xs = p.x_scale + static_cast<size_t>(m) * p.nkb + kb0;
             float w[AHEAD], x[AHEAD];
@@ -368,19 +371,20 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             }
             if (!ok)
                 break;
-            const int n0 = t.nt * NT + col0;
+            const int na = nb * kF8Block, n0 = f8_w_window(p, t.e, na) - t.e * p.N + col0 % kF8Block;
+            const int lo = ma - m0 - row0, hi = mb - m0 - row0;
             if (p.split > 1) {
                 // in the ring's place: the last MMA has read its operands
 #pragma unroll
                 for (int c = 0; c < NC; c += 4)
-                    *reinterpret_cast<float4 *>(smem + f8_sum_at(NT, row0 - rank * 128 + lane, col0 + c)) =
+                    *reinterpret_cast<float4 *>(smem + f8_sum_at(NT, row0 + lane, col0 + c)) =
                         make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
             } else if (p.epilogue == SKG_EPI_FP32)
-                store_tile<SKG_EPI_FP32, NC>(p, t.m0 + row0, t.m1, n0, acc, out);
+                store_tile<SKG_EPI_FP32, NC>(p, m0 + row0, lo, hi, n0, na, acc, out);
             else if (p.epilogue == SKG_EPI_BF16_RESIDUAL)
-                store_tile<SKG_EPI_BF16_RESIDUAL, NC>(p, t.m0 + row0, t.m1, n0, acc, out);
+                store_tile<SKG_EPI_BF16_RESIDUAL, NC>(p, m0 + row0, lo, hi, n0, na, acc, out);
             else
-                store_tile<SKG_EPI_BF16, NC>(p, t.m0 + row0, t.m1, n0, acc, out);
+                store_tile<SKG_EPI_BF16, NC>(p, m0 + row0, lo, hi, n0, na, acc, out);
         }
         if (!ok)
             f8_fail(p.err, &flags[0], kErrTimeoutEpilogue);
@@ -390,8 +394,14 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     tc_fence_before();
     if (p.split > 1) {
         const F8Tile t = f8_tile(p, MT, table, first);
-        f8_join<kF8WideMaxSplit, Sh::kThreads>(p, smem_u32(smem), NT, t.m0 + rank * 128, t.nt * NT, min(128, max(0, t.m1 - t.m0 - rank * 128)),
-                                               part, rank, PAIR);
+        const int ma = t.m0 + rank * 128;
+        int n0[PAIR], na[PAIR];
+#pragma unroll
+        for (int b = 0; b < PAIR; ++b) {
+            na[b] = t.nt * NT + b * kF8Block;
+            n0[b] = f8_w_window(p, t.e, na[b]) - t.e * p.N;
+        }
+        f8_join<kF8WideMaxSplit, Sh::kThreads, PAIR>(p, smem_u32(smem), f8_x_window(p, ma), ma, min(t.m1, ma + 128), n0, na, part, rank, PAIR);
     } else if (PAIR == 2) {
         cluster_sync();                  // no CTA leaves while its peer may still send to it
     } else {
