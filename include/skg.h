@@ -573,7 +573,7 @@ SKG_API skg_status skg_q8_plan_destroy(skg_q8_plan_t plan);
  * to even.  A block of zeros has scale 0 and q = 0.  A block with a value that is
  * not finite has scale NaN and q = 0: a projection that reads it is NaN.
  *
- * skg_quantize_f8 -- M >= 0 rows of any K >= 1: of x, or of silu(gate) * x with
+ * skg_quantize_f8 -- M >= 0 rows of any K in [1, 2^30]: of x, or of silu(gate) * x with
  * silu(g) = g / (1 + exp(-g)); or row i of the output from row rows[i] of those.
  *   x, gate  bf16 rows of K, row strides ldx, ldg >= K; gate may be NULL.  Both may
  *            be halves of one [M, 2K] tensor
@@ -581,7 +581,8 @@ SKG_API skg_status skg_q8_plan_destroy(skg_q8_plan_t plan);
  *            an index outside [0, x_rows) gives a row of q = 0, scale = 0.  Without,
  *            they have M, and x_rows is not read
  *   q, scale e4m3 [M, K] and fp32 [M, ceil(K / 128)], dense
- * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
+ *   Any alignment the element types allow; 16-byte aligned rows are fastest.
+ * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
  */
 SKG_API skg_status skg_quantize_f8(int M, int K, const void *x, size_t ldx, const void *gate, size_t ldg, const int *rows,
                                    int x_rows, void *q, float *scale, void *stream);
@@ -591,7 +592,7 @@ SKG_API skg_status skg_quantize_f8(int M, int K, const void *x, size_t ldx, cons
  * weight), dense, to q e4m3 of the same shape and scale fp32 [experts,
  * ceil(N / 128), ceil(K / 128)].
  * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_ALIGNMENT, SKG_ERR_UNSUPPORTED (more than
- * 2^31 - 1 blocks), SKG_ERR_CUDA.
+ * 2^31 - 1 blocks, K above 2^30), SKG_ERR_CUDA.
  */
 SKG_API skg_status skg_quantize_f8_weights(int experts, int N, int K, const void *W, void *q, float *scale, void *stream);
 

@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kF8MaxK = 131072;
 constexpr int kF8MaxM = 1 << 20;
+constexpr int kF8MaxRow = 1 << 30;    // quantisers: element indexes of a row, and those just behind it, fit 32 bits
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }      // null is aligned
 
@@ -178,6 +179,8 @@ skg_status skg_quantize_f8(int M, int K, const void *x, size_t ldx, const void *
                          x_rows, K);
     if (M > 0 && ((!x && !(rows && x_rows == 0)) || !q || !scale))
         return set_error(SKG_ERR_INVALID_ARG, "%s: x, q and scale must be non-NULL", who);
+    if (K > kF8MaxRow)
+        return set_error(SKG_ERR_UNSUPPORTED, "%s: K must be at most 2^30 (got %d)", who, K);
     if (ldx < static_cast<size_t>(K) || (gate && ldg < static_cast<size_t>(K)))
         return set_error(SKG_ERR_INVALID_ARG, "%s: a row stride of x / gate is below K = %d", who, K);
     if (!aligned(x, 2) || !aligned(gate, 2) || !aligned(rows, 4) || !aligned(scale, 4))
@@ -208,6 +211,8 @@ skg_status skg_quantize_f8_weights(int experts, int N, int K, const void *W, voi
         return set_error(SKG_ERR_INVALID_ARG, "%s: W, q and scale must be non-NULL", who);
     if (!aligned(W, 2) || !aligned(scale, 4))
         return set_error(SKG_ERR_ALIGNMENT, "%s: W or scale misses its element alignment", who);
+    if (K > kF8MaxRow)
+        return set_error(SKG_ERR_UNSUPPORTED, "%s: K must be at most 2^30 (got %d)", who, K);
     F8WeightParams p = {static_cast<const uint16_t *>(W), static_cast<uint8_t *>(q), scale, experts, N, K,
                         ceil_div(N, kF8Block), ceil_div(K, kF8Block)};
     if (static_cast<double>(experts) * p.nb * p.kb > 2147483647.0)

@@ -45,73 +45,119 @@ __device__ __forceinline__ uint32_t two_e4m3(float a, float b)
     return r;
 }
 
-struct Eight {
-    float v[8];
+template <int N>
+struct Values {
+    float v[N];
 };
 
+using Eight = Values<8>;
+
 // max|v| as bits, larger than infinity's where a value is NaN.
-__device__ __forceinline__ uint32_t max_bits(const Eight &e)
+template <int N>
+__device__ __forceinline__ uint32_t max_bits(const Values<N> &e)
 {
-    uint32_t m = 0;
+    float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = max(m, __float_as_uint(e.v[i]) & 0x7FFFFFFFu);
-    return m;
+    for (int i = 0; i < N; ++i)
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(e.v[i])));
+    return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
-__device__ __forceinline__ uint2 to_e4m3(const Eight &e, const BlockScale &b)
+template <int N>
+__device__ __forceinline__ void scale_values(Values<N> &e, const BlockScale &b)
 {
-    float u[8];
+    if (b.up != 1.0f || b.factor == 0.0f) {          // rare
 #pragma unroll
-    for (int i = 0; i < 8; ++i)          // (a factor of 0 does not make a NaN or an infinity 0)
-        u[i] = b.factor == 0.0f ? 0.0f : e.v[i] * b.up * b.factor;
-    return make_uint2(two_e4m3(u[0], u[1]) | two_e4m3(u[2], u[3]) << 16, two_e4m3(u[4], u[5]) | two_e4m3(u[6], u[7]) << 16);
-}
-
-// Eight elements as loaded, zeros where the row ends.  ANY: of any alignment.
-template <bool ANY>
-__device__ __forceinline__ uint4 load8(const uint16_t *row, long long e, int K)
-{
-    uint4 r = make_uint4(0, 0, 0, 0);
-    if constexpr (!ANY) {
-        if (e < K)
-            asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(row + e));
-    } else {
-    uint16_t h[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        h[i] = 0;
-        if (e + i < K)
-            asm volatile("ld.global.u16 %0, [%1];" : "=h"(h[i]) : "l"(row + e + i));
+        for (int i = 0; i < N; ++i)      // (a factor of 0 does not make a NaN or an infinity 0)
+            e.v[i] = b.factor == 0.0f ? 0.0f : e.v[i] * b.up;
     }
-    r.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
-    r.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
-    r.z = h[4] | static_cast<uint32_t>(h[5]) << 16;
-    r.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
-    }
-    return r;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        e.v[i] *= b.factor;
 }
 
-template <bool ANY>
-__device__ __forceinline__ void store8(uint8_t *row, long long e, int K, const uint2 &w)
+__device__ __forceinline__ uint2 to_e4m3(Eight e, const BlockScale &b)
+{
+    scale_values(e, b);
+    return make_uint2(two_e4m3(e.v[0], e.v[1]) | two_e4m3(e.v[2], e.v[3]) << 16,
+                      two_e4m3(e.v[4], e.v[5]) | two_e4m3(e.v[6], e.v[7]) << 16);
+}
+
+// silu(g) x.
+template <int N>
+__device__ __forceinline__ Values<N> gated(const Values<N> &g, const Values<N> &x)
+{
+    Values<N> v;
+    float lowest = g.v[0];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v.v[i] = silu(g.v[i]) * x.v[i];
+        lowest = fminf(lowest, g.v[i]);
+    }
+    if (lowest < kFarGate) {             // rare
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v.v[i] = g.v[i] < kFarGate ? far_gated(g.v[i], x.v[i]) : v.v[i];
+    }
+    return v;
+}
+
+// Eight numbers at element e of a row of K.  ANY: of any alignment; L neighbouring
+// lanes have neighbouring eights (all of them call), and a lane stores the aligned 8
+// bytes that its eight begins in: the end of the lane's before and the beginning of its
+// own.
+template <bool ANY, int L>
+__device__ __forceinline__ void store8(uint8_t *row, int e, int K, const uint2 &w)
 {
     if constexpr (!ANY) {
         if (e < K)
             *reinterpret_cast<uint2 *>(row + e) = w;
     } else {
+        const int lane = static_cast<int>(threadIdx.x) & (L - 1);
+        const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row) + e) & 7;
+        const unsigned long long own = w.x | static_cast<unsigned long long>(w.y) << 32;
+        const unsigned long long before = __shfl_up_sync(0xFFFFFFFFu, own, 1, L);
+        const unsigned long long both = s ? own << (8 * s) | before >> (64 - 8 * s) : own;
+        if ((lane > 0 || s == 0) && e - s + 8 <= K) {
+            *reinterpret_cast<unsigned long long *>(row + (e - s)) = both;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (e + i < K)
-                row[e + i] = static_cast<uint8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+            for (int i = 0; i < 8; ++i)
+                if ((lane > 0 || i >= s) && e - s + i < K)
+                    row[e - s + i] = static_cast<uint8_t>(both >> (8 * i));
+        }
+        if (lane == L - 1) {
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+                if (i >= 8 - s && e + i < K)
+                    row[e + i] = static_cast<uint8_t>(own >> (8 * i));
+        }
     }
 }
 
-__device__ __forceinline__ Eight widen8(const uint4 &w)
+__device__ __forceinline__ Eight widen8(const Raw8 &r)
 {
-    return {{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y), bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)}};
+    Eight e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        e.v[2 * i] = bf16lo(r.w[i]), e.v[2 * i + 1] = bf16hi(r.w[i]);
+    return e;
 }
 
-__device__ __forceinline__ float gated(float g, float x) { return g < kFarGate ? far_gated(g, x) : silu(g) * x; }
+// The row of x that a row of q is of: none where its index is out of range.
+struct RowSource {
+    long long row;
+    bool live;
+};
+
+__device__ __forceinline__ RowSource row_source(const F8RowParams &p, long long row)
+{
+    if (!p.rows)
+        return {row, true};
+    const int r = __ldcg(p.rows + row);
+    const bool live = r >= 0 && r < p.x_rows;
+    return {live ? r : 0, live};
+}
 
 constexpr int kRowWarps = 8;
 
@@ -126,41 +172,29 @@ __global__ void __launch_bounds__(32 * kRowWarps) f8_rows_kernel(const F8RowPara
     if (row >= p.M)
         return;
     const int b0 = static_cast<int>(unit - row * groups) * 2 * P, lane = threadIdx.x & 31, half = lane >> 4;
-    long long from = row;
-    bool live = true;
-    if (p.rows) {
-        const int r = __ldcg(p.rows + row);
-        live = r >= 0 && r < p.x_rows;
-        from = live ? r : 0;
-    }
-    const uint16_t *x = p.x + from * p.ldx;
-    const uint16_t *g = GATE ? p.gate + from * p.ldg : nullptr;
-    const long long e0 = (static_cast<long long>(b0) + half) * kF8Block + (lane & 15) * 8;
-    const int K = live ? p.K : 0;
-    uint4 a[P], c[P];
+    const RowSource from = row_source(p, row);
+    const int e0 = (b0 + half) * kF8Block + (lane & 15) * 8;
+    const int K = from.live ? p.K : 0;
+    RowLoad<ANY> a[P], c[P];
 #pragma unroll
     for (int i = 0; i < P; ++i)
-        a[i] = load8<ANY>(x, e0 + i * 2 * kF8Block, K);
+        a[i].load(p.x + from.row * p.ldx, e0 + i * 2 * kF8Block, K);
     if (GATE) {
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            c[i] = load8<ANY>(g, e0 + i * 2 * kF8Block, K);
+            c[i].load(p.gate + from.row * p.ldg, e0 + i * 2 * kF8Block, K);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        Eight v = widen8(a[i]);
-        if (GATE) {
-            const Eight w = widen8(c[i]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v.v[k] = gated(w.v[k], v.v[k]);
-        }
+        Eight v = widen8(a[i].get());
+        if (GATE)
+            v = gated(widen8(c[i].get()), v);
         uint32_t m = max_bits(v);
 #pragma unroll
         for (int o = 8; o; o >>= 1)
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         const BlockScale s = block_scale(m);
-        store8<ANY>(p.q + row * p.K, e0 + i * 2 * kF8Block, p.K, to_e4m3(v, s));
+        store8<ANY, 32>(p.q + row * p.K, e0 + i * 2 * kF8Block, p.K, to_e4m3(v, s));
         const int b = b0 + 2 * i + half;
         if ((lane & 15) == 0 && b < p.kb)
             p.scale[row * p.kb + b] = s.scale;
@@ -169,7 +203,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) f8_rows_kernel(const F8RowPara
 
 // A CTA takes a block of 128 x 128: 16 lanes a row, 16 rows at a time.
 template <bool ANY>
-__global__ void __launch_bounds__(256) f8_weights_kernel(const F8WeightParams p)
+__global__ void __launch_bounds__(256, 2) f8_weights_kernel(const F8WeightParams p)
 {
     __shared__ uint32_t maxima[8];
     pdl_wait();
@@ -177,19 +211,19 @@ __global__ void __launch_bounds__(256) f8_weights_kernel(const F8WeightParams p)
     const long long block = blockIdx.x, en = block / p.kb;
     const int b = static_cast<int>(block - en * p.kb), e = static_cast<int>(en / p.nb), nb = static_cast<int>(en - static_cast<long long>(e) * p.nb);
     const int t = threadIdx.x, k = (t & 15) * 8;
-    uint4 a[8];
+    RowLoad<ANY> a[8];
     uint32_t m = 0;
-    const long long e0 = static_cast<long long>(b) * kF8Block + k;
+    const int e0 = b * kF8Block + k;
     auto at = [&](int i) {
         return (static_cast<size_t>(e) * p.N + nb * kF8Block + (t >> 4) + 16 * i) * p.K;
     };
     auto inside = [&](int i) { return static_cast<long long>(nb) * kF8Block + (t >> 4) + 16 * i < p.N; };
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        a[i] = load8<ANY>(p.W + at(i), e0, inside(i) ? p.K : 0);
+        a[i].load(p.W + at(i), e0, inside(i) ? p.K : 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        m = max(m, max_bits(widen8(a[i])));
+        m = max(m, max_bits(widen8(a[i].get())));
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if ((t & 31) == 0)
         maxima[t >> 5] = m;
@@ -200,7 +234,7 @@ __global__ void __launch_bounds__(256) f8_weights_kernel(const F8WeightParams p)
     const BlockScale s = block_scale(m);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        store8<ANY>(p.q + at(i), e0, inside(i) ? p.K : 0, to_e4m3(widen8(a[i]), s));
+        store8<ANY, 16>(p.q + at(i), e0, inside(i) ? p.K : 0, to_e4m3(widen8(a[i].get()), s));
     if (t == 0)
         p.scale[block] = s.scale;
 }
@@ -231,10 +265,11 @@ cudaError_t launch_rows(const F8RowParams &p, cudaStream_t s)
         const int groups = (p.kb + blocks - 1) / blocks;
         return launch(kernel, (static_cast<long long>(p.M) * groups + kRowWarps - 1) / kRowWarps, 32 * kRowWarps, s, p, groups);
     };
-    // Many blocks of long rows: eight a warp, for bytes in flight.
-    if (p.kb >= 8 && static_cast<long long>(p.M) * p.kb >= 8 * 16 * 152)
-        return run(f8_rows_kernel<ANY, GATE, 4>, 8);
-    return run(f8_rows_kernel<ANY, GATE, 1>, 2);
+    // Many blocks of long rows: more of them a warp, for bytes in flight.
+    const bool many = p.kb >= 8 && static_cast<long long>(p.M) * p.kb >= 8 * 16 * 152;
+    if (!many)
+        return run(f8_rows_kernel<ANY, GATE, 1>, 2);
+    return run(f8_rows_kernel<ANY, GATE, 4>, 8);
 }
 
 } // namespace

@@ -33,6 +33,84 @@ __device__ __forceinline__ float far_gated(float g, float x)
     return x * e * e * g * e * e;
 }
 
+// Eight elements as loaded.  (Not by the read-only path: the kernel may have
+// started before its inputs were written.)
+struct Raw8 {
+    uint32_t w[4];
+};
+
+__device__ __forceinline__ void load_block(const uint16_t *p, uint32_t *w)
+{
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+}
+
+// A row of bf16 read 8 elements at a time.  ANY: from an address of any
+// alignment, by the two 16-byte blocks around the eight elements; where those
+// reach beyond the row (near its ends), element by element.
+template <bool ANY>
+struct RowLoad {
+    uint32_t w[ANY ? 8 : 4];
+    int d = 0;               // the eight elements begin at element d of w
+
+    __device__ __forceinline__ void load(const uint16_t *row, int e, int K)
+    {
+#pragma unroll
+        for (int i = 0; i < (ANY ? 8 : 4); ++i)
+            w[i] = 0;
+        if constexpr (!ANY) {
+            if (e < K)
+                load_block(row + e, w);
+        } else {
+            d = phase(row, e);
+            if (e - d >= 0 && e - d + (d ? 16 : 8) <= K) {
+                load_block(row + (e - d), w);
+                if (d)
+                    load_block(row + (e - d) + 8, w + 4);
+            } else if (e + 8 > 0 && e < K) {
+                d = 0;
+                uint16_t h[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    h[i] = 0;
+                    if (e + i >= 0 && e + i < K)
+                        asm volatile("ld.global.u16 %0, [%1];" : "=h"(h[i]) : "l"(row + e + i));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = h[2 * i] | static_cast<uint32_t>(h[2 * i + 1]) << 16;
+            }
+        }
+    }
+
+    // Elements by which row + e lies beyond a 16-byte boundary.
+    static __device__ __forceinline__ int phase(const uint16_t *row, int e)
+    {
+        return static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) + static_cast<unsigned>(e)) & 7;
+    }
+
+    __device__ __forceinline__ Raw8 get() const
+    {
+        Raw8 r;
+        if constexpr (!ANY) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r.w[i] = w[i];
+        } else {
+            uint32_t u[6], t[5];
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+                u[i] = d & 4 ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+                t[i] = d & 2 ? u[i + 1] : u[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r.w[i] = d & 1 ? __funnelshift_r(t[i], t[i + 1], 16) : t[i];
+        }
+        return r;
+    }
+};
+
 // Four int8 of a word as four fp16: with the sign bit flipped a byte b is
 // b + 128 in 0..255; as the low byte of fp16 0x6400 it reads 1024 + b + 128,
 // exactly, and 1152 is taken off again.
