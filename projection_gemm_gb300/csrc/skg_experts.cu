@@ -32,13 +32,15 @@ namespace {
 // and CTAs before and the experts before, and the warp goes over its run again and
 // gives each choice its place.  Lanes with the same expert find each other by
 // match_any; all of it is in order, so the sort is stable and nothing is atomic.
-constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCtas = 8;
+constexpr int kSortWarps = 32, kSortCtas = 8;
+constexpr int kSortHeld = 4;             // rounds of 32 choices that a warp holds in registers from one pass to the next
 
 struct SortParams {
     const int *expert;        // [n]
     int *offsets, *rows, *pos;
     int n, k, E;
     int warps, run;           // warps that have choices, and how many each (a multiple of 32)
+    int ctas;
 };
 
 __device__ __forceinline__ int ld_shared_cluster_int(uint32_t addr)
@@ -48,13 +50,13 @@ __device__ __forceinline__ int ld_shared_cluster_int(uint32_t addr)
     return v;
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p, int ctas)
+__global__ void __launch_bounds__(32 * kSortWarps) sort_kernel(const SortParams p)
 {
-    extern __shared__ int hist[];        // [warps][E], then total [E]
-    __shared__ int warp_sum[32];
-    int *total = hist + p.warps * p.E;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
-    for (int i = threadIdx.x; i < p.warps * p.E; i += kSortThreads)
+    extern __shared__ int hist[];        // [warps][E], then total [E], then base [E]
+    __shared__ int warp_sum[kSortWarps];
+    int *total = hist + p.warps * p.E, *base = total + p.E;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x, threads = blockDim.x;
+    for (int i = threadIdx.x; i < p.warps * p.E; i += threads)
         hist[i] = 0;
     __syncthreads();
     pdl_wait();
@@ -65,21 +67,37 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p, 
     int *mine = hist + warp * p.E;
     auto key_at = [&](int s) {           // -1: no expert
         const long long i = begin + s * 32 + lane;
-        const int e = i < p.n ? __ldcg(p.expert + i) : -1;
+        const int e = s < steps && i < p.n ? __ldcg(p.expert + i) : -1;
         return e >= 0 && e < p.E ? e : -1;
     };
-    int next = steps ? key_at(0) : -1;
-    for (int s = 0; s < steps; ++s) {
-        const int key = next;
-        next = s + 1 < steps ? key_at(s + 1) : -1;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+    auto count = [&](int key, unsigned same) {
         if (key >= 0 && lane == __ffs(same) - 1)
             mine[key] += __popc(same);
         __syncwarp();
+    };
+    int held[kSortHeld];
+    unsigned held_same[kSortHeld];
+#pragma unroll
+    for (int s = 0; s < kSortHeld; ++s)
+        held[s] = key_at(s);
+#pragma unroll
+    for (int s = 0; s < kSortHeld; ++s) {
+        held_same[s] = 0;
+        if (s < steps) {
+            held_same[s] = __match_any_sync(0xFFFFFFFFu, held[s]);
+            count(held[s], held_same[s]);
+        }
+    }
+    int next = key_at(kSortHeld);
+    for (int s = kSortHeld; s < steps; ++s) {
+        const int key = next;
+        next = key_at(s + 1);
+        count(key, __match_any_sync(0xFFFFFFFFu, key));
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += kSortThreads) {
+    for (int e = threadIdx.x; e < p.E; e += threads) {
         int sum = 0;
+#pragma unroll 8
         for (int w = 0; w < p.warps; ++w) {
             const int c = hist[w * p.E + e];
             hist[w * p.E + e] = sum;
@@ -87,26 +105,33 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p, 
         }
         total[e] = sum;
     }
-    if (ctas > 1)
+    if (p.ctas > 1)
         cluster_sync();
     else
         __syncthreads();
-    // an expert a thread
-    static_assert(kF8MaxExperts <= kSortThreads, "an expert a thread");
-    const int e = threadIdx.x;
-    int before = 0, all = 0;
-    if (e < p.E) {
-        if (ctas == 1) {
-            all = total[e];
-        } else {
-            for (int c = 0; c < ctas; ++c) {
-                const int v = ld_shared_cluster_int(map_shared_rank(smem_u32(total + e), c));
-                before += c < cta ? v : 0;
-                all += v;
+    // the experts' first rows: up to two experts a thread (threads >= E / 2), added up in their order
+    int all[2], before[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = 2 * threadIdx.x + i;
+        all[i] = before[i] = 0;
+        if (e < p.E) {
+            if (p.ctas == 1) {
+                all[i] = total[e];
+            } else {
+                int v[kSortCtas];
+#pragma unroll
+                for (int c = 0; c < kSortCtas; ++c)
+                    v[c] = ld_shared_cluster_int(map_shared_rank(smem_u32(total + e), c));
+#pragma unroll
+                for (int c = 0; c < kSortCtas; ++c) {
+                    before[i] += c < cta ? v[c] : 0;
+                    all[i] += v[c];
+                }
             }
         }
     }
-    int scan = all;
+    int scan = all[0] + all[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
@@ -115,38 +140,48 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p, 
     if (lane == 31)
         warp_sum[warp] = scan;
     __syncthreads();
-    int lower = lane < warp ? warp_sum[lane] : 0, routed = warp_sum[lane];
-    lower = __reduce_add_sync(0xFFFFFFFFu, lower);
-    routed = __reduce_add_sync(0xFFFFFFFFu, routed);
-    const int start = lower + scan - all;            // of expert e's rows
-    if (cta == 0 && e < p.E)
-        p.offsets[e] = start;
-    if (cta == 0 && e == 0)
+    const int sum = lane < threads / 32 ? warp_sum[lane] : 0;
+    const int lower = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sum : 0), routed = __reduce_add_sync(0xFFFFFFFFu, sum);
+    int start = lower + scan - all[0] - all[1];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = 2 * threadIdx.x + i;
+        if (e < p.E) {
+            base[e] = start + before[i];
+            if (cta == 0)
+                p.offsets[e] = start;
+        }
+        start += all[i];
+    }
+    if (cta == 0 && threadIdx.x == 0)
         p.offsets[p.E] = routed;
-    if (e < p.E)
-        for (int w = 0; w < p.warps; ++w)
-            hist[w * p.E + e] += start + before;
     __syncthreads();
-    next = steps ? key_at(0) : -1;
-    for (int s = 0; s < steps; ++s) {
-        const int key = next;
-        next = s + 1 < steps ? key_at(s + 1) : -1;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+    auto put = [&](int s, int key, unsigned same) {
         const int at = key >= 0 ? mine[key] : 0;
         __syncwarp();
         if (key >= 0 && lane == __ffs(same) - 1)
             mine[key] = at + __popc(same);
         const long long i = begin + s * 32 + lane;
-        const int place = key >= 0 ? at + __popc(same & ((1u << lane) - 1)) : -1;
+        const int place = key >= 0 ? base[key] + at + __popc(same & ((1u << lane) - 1)) : -1;
         if (i < p.n)
             p.pos[i] = place;
         if (key >= 0)
             p.rows[place] = static_cast<int>(i) / p.k;
         __syncwarp();
+    };
+#pragma unroll
+    for (int s = 0; s < kSortHeld; ++s)
+        if (s < steps)
+            put(s, held[s], held_same[s]);
+    next = key_at(kSortHeld);
+    for (int s = kSortHeld; s < steps; ++s) {
+        const int key = next;
+        next = key_at(s + 1);
+        put(s, key, __match_any_sync(0xFFFFFFFFu, key));
     }
-    for (long long i = routed + static_cast<long long>(cta) * kSortThreads + threadIdx.x; i < p.n; i += ctas * kSortThreads)
+    for (long long i = routed + static_cast<long long>(cta) * threads + threadIdx.x; i < p.n; i += p.ctas * threads)
         p.rows[i] = -1;
-    if (ctas > 1)
+    if (p.ctas > 1)
         cluster_sync();                  // no CTA leaves while a peer reads its totals
 }
 
@@ -198,16 +233,17 @@ struct MoveParams {
     int rows, x_rows, N, k, groups;
 };
 
-constexpr int kMoveWarps = 8, kDeep = 4;
+constexpr int kGatherWarps = 8, kCombineWarps = 4;
+constexpr int kDeep = 8;                 // gather: pieces a lane
 constexpr int kMaxN = 1 << 30;           // element indexes of a row, and those just behind it, fit 32 bits
 
 // A warp takes kDeep pieces a lane of one row.
 template <int V>
-__global__ void __launch_bounds__(32 * kMoveWarps) gather_kernel(const MoveParams p)
+__global__ void __launch_bounds__(32 * kGatherWarps) gather_kernel(const MoveParams p)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const long long unit = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+    const long long unit = static_cast<long long>(blockIdx.x) * kGatherWarps + (threadIdx.x >> 5);
     if (unit >= p.units)
         return;
     const long long row = unit / p.groups;
@@ -230,26 +266,28 @@ __global__ void __launch_bounds__(32 * kMoveWarps) gather_kernel(const MoveParam
 
 constexpr int kBatch = 8;                // choices of a token whose rows are on their way together
 
-// A warp takes a piece a lane of one token.
-template <int V>
-__global__ void __launch_bounds__(32 * kMoveWarps) combine_kernel(const MoveParams p)
+// A warp takes PC pieces a lane of one token.
+template <int V, int PC>
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const MoveParams p)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const long long unit = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+    const long long unit = static_cast<long long>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
     if (unit >= p.units)
         return;
     const long long t = unit / p.groups;
-    const int lane = threadIdx.x & 31, n = static_cast<int>(unit - t * p.groups) * (32 * V) + lane * V;
-    const bool live = n < p.N;
-    float acc[V], v[V];
+    const int lane = threadIdx.x & 31, n = static_cast<int>(unit - t * p.groups) * (32 * V * PC) + lane * V;
+    float acc[PC][V];
 #pragma unroll
-    for (int c = 0; c < V; ++c)
-        acc[c] = 0.0f;
-    if (p.res && live) {
-        Piece<V> r;
-        r.load(p.res + t * p.N + n);
-        r.get(acc);
+    for (int i = 0; i < PC; ++i) {
+#pragma unroll
+        for (int c = 0; c < V; ++c)
+            acc[i][c] = 0.0f;
+        if (p.res && n + i * 32 * V < p.N) {
+            Piece<V> r;
+            r.load(p.res + t * p.N + n + i * 32 * V);
+            r.get(acc[i]);
+        }
     }
     for (int j0 = 0; j0 < p.k; j0 += kBatch) {
         int at = -1;
@@ -259,29 +297,38 @@ __global__ void __launch_bounds__(32 * kMoveWarps) combine_kernel(const MovePara
             if (p.weight)
                 w = __ldcg(p.weight + t * p.k + j0 + lane);
         }
-        Piece<V> y[kBatch];
+        Piece<V> y[kBatch][PC];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int from = __shfl_sync(0xFFFFFFFFu, at, j);
-            if (live && from >= 0 && from < p.x_rows)
-                y[j].load(p.x + from * p.ldx + n);
+#pragma unroll
+            for (int i = 0; i < PC; ++i)
+                if (from >= 0 && from < p.x_rows && n + i * 32 * V < p.N)
+                    y[j][i].load(p.x + from * p.ldx + n + i * 32 * V);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int from = __shfl_sync(0xFFFFFFFFu, at, j);
             const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
-            if (live && from >= 0 && from < p.x_rows) {
-                y[j].get(v);
+            if (from >= 0 && from < p.x_rows) {
 #pragma unroll
-                for (int c = 0; c < V; ++c)
-                    acc[c] = fmaf(wj, v[c], acc[c]);
+                for (int i = 0; i < PC; ++i) {
+                    float v[V];
+                    y[j][i].get(v);
+#pragma unroll
+                    for (int c = 0; c < V; ++c)
+                        acc[i][c] = fmaf(wj, v[c], acc[i][c]);
+                }
             }
         }
     }
-    if (live) {
-        Piece<V> r;
-        r.set(acc);
-        r.store(p.out + t * p.N + n);
+#pragma unroll
+    for (int i = 0; i < PC; ++i) {
+        if (n + i * 32 * V < p.N) {
+            Piece<V> r;
+            r.set(acc[i]);
+            r.store(p.out + t * p.N + n + i * 32 * V);
+        }
     }
 }
 
@@ -400,15 +447,15 @@ cudaError_t launch_gather(MoveParams &p, cudaStream_t s)
 {
     p.groups = static_cast<int>((static_cast<long long>(p.N) + 32 * V * kDeep - 1) / (32 * V * kDeep));
     p.units = static_cast<long long>(p.rows) * p.groups;
-    return launch(gather_kernel<V>, (p.units + kMoveWarps - 1) / kMoveWarps, 32 * kMoveWarps, 0, 1, s, p);
+    return launch(gather_kernel<V>, (p.units + kGatherWarps - 1) / kGatherWarps, 32 * kGatherWarps, 0, 1, s, p);
 }
 
-template <int V>
+template <int V, int PC>
 cudaError_t launch_combine_rows(MoveParams &p, cudaStream_t s)
 {
-    p.groups = static_cast<int>((static_cast<long long>(p.N) + 32 * V - 1) / (32 * V));
+    p.groups = static_cast<int>((static_cast<long long>(p.N) + 32 * V * PC - 1) / (32 * V * PC));
     p.units = static_cast<long long>(p.rows) * p.groups;
-    return launch(combine_kernel<V>, (p.units + kMoveWarps - 1) / kMoveWarps, 32 * kMoveWarps, 0, 1, s, p);
+    return launch(combine_kernel<V, PC>, (p.units + kCombineWarps - 1) / kCombineWarps, 32 * kCombineWarps, 0, 1, s, p);
 }
 
 } // namespace
@@ -439,18 +486,19 @@ skg_status skg_experts_sort(int T, int k, int experts, const int *expert, int *o
         return launched(e, who);
     if (__atomic_load_n(&attr_set[dev], __ATOMIC_ACQUIRE) == 0) {
         e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kSortWarps + 1) * kF8MaxExperts * 4);
+                                 (kSortWarps + 2) * kF8MaxExperts * 4);
         if (e != cudaSuccess)
             return launched(e, who);
         __atomic_store_n(&attr_set[dev], 1, __ATOMIC_RELEASE);
     }
-    SortParams p = {expert, offsets, rows, pos, T * k, k, experts, 0, 0};
-    const int ctas = p.n > 4096 ? kSortCtas : 1;
-    const int a_cta = (p.n + ctas - 1) / ctas;
-    p.warps = std::min(kSortWarps, std::max(1, (a_cta + 127) / 128));        // four rounds a warp at the least
+    SortParams p = {expert, offsets, rows, pos, T * k, k, experts, 0, 0, 0};
+    p.ctas = p.n > 32 * kSortHeld * kSortWarps ? kSortCtas : 1;
+    const int a_cta = (p.n + p.ctas - 1) / p.ctas, held = 32 * kSortHeld;
+    p.warps = std::min(kSortWarps, std::max(1, (a_cta + held - 1) / held));
     p.run = (a_cta + 32 * p.warps - 1) / (32 * p.warps) * 32;
-    return launched(launch(sort_kernel, ctas, kSortThreads, static_cast<size_t>(p.warps + 1) * experts * 4, ctas,
-                           static_cast<cudaStream_t>(stream), p, ctas), who);
+    const int threads = std::max(32 * p.warps, (experts + 63) / 64 * 32);   // two experts a thread at the most
+    return launched(launch(sort_kernel, p.ctas, threads, static_cast<size_t>(p.warps + 2) * experts * 4, p.ctas,
+                           static_cast<cudaStream_t>(stream), p), who);
 }
 
 skg_status skg_experts_gather(int R, int T, int N, const void *x, size_t ldx, const int *rows, void *out, void *stream)
@@ -509,7 +557,7 @@ skg_status skg_experts_combine(int T, int k, int R, int N, const void *y, size_t
     p.k = k;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool wide = N % 8 == 0 && ldy % 8 == 0 && aligned(y, 16) && aligned(residual, 16) && aligned(out, 16);
-    return launched(wide ? launch_combine_rows<8>(p, s) : launch_combine_rows<1>(p, s), who);
+    return launched(wide ? launch_combine_rows<8, 1>(p, s) : launch_combine_rows<1, 4>(p, s), who);
 }
 
 skg_status skg_experts_combine_grad(int T, int k, int R, int N, const void *grad_out, const void *y, size_t ldy,
