@@ -592,31 +592,53 @@ class Q8Plan:
 
 
 # --------------------------------------------- the 8-bit floating point path
+# The calls of a decode step take the GPU a few microseconds each, so what they
+# check is one expression, as in Q8Plan.run (skg_experts_combine 7.1 us of host time
+# with a call a tensor, 4.6 so); what that refuses is then named.
+_types = ()
+
+
+def _dtypes():
+    global _types
+    if not _types:
+        import torch
+        _types = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+    return _types
+
+
 def _blocks(n: int) -> int:
     return -(-n // F8_BLOCK)
 
 
-def _indices(t, name, shape) -> int:
-    import torch
-    return _dense(t, name, shape, torch.int32)
+def _sizes(**sizes):
+    for name, v in sizes.items():
+        _int(v, name)
 
 
 def skg_quantize_f8(x, gate, q, scale, rows=None, stream=None):
     """x, gate: bf16 [T, K] (rows may be strided; gate may be None); rows int32 [M], the row of x of each row of q, or
     None (M = T); q float8_e4m3fn [M, K]; scale fp32 [M, ceil(K / 128)]."""
-    import torch
+    bf16, f32, i32, f8 = _dtypes()
     shape = x.shape
     if len(shape) != 2:
         _bad("x must be [T, K]")
-    T, K = _int(shape[0], "T"), _int(shape[1], "K")
-    M = T if rows is None else _int(rows.numel(), "M")
-    ldx = _rows(x, "x", shape, torch.bfloat16)
-    ldg = 0 if gate is None else _rows(gate, "gate", shape, torch.bfloat16)
-    _check(load().skg_quantize_f8(
-        M, K, x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg,
-        None if rows is None or M == 0 else _indices(rows, "rows", (M,)), T,
-        _dense(q, "q", (M, K), torch.float8_e4m3fn), _dense(scale, "scale", (M, _blocks(K)), torch.float32),
-        _stream_of(stream, x)))
+    T, K = shape
+    M = T if rows is None else rows.numel()
+    if T | K | M >= 2**31:
+        _sizes(T=T, K=K, M=M)
+    ldx = _rows(x, "x", shape, bf16)
+    ldg = 0 if gate is None else _rows(gate, "gate", shape, bf16)
+    if not (q.dtype is f8 and q.shape == (M, K) and q.is_contiguous() and q.is_cuda and
+            scale.dtype is f32 and scale.shape == (M, -(-K // F8_BLOCK)) and scale.is_contiguous() and scale.is_cuda):
+        _dense(q, "q", (M, K), f8)
+        _dense(scale, "scale", (M, _blocks(K)), f32)
+    at = None
+    if rows is not None:
+        at = _dense(rows, "rows", (M,), i32)
+    status = load().skg_quantize_f8(M, K, x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg, at, T,
+                                    q.data_ptr(), scale.data_ptr(), _stream_of(stream, x))
+    if status:
+        _check(status)
 
 
 def skg_quantize_f8_weights(W, q, scale, stream=None):
@@ -683,7 +705,7 @@ class F8Plan:
         self.epilogue = _epi(epilogue)
         each = (experts,) if experts else ()
         self._shapes = (M, K), (M, _blocks(K)), (*each, N, K), (*each, _blocks(N), _blocks(K)), (M, N)
-        self._types = (torch.float8_e4m3fn, torch.float32, torch.bfloat16,
+        self._types = (torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.int32,
                        torch.float32 if self.epilogue == SKG_EPI_FP32 else torch.bfloat16)
         self.handle = None
         self.handle = skg_f8_plan(M, N, K, self.epilogue, experts, static_weights)
@@ -691,7 +713,7 @@ class F8Plan:
     def run(self, x, x_scale, W, w_scale, residual, y, offsets=None, stream=None):
         # one expression, as in Q8Plan.run
         mk, mb, nk, nb, mn = self._shapes
-        f8, f32, bf16, out = self._types
+        f8, f32, bf16, i32, out = self._types
         if not (x.dtype is f8 and x.shape == mk and x.is_contiguous() and x.is_cuda and
                 W.dtype is f8 and W.shape == nk and W.is_contiguous() and W.is_cuda and
                 x_scale.dtype is f32 and x_scale.shape == mb and x_scale.is_contiguous() and x_scale.is_cuda and
@@ -703,7 +725,7 @@ class F8Plan:
         if residual is not None:
             _dense(residual, "residual", mn, bf16)
         if offsets is not None:
-            _indices(offsets, "offsets", (self.experts + 1,))
+            _dense(offsets, "offsets", (self.experts + 1,), i32)
         status = load().skg_f8_run(self.handle, x.data_ptr(), x_scale.data_ptr(), W.data_ptr(), w_scale.data_ptr(),
                                    None if residual is None else residual.data_ptr(),
                                    None if offsets is None else offsets.data_ptr(), y.data_ptr(), _stream_of(stream, x))
@@ -734,50 +756,91 @@ class F8Plan:
 # ------------------------------------------- tokens to their experts and back
 def skg_experts_sort(expert, offsets, rows, pos, stream=None):
     """expert int32 [T, k]; offsets int32 [experts + 1]; rows int32 [T * k]; pos int32 [T, k]."""
+    i32 = _dtypes()[2]
     shape = expert.shape
     if len(shape) != 2 or len(offsets.shape) != 1:
         _bad("expert must be [T, k] and offsets [experts + 1]")
-    T, k, E = _int(shape[0], "T"), _int(shape[1], "k"), _int(offsets.shape[0] - 1, "experts")
-    _check(load().skg_experts_sort(T, k, E, _indices(expert, "expert", shape), _indices(offsets, "offsets", (E + 1,)),
-                                   _indices(rows, "rows", (T * k,)), _indices(pos, "pos", shape), _stream_of(stream, expert)))
+    T, k = shape
+    E = offsets.shape[0] - 1
+    if not (T | k | T * k < 2**31 and
+            expert.dtype is i32 and expert.is_contiguous() and expert.is_cuda and
+            offsets.dtype is i32 and offsets.is_contiguous() and offsets.is_cuda and
+            rows.dtype is i32 and rows.shape == (T * k,) and rows.is_contiguous() and rows.is_cuda and
+            pos.dtype is i32 and pos.shape == shape and pos.is_contiguous() and pos.is_cuda):
+        _sizes(T=T, k=k, choices=T * k)
+        for t, name, want in ((expert, "expert", shape), (offsets, "offsets", (E + 1,)), (rows, "rows", (T * k,)),
+                              (pos, "pos", shape)):
+            _dense(t, name, want, i32)
+    status = load().skg_experts_sort(T, k, _int(E, "experts"), expert.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+                                     pos.data_ptr(), _stream_of(stream, expert))
+    if status:
+        _check(status)
 
 
 def skg_experts_gather(x, rows, out, stream=None):
     """x bf16 [T, N] (rows may be strided); rows int32 [R]; out bf16 [R, N]."""
-    import torch
+    bf16, _, i32, _ = _dtypes()
     if len(x.shape) != 2 or len(rows.shape) != 1:
         _bad("x must be [T, N] and rows [R]")
-    T, N, R = _int(x.shape[0], "T"), _int(x.shape[1], "N"), _int(rows.shape[0], "R")
-    ldx = _rows(x, "x", x.shape, torch.bfloat16)
-    _check(load().skg_experts_gather(R, T, N, x.data_ptr(), ldx, _indices(rows, "rows", (R,)),
-                                     _dense(out, "out", (R, N), torch.bfloat16), _stream_of(stream, x)))
+    T, N = x.shape
+    R = rows.shape[0]
+    if not (T | N | R < 2**31 and rows.dtype is i32 and rows.is_contiguous() and rows.is_cuda and
+            out.dtype is bf16 and out.shape == (R, N) and out.is_contiguous() and out.is_cuda):
+        _sizes(T=T, N=N, R=R)
+        _dense(rows, "rows", (R,), i32)
+        _dense(out, "out", (R, N), bf16)
+    status = load().skg_experts_gather(R, T, N, x.data_ptr(), _rows(x, "x", x.shape, bf16), rows.data_ptr(), out.data_ptr(),
+                                       _stream_of(stream, x))
+    if status:
+        _check(status)
 
 
 def _choices(y, pos):
-    import torch
     if len(y.shape) != 2 or len(pos.shape) != 2:
         _bad("y must be [R, N] and pos [T, k]")
-    T, k, R, N = (_int(v, n) for v, n in zip((*pos.shape, *y.shape), ("T", "k", "R", "N")))
-    return T, k, R, N, _rows(y, "y", y.shape, torch.bfloat16), _indices(pos, "pos", pos.shape)
+    (T, k), (R, N) = pos.shape, y.shape
+    if T | k | R | N >= 2**31:
+        _sizes(T=T, k=k, R=R, N=N)
+    return T, k, R, N
 
 
 def skg_experts_combine(y, pos, weight, residual, out, stream=None):
     """y bf16 [R, N] (rows may be strided); pos int32 [T, k]; weight fp32 [T, k] or None; residual bf16 [T, N] or None;
     out bf16 [T, N]."""
-    import torch
-    T, k, R, N, ldy, at = _choices(y, pos)
-    _check(load().skg_experts_combine(
-        T, k, R, N, y.data_ptr(), ldy, at, None if weight is None else _dense(weight, "weight", (T, k), torch.float32),
-        None if residual is None else _dense(residual, "residual", (T, N), torch.bfloat16),
-        _dense(out, "out", (T, N), torch.bfloat16), _stream_of(stream, y)))
+    bf16, f32, i32, _ = _dtypes()
+    T, k, R, N = _choices(y, pos)
+    if not (pos.dtype is i32 and pos.is_contiguous() and pos.is_cuda and
+            out.dtype is bf16 and out.shape == (T, N) and out.is_contiguous() and out.is_cuda and
+            (weight is None or weight.dtype is f32 and weight.shape == (T, k) and weight.is_contiguous() and weight.is_cuda) and
+            (residual is None or residual.dtype is bf16 and residual.shape == (T, N) and residual.is_contiguous() and
+             residual.is_cuda)):
+        for t, name, shape, dtype in ((pos, "pos", (T, k), i32), (out, "out", (T, N), bf16), (weight, "weight", (T, k), f32),
+                                      (residual, "residual", (T, N), bf16)):
+            if t is not None:
+                _dense(t, name, shape, dtype)
+    status = load().skg_experts_combine(
+        T, k, R, N, y.data_ptr(), _rows(y, "y", y.shape, bf16), pos.data_ptr(), None if weight is None else weight.data_ptr(),
+        None if residual is None else residual.data_ptr(), out.data_ptr(), _stream_of(stream, y))
+    if status:
+        _check(status)
 
 
 def skg_experts_combine_grad(grad_out, y, pos, weight, grad_y, grad_weight, stream=None):
     """grad_out bf16 [T, N]; y bf16 [R, N] (rows may be strided); pos int32 [T, k]; weight, grad_weight fp32 [T, k];
     grad_y bf16 [R, N]."""
-    import torch
-    T, k, R, N, ldy, at = _choices(y, pos)
-    _check(load().skg_experts_combine_grad(
-        T, k, R, N, _dense(grad_out, "grad_out", (T, N), torch.bfloat16), y.data_ptr(), ldy, at,
-        _dense(weight, "weight", (T, k), torch.float32), _dense(grad_y, "grad_y", (R, N), torch.bfloat16),
-        _dense(grad_weight, "grad_weight", (T, k), torch.float32), _stream_of(stream, y)))
+    bf16, f32, i32, _ = _dtypes()
+    T, k, R, N = _choices(y, pos)
+    if not (pos.dtype is i32 and pos.is_contiguous() and pos.is_cuda and
+            grad_out.dtype is bf16 and grad_out.shape == (T, N) and grad_out.is_contiguous() and grad_out.is_cuda and
+            grad_y.dtype is bf16 and grad_y.shape == (R, N) and grad_y.is_contiguous() and grad_y.is_cuda and
+            weight.dtype is f32 and weight.shape == (T, k) and weight.is_contiguous() and weight.is_cuda and
+            grad_weight.dtype is f32 and grad_weight.shape == (T, k) and grad_weight.is_contiguous() and grad_weight.is_cuda):
+        for t, name, shape, dtype in ((pos, "pos", (T, k), i32), (grad_out, "grad_out", (T, N), bf16),
+                                      (grad_y, "grad_y", (R, N), bf16), (weight, "weight", (T, k), f32),
+                                      (grad_weight, "grad_weight", (T, k), f32)):
+            _dense(t, name, shape, dtype)
+    status = load().skg_experts_combine_grad(
+        T, k, R, N, grad_out.data_ptr(), y.data_ptr(), _rows(y, "y", y.shape, bf16), pos.data_ptr(), weight.data_ptr(),
+        grad_y.data_ptr(), grad_weight.data_ptr(), _stream_of(stream, y))
+    if status:
+        _check(status)
