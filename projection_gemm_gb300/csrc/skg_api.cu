@@ -403,7 +403,7 @@ skg_status set_error(skg_status st, const char *fmt, ...)
 }
 
 skg_status encode_tiled_2d(CUtensorMap *m, CUtensorMapDataType type, int elem_bytes, const void *base, int rows,
-                           int cols, int box_rows)
+                           int cols, int box_rows, CUtensorMapL2promotion promotion)
 {
     EncodeTiledFn enc = get_encode();
     if (!enc)
@@ -414,7 +414,7 @@ skg_status encode_tiled_2d(CUtensorMap *m, CUtensorMapDataType type, int elem_by
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(m, type, 2, const_cast<void *>(base), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(SKG_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for [%d,%d]", (int)r, rows, cols);
     return SKG_OK;

@@ -328,20 +328,28 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         constexpr int AHEAD = 6;
         bool ok = true;
         int j = 0;
-        for (int tile = first; ok && tile < tiles; tile += step) {
-            const F8Tile t = f8_tile(p, MT, table, tile);
+        float w[AHEAD], x[AHEAD];
+        const float *ws, *xs;
+        bool live;
+        F8Tile t;
+        // A tile's scales, from its first units' on: of the next tile they are on their
+        // way while the outputs of this one are stored.
+        auto begin = [&](int tile) {
+            t = f8_tile(p, MT, table, tile);
             // this CTA's tokens are ma to mb, the window's from m0 on
-            const int ma = t.m0 + rank * 128, mb = min(t.m1, ma + 128), m0 = f8_x_window(p, ma);
-            const int m = m0 + row0 + lane, nb = t.nt * (NT / kF8Block) + col0 / kF8Block;
-            const bool live = m >= ma && m < mb && nb < p.nb;
-            const float *ws = p.w_scale + (static_cast<size_t>(t.e) * p.nb + nb) * p.nkb + kb0;
-            const float *xs = p.x_scale + static_cast<size_t>(m) * p.nkb + kb0;
-            float w[AHEAD], x[AHEAD];
+            const int ma = t.m0 + rank * 128, mb = min(t.m1, ma + 128);
+            const int m = f8_x_window(p, ma) + row0 + lane, nb = t.nt * (NT / kF8Block) + col0 / kF8Block;
+            live = m >= ma && m < mb && nb < p.nb;
+            ws = p.w_scale + (static_cast<size_t>(t.e) * p.nb + nb) * p.nkb + kb0;
+            xs = p.x_scale + static_cast<size_t>(m) * p.nkb + kb0;
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 w[i] = live && i < units ? __ldcg(ws + i) : 0.0f;
                 x[i] = live && i < units ? __ldca(xs + i) : 0.0f;
             }
+        };
+        begin(first);
+        for (int tile = first; ok && tile < tiles; tile += step) {
             float acc[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -371,8 +379,10 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             }
             if (!ok)
                 break;
-            const int na = nb * kF8Block, n0 = f8_w_window(p, t.e, na) - t.e * p.N + col0 % kF8Block;
-            const int lo = ma - m0 - row0, hi = mb - m0 - row0;
+            const int na = t.nt * NT + col0 / kF8Block * kF8Block, n0 = f8_w_window(p, t.e, na) - t.e * p.N + col0 % kF8Block;
+            const int ma = t.m0 + rank * 128, m0 = f8_x_window(p, ma), lo = ma - m0 - row0, hi = min(t.m1, ma + 128) - m0 - row0;
+            if (tile + step < tiles)
+                begin(tile + step);
             if (p.split > 1) {
                 // in the ring's place: the last MMA has read its operands
 #pragma unroll

@@ -187,7 +187,7 @@ skg_status set_error(skg_status st, const char *fmt, ...);
 // 2-D row-major [rows, cols] of elem_bytes-wide elements, dense, read in boxes
 // of [box_rows, 128 bytes] with the 128-byte swizzle, zero outside the tensor.
 skg_status encode_tiled_2d(CUtensorMap *m, CUtensorMapDataType type, int elem_bytes, const void *base, int rows,
-                           int cols, int box_rows);
+                           int cols, int box_rows, CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 // Everything one split-K launch needs, worked out on the host without
 // allocating: the checks of skg_run, the launch shape the picker chooses on
