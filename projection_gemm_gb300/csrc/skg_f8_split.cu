@@ -241,22 +241,31 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         constexpr int H = NC >= 32 ? 2 : 1;              // 16 columns read at a time, or 32
         bool ok = true;
         int j = 0;
-        for (int tile = first; ok && tile < tiles; tile += step) {
-            const F8Tile t = f8_tile(p, MT, table, tile);
-            // tokens m0 + lo to m0 + hi of the window, and this thread's channel of the other
-            const int m0 = f8_x_window(p, t.m0), lo = t.m0 - m0, hi = min(t.m1, t.m0 + MT) - m0;
-            const float *ws = p.w_scale + (static_cast<size_t>(t.e) * p.nb + t.nt) * p.nkb + kb0;
-            const float *xs = p.x_scale + static_cast<size_t>(m0 + lane) * p.nkb + kb0;
-            float w[AHEAD], x[AHEAD][CP];
-            auto fetch = [&](int kb, float &wv, float (&xv)[CP]) {
-                wv = kb < units ? __ldcg(ws + kb) : 0.0f;
+        float w[AHEAD], x[AHEAD][CP];
+        const float *ws, *xs;
+        F8Tile t;
+        int m0, lo, hi;                  // tokens m0 + lo to m0 + hi of the window are the tile's
+        auto fetch = [&](int kb, float &wv, float (&xv)[CP]) {
+            wv = kb < units ? __ldcg(ws + kb) : 0.0f;
 #pragma unroll
-                for (int c = 0; c < CP; ++c)
-                    xv[c] = kb < units && lane + 32 * c >= lo && lane + 32 * c < hi ? __ldca(xs + static_cast<size_t>(32 * c) * p.nkb + kb) : 0.0f;
-            };
+            for (int c = 0; c < CP; ++c)
+                xv[c] = kb < units && lane + 32 * c >= lo && lane + 32 * c < hi ? __ldca(xs + static_cast<size_t>(32 * c) * p.nkb + kb) : 0.0f;
+        };
+        // A tile's scales, from its first units' on: of the next tile they are on their
+        // way while the outputs of this one are stored.
+        auto begin = [&](int tile) {
+            t = f8_tile(p, MT, table, tile);
+            m0 = f8_x_window(p, t.m0);
+            lo = t.m0 - m0;
+            hi = min(t.m1, t.m0 + MT) - m0;
+            ws = p.w_scale + (static_cast<size_t>(t.e) * p.nb + t.nt) * p.nkb + kb0;
+            xs = p.x_scale + static_cast<size_t>(m0 + lane) * p.nkb + kb0;
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i)
                 fetch(i, w[i], x[i]);
+        };
+        begin(first);
+        for (int tile = first; ok && tile < tiles; tile += step) {
             float acc[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -309,15 +318,17 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             if (!ok)
                 break;
             if (p.split == 1) {
-                const int n = f8_w_window(p, t.e, t.nt * kTileN) - t.e * p.N + row;
-                if (n < t.nt * kTileN || n >= p.N)
-                    continue;
+                const int n = f8_w_window(p, t.e, t.nt * kTileN) - t.e * p.N + row, from = m0, first_c = lo;
+                const int end_c = n >= t.nt * kTileN && n < p.N ? hi : 0;
+                if (tile + step < tiles)
+                    begin(tile + step);
                 if (p.epilogue == SKG_EPI_FP32)
-                    store_columns<SKG_EPI_FP32>(p, m0, n, lo, hi, acc);
+                    store_columns<SKG_EPI_FP32>(p, from, n, first_c, end_c, acc);
                 else if (p.epilogue == SKG_EPI_BF16_RESIDUAL)
-                    store_columns<SKG_EPI_BF16_RESIDUAL>(p, m0, n, lo, hi, acc);
+                    store_columns<SKG_EPI_BF16_RESIDUAL>(p, from, n, first_c, end_c, acc);
                 else
-                    store_columns<SKG_EPI_BF16>(p, m0, n, lo, hi, acc);
+                    store_columns<SKG_EPI_BF16>(p, from, n, first_c, end_c, acc);
+                __syncwarp();
             } else {
                 // in the ring's place: the last MMA has read its operands
 #pragma unroll
