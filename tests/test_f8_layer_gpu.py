@@ -1,0 +1,266 @@
+"""The 8-bit floating point path's and the experts' operators together on a GB300:
+a layer of experts stage by stage, in graphs, on several streams, back to back, and
+what a plan reports."""
+import pytest
+import torch
+
+from projection_gemm_gb300 import skg
+from projection_gemm_gb300.f8_experts import F8Experts, main
+from tests import f8_reference as R
+from tests.test_experts_gpu import U
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from projection_gemm_gb300 import build
+    build.build()
+    skg.load()
+    assert torch.cuda.is_available()
+
+
+def normal(g, *shape, std=1.0):
+    return (torch.randn(*shape, generator=g) * std).to(torch.bfloat16).cuda()
+
+
+def make(T, k, E, hidden, inner, seed=1, dropped=0.0, router=False):
+    g = torch.Generator().manual_seed(seed)
+    W1, W2 = normal(g, E, 2 * inner, hidden, std=hidden ** -0.5), normal(g, E, hidden, inner, std=inner ** -0.5)
+    layer = F8Experts(T, k, W1, W2, normal(g, E, hidden) if router else None)
+    return layer, choices(g, T, k, E, hidden, dropped)
+
+
+def choices(g, T, k, E, hidden, dropped=0.0):
+    expert = torch.topk(torch.randn(T, E, generator=g), k, 1).indices.int()
+    expert[torch.rand(T, k, generator=g) < dropped] = -1
+    return normal(g, T, hidden), normal(g, T, hidden), expert.cuda(), torch.rand(T, k, generator=g).cuda()
+
+
+@pytest.mark.parametrize("T,k,E,hidden,inner,dropped", [(1, 2, 4, 256, 128, 0.0), (37, 3, 12, 400, 272, 0.2),
+                                                        (64, 8, 64, 1024, 256, 0.0), (700, 4, 6, 512, 640, 0.1), (5, 2, 3, 144, 48, 1.0)])
+def test_layer_stage_by_stage(T, k, E, hidden, inner, dropped):
+    layer, (x, res, expert, weight) = make(T, k, E, hidden, inner, dropped=dropped)
+    out = layer.run(x, res, expert, weight)
+    layer.check()
+    at = layer.offsets.tolist()
+    n = at[-1]
+    assert n == int((expert >= 0).sum())
+    rows = layer.rows[:n].long()
+    if n:
+        R.check_quantised(x[rows], layer.q[:n], layer.q_scale[:n])
+        R.check_gated(layer.u[:n, inner:], layer.u[:n, :inner], layer.a[:n], layer.a_scale[:n])
+    for e in range(E):
+        s = slice(at[e], at[e + 1])
+        if s.stop > s.start:
+            R.check_linear(layer.q[s], layer.q_scale[s], layer.gate_up[e], layer.gate_up_scale[e], None, layer.u[s])
+            R.check_linear(layer.a[s], layer.a_scale[s], layer.down[e], layer.down_scale[e], None, layer.d[s])
+    live = layer.pos >= 0
+    terms = torch.where(live[..., None], layer.d[layer.pos.clamp(min=0).long()].double(), 0.0) * weight.double()[..., None]
+    want, mass = res.double() + terms.sum(1), res.double().abs() + terms.abs().sum(1)
+    assert bool(((out.double() - want).abs() <= (k + 1) * U * mass * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()).all())
+    layer.close()
+
+
+@pytest.mark.parametrize("T,k,E", [(4, 2, 16), (300, 4, 5)])
+def test_layer_in_a_graph_with_other_inputs(T, k, E):
+    """Captured once on a stream of its own, replayed for other tokens and choices (also none at all): the bits of the
+    eager step."""
+    hidden, inner = 512, 256
+    layer, _ = make(T, k, E, hidden, inner)
+    g = torch.Generator().manual_seed(7)
+    inputs = [choices(g, T, k, E, hidden, d) for d in (0.0, 0.5, 1.0, 0.0)]
+    want = [layer.run(*i).clone() for i in inputs]
+    held = [t.clone() for t in inputs[0]]
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        layer.run(*held)
+    for _ in range(3):
+        for i, w in zip(inputs, want):
+            for h, t in zip(held, i):
+                h.copy_(t)
+            graph.replay()
+            assert torch.equal(layer.out, w)
+    layer.check()
+    layer.close()
+
+
+def test_one_plan_in_several_streams_and_graphs_at_once():
+    g = torch.Generator().manual_seed(3)
+    M, N, K, E = 96, 640, 1024, 6
+    W = (torch.randn(E, N, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    ws = torch.rand(E, 5, 8, generator=g).cuda()
+    plan = skg.F8Plan(M, N, K, "bf16", experts=E)
+    jobs = []
+    for i in range(4):
+        x = (torch.randn(M, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+        xs = torch.rand(M, 8, generator=g).cuda()
+        cuts = torch.sort(torch.randint(0, M + 1, (E - 1,), generator=g)).values.int()
+        offsets = torch.cat([torch.zeros(1, dtype=torch.int32), cuts, torch.full((1,), M, dtype=torch.int32)]).cuda()
+        y = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+        plan.run(x, xs, W, ws, None, y, offsets=offsets)
+        jobs.append((x, xs, offsets, y.clone(), y, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    graphs = []
+    for x, xs, offsets, want, y, s in jobs[2:]:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            plan.run(x, xs, W, ws, None, y, offsets=offsets)
+        graphs.append(graph)
+    for _ in range(20):
+        for x, xs, offsets, want, y, s in jobs:
+            y.zero_()
+        torch.cuda.synchronize()
+        for x, xs, offsets, want, y, s in jobs[:2]:
+            plan.run(x, xs, W, ws, None, y, offsets=offsets, stream=s)
+        for graph, job in zip(graphs, jobs[2:]):
+            with torch.cuda.stream(job[5]):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want) for _, _, _, want, y, _ in jobs)
+    plan.check()
+
+
+@pytest.mark.parametrize("M,N,K,launch", [(1, 2048, 2048, None), (16, 512, 4096, (1, 16, 8)), (64, 1024, 1024, (1, 64, 1)),
+                                          (200, 1024, 1024, (2, 128, 2)), (300, 1024, 1024, (2, 256, 1))])
+def test_chain_reads_what_the_kernel_before_wrote(M, N, K, launch):
+    """Quantiser and projection in turn, each early by programmatic launch, weights static: 200 links without a
+    synchronisation, each from a different scale of x, against the same links one at a time."""
+    g = torch.Generator().manual_seed(5)
+    x = normal(g, M, K)
+    W = (torch.randn(N, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    ws = torch.rand(R.blocks(N), R.blocks(K), generator=g).cuda()
+    plan = skg.F8Plan(M, N, K, "bf16", static_weights=True)
+    if launch:
+        plan.force(*launch)
+    inputs = [x * (2.0 ** (i % 5)) * (1 - 2 * (i % 2)) for i in range(8)]
+    q, s = torch.empty(M, K, device="cuda").to(R.F8), torch.empty(M, R.blocks(K), device="cuda")
+    ys = [torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(200)]
+    want = []
+    for v in inputs:
+        skg.skg_quantize_f8(v, None, q, s)
+        torch.cuda.synchronize()
+        plan.run(q, s, W, ws, None, ys[0])
+        torch.cuda.synchronize()
+        want.append(ys[0].clone())
+    for i, y in enumerate(ys):
+        skg.skg_quantize_f8(inputs[i % 8], None, q, s)
+        plan.run(q, s, W, ws, None, y)
+    torch.cuda.synchronize()
+    plan.check()
+    assert all(torch.equal(y, want[i % 8]) for i, y in enumerate(ys))
+
+
+@pytest.mark.parametrize("launch", [(1, 16, 3), (1, 64, 1), (2, 128, 1), (2, 256, 2)])
+def test_a_row_does_not_depend_on_the_others(launch):
+    g = torch.Generator().manual_seed(6)
+    M, N, K = 290, 384, 1040
+    x = (torch.randn(M, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    W = (torch.randn(N, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    xs, ws = torch.rand(M, 9, generator=g).cuda(), torch.rand(3, 9, generator=g).cuda()
+
+    def run(order):
+        y = torch.empty(len(order), N, device="cuda")
+        plan = skg.F8Plan(len(order), N, K, "fp32")
+        plan.force(*launch)
+        plan.run(x[order].contiguous(), xs[order].contiguous(), W, ws, None, y)
+        plan.check()
+        return y
+
+    whole = run(torch.arange(M, device="cuda"))
+    order = torch.randperm(M, generator=g).cuda()
+    assert torch.equal(run(order), whole[order])
+    assert torch.equal(run(order[:7]), whole[order[:7]])
+    again = run(torch.arange(M, device="cuda"))
+    assert torch.equal(again, whole)
+
+
+def test_a_wait_that_runs_out_is_reported_once():
+    plan = skg.F8Plan(2, 128, 128, "bf16")
+    skg.skg_f8_debug_wait_timeout(plan.handle, 1000000)
+    with pytest.raises(skg.SkgError) as e:
+        plan.check()
+    assert e.value.status == skg.SKG_ERR_DEVICE_TIMEOUT
+    plan.check()
+    skg.skg_f8_debug_wait_timeout(plan.handle, 1000000)
+    torch.cuda.synchronize()
+    x, xs = torch.zeros(2, 128, device="cuda").to(R.F8), torch.zeros(2, 1, device="cuda")
+    W, ws = torch.zeros(128, 128, device="cuda").to(R.F8), torch.zeros(1, 1, device="cuda")
+    y = torch.empty(2, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(skg.SkgError) as e:
+        plan.run(x, xs, W, ws, None, y)
+    assert e.value.status == skg.SKG_ERR_DEVICE_TIMEOUT
+    plan.run(x, xs, W, ws, None, y)
+    plan.check()
+    assert bool((y == 0).all())
+
+
+def test_run_refuses_what_does_not_belong_to_the_plan():
+    E, M, N, K = 3, 8, 128, 256
+    x, xs = torch.zeros(M, K, device="cuda").to(R.F8), torch.zeros(M, 2, device="cuda")
+    W, ws = torch.zeros(E, N, K, device="cuda").to(R.F8), torch.zeros(E, 1, 2, device="cuda")
+    y, off = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda"), torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    one, some = skg.F8Plan(M, N, K, "bf16"), skg.F8Plan(M, N, K, "bf16", experts=E)
+    res = skg.F8Plan(M, N, K, "bf16_residual")
+    bad = [
+        lambda: one.run(x, xs, W[0], ws[0], None, y, offsets=off), lambda: some.run(x, xs, W, ws, None, y),
+        lambda: one.run(x, xs, W[0], ws[0], y, y), lambda: res.run(x, xs, W[0], ws[0], None, y),
+        lambda: one.run(x, xs[:, :1].contiguous(), W[0], ws[0], None, y), lambda: one.run(x, xs, W, ws, None, y),
+        lambda: some.run(x, xs, W, ws, None, y, offsets=off[:3].contiguous()),
+        lambda: some.run(x, xs, W, ws, None, y, offsets=off.long()),
+        lambda: one.run(x.float(), xs, W[0], ws[0], None, y), lambda: one.run(x, xs, W[0], ws[0], None, y.float()),
+        lambda: one.run(x.t().contiguous().t(), xs, W[0], ws[0], None, y),
+    ]
+    for call in bad:
+        with pytest.raises(skg.SkgError) as e:
+            call()
+        assert e.value.status == skg.SKG_ERR_INVALID_ARG
+    with pytest.raises(skg.SkgError) as e:                  # a slice that is not 16-byte aligned
+        buf = torch.zeros(M * K + 8, device="cuda").to(R.F8)
+        one.run(buf[8:].view(M, K), xs, W[0], ws[0], None, y)
+    assert e.value.status == skg.SKG_ERR_ALIGNMENT
+    for kw, status in ((dict(kind=3), skg.SKG_ERR_INVALID_ARG), (dict(kind=1, m_tile=128), skg.SKG_ERR_INVALID_ARG),
+                       (dict(kind=2, m_tile=64), skg.SKG_ERR_INVALID_ARG), (dict(kind=1, split_k=9), skg.SKG_ERR_INVALID_ARG),
+                       (dict(kind=2, split_k=5), skg.SKG_ERR_INVALID_ARG), (dict(split_k=-1), skg.SKG_ERR_INVALID_ARG)):
+        with pytest.raises(skg.SkgError) as e:
+            one.force(**kw)
+        assert e.value.status == status
+
+
+@pytest.mark.parametrize("M,N,K,epilogue,launch", [
+    (3, 130, 256, "bf16", (1, 16, 2)), (40, 129, 400, "bf16_residual", (2, 128, 1)), (300, 136, 272, "fp32", (2, 256, 1)),
+    (300, 136, 272, "bf16", (2, 256, 2)), (70, 200, 144, "bf16", (1, 64, 1))])
+def test_outputs_of_any_alignment_and_nothing_beyond_them(M, N, K, epilogue, launch):
+    """y and residual inside larger tensors, one element off: the results of aligned ones, and their neighbours stay."""
+    g = torch.Generator().manual_seed(M + N)
+    x = (torch.randn(M, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    W = (torch.randn(N, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    xs, ws = torch.rand(M, R.blocks(K), generator=g).cuda(), torch.rand(R.blocks(N), R.blocks(K), generator=g).cuda()
+    dtype = torch.float32 if epilogue == "fp32" else torch.bfloat16
+    plan = skg.F8Plan(M, N, K, epilogue)
+    plan.force(*launch)
+
+    def run(off):
+        big = torch.full((M * N + 64,), 3.0, dtype=dtype, device="cuda")
+        y = big[off:off + M * N].view(M, N)
+        r = None
+        if epilogue == "bf16_residual":
+            held = torch.zeros(M * N + off, dtype=torch.bfloat16, device="cuda")
+            held[off:] = torch.ones(M * N, dtype=torch.bfloat16, device="cuda")
+            r = held[off:].view(M, N)
+        plan.run(x, xs, W, ws, r, y)
+        plan.check()
+        assert bool((big[:off] == 3).all()) and bool((big[off + M * N:] == 3).all())
+        return y.clone()
+
+    first = run(0)
+    for off in (1, 2, 4, 7):
+        assert torch.equal(run(off), first)
+
+
+def test_example_runs(capsys):
+    main(["4", "256", "128", "8", "2"])
+    main(["100", "512", "256", "6", "3"])
+    assert capsys.readouterr().out.count("unquantised") == 2
