@@ -264,3 +264,81 @@ def test_example_runs(capsys):
     main(["4", "256", "128", "8", "2"])
     main(["100", "512", "256", "6", "3"])
     assert capsys.readouterr().out.count("unquantised") == 2
+
+
+@pytest.mark.parametrize("launch", [(1, 16, 1), (1, 32, 4), (1, 64, 1), (2, 128, 2), (2, 256, 1)])
+def test_nan_numbers_stay_in_their_row_and_channel(launch):
+    g = torch.Generator().manual_seed(8)
+    M, N, K = 50, 260, 272
+    x = (torch.randn(M, K, generator=g) * 100).clamp(-448, 448)
+    W = (torch.randn(N, K, generator=g) * 100).clamp(-448, 448)
+    x[7, 200], x[20, 0], W[130, 271], W[259, 5] = (float("nan"),) * 4
+    xs, ws = torch.rand(M, 3, generator=g).cuda(), torch.rand(3, 3, generator=g).cuda()
+    y = torch.empty(M, N, device="cuda")
+    plan = skg.F8Plan(M, N, K, "fp32")
+    plan.force(*launch)
+    plan.run(x.to(R.F8).cuda(), xs, W.to(R.F8).cuda(), ws, None, y)
+    plan.check()
+    bad = torch.zeros(M, N, dtype=torch.bool)
+    bad[[7, 20]] = True
+    bad[:, [130, 259]] = True
+    assert torch.equal(y.isnan().cpu(), bad)
+
+
+# ------------------------------------------------------------------------------ beyond 2^31 elements
+def test_quantiser_and_rows_beyond_31_bits():
+    N, T = 7168, 4096
+    M = 2 ** 31 // N + 700
+    g = torch.Generator().manual_seed(9)
+    x = normal(g, T, N)
+    rows = (torch.arange(M, device="cuda", dtype=torch.int32) * 5) % T
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    skg.skg_experts_gather(x, rows, out)
+    for s in (slice(0, 64), slice(M - 600, M)):
+        assert torch.equal(out[s], x[rows[s].long()])
+    q, scale = torch.empty(M, N, dtype=R.F8, device="cuda"), torch.empty(M, 56, device="cuda")
+    skg.skg_quantize_f8(out, None, q, scale)
+    R.check_quantised(out[M - 600:], q[M - 600:], scale[M - 600:])
+    pos = torch.arange(M - 64, M, device="cuda", dtype=torch.int32).view(16, 4)
+    back = torch.empty(16, N, dtype=torch.bfloat16, device="cuda")
+    skg.skg_experts_combine(out, pos, None, None, back)
+    want = out[pos.long()].double().sum(1)
+    assert bool(((back.double() - want).abs() <= 2.0 ** -8 * want.abs() + 4 * U * out[pos.long()].double().abs().sum(1) * 2).all())
+    grad_w = torch.empty(16, 4, device="cuda")
+    skg.skg_experts_combine_grad(back, out, pos, torch.full((16, 4), 2.0, device="cuda"), out, grad_w)
+    assert torch.equal(out[M - 64:], (2 * back).repeat_interleave(4, 0))
+
+
+@pytest.mark.parametrize("launch", [(1, 64, 1), (2, 128, 1), (2, 256, 1)])
+def test_projection_to_more_than_31_bits_of_outputs(launch):
+    M, N, K = 2 ** 18, 8200, 16
+    g = torch.Generator().manual_seed(10)
+    x = (torch.randn(M, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    W = (torch.randn(N, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    xs, ws = torch.rand(M, 1, generator=g).cuda(), torch.rand(R.blocks(N), 1, generator=g).cuda()
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    plan = skg.F8Plan(M, N, K, "bf16")
+    plan.force(*launch)
+    plan.run(x, xs, W, ws, None, y)
+    plan.check()
+    for s in (slice(0, 300), slice(M - 300, M)):
+        R.check_linear(x[s], xs[s], W, ws, None, y[s])
+
+
+def test_experts_whose_weights_are_more_than_32_bits():
+    E, N, K, M = 300, 2048, 8192, 24
+    W = torch.randint(0, 120, (E, N, K), dtype=torch.uint8, device="cuda").view(R.F8)
+    g = torch.Generator().manual_seed(11)
+    x = (torch.randn(M, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    xs, ws = torch.rand(M, 64, generator=g).cuda(), torch.rand(E, 16, 64, generator=g).cuda()
+    counts = torch.zeros(E, dtype=torch.int32)
+    counts[[0, 150, 298, 299]] = torch.tensor([2, 3, 1, 18], dtype=torch.int32)
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int32), counts.cumsum(0).int()]).cuda()
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    plan = skg.F8Plan(M, N, K, "bf16", experts=E)
+    plan.run(x, xs, W, ws, None, y, offsets=offsets)
+    plan.check()
+    at = offsets.tolist()
+    for e in (0, 150, 298, 299):
+        s = slice(at[e], at[e + 1])
+        R.check_linear(x[s], xs[s], W[e], ws[e], None, y[s])
