@@ -648,8 +648,9 @@ SKG_API skg_status skg_f8_plan(int M, int N, int K, int epilogue, int experts, i
  *            first and behind the last of them are left as they were in y.  Other
  *            numbers are taken as the nearest that are allowed, in order
  *   y        [M,N] bf16 (fp32 for SKG_EPI_FP32); must not overlap the inputs
- * Sums of products and over blocks are fp32, the residual is added in fp32, and the
- * result is rounded once.  The order of the sum over blocks depends on the launch
+ * Sums of products and over blocks are fp32, a block's two scales are multiplied in
+ * fp32 before they meet its sum (their product should be a normal number), the
+ * residual is added in fp32, and the result is rounded once.  The order of the sum over blocks depends on the launch
  * shape: a plan gives the same bits each time, and a row's result does not depend
  * on the other rows.
  * Allocates nothing and keeps no workspace: runs of a plan may be in flight at the
@@ -724,7 +725,7 @@ SKG_API skg_status skg_experts_combine(int T, int k, int R, int N, const void *y
  *                    goes to are left as they were.  bf16 [R, N] dense
  *   grad_weight[t,j] = <grad_out[t], y[pos[t,j]]>, fp32, 0 where a choice was left out
  *   grad_out bf16 [T, N] dense; the others as for skg_experts_combine.  (The
- *   residual's gradient is grad_out itself.)
+ *   residual's gradient is grad_out itself.)  grad_y may be y where ldy = N
  * A sorted row belongs to one choice: where pos has the same row twice, grad_y has
  * one of the two.
  * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.

@@ -11,6 +11,13 @@
 //
 // Sums are fp32 in a fixed order, rounded once, so a call gives the same bits
 // each time.
+//
+// What bounds the rows' kernels is HBM (copy peak 6.71 TB/s).  4096 tokens, 8 choices
+// each, rows of 7168: gather 97 us (5.4 TB/s, nearly all of it writes; hints to keep
+// x in the L2 change nothing), combination 93 us (6.3; CTAs of 8 warps 110), without
+// residual 81, gradients 166 (6.0).  Rows of odd length move an element a lane: 1001 tokens,
+// 3 choices, 2001: 5.0, 7.4 and 14.4 us.  The sort is latency: 8 choices 2.1 us, 128 3.5,
+// 32768 10.9 (8 CTAs); 524288 141, by the scattered stores of 8 SMs.
 #include <algorithm>
 #include <cstdint>
 

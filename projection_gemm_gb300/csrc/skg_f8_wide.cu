@@ -3,21 +3,44 @@
 //
 //   y[m, n] = sum_b xs[m, b] ws[n / 128, b] sum_(k in block b) x[m, k] W[n, k]
 //
-// The arithmetic is that of skg_f8_split.cu.  Two CTAs work as one
-// (cta_group::2): 256 tokens x 256 channels, each CTA with its 128 rows of x (A),
-// half of the rows of W (B) and the accumulator of its tokens, 128 lanes x 256
-// columns.  A token a lane makes a unit's scale one number a thread: xs of its
-// token times ws of the 128 channels that its warp has.  Two accumulators take
-// all of the SM's tensor memory.
+// The arithmetic is that of skg_f8_split.cu.  Tokens are the MMA's M: a token a lane
+// makes a unit's scale one number a thread, xs of its token times ws of the 128
+// channels that its warp has.  Two forms:
+//   PAIR = 1  a CTA computes 128 tokens x 128 channels, with four accumulators
+//   PAIR = 2  two CTAs work as one (cta_group::2): 256 x 256, each with its 128 rows
+//             of x (A), half of the rows of W (B) and its tokens' sums, 128 lanes x 256
+//             columns; two accumulators take all of the SM's tensor memory
+// Persistent over tiles, or, where those are fewer than the SMs, with K split over
+// the CTAs or pairs of a cluster, joined as in skg_f8_split.cu.
 //
-// What bounds it is the tensor core: a unit of 128 k is 512 cycles of an SM's
-// MMAs, in which 8 warps take the 128 x 256 sums of the unit before into
-// registers.
+// Roles of a CTA (one per SM):
+//   1 + 1     TMA; TMEM and, in the first CTA of a pair, MMA issue for both
+//   8 warps   accumulators into registers; at a tile's end the next tile's first
+//             scales are requested, then residual, rounding and store, while that
+//             tile's first units are computed
+// An epilogue thread of a pair holds 128 sums and 64 more on their way from tensor
+// memory, so the first warpgroup gives up registers (56 a thread, 224 for the others).
 //
-// Roles of a CTA (one per SM, pairs persistent over tiles):
-//   1 + 1     TMA; TMEM and, in the first CTA of the pair, MMA issue for both
-//   8 warps   accumulators into registers, and the tile's end: residual,
-//             rounding, store, while the next tile's first two units are computed
+// What bounds it.  A unit of 128 k is 512 cycles of an SM's MMAs; without the epilogue's
+// additions it takes 650 (operands are written to and read from shared memory at
+// 100 bytes a cycle), with them 780: all 128 x 256 sums go through the registers
+// once a unit, and the accumulator is free again only when they have.  Measured:
+// 4096 x 12288 x 7168 269-301 us (2.4 to 2.7 PFLOP/s; cuBLAS reaches 1.96 in bf16), of which
+// 8% is the last of 10.1 waves; 1024 x 7168 x 7168 52 us; 16384 rows of 32 experts,
+// 4096 x 4096, 268-302 us; by tiles of 128: 128 x 7168 x 7168 17.0 us (K split in 2; 22 unsplit),
+// 256 x 4096 x 4096 12.8, 333 x 5001 x 4112 20.1 (rows that begin 16 bytes off a line:
+// 16 with K = 4096), 2048 rows of 32 experts, 4096 x 4096, 108 (5.0 TB/s of weights).
+// Steps at 4096 x 4864 x 7168, now 105 us (with, and without it at that step):
+//   sums added two at a time by fma.rn.f32x2            116, 111
+//   scales requested 2, 4, 8 units ahead                150, 124, 116 (6: 113 where 8 spill)
+//   scales brought to shared memory by two warps        111, 111
+//   outputs stored by each lane, 8 bytes at a time      134, 116
+//   the next tile's scales requested after the store    113, 105
+//   16 epilogue warps of 64 columns, scales 2 ahead     154, 134
+//   MMAs of half a unit, each with its own barriers     126, 128 (x is read twice)
+//   waits that poll without a pause                     136, 126
+// Outputs copied by the copy engine out of 68 KB of shared memory (4 stages instead of 5)
+// took the same time, and tiles of 128 longer.
 //
 // Every wait is bounded as in skg_f8_split.cu.
 #include <algorithm>
