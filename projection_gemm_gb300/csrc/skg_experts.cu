@@ -15,9 +15,11 @@
 // What bounds the rows' kernels is HBM (copy peak 6.71 TB/s).  4096 tokens, 8 choices
 // each, rows of 7168: gather 97 us (5.4 TB/s, nearly all of it writes; hints to keep
 // x in the L2 change nothing), combination 93 us (6.3; CTAs of 8 warps 110), without
-// residual 81, gradients 166 (6.0).  Rows of odd length move an element a lane: 1001 tokens,
-// 3 choices, 2001: 5.0, 7.4 and 14.4 us.  The sort is latency: 8 choices 2.1 us, 128 3.5,
-// 32768 10.9 (8 CTAs); 524288 141, by the scattered stores of 8 SMs.
+// residual 81, gradients 166 (6.0).  Rows that are not whole blocks of 16 bytes move 4, 2 or 1
+// elements a lane: 1001 tokens, 3 choices, rows of 2004, 2002, 2001: gather 4.2, 3.8, 5.0,
+// combination 4.6, 5.2, 7.4, gradients 8.3, 8.3, 11.6 us (aligned blocks that two lanes fill
+// by shuffles, for rows of any alignment: 9, 12, 35).  The sort is latency: 8 choices 2.1 us,
+// 128 3.5, 32768 10.9 (8 CTAs); 524288 141, by the scattered stores of 8 SMs.
 #include <algorithm>
 #include <cstdint>
 
@@ -193,7 +195,12 @@ __global__ void __launch_bounds__(32 * kSortWarps) sort_kernel(const SortParams 
 }
 
 // ---------------------------------------------------------------- rows moved
-// V elements at a time: 8 where everything is 16-byte aligned, else 1.
+__device__ __forceinline__ uint32_t two_bf16(float a, float b)
+{
+    return f32_to_bf16(a) | static_cast<uint32_t>(f32_to_bf16(b)) << 16;
+}
+
+// V elements at a time: as many of 8, 4, 2, 1 as every row's alignment allows.
 template <int V>
 struct Piece;
 
@@ -213,9 +220,31 @@ struct Piece<8> {
     }
     __device__ __forceinline__ void set(const float (&v)[8])
     {
-        auto two = [](float a, float b) { return f32_to_bf16(a) | static_cast<uint32_t>(f32_to_bf16(b)) << 16; };
-        w = make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7]));
+        w = make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]), two_bf16(v[6], v[7]));
     }
+};
+
+template <>
+struct Piece<4> {
+    uint2 w;
+    __device__ __forceinline__ void load(const uint16_t *p)
+    {
+        asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+    }
+    __device__ __forceinline__ void zero() { w = make_uint2(0, 0); }
+    __device__ __forceinline__ void store(uint16_t *p) const { __stcs(reinterpret_cast<uint2 *>(p), w); }
+    __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y); }
+    __device__ __forceinline__ void set(const float (&v)[4]) { w = make_uint2(two_bf16(v[0], v[1]), two_bf16(v[2], v[3])); }
+};
+
+template <>
+struct Piece<2> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const uint16_t *p) { asm volatile("ld.global.u32 %0, [%1];" : "=r"(w) : "l"(p)); }
+    __device__ __forceinline__ void zero() { w = 0; }
+    __device__ __forceinline__ void store(uint16_t *p) const { __stcs(reinterpret_cast<uint32_t *>(p), w); }
+    __device__ __forceinline__ void get(float (&v)[2]) const { v[0] = bf16lo(w), v[1] = bf16hi(w); }
+    __device__ __forceinline__ void set(const float (&v)[2]) { w = two_bf16(v[0], v[1]); }
 };
 
 template <>
@@ -342,7 +371,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const MoveP
 // A CTA takes a token.
 constexpr int kGradThreads = 256;
 
-template <int V>
+template <int V, int PC>
 __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const MoveParams p)
 {
     __shared__ float sums[kBatch][kGradThreads / 32];
@@ -360,28 +389,39 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const MovePa
             w[j] = at[j] >= 0 ? __ldcg(p.weight + t * p.k + j0 + j) : 0.0f;
             dot[j] = 0.0f;
         }
-        for (int n = threadIdx.x * V; n < p.N; n += kGradThreads * V) {
-            Piece<V> g, y[kBatch];
-            g.load(p.res + t * p.N + n);
+        for (int n0 = threadIdx.x * V; n0 < p.N; n0 += kGradThreads * V * PC) {
+            Piece<V> g[PC], y[kBatch][PC];
+#pragma unroll
+            for (int i = 0; i < PC; ++i)
+                if (n0 + i * kGradThreads * V < p.N)
+                    g[i].load(p.res + t * p.N + n0 + i * kGradThreads * V);
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
-                if (at[j] >= 0)
-                    y[j].load(p.x + at[j] * p.ldx + n);
-            float gv[V];
-            g.get(gv);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                if (at[j] >= 0) {
-                    float v[V], d[V];
-                    y[j].get(v);
+                for (int i = 0; i < PC; ++i)
+                    if (at[j] >= 0 && n0 + i * kGradThreads * V < p.N)
+                        y[j][i].load(p.x + at[j] * p.ldx + n0 + i * kGradThreads * V);
 #pragma unroll
-                    for (int c = 0; c < V; ++c) {
-                        dot[j] = fmaf(gv[c], v[c], dot[j]);
-                        d[c] = w[j] * gv[c];
+            for (int i = 0; i < PC; ++i) {
+                const int n = n0 + i * kGradThreads * V;
+                if (n >= p.N)
+                    continue;
+                float gv[V];
+                g[i].get(gv);
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    if (at[j] >= 0) {
+                        float v[V], d[V];
+                        y[j][i].get(v);
+#pragma unroll
+                        for (int c = 0; c < V; ++c) {
+                            dot[j] = fmaf(gv[c], v[c], dot[j]);
+                            d[c] = w[j] * gv[c];
+                        }
+                        Piece<V> o;
+                        o.set(d);
+                        o.store(p.out + static_cast<size_t>(at[j]) * p.N + n);
                     }
-                    Piece<V> o;
-                    o.set(d);
-                    o.store(p.out + static_cast<size_t>(at[j]) * p.N + n);
                 }
             }
         }
@@ -465,6 +505,15 @@ cudaError_t launch_combine_rows(MoveParams &p, cudaStream_t s)
     return launch(combine_kernel<V, PC>, (p.units + kCombineWarps - 1) / kCombineWarps, 32 * kCombineWarps, 0, 1, s, p);
 }
 
+// Elements that every row allows to be moved together.
+int width(const MoveParams &p)
+{
+    for (int v = 8; v > 1; v /= 2)
+        if (p.N % v == 0 && p.ldx % v == 0 && aligned(p.x, 2 * v) && aligned(p.res, 2 * v) && aligned(p.out, 2 * v))
+            return v;
+    return 1;
+}
+
 } // namespace
 } // namespace skg
 
@@ -532,8 +581,9 @@ skg_status skg_experts_gather(int R, int T, int N, const void *x, size_t ldx, co
     p.x_rows = T;
     p.N = N;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool wide = N % 8 == 0 && ldx % 8 == 0 && aligned(x, 16) && aligned(out, 16);
-    return launched(wide ? launch_gather<8>(p, s) : launch_gather<1>(p, s), who);
+    const int v = width(p);
+    return launched(v == 8 ? launch_gather<8>(p, s) : v == 4 ? launch_gather<4>(p, s) : v == 2 ? launch_gather<2>(p, s)
+                                                                                               : launch_gather<1>(p, s), who);
 }
 
 skg_status skg_experts_combine(int T, int k, int R, int N, const void *y, size_t ldy, const int *pos, const float *weight,
@@ -563,8 +613,11 @@ skg_status skg_experts_combine(int T, int k, int R, int N, const void *y, size_t
     p.N = N;
     p.k = k;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool wide = N % 8 == 0 && ldy % 8 == 0 && aligned(y, 16) && aligned(residual, 16) && aligned(out, 16);
-    return launched(wide ? launch_combine_rows<8, 1>(p, s) : launch_combine_rows<1, 4>(p, s), who);
+    const int v = width(p);
+    return launched(v == 8   ? launch_combine_rows<8, 1>(p, s)
+                    : v == 4 ? launch_combine_rows<4, 2>(p, s)
+                    : v == 2 ? launch_combine_rows<2, 4>(p, s)
+                             : launch_combine_rows<1, 4>(p, s), who);
 }
 
 skg_status skg_experts_combine_grad(int T, int k, int R, int N, const void *grad_out, const void *y, size_t ldy,
@@ -596,9 +649,11 @@ skg_status skg_experts_combine_grad(int T, int k, int R, int N, const void *grad
     p.N = N;
     p.k = k;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool wide = N % 8 == 0 && ldy % 8 == 0 && aligned(y, 16) && aligned(grad_out, 16) && aligned(grad_y, 16);
-    return launched(wide ? launch(combine_grad_kernel<8>, T, kGradThreads, 0, 1, s, p)
-                         : launch(combine_grad_kernel<1>, T, kGradThreads, 0, 1, s, p), who);
+    const int v = width(p);
+    return launched(v == 8   ? launch(combine_grad_kernel<8, 1>, T, kGradThreads, 0, 1, s, p)
+                    : v == 4 ? launch(combine_grad_kernel<4, 1>, T, kGradThreads, 0, 1, s, p)
+                    : v == 2 ? launch(combine_grad_kernel<2, 2>, T, kGradThreads, 0, 1, s, p)
+                             : launch(combine_grad_kernel<1, 2>, T, kGradThreads, 0, 1, s, p), who);
 }
 
 } // extern "C"

@@ -5,16 +5,17 @@
 //
 // v, the quotient and the product are fp32, and the product is rounded once, half
 // to even.  A block is read once: its values stay in registers through the
-// maximum.  16 lanes take a block of a row, 8 values a lane; a CTA takes a block of a
-// weight.  Rows that are not 16-byte aligned are read in 16-byte blocks shifted into
-// place, and their numbers stored in aligned words that two lanes fill.
+// maximum.  8 lanes take a block of a row, 16 values a lane; a CTA takes a block of a
+// weight.  Rows that are not aligned are read in 16-byte blocks shifted into place, and
+// their numbers stored in aligned words that two lanes fill.
 //
-// What bounds it is HBM where rows are aligned: 8192 x 7168 30.5 us (5.8 TB/s of 6.71),
-// weight 12288 x 7168 48 us (5.5); gated by silu it is nearly instructions (78% of
-// the issue slots): 4096 x 16384 61 us (5.5 TB/s).  Instructions elsewhere: 8191 x
-// 7169 76 us, weight 5001 x 4113 29 us (89 and 40 with single elements loaded and
-// stored), rows of 4096 tokens taken 8 times each 106 us; 512 rows of 7168 4.1 us.
-// With 2 or 4 blocks a warp instead of 8, 8192 x 7168 took 44 and 35 us.
+// What bounds it is HBM where rows are aligned: 8192 x 7168 29 us (6.1 TB/s of 6.71),
+// 65536 x 256 8.1, weight 12288 x 7168 42 us (6.3); gated by silu nearly instructions:
+// 4096 x 16384 60 us (5.6 TB/s).  Instructions elsewhere: 8191 x 7169 56 us, gated 4095 x
+// 16383 104, weight 5001 x 4113 22.5 us, rows of 4096 tokens taken 8 times each 92 us;
+// 512 rows of 7168 take 3.6 us.  (With 16 lanes a block, 8 values a lane, each of which
+// works out its block's scale: 30.5, 12, 48; 61; 76, 144, 29, 106.  With single elements
+// loaded and stored where rows are not aligned: 89, 176, 40.)
 #include <algorithm>
 
 #include "skg_f8_internal.h"
@@ -59,8 +60,6 @@ struct Values {
     float v[N];
 };
 
-using Eight = Values<8>;
-
 // max|v| as bits, larger than infinity's where a value is NaN.
 template <int N>
 __device__ __forceinline__ uint32_t max_bits(const Values<N> &e)
@@ -85,11 +84,25 @@ __device__ __forceinline__ void scale_values(Values<N> &e, const BlockScale &b)
         e.v[i] *= b.factor;
 }
 
-__device__ __forceinline__ uint2 to_e4m3(Eight e, const BlockScale &b)
+// 16 values as numbers, 8 to a word.
+struct Numbers {
+    uint32_t u[4];
+
+    __device__ __forceinline__ unsigned long long eight(int h) const { return u[2 * h] | static_cast<unsigned long long>(u[2 * h + 1]) << 32; }
+};
+
+__device__ __forceinline__ Numbers to_e4m3(Values<16> e, const BlockScale &b)
 {
     scale_values(e, b);
-    return make_uint2(two_e4m3(e.v[0], e.v[1]) | two_e4m3(e.v[2], e.v[3]) << 16,
-                      two_e4m3(e.v[4], e.v[5]) | two_e4m3(e.v[6], e.v[7]) << 16);
+    Numbers n;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = two_e4m3(e.v[8 * i], e.v[8 * i + 1]) | two_e4m3(e.v[8 * i + 2], e.v[8 * i + 3]) << 16;
+        const uint32_t hi = two_e4m3(e.v[8 * i + 4], e.v[8 * i + 5]) | two_e4m3(e.v[8 * i + 6], e.v[8 * i + 7]) << 16;
+        n.u[2 * i] = lo;
+        n.u[2 * i + 1] = hi;
+    }
+    return n;
 }
 
 // silu(g) x.
@@ -111,47 +124,66 @@ __device__ __forceinline__ Values<N> gated(const Values<N> &g, const Values<N> &
     return v;
 }
 
-// Eight numbers at element e of a row of K.  ANY: of any alignment; L neighbouring
-// lanes have neighbouring eights (all of them call), and a lane stores the aligned 8
-// bytes that its eight begins in: the end of the lane's before and the beginning of its
+// 16 numbers at element e of a row of K.  ANY: of any alignment; L neighbouring lanes
+// have neighbouring sixteens (all of them call), and a lane stores the two aligned
+// words that its eights begin in: the end of what comes before and the beginning of its
 // own.
 template <bool ANY, int L>
-__device__ __forceinline__ void store8(uint8_t *row, int e, int K, const uint2 &w)
+__device__ __forceinline__ void store16(uint8_t *row, int e, int K, const Numbers &n)
 {
     if constexpr (!ANY) {
-        if (e < K)
-            *reinterpret_cast<uint2 *>(row + e) = w;
+        if (e < K)                       // K is a multiple of 16
+            *reinterpret_cast<uint4 *>(row + e) = make_uint4(n.u[0], n.u[1], n.u[2], n.u[3]);
     } else {
         const int lane = static_cast<int>(threadIdx.x) & (L - 1);
         const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row) + e) & 7;
-        const unsigned long long own = w.x | static_cast<unsigned long long>(w.y) << 32;
-        const unsigned long long before = __shfl_up_sync(0xFFFFFFFFu, own, 1, L);
-        const unsigned long long both = s ? own << (8 * s) | before >> (64 - 8 * s) : own;
-        if ((lane > 0 || s == 0) && e - s + 8 <= K) {
-            *reinterpret_cast<unsigned long long *>(row + (e - s)) = both;
-        } else {
+        unsigned long long before = __shfl_up_sync(0xFFFFFFFFu, n.eight(1), 1, L);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if ((lane > 0 || i >= s) && e - s + i < K)
-                    row[e - s + i] = static_cast<uint8_t>(both >> (8 * i));
+        for (int h = 0; h < 2; ++h, e += 8) {
+            const unsigned long long both = s ? n.eight(h) << (8 * s) | before >> (64 - 8 * s) : n.eight(h);
+            const bool first = lane == 0 && h == 0;          // what comes before is not this warp's
+            if ((!first || s == 0) && e - s + 8 <= K) {
+                *reinterpret_cast<unsigned long long *>(row + (e - s)) = both;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if ((!first || i >= s) && e - s + i < K)
+                        row[e - s + i] = static_cast<uint8_t>(both >> (8 * i));
+            }
+            before = n.eight(h);
         }
-        if (lane == L - 1) {
+        if (lane == L - 1) {             // nor what comes after: the end of the last eight
 #pragma unroll
             for (int i = 1; i < 8; ++i)
-                if (i >= 8 - s && e + i < K)
-                    row[e + i] = static_cast<uint8_t>(own >> (8 * i));
+                if (i >= 8 - s && e - 8 + i < K)
+                    row[e - 8 + i] = static_cast<uint8_t>(n.eight(1) >> (8 * i));
         }
     }
 }
 
-__device__ __forceinline__ Eight widen8(const Raw8 &r)
-{
-    Eight e;
+// 16 values of a row from element e on, zeros where it ends.
+template <bool ANY>
+struct Load16 {
+    RowLoad<ANY> a, b;
+
+    __device__ __forceinline__ void load(const uint16_t *row, int e, int K)
+    {
+        a.load(row, e, K);
+        b.load(row, e + 8, K);
+    }
+
+    __device__ __forceinline__ Values<16> get() const
+    {
+        const Raw8 x = a.get(), y = b.get();
+        Values<16> v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        e.v[2 * i] = bf16lo(r.w[i]), e.v[2 * i + 1] = bf16hi(r.w[i]);
-    return e;
-}
+        for (int i = 0; i < 4; ++i) {
+            v.v[2 * i] = bf16lo(x.w[i]), v.v[2 * i + 1] = bf16hi(x.w[i]);
+            v.v[8 + 2 * i] = bf16lo(y.w[i]), v.v[9 + 2 * i] = bf16hi(y.w[i]);
+        }
+        return v;
+    }
+};
 
 // The row of x that a row of q is of: none where its index is out of range.
 struct RowSource {
@@ -170,69 +202,79 @@ __device__ __forceinline__ RowSource row_source(const F8RowParams &p, long long 
 
 constexpr int kRowWarps = 8;
 
-// A warp takes 2 P blocks of a row, 16 lanes a block, 8 values a lane.
-template <bool ANY, bool GATE, int P>
-__global__ void __launch_bounds__(32 * kRowWarps) f8_rows_kernel(const F8RowParams p, int groups)
+// A warp takes 4 P blocks of a row, 8 lanes a block, 16 values a lane.  SHORT: rows of
+// fewer than 4 blocks, whose warps take 4 blocks of neighbouring rows.
+constexpr int kLanes = kF8Block / 16;
+constexpr int kWarpBlocks = 32 / kLanes;
+
+// (16 blocks a warp take 66 registers if they may, and 105 us instead of 92 for rows that come
+// from the L2: three CTAs an SM instead of four.)
+template <bool ANY, bool GATE, bool SHORT, int P>
+__global__ void __launch_bounds__(32 * kRowWarps, P == 4 ? 4 : 0) f8_rows_kernel(const F8RowParams p, int groups)
 {
+    constexpr int B = kWarpBlocks;
     pdl_wait();
     pdl_launch_dependents();
-    const long long unit = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    const long long warp = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const long long unit = SHORT ? warp * B + lane / kLanes : warp;
     const long long row = unit / groups;
-    if (row >= p.M)
+    // (SHORT: beyond the last row, as on a row of nothing, for the sake of the other lanes)
+    const bool beyond = row >= p.M;
+    if (!SHORT && beyond)
         return;
-    const int b0 = static_cast<int>(unit - row * groups) * 2 * P, lane = threadIdx.x & 31, half = lane >> 4;
-    const RowSource from = row_source(p, row);
-    const int e0 = (b0 + half) * kF8Block + (lane & 15) * 8;
+    const int b0 = static_cast<int>(unit - row * groups) * (SHORT ? 1 : B * P) + (SHORT ? 0 : lane / kLanes);
+    const RowSource from = beyond ? RowSource{0, false} : row_source(p, row);
+    const int e0 = b0 * kF8Block + lane % kLanes * 16;
     const int K = from.live ? p.K : 0;
-    RowLoad<ANY> a[P], c[P];
+    Load16<ANY> a[P], c[P];
 #pragma unroll
     for (int i = 0; i < P; ++i)
-        a[i].load(p.x + from.row * p.ldx, e0 + i * 2 * kF8Block, K);
+        a[i].load(p.x + from.row * p.ldx, e0 + i * B * kF8Block, K);
     if (GATE) {
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            c[i].load(p.gate + from.row * p.ldg, e0 + i * 2 * kF8Block, K);
+            c[i].load(p.gate + from.row * p.ldg, e0 + i * B * kF8Block, K);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        Eight v = widen8(a[i].get());
+        Values<16> v = a[i].get();
         if (GATE)
-            v = gated(widen8(c[i].get()), v);
+            v = gated(c[i].get(), v);
         uint32_t m = max_bits(v);
 #pragma unroll
-        for (int o = 8; o; o >>= 1)
+        for (int o = kLanes / 2; o; o >>= 1)
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         const BlockScale s = block_scale(m);
-        store8<ANY, 32>(p.q + row * p.K, e0 + i * 2 * kF8Block, p.K, to_e4m3(v, s));
-        const int b = b0 + 2 * i + half;
-        if ((lane & 15) == 0 && b < p.kb)
+        store16<ANY, SHORT ? kLanes : 32>(p.q + row * p.K, e0 + i * B * kF8Block, beyond ? 0 : p.K, to_e4m3(v, s));
+        const int b = b0 + i * B;
+        if (lane % kLanes == 0 && b < p.kb && !beyond)
             p.scale[row * p.kb + b] = s.scale;
     }
 }
 
-// A CTA takes a block of 128 x 128: 16 lanes a row, 16 rows at a time.
+// A CTA takes a block of 128 x 128: 8 lanes a row, 32 rows at a time.
 template <bool ANY>
-__global__ void __launch_bounds__(256, 2) f8_weights_kernel(const F8WeightParams p)
+__global__ void __launch_bounds__(256, 3) f8_weights_kernel(const F8WeightParams p)
 {
+    constexpr int ROWS = 256 / kLanes, P = kF8Block / ROWS;
     __shared__ uint32_t maxima[8];
     pdl_wait();
     pdl_launch_dependents();
     const long long block = blockIdx.x, en = block / p.kb;
     const int b = static_cast<int>(block - en * p.kb), e = static_cast<int>(en / p.nb), nb = static_cast<int>(en - static_cast<long long>(e) * p.nb);
-    const int t = threadIdx.x, k = (t & 15) * 8;
-    RowLoad<ANY> a[8];
+    const int t = threadIdx.x;
+    Load16<ANY> a[P];
     uint32_t m = 0;
-    const int e0 = b * kF8Block + k;
-    auto at = [&](int i) {
-        return (static_cast<size_t>(e) * p.N + nb * kF8Block + (t >> 4) + 16 * i) * p.K;
-    };
-    auto inside = [&](int i) { return static_cast<long long>(nb) * kF8Block + (t >> 4) + 16 * i < p.N; };
+    const int e0 = b * kF8Block + t % kLanes * 16;
+    auto at = [&](int i) { return (static_cast<size_t>(e) * p.N + nb * kF8Block + t / kLanes + ROWS * i) * p.K; };
+    auto inside = [&](int i) { return static_cast<long long>(nb) * kF8Block + t / kLanes + ROWS * i < p.N; };
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < P; ++i)
         a[i].load(p.W + at(i), e0, inside(i) ? p.K : 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = max(m, max_bits(widen8(a[i].get())));
+    for (int i = 0; i < P; ++i)
+        m = max(m, max_bits(a[i].get()));
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if ((t & 31) == 0)
         maxima[t >> 5] = m;
@@ -242,8 +284,8 @@ __global__ void __launch_bounds__(256, 2) f8_weights_kernel(const F8WeightParams
         m = max(m, maxima[i]);
     const BlockScale s = block_scale(m);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        store8<ANY, 16>(p.q + at(i), e0, inside(i) ? p.K : 0, to_e4m3(widen8(a[i].get()), s));
+    for (int i = 0; i < P; ++i)
+        store16<ANY, kLanes>(p.q + at(i), e0, inside(i) ? p.K : 0, to_e4m3(a[i].get(), s));
     if (t == 0)
         p.scale[block] = s.scale;
 }
@@ -267,26 +309,41 @@ cudaError_t launch(void (*kernel)(P, A...), long long grid, unsigned threads, cu
 
 bool multiple(const void *ptr, size_t bytes) { return reinterpret_cast<uintptr_t>(ptr) % bytes == 0; }
 
+// Blocks a warp: 4, or for many blocks 8 or 16, for bytes in flight, if rows leave few
+// of them over.  Measured with 4, 8, 16: 8192 x 7168 39, 29.5, 28.7 us, gated 4096 x
+// 16384 68, 61, 62; of any alignment 8191 x 7169 -, 56, 71, gated 4095 x 16383 104,
+// 121, 233.
 template <bool ANY, bool GATE>
 cudaError_t launch_rows(const F8RowParams &p, cudaStream_t s)
 {
-    auto run = [&](auto kernel, int blocks) {
-        const int groups = (p.kb + blocks - 1) / blocks;
-        return launch(kernel, (static_cast<long long>(p.M) * groups + kRowWarps - 1) / kRowWarps, 32 * kRowWarps, s, p, groups);
+    auto run = [&](auto kernel, int groups, long long warps) {
+        return launch(kernel, (warps + kRowWarps - 1) / kRowWarps, 32 * kRowWarps, s, p, groups);
     };
-    // Many blocks of long rows: more of them a warp, for bytes in flight.
-    const bool many = p.kb >= 8 && static_cast<long long>(p.M) * p.kb >= 8 * 16 * 152;
-    if (!many)
-        return run(f8_rows_kernel<ANY, GATE, 1>, 2);
-    return run(f8_rows_kernel<ANY, GATE, 4>, 8);
+    if (p.kb < kWarpBlocks) {
+        const long long warps = (static_cast<long long>(p.M) * p.kb + kWarpBlocks - 1) / kWarpBlocks;
+        return run(f8_rows_kernel<ANY, GATE, true, 1>, p.kb, warps);
+    }
+    auto groups = [&](int P) { return (p.kb + kWarpBlocks * P - 1) / (kWarpBlocks * P); };
+    auto fits = [&](int P) {
+        return static_cast<long long>(p.M) * p.kb >= 8 * 16 * 152 && groups(P) * kWarpBlocks * P <= p.kb + p.kb / 6;
+    };
+    if constexpr (!ANY && !GATE) {
+        if (fits(4))
+            return run(f8_rows_kernel<ANY, GATE, false, 4>, groups(4), static_cast<long long>(p.M) * groups(4));
+    }
+    if constexpr (!ANY || !GATE) {
+        if (fits(2))
+            return run(f8_rows_kernel<ANY, GATE, false, 2>, groups(2), static_cast<long long>(p.M) * groups(2));
+    }
+    return run(f8_rows_kernel<ANY, GATE, false, 1>, groups(1), static_cast<long long>(p.M) * groups(1));
 }
 
 } // namespace
 
 cudaError_t launch_f8_quantize(const F8RowParams &p, cudaStream_t s)
 {
-    const bool aligned = p.K % 8 == 0 && p.ldx % 8 == 0 && (!p.gate || p.ldg % 8 == 0) && multiple(p.x, 16) &&
-                         multiple(p.gate, 16) && multiple(p.q, 8);           // null is aligned
+    const bool aligned = p.K % 16 == 0 && p.ldx % 8 == 0 && (!p.gate || p.ldg % 8 == 0) && multiple(p.x, 16) &&
+                         multiple(p.gate, 16) && multiple(p.q, 16);           // null is aligned
     if (p.gate)
         return aligned ? launch_rows<false, true>(p, s) : launch_rows<true, true>(p, s);
     return aligned ? launch_rows<false, false>(p, s) : launch_rows<true, false>(p, s);
@@ -294,7 +351,7 @@ cudaError_t launch_f8_quantize(const F8RowParams &p, cudaStream_t s)
 
 cudaError_t launch_f8_quantize_weights(const F8WeightParams &p, cudaStream_t s)
 {
-    const bool aligned = p.K % 8 == 0 && multiple(p.W, 16) && multiple(p.q, 8);
+    const bool aligned = p.K % 16 == 0 && multiple(p.W, 16) && multiple(p.q, 16);
     const long long grid = static_cast<long long>(p.E) * p.nb * p.kb;
     return aligned ? launch(f8_weights_kernel<false>, grid, 256, s, p) : launch(f8_weights_kernel<true>, grid, 256, s, p);
 }

@@ -80,7 +80,7 @@ def test_sort_of_no_tokens():
     assert bool((offsets == 0).all())
 
 
-SIZES = [1, 7, 8, 256, 1000, 1001, 4104]
+SIZES = [1, 2, 4, 7, 8, 256, 1000, 1001, 1002, 1004, 4104]
 
 
 @pytest.mark.parametrize("N", SIZES)
@@ -96,7 +96,7 @@ def test_gather(T, R, N):
     assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("N,ld,off", [(64, 72, 0), (64, 65, 1), (100, 300, 3), (256, 264, 8)])
+@pytest.mark.parametrize("N,ld,off", [(64, 72, 0), (64, 65, 1), (64, 66, 2), (64, 68, 4), (100, 300, 3), (256, 264, 8), (256, 264, 4)])
 def test_strided_rows(N, ld, off):
     g = gen(4, N, ld)
     T, k = 12, 3

@@ -47,8 +47,9 @@ def rows_out(M, K):
 
 
 # ------------------------------------------------------------------------------------------------ quantiser
-@pytest.mark.parametrize("M", [1, 5, 300])
-@pytest.mark.parametrize("K", [1, 7, 8, 127, 128, 129, 136, 1000, 1024, 1032, 4112, 5001, 7168])
+@pytest.mark.parametrize("M", [1, 5, 300, 3001])
+@pytest.mark.parametrize("K", [1, 7, 8, 127, 128, 129, 136, 144, 256, 300, 384, 400, 1000, 1024, 1032, 1040, 2048, 4112, 5001,
+                               7168])
 def test_quantise_rows(M, K):
     g = gen(1, M, K)
     x = normal(g, M, K, std=1.5)
@@ -68,7 +69,7 @@ def test_quantise_strides_and_offsets(K, ld, off):
     R.check_quantised(x.contiguous(), q, s)
 
 
-@pytest.mark.parametrize("M,K", [(3, 5), (17, 640), (64, 1003), (300, 4096)])
+@pytest.mark.parametrize("M,K", [(3, 5), (17, 640), (64, 1003), (300, 4096), (1000, 208), (2001, 2064), (1500, 2051), (9, 48)])
 def test_quantise_gated_halves_of_one_tensor(M, K):
     g = gen(3, M, K)
     both = normal(g, M, 2 * K, std=2.0)
