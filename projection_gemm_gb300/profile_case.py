@@ -5,12 +5,15 @@ usage: python -m projection_gemm_gb300.profile_case M N K [epilogue] [launches]
                                                     [--kind gemv|tc] [--split S] [--stages D] [--burst B]
        python -m projection_gemm_gb300.profile_case M --chain-group [--independent] [launches]
        python -m projection_gemm_gb300.profile_case --q8 linear M N K [epilogue] | norm M K | quant M K | gate M K
+       python -m projection_gemm_gb300.profile_case --f8 linear M N K [experts] | quant M K | gate M K | weight N K
+                                                         | tokens T k experts N
 The operands are the seeded synthetic tensors of `inputs.py` (seed 11); the
 default plan is used unless --kind (skg_plan_force_kernel) or --split /
 --stages / --burst (skg_plan_force) force a configuration.  --chain-group runs the five decode-layer chain
 projections at M as one group launch (skg_group, each projection ordered
 after the previous one, or with --independent in no order) instead.  --q8
-runs one operator of the 8-bit path three times on normal rows.  The
+runs one operator of the 8-bit path three times on normal rows, --f8 one of the
+8-bit floating point path or (tokens) the experts' four on random choices.  The
 process exits non-zero on any library error.
 """
 import argparse
@@ -78,7 +81,73 @@ def q8(op, *sizes):
     print("ok")
 
 
+def f8(op, *sizes):
+    g = torch.Generator(device="cuda").manual_seed(11)
+    sizes = [int(v) for v in sizes]
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16)
+
+    def empty(*shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device="cuda")
+
+    def blocks(n):
+        return -(-n // skg.F8_BLOCK)
+
+    def rows(x, gate=None):
+        q, s = empty(*x.shape, dtype=torch.float8_e4m3fn), empty(x.shape[0], blocks(x.shape[1]))
+        skg.skg_quantize_f8(x, gate, q, s)
+        return q, s
+
+    def weights(W):
+        q, s = empty(*W.shape, dtype=torch.float8_e4m3fn), empty(*W.shape[:-2], blocks(W.shape[-2]), blocks(W.shape[-1]))
+        skg.skg_quantize_f8_weights(W, q, s)
+        return q, s
+
+    if op == "linear":
+        (M, N, K), E = sizes[:3], sizes[3] if len(sizes) > 3 else 0
+        (x, xs), (W, ws) = rows(normal(M, K)), weights(normal(*((E,) if E else ()), N, K))
+        offsets = None
+        if E:                            # each row's expert at random
+            chosen = torch.randint(E, (M,), generator=g, device="cuda")
+            offsets = torch.nn.functional.pad(torch.bincount(chosen, minlength=E).cumsum(0), (1, 0)).int()
+        y = empty(M, N, dtype=torch.bfloat16)
+        plan = skg.F8Plan(M, N, K, "bf16", experts=E)
+        print(plan.info())
+        for _ in range(3):
+            plan.run(x, xs, W, ws, None, y, offsets=offsets)
+        plan.check()
+        plan.close()
+    elif op == "tokens":
+        T, k, E, N = sizes
+        expert = torch.topk(torch.randn(T, E, generator=g, device="cuda"), k, dim=1).indices.int()
+        weight, grad_weight = torch.rand(T, k, generator=g, device="cuda"), empty(T, k)
+        x, y, out = normal(T, N), normal(T * k, N), empty(T, N, dtype=torch.bfloat16)
+        offsets, at, pos = (empty(*n, dtype=torch.int32) for n in ((E + 1,), (T * k,), (T, k)))
+        for _ in range(3):
+            skg.skg_experts_sort(expert, offsets, at, pos)
+            skg.skg_experts_gather(x, at, y)
+            skg.skg_experts_combine(y, pos, weight, x, out)
+            skg.skg_experts_combine_grad(out, y, pos, weight, y, grad_weight)
+    else:
+        x = normal(*sizes)
+        gate = normal(*sizes) if op == "gate" else None
+        for _ in range(3):
+            if op == "weight":
+                weights(x)
+            else:
+                rows(x, gate)
+    torch.cuda.synchronize()
+    print("ok")
+
+
 def main(argv):
+    if argv and argv[0] == "--f8":
+        build.build()
+        skg.load()
+        torch.cuda.set_device(0)
+        f8(*argv[1:])
+        return
     if argv and argv[0] == "--q8":
         build.build()
         skg.load()
