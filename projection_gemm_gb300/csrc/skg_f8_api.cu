@@ -87,38 +87,46 @@ long long slots_of(int kind, int m_tile, int split, int num_sms)
 // its epilogue, a tile's end, and a launch's ends.
 //
 //                     unit: one CTA an SM, two   tile   ends   with K split
-//   SPLIT 16 tokens         0.27  0.40           0.6    2.8    4.9
-//         32                0.30  0.46           0.8    2.8    4.9
-//         64                0.43  0.85           1.2    2.8    4.9
-//   WIDE 128                0.33  -              1.0    3.0    6.8
+//   SPLIT 16 tokens         0.27  0.36           0.6    2.8    4.9
+//         32                0.30  0.38           1.2    2.8    4.9
+//         64                0.31  0.60           1.2    2.8    4.9
+//   WIDE 128                0.33  -              1.0    2.5    6.3
 //        256 (pairs)        0.39  -              2.0    4.0    7.8
 //
-// A tile of the wide kernel takes 2 more where rows of the output are not aligned.
-// The weights come from HBM at 6.3 TB/s at the most.  Where that is what bounds the
-// split kernel, its ends with K split are 8.3 less 0.0225 a CTA: few CTAs take longer until
-// enough of the weights is on its way.  With experts, clusters start 1.3 later.
+// A unit takes a quarter more where rows of x and W begin between lines of 128 bytes,
+// a tile of the wide kernel 2 more where rows of the output are not aligned.  The
+// weights come from HBM at 6.3 TB/s at the most, by the wide kernel at 5.6.  Where that
+// is about what bounds the split kernel, its ends with K split are 8.3 less 0.0225 a
+// CTA: few CTAs take longer until enough of the weights is on its way.  Clusters of 3,
+// 5, 6 or 7 take 0.4 longer, and with experts all start 1.3 later.  (Of 123 shapes of
+// 1 to 5952 rows, with and without experts, the launch chosen is within 8% of the
+// fastest for 114 and within 16% for all.)
 double launch_us(const skg_f8_plan_desc &d, int kind, int m_tile, int split, int num_sms)
 {
-    const double sms = num_sms, m_tiles = token_tiles(d, m_tile, false), tiles = m_tiles * ceil_div(d.N, n_tile_of(kind, m_tile));
+    const double sms = num_sms, tiles = token_tiles(d, m_tile, false) * ceil_div(d.N, n_tile_of(kind, m_tile));
     const int units = ceil_div(ceil_div(d.K, kF8Block), split);
     const double slots = static_cast<double>(slots_of(kind, m_tile, split, num_sms));
     const double at_once = std::min(tiles, slots) * split;            // CTAs, or pairs of them
     double waves = std::ceil(tiles / slots);
-    if (split == 1 && waves > 2.0)
-        waves = tiles / slots + 0.5;     // persistent: not all end together
-    const double hbm = taken(d) * d.N * d.K / 6.3e6;
+    if (split == 1 && (d.experts ? tiles > 0.8 * slots : waves > 2.0))
+        waves = tiles / slots + 0.5;     // persistent, not all end together; or not known exactly
+    const double hbm = taken(d) * d.N * d.K / (kind == SKG_F8_KERNEL_WIDE ? 5.6e6 : 6.3e6);
     double unit, tile, ends;
     if (kind == SKG_F8_KERNEL_WIDE) {
         unit = m_tile == 128 ? 0.33 : 0.39;
         tile = (m_tile == 128 ? 1.0 : 2.0) + (d.N % 8 != 0 ? 2.0 : 0.0);
-        ends = (m_tile == 128 ? 3.0 : 4.0) + (split > 1 ? 3.8 : 0.0);
+        ends = (m_tile == 128 ? 2.5 : 4.0) + (split > 1 ? 3.8 : 0.0);
     } else {
         const bool two = at_once > sms;
-        unit = m_tile == 16 ? (two ? 0.40 : 0.27) : m_tile == 32 ? (two ? 0.46 : 0.30) : (two ? 0.85 : 0.43);
-        tile = m_tile == 16 ? 0.6 : m_tile == 32 ? 0.8 : 1.2;
-        ends = split == 1 ? 2.8 : waves * (unit * units + tile) > hbm ? 4.9 : std::max(2.0, 8.3 - 0.0225 * at_once * 152.0 / sms);
+        unit = m_tile == 16 ? (two ? 0.36 : 0.27) : m_tile == 32 ? (two ? 0.38 : 0.30) : (two ? 0.60 : 0.31);
+        tile = m_tile == 16 ? 0.6 : 1.2;
+        ends = split == 1 ? 2.8 : 4.9;
     }
-    return std::max(hbm, waves * (unit * units + tile)) + ends + (d.experts && split > 1 ? 1.3 : 0.0);
+    const double own = waves * (unit * (d.K % kF8Block ? 1.25 : 1.0) * units + tile);
+    if (kind == SKG_F8_KERNEL_SPLIT && split > 1 && own < 1.3 * hbm && hbm > 4.0)
+        ends = std::max(2.0, 8.3 - 0.0225 * at_once * 152.0 / sms);
+    ends += ((split & (split - 1)) != 0 ? 0.4 : 0.0) + (d.experts && split > 1 ? 1.3 : 0.0);
+    return std::pow(std::pow(hbm, 4) + std::pow(own, 4), 0.25) + ends;       // the larger, or a little more where they are close
 }
 
 // The launch that takes the least time, given a kernel, a tile and the CTAs that

@@ -247,14 +247,25 @@ __device__ __forceinline__ void f8_join(const F8LinearParams &p, uint32_t smem, 
                 }
             }
         } else {
+            float s[4] = {};
+#pragma unroll
+            for (int r = 0; r < MAX_SPLIT; ++r) {
+                if (r < p.split) {
+                    float v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = ld_shared_cluster_f32(map_shared_rank(smem + f8_sum_at(channels, m - m0, b * kF8Block + lane + 32 * k),
+                                                                     first + r * rank_step));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        s[k] += v[k];
+                }
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int c = b * kF8Block + lane + 32 * k, n = first_n + lane + 32 * k;
-                float s = 0.0f;
-                for (int r = 0; r < p.split; ++r)
-                    s += ld_shared_cluster_f32(map_shared_rank(smem + f8_sum_at(channels, m - m0, c), first + r * rank_step));
+                const int n = first_n + lane + 32 * k;
                 if (n >= least && n < p.N)
-                    f8_store(p, m, n, s);
+                    f8_store(p, m, n, s[k]);
             }
         }
     }
