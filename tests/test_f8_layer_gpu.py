@@ -342,3 +342,89 @@ def test_experts_whose_weights_are_more_than_32_bits():
     for e in (0, 150, 298, 299):
         s = slice(at[e], at[e + 1])
         R.check_linear(x[s], xs[s], W[e], ws[e], None, y[s])
+
+
+# --------------------------------------------------------------------------------- ends of the sizes
+@pytest.mark.parametrize("launch", [None, (1, 16, 8), (1, 64, 1), (2, 128, 4), (2, 256, 1)])
+def test_longest_k(launch):
+    M, N, K = 3, 130, 131072
+    g = torch.Generator().manual_seed(12)
+    x = (torch.randn(M, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    W = (torch.randn(N, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    xs, ws = torch.rand(M, K // 128, generator=g).cuda(), torch.rand(2, K // 128, generator=g).cuda()
+    y = torch.empty(M, N, device="cuda")
+    plan = skg.F8Plan(M, N, K, "fp32")
+    if launch:
+        plan.force(*launch)
+    plan.run(x, xs, W, ws, None, y)
+    plan.check()
+    R.check_linear(x, xs, W, ws, None, y)
+
+
+@pytest.mark.parametrize("experts", [0, 1024])
+def test_most_rows(experts):
+    M, N, K = 2 ** 20, 40, 48
+    g = torch.Generator().manual_seed(13)
+    x = (torch.randn(M, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    W = (torch.randn(max(1, experts), N, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    xs, ws = torch.rand(M, 1, generator=g).cuda(), torch.rand(max(1, experts), 1, 1, generator=g).cuda()
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    plan = skg.F8Plan(M, N, K, "bf16", experts=experts)
+    if not experts:
+        plan.run(x, xs, W[0], ws[0], None, y)
+        plan.check()
+        R.check_linear(x, xs, W[0], ws[0], None, y)
+        return
+    cuts = torch.sort(torch.randint(0, M + 1, (experts - 1,), generator=g)).values.int()
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int32), cuts, torch.full((1,), M, dtype=torch.int32)]).cuda()
+    plan.run(x, xs, W, ws, None, y, offsets=offsets)
+    plan.check()
+    at = offsets.tolist()
+    for e in range(experts):
+        s = slice(at[e], at[e + 1])
+        if s.stop > s.start:
+            R.check_linear(x[s], xs[s], W[e], ws[e], None, y[s])
+
+
+def test_most_channels():
+    """All weights but those of some channels are zeros."""
+    N, K = 2 ** 31 - 256, 16
+    at = torch.tensor([0, 127, 128, 2 ** 30 + 5, N - 257, N - 128, N - 1], device="cuda")
+    g = torch.Generator().manual_seed(14)
+    rows = (torch.randn(len(at), K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    W = torch.zeros(N, K, dtype=torch.uint8, device="cuda")
+    W[at] = rows.view(torch.uint8)
+    x = (torch.randn(1, K, generator=g) * 100).clamp(-448, 448).to(R.F8).cuda()
+    xs, ws = torch.ones(1, 1, device="cuda"), torch.ones(R.blocks(N), 1, device="cuda")
+    y = torch.full((1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    plan = skg.F8Plan(1, N, K, "bf16")
+    plan.run(x, xs, W.view(R.F8), ws, None, y)
+    plan.check()
+    R.check_linear(x, xs, rows, torch.ones(1, 1, device="cuda"), None, y[:, at])
+    assert int((y != 0).sum()) == int((y[:, at] != 0).sum())
+
+
+def test_longest_row_to_quantise():
+    K = 2 ** 30
+    x = torch.empty(1, K, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(15))
+    q, s = torch.empty(1, K, dtype=R.F8, device="cuda"), torch.empty(1, K // 128, device="cuda")
+    skg.skg_quantize_f8(x, None, q, s)
+    for a in (0, K // 2, K - 2 ** 16):
+        p = slice(a, a + 2 ** 16)
+        R.check_quantised(x[:, p], q[:, p].contiguous(), s[:, a // 128:a // 128 + 512])
+
+
+def test_sort_of_the_most_choices():
+    T, k, E = 2 ** 21, 8, 1000
+    expert = torch.randint(-1, E, (T, k), generator=torch.Generator(device="cuda").manual_seed(16), device="cuda", dtype=torch.int32)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    rows, pos = torch.empty(T * k, dtype=torch.int32, device="cuda"), torch.empty(T, k, dtype=torch.int32, device="cuda")
+    skg.skg_experts_sort(expert, offsets, rows, pos)
+    key = torch.where(expert.flatten() >= 0, expert.flatten(), E).long()
+    order = torch.sort(key, stable=True).indices
+    n = int((key < E).sum())
+    assert torch.equal(offsets[1:].long(), torch.bincount(key, minlength=E + 1)[:E].cumsum(0)) and int(offsets[0]) == 0
+    assert torch.equal(rows[:n].long(), order[:n] // k) and bool((rows[n:] == -1).all())
+    want = torch.full((T * k,), -1, dtype=torch.long, device="cuda")
+    want[order[:n]] = torch.arange(n, device="cuda")
+    assert torch.equal(pos.flatten().long(), want)
