@@ -582,6 +582,7 @@ SKG_API skg_status skg_q8_plan_destroy(skg_q8_plan_t plan);
  *            they have M, and x_rows is not read
  *   q, scale e4m3 [M, K] and fp32 [M, ceil(K / 128)], dense
  *   Any alignment the element types allow; 16-byte aligned rows are fastest.
+ *   q and scale must not overlap the inputs.
  * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
  */
 SKG_API skg_status skg_quantize_f8(int M, int K, const void *x, size_t ldx, const void *gate, size_t ldg, const int *rows,
@@ -650,9 +651,9 @@ SKG_API skg_status skg_f8_plan(int M, int N, int K, int epilogue, int experts, i
  *   y        [M,N] bf16 (fp32 for SKG_EPI_FP32); must not overlap the inputs
  * Sums of products and over blocks are fp32, a block's two scales are multiplied in
  * fp32 before they meet its sum (their product should be a normal number), the
- * residual is added in fp32, and the result is rounded once.  The order of the sum over blocks depends on the launch
- * shape: a plan gives the same bits each time, and a row's result does not depend
- * on the other rows.
+ * residual is added in fp32, and the result is rounded once.  The order of the sum
+ * over blocks depends on the launch shape: a plan gives the same bits each time,
+ * and a row's result does not depend on the other rows.
  * Allocates nothing and keeps no workspace: runs of a plan may be in flight at the
  * same time.  The plan's device must be the current one.
  * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_ALIGNMENT, SKG_ERR_DEVICE_TIMEOUT
@@ -684,7 +685,8 @@ SKG_API skg_status skg_f8_plan_destroy(skg_f8_plan_t plan);
 
 /*
  * Tokens to their experts and back.  T tokens choose k experts each; the T * k
- * choices become R = T * k rows, sorted by expert.
+ * choices become R = T * k rows, sorted by expert.  Outputs must not overlap
+ * inputs except as said.
  *
  * skg_experts_sort -- from expert int32 [T, k]:
  *   offsets  int32 [experts + 1]: expert e has the sorted rows offsets[e] to offsets[e + 1]
@@ -726,8 +728,9 @@ SKG_API skg_status skg_experts_combine(int T, int k, int R, int N, const void *y
  *   grad_weight[t,j] = <grad_out[t], y[pos[t,j]]>, fp32, 0 where a choice was left out
  *   grad_out bf16 [T, N] dense; the others as for skg_experts_combine.  (The
  *   residual's gradient is grad_out itself.)  grad_y may be y where ldy = N
- * A sorted row belongs to one choice: where pos has the same row twice, grad_y has
- * one of the two.
+ * A sorted row belongs to one choice: where pos has the same row twice, each element
+ * of grad_y is of one of the two (and where grad_y is y, their grad_weight may be of
+ * a row that has been written already).
  * Errors: SKG_ERR_INVALID_ARG, SKG_ERR_UNSUPPORTED, SKG_ERR_ALIGNMENT, SKG_ERR_CUDA.
  */
 SKG_API skg_status skg_experts_combine_grad(int T, int k, int R, int N, const void *grad_out, const void *y, size_t ldy,

@@ -238,3 +238,40 @@ def test_the_same_call_gives_the_same_bits():
     for _ in range(3):
         again = check_combine(y, pos, w, None), *check_grad(go, y, pos, w)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("N", [1, 2, 4, 8, 1031, 2050, 5000, 7168])
+@pytest.mark.parametrize("k", [1, 8, 19])
+def test_combine_grad_in_place_of_y(N, k):
+    g = gen(10, N, k)
+    T = 37
+    pos = torch.randperm(T * k, generator=g).int().view(T, k)
+    pos[torch.rand(T, k, generator=g) < 0.2] = -1
+    pos = pos.cuda()
+    y, go, w = normal(g, T * k, N), normal(g, T, N), torch.randn(T, k, generator=g).cuda()
+    want_y, want_w = check_grad(go, y, pos, w)
+    nobody = torch.ones(T * k, dtype=torch.bool, device="cuda")
+    nobody[pos[pos >= 0].long()] = False
+    want_y[nobody] = y[nobody]
+    both, grad_weight = y.clone(), torch.empty_like(w)
+    skg.skg_experts_combine_grad(go, both, pos, w, both, grad_weight)
+    assert torch.equal(both, want_y) and torch.equal(grad_weight, want_w)
+
+
+@pytest.mark.parametrize("N", [1, 6, 1031, 7168])
+def test_a_row_of_several_choices(N):
+    """Combined as often as it is chosen; each element of its gradient is of one of those choices."""
+    g = gen(11, N)
+    T, k, rows = 50, 11, 9
+    pos = torch.randint(0, rows, (T, k), generator=g, dtype=torch.int32).cuda()
+    y, go, w = normal(g, rows, N), normal(g, T, N), torch.randn(T, k, generator=g).cuda()
+    check_combine(y, pos, w, None)
+    grad_y, grad_weight = torch.empty_like(y), torch.empty_like(w)
+    skg.skg_experts_combine_grad(go, y, pos, w, grad_y, grad_weight)
+    v, _ = picked(y, pos)
+    gd = go.double()[:, None]
+    tol = (N / 256 + 21) * U * (v * gd).abs().sum(2)
+    assert bool(((grad_weight.double() - (v * gd).sum(2)).abs() <= tol).all())
+    each = (w[..., None] * go[:, None]).bfloat16()          # one product, rounded once more: the kernel's two operations
+    for r in range(rows):
+        assert bool((each[pos == r] == grad_y[r]).any(0).all())
