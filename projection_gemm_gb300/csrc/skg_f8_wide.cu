@@ -227,6 +227,17 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     cluster_sync();                      // the peer's barriers exist before anything is sent there
     tc_fence_after();
     constexpr uint32_t tmem_base = 0;    // all 512 columns are this CTA's
+    // Of a pair, both CTAs' copies, MMAs and epilogues arrive at these barriers (at full and
+    // aempty in the first CTA, at empty and afull by the MMA's commits to both), so a
+    // wait acquires at cluster scope: at the CTA's it would order nothing of the peer's
+    // before what follows it, such as the MMA that overwrites an accumulator that
+    // the peer has read.
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if constexpr (PAIR == 2)
+            return mbar_wait_cluster(bar, parity, p.timeout_ns, &flags[0]);
+        else
+            return mbar_wait(bar, parity, p.timeout_ns, &flags[0]);
+    };
     if (warp != Sh::kTmaWarp)            // the bounded waits do not count the previous kernel's time
         pdl_wait();
 
@@ -266,7 +277,7 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 for (int kb = 0; kb < units; ++kb, ++j) {
                     if (j < ahead)
                         continue;
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[j % S], ((j / S) & 1) ^ 1, p.timeout_ns, &flags[0]));
+                    ok = __all_sync(0xFFFFFFFFu, wait(&empty[j % S], ((j / S) & 1) ^ 1));
                     if (!ok)
                         break;
                     if (leader) {
@@ -299,8 +310,7 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 int sl = 0, phase = 0;
                 for (int j = 0; j < total; ++j) {
                     const int t = j % NA;
-                    ok = mbar_wait(&aempty[t], ((j / NA) & 1) ^ 1, p.timeout_ns, &flags[0]) &&
-                         mbar_wait(&full[sl], phase, p.timeout_ns, &flags[0]);
+                    ok = wait(&aempty[t], ((j / NA) & 1) ^ 1) && wait(&full[sl], phase);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok)
                         break;
@@ -387,7 +397,7 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     w[i] = more ? __ldcg(ws + kb + i + AHEAD) : 0.0f;
                     x[i] = more ? __ldca(xs + kb + i + AHEAD) : 0.0f;
                     const int a = j % NA;
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&afull[a], (j / NA) & 1, p.timeout_ns, &flags[0]));
+                    ok = __all_sync(0xFFFFFFFFu, wait(&afull[a], (j / NA) & 1));
                     if (!ok)
                         break;
                     tc_fence_after();
