@@ -27,9 +27,11 @@
 // which an epilogue warp needs a scale a column from shared memory, took 1024 x 7168
 // x 7168 212 us, where the wide kernel's tiles of 128 take 62.
 //
-// Every wait is bounded; on expiry a thread records the timeout in the plan's
-// error word, raises the CTA's abort flag, waits for its own copies and MMAs,
-// and the CTA goes on to the cluster's barriers, frees its TMEM and returns.
+// Every wait is bounded; on expiry a thread records the timeout in the plan's error
+// word and raises the CTA's abort flag, and the issuer waits for its MMAs.  Once
+// every role has ended the producer waits for its copies in flight, and the CTA goes on
+// to the cluster's barriers, frees its TMEM and returns.  (That the roles meet before
+// the cluster does takes 0.1 to 0.2 us.)
 #include <algorithm>
 
 #include "skg_f8_internal.h"
@@ -159,6 +161,7 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         pdl_wait();
     }
 
+    int issued = 0;                      // units whose copies this thread has issued
     if (warp == Sh::kTmaWarp) {
         // -------------------------------------------------------- TMA producer
         if (lane == 0) {
@@ -198,12 +201,7 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             }
             if (!ok)
                 f8_fail(p.err, &flags[0], kErrTimeoutProducer);
-            if (flags[0]) {              // abort: let every copy land before exit
-                volatile int never = 0;
-                j = max(j, ahead);
-                for (int k = 0; k < S && k < j; ++k)
-                    mbar_wait(&full[(j - 1 - k) % S], ((j - 1 - k) / S) & 1, kDefaultTimeoutNs, &never);
-            }
+            issued = max(j, ahead);
         }
     } else if (warp == Sh::kMmaWarp) {
         // ---------------------------------------------------------- MMA issuer
@@ -351,12 +349,17 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 
     __syncwarp();
     tc_fence_before();
+    __syncthreads();                     // from here on no role raises the abort flag any more
+    if (issued && flags[0]) {            // abort: every copy lands before sums are read in the ring's place and before exit
+        volatile int never = 0;
+        for (int u = max(0, issued - S); u < issued; ++u)
+            mbar_wait(&full[u % S], (u / S) & 1, kDefaultTimeoutNs, &never);
+    }
+    __syncwarp();
     if (p.split > 1) {
         const F8Tile t = f8_tile(p, MT, table, first);
         const int n0[1] = {f8_w_window(p, t.e, t.nt * kTileN) - t.e * p.N}, na[1] = {t.nt * kTileN};
         f8_join<kF8SplitMax, Sh::kThreads, 1>(p, smem_u32(smem), f8_x_window(p, t.m0), t.m0, min(t.m1, t.m0 + MT), n0, na, rank, 0, 1);
-    } else {
-        __syncthreads();
     }
     if (warp == Sh::kMmaWarp) {
         tc_fence_after();

@@ -289,11 +289,6 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             }
             if (!ok)
                 f8_fail(p.err, &flags[0], kErrTimeoutProducer);
-            if (flags[0]) {                  // abort: let every copy land before exit, a few microseconds after its issue
-                const uint64_t t0 = globaltimer_ns();    // (the second CTA's are counted in the first)
-                while (globaltimer_ns() - t0 < kLandNs) {
-                }
-            }
         } else if (warp == Sh::kMmaWarp) {
             // ---------------------------------------------------------- MMA issuer
             if (rank == 0) {
@@ -435,6 +430,15 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 
     __syncwarp();
     tc_fence_before();
+    __syncthreads();                     // from here on no role raises the abort flag any more
+    // Abort: every copy lands, a few microseconds after its issue, before sums are read in the
+    // ring's place and before exit.  (By time: the second CTA's copies are counted in the
+    // first, whose abort that one learns of as its accumulators stay away.)
+    if (warp == Sh::kTmaWarp && flags[0]) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kLandNs) {
+        }
+    }
     if (p.split > 1) {
         const F8Tile t = f8_tile(p, MT, table, first);
         const int ma = t.m0 + rank * 128;
@@ -447,8 +451,6 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         f8_join<kF8WideMaxSplit, Sh::kThreads, PAIR>(p, smem_u32(smem), f8_x_window(p, ma), ma, min(t.m1, ma + 128), n0, na, part, rank, PAIR);
     } else if (PAIR == 2) {
         cluster_sync();                  // no CTA leaves while its peer may still send to it
-    } else {
-        __syncthreads();
     }
     if (warp == Sh::kMmaWarp) {
         tc_fence_after();

@@ -26,6 +26,21 @@ def test_waits_of_a_pair_are_at_cluster_scope():
     assert (pair, single) == ("mbar_wait_cluster", "mbar_wait")
 
 
+@pytest.mark.parametrize("name,landed", [("skg_f8_split.cu", "mbar_wait(&full["), ("skg_f8_wide.cu", "kLandNs")])
+def test_copies_land_before_a_cta_that_aborts_goes_on(name, landed):
+    """Whoever raises the abort flag may do so long after the producer's last copy, so the flag is looked at when every
+    role has ended, before sums are read in the ring's place, before the cluster's last barrier and before exit."""
+    src = kernel_source(name)
+    src = src[:src.index("cudaError_t launch_shape")]
+    raised = src.rindex("f8_fail(")
+    met = src.index("__syncthreads();", raised)
+    looked = re.search(r"if \([^{;]*flags\[0\]\) \{", src[met:])
+    assert looked
+    looked = met + looked.start()
+    assert looked < src.index(landed, looked) < src.index("f8_join<", looked)
+    assert not re.search(r"if \([^{;]*flags\[0\]\)", src[:met])          # and not only sooner
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K,split,E", [(5000, 2100, 512, 1, 0), (700, 1032, 4112, 3, 0), (3000, 520, 1040, 1, 7),
                                            (256, 256, 4096, 4, 0)])
