@@ -568,6 +568,10 @@ SKG_API skg_status skg_q8_plan_destroy(skg_q8_plan_t plan);
  * (Divisions of indexes round down; the last block of a row or column is short
  * where 128 does not divide it.)  These are serving operators: no gradients.
  *
+ * These calls, and those of the experts' tokens below, launch on the current device,
+ * on which the stream and every pointer have to be.  (The Python binding refuses
+ * tensors of another device than the current one.)
+ *
  * Quantising a block of values v (fp32): scale = max|v| / 448, q = e4m3(v * f) with
  * f = 448 / max|v|, each operation rounded to fp32 and the product to e4m3, half
  * to even.  A block of zeros has scale 0 and q = 0.  A block with a value that is

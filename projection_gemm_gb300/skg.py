@@ -436,10 +436,18 @@ def _int(v, name) -> int:
     return v
 
 
-def _rows(t, name, shape, dtype) -> int:
+def _device(t, name, device):
+    """The tensors of a call are on one device."""
+    if t.get_device() != device:
+        _bad(f"{name} is on device {t.get_device()}, other tensors of this call on {device}")
+
+
+def _rows(t, name, shape, dtype, device=None) -> int:
     """Row stride of a tensor of `shape` [M, K] whose rows are contiguous."""
     if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
         _bad(f"{name} must be a CUDA tensor {list(shape)} of {dtype}")
+    if device is not None:
+        _device(t, name, device)
     if t.is_contiguous():
         return shape[1]
     ld, one = t.stride()
@@ -448,19 +456,23 @@ def _rows(t, name, shape, dtype) -> int:
     return ld
 
 
-def _dense(t, name, shape, dtype) -> int:
+def _dense(t, name, shape, dtype, device=None) -> int:
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         _bad(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
+    if device is not None:
+        _device(t, name, device)
     return t.data_ptr()
 
 
 def _stream_of(stream, t):
     """The given stream, or the current one of t's device (the raw handle: a
-    decode step's calls are short enough for a Stream object to show)."""
-    if stream is not None:
-        return _stream(stream)
+    decode step's calls are short enough for a Stream object to show), which has
+    to be the current device: kernels are launched there."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    device, current = t.get_device(), torch._C._cuda_getDevice()
+    if device != current:
+        _bad(f"the tensors are on device {device}, the current one is {current}")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def skg_rmsnorm_q8(x, residual, gamma, eps: float, h, q, scale, y=None, stream=None):
@@ -626,15 +638,16 @@ def skg_quantize_f8(x, gate, q, scale, rows=None, stream=None):
     M = T if rows is None else rows.numel()
     if T | K | M >= 2**31:
         _sizes(T=T, K=K, M=M)
-    ldx = _rows(x, "x", shape, bf16)
-    ldg = 0 if gate is None else _rows(gate, "gate", shape, bf16)
-    if not (q.dtype is f8 and q.shape == (M, K) and q.is_contiguous() and q.is_cuda and
-            scale.dtype is f32 and scale.shape == (M, -(-K // F8_BLOCK)) and scale.is_contiguous() and scale.is_cuda):
-        _dense(q, "q", (M, K), f8)
-        _dense(scale, "scale", (M, _blocks(K)), f32)
+    ldx, dev = _rows(x, "x", shape, bf16), x.get_device()
+    ldg = 0 if gate is None else _rows(gate, "gate", shape, bf16, dev)
+    if not (q.dtype is f8 and q.shape == (M, K) and q.is_contiguous() and q.get_device() == dev and
+            scale.dtype is f32 and scale.shape == (M, -(-K // F8_BLOCK)) and scale.is_contiguous() and
+            scale.get_device() == dev):
+        _dense(q, "q", (M, K), f8, dev)
+        _dense(scale, "scale", (M, _blocks(K)), f32, dev)
     at = None
     if rows is not None:
-        at = _dense(rows, "rows", (M,), i32)
+        at = _dense(rows, "rows", (M,), i32, dev)
     status = load().skg_quantize_f8(M, K, x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg, at, T,
                                     q.data_ptr(), scale.data_ptr(), _stream_of(stream, x))
     if status:
@@ -649,9 +662,10 @@ def skg_quantize_f8_weights(W, q, scale, stream=None):
     if len(shape) not in (2, 3):
         _bad("W must be [N, K] or [E, N, K]")
     E, N, K = (_int(v, n) for v, n in zip((1, *shape)[-3:], ("E", "N", "K")))
+    dev = W.get_device()
     _check(load().skg_quantize_f8_weights(
-        E, N, K, _dense(W, "W", shape, torch.bfloat16), _dense(q, "q", shape, torch.float8_e4m3fn),
-        _dense(scale, "scale", (*shape[:-2], _blocks(N), _blocks(K)), torch.float32), _stream_of(stream, W)))
+        E, N, K, _dense(W, "W", shape, torch.bfloat16), _dense(q, "q", shape, torch.float8_e4m3fn, dev),
+        _dense(scale, "scale", (*shape[:-2], _blocks(N), _blocks(K)), torch.float32, dev), _stream_of(stream, W)))
 
 
 def skg_f8_plan_query(M: int, N: int, K: int, epilogue, experts: int, num_sms: int) -> dict:
@@ -714,18 +728,19 @@ class F8Plan:
         # one expression, as in Q8Plan.run
         mk, mb, nk, nb, mn = self._shapes
         f8, f32, bf16, i32, out = self._types
+        dev = x.get_device()
         if not (x.dtype is f8 and x.shape == mk and x.is_contiguous() and x.is_cuda and
-                W.dtype is f8 and W.shape == nk and W.is_contiguous() and W.is_cuda and
-                x_scale.dtype is f32 and x_scale.shape == mb and x_scale.is_contiguous() and x_scale.is_cuda and
-                w_scale.dtype is f32 and w_scale.shape == nb and w_scale.is_contiguous() and w_scale.is_cuda and
-                y.dtype is out and y.shape == mn and y.is_contiguous() and y.is_cuda):
+                W.dtype is f8 and W.shape == nk and W.is_contiguous() and W.get_device() == dev and
+                x_scale.dtype is f32 and x_scale.shape == mb and x_scale.is_contiguous() and x_scale.get_device() == dev and
+                w_scale.dtype is f32 and w_scale.shape == nb and w_scale.is_contiguous() and w_scale.get_device() == dev and
+                y.dtype is out and y.shape == mn and y.is_contiguous() and y.get_device() == dev):
             for t, name, shape, dtype in ((x, "x", mk, f8), (x_scale, "x_scale", mb, f32), (W, "W", nk, f8),
                                           (w_scale, "w_scale", nb, f32), (y, "y", mn, out)):
-                _dense(t, name, shape, dtype)
+                _dense(t, name, shape, dtype, dev)
         if residual is not None:
-            _dense(residual, "residual", mn, bf16)
+            _dense(residual, "residual", mn, bf16, dev)
         if offsets is not None:
-            _dense(offsets, "offsets", (self.experts + 1,), i32)
+            _dense(offsets, "offsets", (self.experts + 1,), i32, dev)
         status = load().skg_f8_run(self.handle, x.data_ptr(), x_scale.data_ptr(), W.data_ptr(), w_scale.data_ptr(),
                                    None if residual is None else residual.data_ptr(),
                                    None if offsets is None else offsets.data_ptr(), y.data_ptr(), _stream_of(stream, x))
@@ -762,15 +777,16 @@ def skg_experts_sort(expert, offsets, rows, pos, stream=None):
         _bad("expert must be [T, k] and offsets [experts + 1]")
     T, k = shape
     E = offsets.shape[0] - 1
+    dev = expert.get_device()
     if not (T | k | T * k < 2**31 and
             expert.dtype is i32 and expert.is_contiguous() and expert.is_cuda and
-            offsets.dtype is i32 and offsets.is_contiguous() and offsets.is_cuda and
-            rows.dtype is i32 and rows.shape == (T * k,) and rows.is_contiguous() and rows.is_cuda and
-            pos.dtype is i32 and pos.shape == shape and pos.is_contiguous() and pos.is_cuda):
+            offsets.dtype is i32 and offsets.is_contiguous() and offsets.get_device() == dev and
+            rows.dtype is i32 and rows.shape == (T * k,) and rows.is_contiguous() and rows.get_device() == dev and
+            pos.dtype is i32 and pos.shape == shape and pos.is_contiguous() and pos.get_device() == dev):
         _sizes(T=T, k=k, choices=T * k)
         for t, name, want in ((expert, "expert", shape), (offsets, "offsets", (E + 1,)), (rows, "rows", (T * k,)),
                               (pos, "pos", shape)):
-            _dense(t, name, want, i32)
+            _dense(t, name, want, i32, dev)
     status = load().skg_experts_sort(T, k, _int(E, "experts"), expert.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
                                      pos.data_ptr(), _stream_of(stream, expert))
     if status:
@@ -784,11 +800,13 @@ def skg_experts_gather(x, rows, out, stream=None):
         _bad("x must be [T, N] and rows [R]")
     T, N = x.shape
     R = rows.shape[0]
-    if not (T | N | R < 2**31 and rows.dtype is i32 and rows.is_contiguous() and rows.is_cuda and
-            out.dtype is bf16 and out.shape == (R, N) and out.is_contiguous() and out.is_cuda):
+    dev = x.get_device()
+    if not (T | N | R < 2**31 and rows.dtype is i32 and rows.is_contiguous() and x.is_cuda and rows.get_device() == dev and
+            out.dtype is bf16 and out.shape == (R, N) and out.is_contiguous() and out.get_device() == dev):
         _sizes(T=T, N=N, R=R)
-        _dense(rows, "rows", (R,), i32)
-        _dense(out, "out", (R, N), bf16)
+        _rows(x, "x", x.shape, bf16)
+        _dense(rows, "rows", (R,), i32, dev)
+        _dense(out, "out", (R, N), bf16, dev)
     status = load().skg_experts_gather(R, T, N, x.data_ptr(), _rows(x, "x", x.shape, bf16), rows.data_ptr(), out.data_ptr(),
                                        _stream_of(stream, x))
     if status:
@@ -809,15 +827,18 @@ def skg_experts_combine(y, pos, weight, residual, out, stream=None):
     out bf16 [T, N]."""
     bf16, f32, i32, _ = _dtypes()
     T, k, R, N = _choices(y, pos)
-    if not (pos.dtype is i32 and pos.is_contiguous() and pos.is_cuda and
-            out.dtype is bf16 and out.shape == (T, N) and out.is_contiguous() and out.is_cuda and
-            (weight is None or weight.dtype is f32 and weight.shape == (T, k) and weight.is_contiguous() and weight.is_cuda) and
+    dev = y.get_device()
+    if not (pos.dtype is i32 and pos.is_contiguous() and y.is_cuda and pos.get_device() == dev and
+            out.dtype is bf16 and out.shape == (T, N) and out.is_contiguous() and out.get_device() == dev and
+            (weight is None or weight.dtype is f32 and weight.shape == (T, k) and weight.is_contiguous() and
+             weight.get_device() == dev) and
             (residual is None or residual.dtype is bf16 and residual.shape == (T, N) and residual.is_contiguous() and
-             residual.is_cuda)):
+             residual.get_device() == dev)):
+        _rows(y, "y", y.shape, bf16)
         for t, name, shape, dtype in ((pos, "pos", (T, k), i32), (out, "out", (T, N), bf16), (weight, "weight", (T, k), f32),
                                       (residual, "residual", (T, N), bf16)):
             if t is not None:
-                _dense(t, name, shape, dtype)
+                _dense(t, name, shape, dtype, dev)
     status = load().skg_experts_combine(
         T, k, R, N, y.data_ptr(), _rows(y, "y", y.shape, bf16), pos.data_ptr(), None if weight is None else weight.data_ptr(),
         None if residual is None else residual.data_ptr(), out.data_ptr(), _stream_of(stream, y))
@@ -830,15 +851,19 @@ def skg_experts_combine_grad(grad_out, y, pos, weight, grad_y, grad_weight, stre
     grad_y bf16 [R, N]."""
     bf16, f32, i32, _ = _dtypes()
     T, k, R, N = _choices(y, pos)
-    if not (pos.dtype is i32 and pos.is_contiguous() and pos.is_cuda and
-            grad_out.dtype is bf16 and grad_out.shape == (T, N) and grad_out.is_contiguous() and grad_out.is_cuda and
-            grad_y.dtype is bf16 and grad_y.shape == (R, N) and grad_y.is_contiguous() and grad_y.is_cuda and
-            weight.dtype is f32 and weight.shape == (T, k) and weight.is_contiguous() and weight.is_cuda and
-            grad_weight.dtype is f32 and grad_weight.shape == (T, k) and grad_weight.is_contiguous() and grad_weight.is_cuda):
+    dev = y.get_device()
+    if not (pos.dtype is i32 and pos.is_contiguous() and y.is_cuda and pos.get_device() == dev and
+            grad_out.dtype is bf16 and grad_out.shape == (T, N) and grad_out.is_contiguous() and
+            grad_out.get_device() == dev and
+            grad_y.dtype is bf16 and grad_y.shape == (R, N) and grad_y.is_contiguous() and grad_y.get_device() == dev and
+            weight.dtype is f32 and weight.shape == (T, k) and weight.is_contiguous() and weight.get_device() == dev and
+            grad_weight.dtype is f32 and grad_weight.shape == (T, k) and grad_weight.is_contiguous() and
+            grad_weight.get_device() == dev):
+        _rows(y, "y", y.shape, bf16)
         for t, name, shape, dtype in ((pos, "pos", (T, k), i32), (grad_out, "grad_out", (T, N), bf16),
                                       (grad_y, "grad_y", (R, N), bf16), (weight, "weight", (T, k), f32),
                                       (grad_weight, "grad_weight", (T, k), f32)):
-            _dense(t, name, shape, dtype)
+            _dense(t, name, shape, dtype, dev)
     status = load().skg_experts_combine_grad(
         T, k, R, N, grad_out.data_ptr(), y.data_ptr(), _rows(y, "y", y.shape, bf16), pos.data_ptr(), weight.data_ptr(),
         grad_y.data_ptr(), grad_weight.data_ptr(), _stream_of(stream, y))
