@@ -436,18 +436,16 @@ def _int(v, name) -> int:
     return v
 
 
-def _device(t, name, device):
-    """The tensors of a call are on one device."""
-    if t.get_device() != device:
-        _bad(f"{name} is on device {t.get_device()}, other tensors of this call on {device}")
+def _elsewhere(t, name, device):
+    _bad(f"{name} is on device {t.get_device()}, other tensors of this call on {device}")
 
 
 def _rows(t, name, shape, dtype, device=None) -> int:
     """Row stride of a tensor of `shape` [M, K] whose rows are contiguous."""
     if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
         _bad(f"{name} must be a CUDA tensor {list(shape)} of {dtype}")
-    if device is not None:
-        _device(t, name, device)
+    if device is not None and t.get_device() != device:
+        _elsewhere(t, name, device)
     if t.is_contiguous():
         return shape[1]
     ld, one = t.stride()
@@ -459,20 +457,25 @@ def _rows(t, name, shape, dtype, device=None) -> int:
 def _dense(t, name, shape, dtype, device=None) -> int:
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         _bad(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
-    if device is not None:
-        _device(t, name, device)
+    if device is not None and t.get_device() != device:
+        _elsewhere(t, name, device)
     return t.data_ptr()
 
 
-def _stream_of(stream, t):
-    """The given stream, or the current one of t's device (the raw handle: a
-    decode step's calls are short enough for a Stream object to show), which has
-    to be the current device: kernels are launched there."""
-    import torch
-    device, current = t.get_device(), torch._C._cuda_getDevice()
-    if device != current:
-        _bad(f"the tensors are on device {device}, the current one is {current}")
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+_C = None
+
+
+def _stream_of(stream, device):
+    """The given stream, or the current one of the tensors' device (the raw handle: a
+    decode step's calls are short enough for a Stream object to show), which has to
+    be the current device: kernels are launched there."""
+    global _C
+    if _C is None:
+        import torch
+        _C = torch._C
+    if device != _C._cuda_getDevice():
+        _bad(f"the tensors are on device {device}, the current one is {_C._cuda_getDevice()}")
+    return _C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def skg_rmsnorm_q8(x, residual, gamma, eps: float, h, q, scale, y=None, stream=None):
@@ -483,14 +486,14 @@ def skg_rmsnorm_q8(x, residual, gamma, eps: float, h, q, scale, y=None, stream=N
     if len(shape) != 2:
         _bad("x must be [M, K]")
     M, K = _int(shape[0], "M"), _int(shape[1], "K")
-    ldx = _rows(x, "x", shape, bf16)
-    ldr = 0 if residual is None else _rows(residual, "residual", shape, bf16)
-    ldh = 0 if h is None else _rows(h, "h", shape, bf16)
+    ldx, dev = _rows(x, "x", shape, bf16), x.get_device()
+    ldr = 0 if residual is None else _rows(residual, "residual", shape, bf16, dev)
+    ldh = 0 if h is None else _rows(h, "h", shape, bf16, dev)
     _check(load().skg_rmsnorm_q8(
         M, K, eps, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
-        None if gamma is None else _dense(gamma, "gamma", (K,), bf16), None if h is None else h.data_ptr(), ldh,
-        None if y is None else _dense(y, "y", shape, bf16), _dense(q, "q", shape, torch.int8),
-        _dense(scale, "scale", (M,), torch.float32), _stream_of(stream, x)))
+        None if gamma is None else _dense(gamma, "gamma", (K,), bf16, dev), None if h is None else h.data_ptr(), ldh,
+        None if y is None else _dense(y, "y", shape, bf16, dev), _dense(q, "q", shape, torch.int8, dev),
+        _dense(scale, "scale", (M,), torch.float32, dev), _stream_of(stream, dev)))
 
 
 def skg_quantize_q8(x, gate, q, scale, stream=None):
@@ -500,11 +503,11 @@ def skg_quantize_q8(x, gate, q, scale, stream=None):
     if len(shape) != 2:
         _bad("x must be [M, K]")
     M, K = _int(shape[0], "M"), _int(shape[1], "K")
-    ldx = _rows(x, "x", shape, torch.bfloat16)
-    ldg = 0 if gate is None else _rows(gate, "gate", shape, torch.bfloat16)
+    ldx, dev = _rows(x, "x", shape, torch.bfloat16), x.get_device()
+    ldg = 0 if gate is None else _rows(gate, "gate", shape, torch.bfloat16, dev)
     _check(load().skg_quantize_q8(
-        M, K, x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg, _dense(q, "q", shape, torch.int8),
-        _dense(scale, "scale", (M,), torch.float32), _stream_of(stream, x)))
+        M, K, x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg, _dense(q, "q", shape, torch.int8, dev),
+        _dense(scale, "scale", (M,), torch.float32, dev), _stream_of(stream, dev)))
 
 
 def skg_q8_plan_query(M: int, N: int, K: int, epilogue, num_sms: int) -> dict:
@@ -567,18 +570,19 @@ class Q8Plan:
         # refuses is then named.
         mk, m, nk, n, mn = self._shapes
         i8, f32, bf16, out = self._types
+        dev = x.get_device()
         if not (x.dtype is i8 and x.shape == mk and x.is_contiguous() and x.is_cuda and
-                W.dtype is i8 and W.shape == nk and W.is_contiguous() and W.is_cuda and
-                x_scale.dtype is f32 and x_scale.shape == m and x_scale.is_contiguous() and x_scale.is_cuda and
-                w_scale.dtype is f32 and w_scale.shape == n and w_scale.is_contiguous() and w_scale.is_cuda and
-                y.dtype is out and y.shape == mn and y.is_contiguous() and y.is_cuda):
+                W.dtype is i8 and W.shape == nk and W.is_contiguous() and W.get_device() == dev and
+                x_scale.dtype is f32 and x_scale.shape == m and x_scale.is_contiguous() and x_scale.get_device() == dev and
+                w_scale.dtype is f32 and w_scale.shape == n and w_scale.is_contiguous() and w_scale.get_device() == dev and
+                y.dtype is out and y.shape == mn and y.is_contiguous() and y.get_device() == dev):
             for t, name, shape, dtype in ((x, "x", mk, i8), (x_scale, "x_scale", m, f32), (W, "W", nk, i8),
                                           (w_scale, "w_scale", n, f32), (y, "y", mn, out)):
-                _dense(t, name, shape, dtype)
+                _dense(t, name, shape, dtype, dev)
         if residual is not None:
-            _dense(residual, "residual", mn, bf16)
+            _dense(residual, "residual", mn, bf16, dev)
         status = load().skg_q8_run(self.handle, x.data_ptr(), x_scale.data_ptr(), W.data_ptr(), w_scale.data_ptr(),
-                                   None if residual is None else residual.data_ptr(), y.data_ptr(), _stream_of(stream, x))
+                                   None if residual is None else residual.data_ptr(), y.data_ptr(), _stream_of(stream, dev))
         if status:
             _check(status)
 
@@ -649,7 +653,7 @@ def skg_quantize_f8(x, gate, q, scale, rows=None, stream=None):
     if rows is not None:
         at = _dense(rows, "rows", (M,), i32, dev)
     status = load().skg_quantize_f8(M, K, x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg, at, T,
-                                    q.data_ptr(), scale.data_ptr(), _stream_of(stream, x))
+                                    q.data_ptr(), scale.data_ptr(), _stream_of(stream, dev))
     if status:
         _check(status)
 
@@ -665,7 +669,7 @@ def skg_quantize_f8_weights(W, q, scale, stream=None):
     dev = W.get_device()
     _check(load().skg_quantize_f8_weights(
         E, N, K, _dense(W, "W", shape, torch.bfloat16), _dense(q, "q", shape, torch.float8_e4m3fn, dev),
-        _dense(scale, "scale", (*shape[:-2], _blocks(N), _blocks(K)), torch.float32, dev), _stream_of(stream, W)))
+        _dense(scale, "scale", (*shape[:-2], _blocks(N), _blocks(K)), torch.float32, dev), _stream_of(stream, dev)))
 
 
 def skg_f8_plan_query(M: int, N: int, K: int, epilogue, experts: int, num_sms: int) -> dict:
@@ -743,7 +747,7 @@ class F8Plan:
             _dense(offsets, "offsets", (self.experts + 1,), i32, dev)
         status = load().skg_f8_run(self.handle, x.data_ptr(), x_scale.data_ptr(), W.data_ptr(), w_scale.data_ptr(),
                                    None if residual is None else residual.data_ptr(),
-                                   None if offsets is None else offsets.data_ptr(), y.data_ptr(), _stream_of(stream, x))
+                                   None if offsets is None else offsets.data_ptr(), y.data_ptr(), _stream_of(stream, dev))
         if status:
             _check(status)
 
@@ -788,7 +792,7 @@ def skg_experts_sort(expert, offsets, rows, pos, stream=None):
                               (pos, "pos", shape)):
             _dense(t, name, want, i32, dev)
     status = load().skg_experts_sort(T, k, _int(E, "experts"), expert.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
-                                     pos.data_ptr(), _stream_of(stream, expert))
+                                     pos.data_ptr(), _stream_of(stream, dev))
     if status:
         _check(status)
 
@@ -808,7 +812,7 @@ def skg_experts_gather(x, rows, out, stream=None):
         _dense(rows, "rows", (R,), i32, dev)
         _dense(out, "out", (R, N), bf16, dev)
     status = load().skg_experts_gather(R, T, N, x.data_ptr(), _rows(x, "x", x.shape, bf16), rows.data_ptr(), out.data_ptr(),
-                                       _stream_of(stream, x))
+                                       _stream_of(stream, dev))
     if status:
         _check(status)
 
@@ -841,7 +845,7 @@ def skg_experts_combine(y, pos, weight, residual, out, stream=None):
                 _dense(t, name, shape, dtype, dev)
     status = load().skg_experts_combine(
         T, k, R, N, y.data_ptr(), _rows(y, "y", y.shape, bf16), pos.data_ptr(), None if weight is None else weight.data_ptr(),
-        None if residual is None else residual.data_ptr(), out.data_ptr(), _stream_of(stream, y))
+        None if residual is None else residual.data_ptr(), out.data_ptr(), _stream_of(stream, dev))
     if status:
         _check(status)
 
@@ -866,6 +870,6 @@ def skg_experts_combine_grad(grad_out, y, pos, weight, grad_y, grad_weight, stre
             _dense(t, name, shape, dtype, dev)
     status = load().skg_experts_combine_grad(
         T, k, R, N, grad_out.data_ptr(), y.data_ptr(), _rows(y, "y", y.shape, bf16), pos.data_ptr(), weight.data_ptr(),
-        grad_y.data_ptr(), grad_weight.data_ptr(), _stream_of(stream, y))
+        grad_y.data_ptr(), grad_weight.data_ptr(), _stream_of(stream, dev))
     if status:
         _check(status)

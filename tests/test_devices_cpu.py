@@ -6,7 +6,7 @@ import torch
 
 from projection_gemm_gb300 import skg
 
-BF, F32, I32, F8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+BF, F32, I32, F8, I8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn, torch.int8
 
 
 class OnDevice:
@@ -55,8 +55,20 @@ def f8_plan(epilogue, experts):
     return plan
 
 
+def q8_plan():
+    plan = object.__new__(skg.Q8Plan)
+    plan.handle = None
+    plan._shapes = (4, 256), (4,), (128, 256), (128,), (4, 128)
+    plan._types = I8, F32, BF, BF
+    return plan
+
+
 T = OnDevice
 CALLS = {
+    "rmsnorm_q8": (lambda x, r, g, h, q, s, y, stream=None: skg.skg_rmsnorm_q8(x, r, g, 1e-6, h, q, s, y, stream),
+                   lambda: [T(BF, 4, 256), T(BF, 4, 256), T(BF, 256), T(BF, 4, 256), T(I8, 4, 256), T(F32, 4), T(BF, 4, 256)]),
+    "quantize_q8": (skg.skg_quantize_q8, lambda: [T(BF, 4, 256), T(BF, 4, 256), T(I8, 4, 256), T(F32, 4)]),
+    "Q8Plan.run": (q8_plan().run, lambda: [T(I8, 4, 256), T(F32, 4), T(I8, 128, 256), T(F32, 128), T(BF, 4, 128), T(BF, 4, 128)]),
     "quantize_f8": (skg.skg_quantize_f8, lambda: [T(BF, 4, 256), T(BF, 4, 256), T(F8, 6, 256), T(F32, 6, 2), T(I32, 6)]),
     "quantize_f8_weights": (skg.skg_quantize_f8_weights, lambda: [T(BF, 3, 200, 256), T(F8, 3, 200, 256), T(F32, 3, 2, 2)]),
     "F8Plan.run": (f8_plan("bf16_residual", 3).run, lambda: [T(F8, 4, 256), T(F32, 4, 2), T(F8, 3, 128, 256), T(F32, 3, 1, 2),
