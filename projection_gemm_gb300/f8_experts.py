@@ -17,6 +17,7 @@ usage: python -m projection_gemm_gb300.f8_experts [tokens] [hidden] [inner] [exp
 """
 from __future__ import annotations
 
+import contextlib
 import sys
 
 import torch
@@ -31,6 +32,13 @@ def quantize_weights(W: torch.Tensor):
     scale = torch.empty(E, -(-N // 128), -(-K // 128), dtype=torch.float32, device=W.device)
     skg.skg_quantize_f8_weights(W, q, scale)
     return q, scale
+
+
+def on_stream(stream):
+    """torch's operators on the stream that the library's calls are given: a stream, its handle, or None for the current."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 class F8Experts:
@@ -66,8 +74,9 @@ class F8Experts:
     def route(self, x, stream=None):
         """(expert int32, weight fp32) [T, k]: the k best experts of each token by the router's softmax."""
         self.p_router.run(x, self.W_router, None, self.scores, stream)
-        weight, expert = torch.topk(torch.softmax(self.scores, dim=1), self.k, dim=1)
-        return expert.to(torch.int32), weight
+        with on_stream(stream):
+            weight, expert = torch.topk(torch.softmax(self.scores, dim=1), self.k, dim=1)
+            return expert.to(torch.int32), weight
 
     def run(self, x, residual, expert, weight, stream=None):
         """One step; x, residual bf16 [T, hidden] (residual may be None), expert int32 and weight fp32 [T, k].  Returns
