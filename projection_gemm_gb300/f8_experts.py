@@ -51,7 +51,6 @@ class F8Experts:
         self.T, self.k, self.E, self.hidden, self.inner = T, k, E, hidden, inner
         self.gate_up, self.gate_up_scale = quantize_weights(W_gate_up)
         self.down, self.down_scale = quantize_weights(W_down)
-        torch.cuda.current_stream().synchronize()        # from here on the weights are static
         R, dev = T * k, W_down.device
         self.p_up = skg.F8Plan(R, 2 * inner, hidden, "bf16", experts=E, static_weights=True)
         self.p_down = skg.F8Plan(R, hidden, inner, "bf16", experts=E, static_weights=True)
@@ -70,6 +69,8 @@ class F8Experts:
         if W_router is not None:
             self.p_router = skg.Plan(T, E, hidden, "fp32")      # T <= 64
             self.scores = empty(T, E, dtype=torch.float32)
+        # from here on the weights are static, and the zeros there for a step on any stream
+        torch.cuda.current_stream().synchronize()
 
     def route(self, x, stream=None):
         """(expert int32, weight fp32) [T, k]: the k best experts of each token by the router's softmax."""

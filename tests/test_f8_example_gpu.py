@@ -42,3 +42,18 @@ def test_route_reads_its_own_scores_on_the_given_stream(handle):
     assert torch.equal(expert, want_expert) and torch.equal(weight, want_weight)
     layer.check()
     layer.close()
+
+
+def test_a_new_layer_is_there_for_a_step_on_any_stream(monkeypatch):
+    """What it starts its buffers with has been written when it is handed out, so that it cannot land in a step's."""
+    given = weights()
+    zeros = torch.zeros
+
+    def late(*args, **kw):
+        torch.cuda._sleep(LONG)
+        return zeros(*args, **kw)
+
+    monkeypatch.setattr(torch, "zeros", late)
+    layer = F8Experts(T, K_BEST, *given)
+    assert torch.cuda.current_stream().query()
+    layer.close()
