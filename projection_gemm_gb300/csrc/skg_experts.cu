@@ -200,7 +200,8 @@ __device__ __forceinline__ uint32_t two_bf16(float a, float b)
     return f32_to_bf16(a) | static_cast<uint32_t>(f32_to_bf16(b)) << 16;
 }
 
-// V elements at a time: as many of 8, 4, 2, 1 as every row's alignment allows.
+// V elements at a time: as many of 8, 4, 2, 1 as every row's alignment allows.  (The
+// loads' "memory" keeps a row's stores behind them where gradients take y's place.)
 template <int V>
 struct Piece;
 
@@ -209,7 +210,7 @@ struct Piece<8> {
     uint4 w;
     __device__ __forceinline__ void load(const uint16_t *p)
     {
-        asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
+        asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p) : "memory");
     }
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void store(uint16_t *p) const { __stcs(reinterpret_cast<uint4 *>(p), w); }
@@ -229,7 +230,7 @@ struct Piece<4> {
     uint2 w;
     __device__ __forceinline__ void load(const uint16_t *p)
     {
-        asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+        asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p) : "memory");
     }
     __device__ __forceinline__ void zero() { w = make_uint2(0, 0); }
     __device__ __forceinline__ void store(uint16_t *p) const { __stcs(reinterpret_cast<uint2 *>(p), w); }
@@ -240,7 +241,7 @@ struct Piece<4> {
 template <>
 struct Piece<2> {
     uint32_t w;
-    __device__ __forceinline__ void load(const uint16_t *p) { asm volatile("ld.global.u32 %0, [%1];" : "=r"(w) : "l"(p)); }
+    __device__ __forceinline__ void load(const uint16_t *p) { asm volatile("ld.global.u32 %0, [%1];" : "=r"(w) : "l"(p) : "memory"); }
     __device__ __forceinline__ void zero() { w = 0; }
     __device__ __forceinline__ void store(uint16_t *p) const { __stcs(reinterpret_cast<uint32_t *>(p), w); }
     __device__ __forceinline__ void get(float (&v)[2]) const { v[0] = bf16lo(w), v[1] = bf16hi(w); }
@@ -250,7 +251,7 @@ struct Piece<2> {
 template <>
 struct Piece<1> {
     uint16_t w;
-    __device__ __forceinline__ void load(const uint16_t *p) { asm volatile("ld.global.u16 %0, [%1];" : "=h"(w) : "l"(p)); }
+    __device__ __forceinline__ void load(const uint16_t *p) { asm volatile("ld.global.u16 %0, [%1];" : "=h"(w) : "l"(p) : "memory"); }
     __device__ __forceinline__ void zero() { w = 0; }
     __device__ __forceinline__ void store(uint16_t *p) const { *p = w; }
     __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = bf16_to_f32(w); }
