@@ -28,10 +28,9 @@
 // x 7168 212 us, where the wide kernel's tiles of 128 take 62.
 //
 // Every wait is bounded; on expiry a thread records the timeout in the plan's error
-// word and raises the CTA's abort flag, and the issuer waits for its MMAs.  Once
-// every role has ended the producer waits for its copies in flight, and the CTA goes on
-// to the cluster's barriers, frees its TMEM and returns.  (That the roles meet before
-// the cluster does takes 0.1 to 0.2 us.)
+// word and raises the CTA's abort flag, and the issuer waits for its MMAs.  The CTA
+// goes on to the cluster's barriers; behind them, every role having ended, the producer
+// waits for its copies in flight, and the CTA frees its TMEM and returns.
 #include <algorithm>
 
 #include "skg_f8_internal.h"
@@ -349,17 +348,19 @@ f8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 
     __syncwarp();
     tc_fence_before();
-    __syncthreads();                     // from here on no role raises the abort flag any more
-    if (issued && flags[0]) {            // abort: every copy lands before sums are read in the ring's place and before exit
-        volatile int never = 0;
-        for (int u = max(0, issued - S); u < issued; ++u)
-            mbar_wait(&full[u % S], (u / S) & 1, kDefaultTimeoutNs, &never);
-    }
-    __syncwarp();
     if (p.split > 1) {
         const F8Tile t = f8_tile(p, MT, table, first);
         const int n0[1] = {f8_w_window(p, t.e, t.nt * kTileN) - t.e * p.N}, na[1] = {t.nt * kTileN};
         f8_join<kF8SplitMax, Sh::kThreads, 1>(p, smem_u32(smem), f8_x_window(p, t.m0), t.m0, min(t.m1, t.m0 + MT), n0, na, rank, 0, 1);
+    } else {
+        __syncthreads();
+    }
+    // Abort: every copy lands before the CTA exits.  (Looked at here, where no role raises the
+    // flag any more; what a join has read meanwhile is of a launch that is reported.)
+    if (issued && flags[0]) {
+        volatile int never = 0;
+        for (int u = max(0, issued - S); u < issued; ++u)
+            mbar_wait(&full[u % S], (u / S) & 1, kDefaultTimeoutNs, &never);
     }
     if (warp == Sh::kMmaWarp) {
         tc_fence_after();

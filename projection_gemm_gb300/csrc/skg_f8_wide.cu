@@ -55,8 +55,6 @@ namespace {
 
 #include "skg_f8_tc_common.cuh"
 
-constexpr uint64_t kLandNs = 10000000;               // 10 ms: far longer than any copy takes
-
 template <int PAIR>
 struct WideShape {
     static constexpr int MT = 128 * PAIR, NT = 128 * PAIR;   // tokens and channels of a tile
@@ -431,14 +429,11 @@ f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     __syncwarp();
     tc_fence_before();
     __syncthreads();                     // from here on no role raises the abort flag any more
-    // Abort: every copy lands, a few microseconds after its issue, before sums are read in the
-    // ring's place and before exit.  (By time: the second CTA's copies are counted in the
-    // first, whose abort that one learns of as its accumulators stay away.)
-    if (warp == Sh::kTmaWarp && flags[0]) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < kLandNs) {
-        }
-    }
+    // Abort: every copy lands before sums are read in the ring's place and before exit.  (By
+    // time: the second CTA's copies are counted in the first, whose abort that one
+    // learns of as its accumulators stay away.)
+    if (warp == Sh::kTmaWarp && flags[0])
+        wait_landed();
     if (p.split > 1) {
         const F8Tile t = f8_tile(p, MT, table, first);
         const int ma = t.m0 + rank * 128;

@@ -258,7 +258,6 @@ __global__ void __launch_bounds__(kTcThreads, (MPAD <= 32) ? 3 : 2) splitk_group
                 }
                 if (armed < pre) {
                     group_failure(g, &flags[0], kErrTimeoutProducer);
-                    it += armed;      // the drain below waits for these copies
                     ok = false;
                     break;
                 }
@@ -272,8 +271,6 @@ __global__ void __launch_bounds__(kTcThreads, (MPAD <= 32) ? 3 : 2) splitk_group
                         if (!wait_counter(&g.done[U.j - 1], static_cast<unsigned>(g.proj[U.j - 1].n_tiles),
                                           g.timeout_ns, &flags[0])) {
                             group_failure(g, &flags[0], kErrTimeoutProducer);
-                            // the W copies above were issued: wait for them below
-                            it += pre;
                             ok = false;
                             break;
                         }
@@ -297,16 +294,6 @@ __global__ void __launch_bounds__(kTcThreads, (MPAD <= 32) ? 3 : 2) splitk_group
                     mbar_arrive_expect_tx(&full[s], kWBytes + Sh::kXBytes);
                     tma_load_2d(sW + s * kWBytes, &P.tmW, &full[s], (U.kb_begin + i) * kBlockK, tile_row, pol_w);
                     tma_load_2d(sX + s * Sh::kXBytes, &P.tmX, &full[s], (U.kb_begin + i) * kBlockK, 0, pol_x);
-                }
-            }
-            if (flags[0]) {
-                // Abort: copies this thread issued land before the CTA exits.
-                // (A stage armed for W and x whose x never came cannot
-                // complete; its W bytes have landed once the wait times out.)
-                for (int s = 0; s < S && s < it; ++s) {
-                    const int last = s + S * ((it - 1 - s) / S);
-                    volatile int never = 0;
-                    mbar_wait(&full[s], (last / S) & 1, g.timeout_ns, &never);
                 }
             }
         }
@@ -535,6 +522,11 @@ __global__ void __launch_bounds__(kTcThreads, (MPAD <= 32) ? 3 : 2) splitk_group
             g.done[kGroupDoneExit] = 0;
         }
     }
+    // Abort: copies of this CTA land before it exits.  (Looked at here, where
+    // no role raises the flag any more; by time, as a stage armed for W and x
+    // whose x never came cannot complete.)
+    if (warp == 0 && flags[0])
+        wait_landed();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, Sh::kTmemCols);

@@ -199,6 +199,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
+// Of a CTA that aborts: long enough (10 ms) for every copy that it has issued to land,
+// which takes a few microseconds.
+__device__ __forceinline__ void wait_landed()
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 10000000) {
+    }
+}
+
 // Contiguous global -> shared copy by the copy engine (no tensor map):
 // both addresses 16-byte aligned, bytes a multiple of 16; completion is
 // counted in bytes on `bar`.

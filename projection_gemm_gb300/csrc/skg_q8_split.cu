@@ -35,9 +35,10 @@
 // units requested in pairs, or another start in K for each tile changed nothing
 // (28.8, 29.3, 28.2 us).
 //
-// Every wait is bounded; on expiry a thread records the timeout in the plan's
-// error word, raises the CTA's abort flag, waits for its own copies and MMAs,
-// and the CTA goes on to the cluster's barriers, frees its TMEM and returns.
+// Every wait is bounded; on expiry a thread records the timeout in the plan's error
+// word and raises the CTA's abort flag, and the issuer waits for its MMAs.  The CTA
+// goes on to the cluster's barriers; behind them, every role having ended, the producer
+// waits for its copies in flight, and the CTA frees its TMEM and returns.
 #include <algorithm>
 
 #include "skg_internal.h"
@@ -134,6 +135,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         pdl_wait();
     }
 
+    int issued = 0;                      // units whose copies this thread has issued
     if (warp == Sh::kTmaWarp) {
         // -------------------------------------------------------- TMA producer
         if (lane == 0) {
@@ -165,11 +167,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 load_w(j);
                 load_x(j);
             }
-            if (flags[0]) {              // abort: let every copy land before exit
-                volatile int never = 0;
-                for (int k = 0; k < S && k < j; ++k)
-                    mbar_wait(&wfull[k], ((j - 1 - k) / S) & 1, kDefaultTimeoutNs, &never);
-            }
+            issued = j;
         }
     } else if (warp == Sh::kMmaWarp) {
         // ---------------------------------------------------------- MMA issuer
@@ -362,6 +360,13 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         join_and_store<8, Sh::kThreads>(p.g, smem_u32(smem), m0, n0, min(MT, p.g.M - m0), p.split, rank, 1, 0, p.vec4 != 0);
     } else {
         __syncthreads();
+    }
+    // Abort: every copy lands before the CTA exits.  (Looked at here, where no role raises the
+    // flag any more; what a join has read meanwhile is of a launch that is reported.)
+    if (issued && flags[0]) {
+        volatile int never = 0;
+        for (int u = max(0, issued - S); u < issued; ++u)
+            mbar_wait(&wfull[u % S], (u / S) & 1, kDefaultTimeoutNs, &never);
     }
     if (warp == Sh::kMmaWarp) {
         tc_fence_after();

@@ -194,16 +194,6 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     auto wait_widened = [&](uint32_t u) {
         return u < S || __all_sync(0xFFFFFFFFu, mbar_wait(&widened[(u - S) % XOPS], (u - S) / XOPS & 1, p.timeout_ns, &flags[0]));
     };
-    // A producer's end: on an abort, every copy of its first u units lands before it exits.
-    auto drain_ring = [&](bool ok, uint32_t u) {
-        if (!ok)
-            q8_fail(p.err, &flags[0], kErrTimeoutProducer);
-        if (flags[0]) {
-            volatile int never = 0;
-            for (uint32_t k = 0; k < S && k < u; ++k)
-                mbar_wait(&full[k], (u - 1 - k) / S & 1, kDefaultTimeoutNs, &never);
-        }
-    };
     // x of the second CTA's pairs of units r, r + 2, ... has been widened: passed on to the issuer.
     auto relay = [&](int r) {
         bool ok = true;
@@ -252,7 +242,8 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 load(u, kb);
             }
         }
-        drain_ring(ok, max(u, ahead));
+        if (!ok)
+            q8_fail(p.err, &flags[0], kErrTimeoutProducer);
     } else if (warp == Sh::kTmaXWarp) {
         // ------------------------------------------------------ TMA producer of x
         const bool leader = elect_one();
@@ -292,11 +283,8 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 mbar_arrive(&full[u % S]);
             __syncwarp();
         }
-        if (flags[0]) {
-            volatile int never = 0;
-            mbar_wait(x0full, 0, kDefaultTimeoutNs, &never);
-        }
-        drain_ring(ok, issued);
+        if (!ok)
+            q8_fail(p.err, &flags[0], kErrTimeoutProducer);
     } else if (warp == Sh::kMmaWarp) {
         // ---------------------------------------------------------- MMA issuer
         if (rank == 0) {
@@ -455,6 +443,10 @@ q8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 
     __syncwarp();
     tc_fence_before();
+    __syncthreads();                     // from here on no role raises the abort flag any more
+    // Abort: every copy lands before sums are read in the ring's place and before exit.
+    if (warp == Sh::kTmaWarp && flags[0])
+        wait_landed();
     if (p.split == 1) {
         cluster_sync();                  // no CTA leaves while its peer may still send to it
     } else {

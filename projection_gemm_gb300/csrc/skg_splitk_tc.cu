@@ -145,6 +145,7 @@ splitk_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         tmem_base = *tmem_slot;
     }
 
+    int issued = 0;       // k-blocks whose copies this thread has issued
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         if (lane == 0 && nk > 0) {
@@ -164,7 +165,7 @@ splitk_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             pdl_wait();  // activations only from here on
             for (int i = 0; i < pre; ++i)
                 tma_load_2d(sX + i * Sh::kXBytes, &tmX, &full[i], (kb_begin + i) * kBlockK, 0, pol_x);
-            int issued = pre;
+            issued = pre;
             // Steady state: wait until `burst` consecutive ring slots are free,
             // then request their k-blocks back to back, so the bytes of each
             // W row arrive at the memory system together.
@@ -196,14 +197,6 @@ splitk_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             // launch to ask the L2 for this CTA's slice of the next
             // projection's weight.
             prefetch_next_slice(p.next_w, p.next_bytes, blockIdx.x, gridDim.x, policy_evict_last());
-            if (flags[0]) {
-                // Abort: let every copy this thread issued land before exit.
-                for (int s = 0; s < S && s < issued; ++s) {
-                    const int last = s + S * ((issued - 1 - s) / S);
-                    volatile int never = 0;
-                    mbar_wait(&full[s], (last / S) & 1, p.timeout_ns, &never);
-                }
-            }
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
@@ -381,6 +374,15 @@ splitk_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (issued && flags[0]) {
+        // Abort: let every copy this thread issued land before exit.  (Looked
+        // at here, where no role raises the flag any more.)
+        for (int s = 0; s < S && s < issued; ++s) {
+            const int last = s + S * ((issued - 1 - s) / S);
+            volatile int never = 0;
+            mbar_wait(&full[s], (last / S) & 1, p.timeout_ns, &never);
+        }
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, Sh::kTmemCols);

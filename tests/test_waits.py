@@ -1,6 +1,7 @@
-"""Waits of the 8-bit floating point path's tcgen05 kernels.  What they order cannot be
-seen from their results, so their source is read; the forms that they belong to
-are then run again and again beside each other."""
+"""Waits of the tcgen05 kernels.  What they order, and what becomes of a launch one of
+whose waits runs out, cannot be seen from results, so their source is read; the
+pairs of CTAs of the 8-bit floating point path are then run again and again
+beside each other."""
 import os
 import re
 
@@ -26,19 +27,24 @@ def test_waits_of_a_pair_are_at_cluster_scope():
     assert (pair, single) == ("mbar_wait_cluster", "mbar_wait")
 
 
-@pytest.mark.parametrize("name,landed", [("skg_f8_split.cu", "mbar_wait(&full["), ("skg_f8_wide.cu", "kLandNs")])
-def test_copies_land_before_a_cta_that_aborts_goes_on(name, landed):
+@pytest.mark.parametrize("name,fail,landed,before", [
+    ("skg_f8_split.cu", "f8_fail", "mbar_wait(&full[", "tmem_dealloc"),
+    ("skg_f8_wide.cu", "f8_fail", "wait_landed()", "cluster_sync();"),
+    ("skg_q8_split.cu", "q8_fail", "mbar_wait(&wfull[", "tmem_dealloc"),
+    ("skg_q8_wide.cu", "q8_fail", "wait_landed()", "cluster_sync();"),
+    ("skg_splitk_tc.cu", "record_failure", "mbar_wait(&full[", "tmem_dealloc"),
+    ("skg_group_tc.cu", "group_failure", "wait_landed()", "tmem_dealloc")])
+def test_copies_land_before_a_cta_that_aborts_leaves(name, fail, landed, before):
     """Whoever raises the abort flag may do so long after the producer's last copy, so the flag is looked at when every
-    role has ended, before sums are read in the ring's place, before the cluster's last barrier and before exit."""
+    role has ended; and before exit, or, where a peer's copies are counted here, before the pair's last barrier."""
     src = kernel_source(name)
-    src = src[:src.index("cudaError_t launch_shape")]
-    raised = src.rindex("f8_fail(")
-    met = src.index("__syncthreads();", raised)
-    looked = re.search(r"if \([^{;]*flags\[0\]\) \{", src[met:])
+    src = src[:src.index("\ncudaError_t ")]
+    met = src.index("__syncthreads();", src.rindex(fail + "("))
+    looked = re.search(r"if \([^{;]*flags\[0\]\)", src[met:])
     assert looked
     looked = met + looked.start()
-    assert looked < src.index(landed, looked) < src.index("f8_join<", looked)
-    assert not re.search(r"if \([^{;]*flags\[0\]\)", src[:met])          # and not only sooner
+    assert looked < src.index(landed, looked) < src.index(before, met)
+    assert not re.search(r"if \([^{;&]*flags\[0\]\) \{", src[:met])      # and not only sooner
 
 
 @pytest.mark.gpu
