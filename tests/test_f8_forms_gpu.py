@@ -75,3 +75,28 @@ def test_special_values_in_every_block_of_a_warp(M, K):
     q, s = rows_out(M, K)
     skg.skg_quantize_f8(x, None, q, s)
     R.check_quantised(x, q, s)
+
+
+@pytest.mark.parametrize("M,K,tall", [(512, 7168, 1), (300, 2051, 1), (1001, 1040, 128)])
+def test_numbers_are_the_nearest_to_the_exact_quotient_but_for_ties(M, K, tall):
+    """Of v 448 / max, in 64 bits.  In steps of e4m3 it is 448 V / (A 2^m), V and A of 8 bits: half way between two
+    numbers, or at least 1 / (2 A 2^m) off that, which is above 1e-8 wherever a number that is not 0 is near.  The fp32
+    product is off by 2 units of 2^-24, so only a tie T can fall on the other side: where 448 / max is rounded by d and
+    the product's exact T (1 + d) is half a unit or more from T.  (That goes by the maximum: of one block no tie may, or
+    a good part of them, so there is no share to hold them to.)"""
+    v = normal(torch.Generator().manual_seed(M + K), M, K, std=1.5)
+    q = torch.empty(M, K, dtype=R.F8, device="cuda")
+    mb, kb = -(-M // tall), R.blocks(K)
+    s = torch.empty(mb, kb, device="cuda")
+    if tall > 1:
+        skg.skg_quantize_f8_weights(v, q, s)
+    else:
+        skg.skg_quantize_f8(v, None, q, s)
+    pad = torch.nn.functional.pad(v.double(), (0, kb * 128 - K, 0, mb * tall - M)).view(mb, tall, kb, 128)
+    t = (pad * 448 / pad.abs().amax(dim=(1, 3), keepdim=True)).view(mb * tall, kb * 128)[:M, :K]
+    steps = t / R.step(t)
+    tie = (steps - steps.floor() - 0.5).abs() < 1e-10
+    off = (q.double() - t).abs() > R.step(t) * (0.5 + 1e-10)
+    assert not bool(off.any())                              # a tie gives either neighbour
+    wrong = (q.double() - R.e4m3(t)) != 0
+    assert bool((tie | ~wrong).all()) and 0 < int(tie.sum()) < M * K // 50
