@@ -732,6 +732,8 @@ SKG_API skg_status skg_experts_combine(int T, int k, int R, int N, const void *y
  *   grad_weight[t,j] = <grad_out[t], y[pos[t,j]]>, fp32, 0 where a choice was left out
  *   grad_out bf16 [T, N] dense; the others as for skg_experts_combine.  (The
  *   residual's gradient is grad_out itself.)  grad_y may be y where ldy = N
+ * From grad_y a program goes on through the projections that it trains; the 8-bit
+ * ones above have no gradients.
  * A sorted row belongs to one choice: where pos has the same row twice, each element
  * of grad_y is of one of the two (and where grad_y is y, their grad_weight may be of
  * a row that has been written already).

@@ -29,8 +29,9 @@ namespace {
 // A block's scale and the factor that takes a value to its e4m3 number, from the
 // bits of max|v| (|NaN| > infinity > every finite value, as integers).  A block of
 // zeros has scale 0.  One with a value that is not finite has scale NaN and
-// numbers 0, so that whatever it multiplies is NaN.  Below 1e-30 the quotient 448 /
-// max would leave fp32's range: both are raised by 2^100, which is exact.
+// numbers 0, so that whatever it multiplies is NaN.  Below 1.3e-36 the quotient 448 /
+// max would leave fp32's range: from 1e-30 down, a margin, both are raised by 2^100,
+// which is exact.
 struct BlockScale {
     float scale, up, factor;
 };
@@ -105,7 +106,10 @@ __device__ __forceinline__ Numbers to_e4m3(Values<16> e, const BlockScale &b)
     return n;
 }
 
-// silu(g) x.
+// silu(g) x, by the fast exponential.  Of 201 million gated normal values 573 get another
+// number than in 64 bits, in plain 32-bit operations 588, with expf 555, with expf and
+// an IEEE quotient 554: what is left is v's rounding beside a border.  expf takes 4096 x
+// 16384 from 60 to 70 us, with the quotient to 80.
 template <int N>
 __device__ __forceinline__ Values<N> gated(const Values<N> &g, const Values<N> &x)
 {

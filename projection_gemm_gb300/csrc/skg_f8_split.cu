@@ -10,7 +10,7 @@
 // What bounds it is W's way from HBM.  Tile: 128 rows of W are the MMA's M (the
 // scale of a weight block is then one number), MT tokens its N.  A cluster of S
 // CTAs computes a tile, CTA r the r-th part of K; with S = 1 CTAs are persistent
-// over tiles.  Two CTAs an SM, with 160 to 190 KB of W on its way.  Roles of a CTA:
+// over tiles.  Two CTAs an SM, with 160 KB of W on its way (128 KB at 64 tokens).  Roles of a CTA:
 //   1 + 1     TMA; TMEM and MMA issue
 //   4         accumulators into registers, and the tile's end: residual,
 //             rounding, store
@@ -20,7 +20,7 @@
 //
 // Measured, weights from HBM (copy peak 6.71 TB/s): 1 x 12288 x 7168 15.5 us (5.7 TB/s
 // of weights), 16 x 7168 x 16384 21.4, 64 x 7168 x 16384 23.7 (5.0), 64 x 7168 x 7168
-// 13.4; 128 rows of 384 experts, 2048 x 4096, 111 to 123 us (6.2 to 6.9 TB/s); one
+// 13.4; 128 rows of 384 experts, 2048 x 4096, 108 to 123 us (6.2 to 7.1 TB/s); one
 // token's 8 experts of 384, 2048 x 4096, 13.9 us, of 64, 1024 x 1024, 5.9 us.  A
 // launch's ends take 3 to 5 us (with experts the offsets are read first); between
 // them W comes at 6.3 TB/s.  Unsplit, 64 x 7168 x 7168 takes 21 us; 128 tokens a tile, in

@@ -27,7 +27,7 @@
 // once a unit, and the accumulator is free again only when they have.  Measured:
 // 4096 x 12288 x 7168 269-301 us (2.4 to 2.7 PFLOP/s; cuBLAS reaches 1.96 in bf16), of which
 // 8% is the last of 10.1 waves; 1024 x 7168 x 7168 52 us; 16384 rows of 32 experts,
-// 4096 x 4096, 268-302 us; by tiles of 128: 128 x 7168 x 7168 17.0 us (K split in 2; 22 unsplit),
+// 4096 x 4096, 268-313 us; by tiles of 128: 128 x 7168 x 7168 17.0 us (K split in 2; 22 unsplit),
 // 256 x 4096 x 4096 12.8, 333 x 5001 x 4112 20.1 (rows that begin 16 bytes off a line:
 // 16 with K = 4096), 2048 rows of 32 experts, 4096 x 4096, 108 (5.0 TB/s of weights).
 // Steps at 4096 x 4864 x 7168, now 105 us (with, and without it at that step):

@@ -610,7 +610,7 @@ class Q8Plan:
 # --------------------------------------------- the 8-bit floating point path
 # The calls of a decode step take the GPU a few microseconds each, so what they
 # check is one expression, as in Q8Plan.run (skg_experts_combine 7.1 us of host time
-# with a call a tensor, 4.6 so); what that refuses is then named.
+# with a call a tensor, 5.5 so); what that refuses is then named.
 _types = ()
 
 
